@@ -149,6 +149,176 @@ def attn_decode(q, k, v, *, scale=None, workspace=None, out=None, lse=None, stre
     return out, lse
 
 
+def _on_stream(device, stream):
+    """(raw stream handle, torch stream when it is not ``device``'s current one)
+    for a call over tensors of ``device``."""
+    import torch
+
+    current = torch.cuda.current_stream(device)
+    if stream is None:
+        return int(current.cuda_stream), None
+    if isinstance(stream, int):
+        if stream == int(current.cuda_stream):
+            return stream, None
+        return stream, torch.cuda.ExternalStream(stream, device=device)
+    return int(stream.cuda_stream), None if stream == current else stream
+
+
+def _keep_for(stream, *tensors):
+    """Memory allocated here for a call on another stream than the current one
+    must not be handed out again before that stream is done with it."""
+    if stream is not None:
+        for t in tensors:
+            t.record_stream(stream)
+
+
+def _cuda_tensor(name, t, shape, dtype, device=None):
+    """A contiguous CUDA tensor of this shape (None: any size) and dtype, on
+    ``device``."""
+    import torch
+
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dtype:
+        raise TypeError(f"{name} must be a {str(dtype).replace('torch.', '')} CUDA tensor")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the other tensors are on {device}")
+    if t.dim() != len(shape) or any(a is not None and a != b for a, b in zip(shape, t.shape)):
+        want = ", ".join("*" if a is None else str(a) for a in shape)
+        raise ValueError(f"{name} must be [{want}], not {list(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t
+
+
+def attn_decode_ragged_workspace_bytes(B, C, n_q, n_kv, d_h=128, weighted=False) -> int:
+    return int(_abi.load().attn_decode_ragged_workspace_bytes(
+        int(B), int(C), int(n_q), int(n_kv), int(d_h), int(bool(weighted))))
+
+
+def attn_decode_ragged_fwd(q, k, v, lens, weights, o, lse, workspace, workspace_bytes, B, C, n_q,
+                           n_kv, d_h, scale, stream=None) -> int:
+    """Direct call of the ragged decode C entry point; returns the raw status code."""
+    lib = _abi.load()
+    return int(lib.attn_decode_ragged_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(lens), _ptr(weights),
+                                          _ptr(o), _ptr(lse), _ptr(workspace),
+                                          int(workspace_bytes), int(B), int(C), int(n_q),
+                                          int(n_kv), int(d_h), float(scale),
+                                          _stream_handle(stream)))
+
+
+def attn_decode_ragged(q, k, v, lens, *, weights=None, scale=None, workspace=None, out=None,
+                       lse=None, stream=None):
+    """One decode step against caches of different lengths: q bf16 [B, 1, n_q, 128],
+    k/v bf16 [B, C, n_kv, 128] of which sequence b holds the first lens[b]
+    positions (lens: int32 CUDA tensor [B], clamped to 0 .. C).
+
+    Returns (o bf16 [B, 1, n_q, 128], lse fp32 [B, n_q, 1]); a sequence of
+    length 0 gets o = 0 and lse = -inf. ``weights`` (fp32 [B, n_kv, C]), when
+    given, is updated in place: every cached position's softmax weight, summed
+    over its group's query heads, is added to it. ``workspace`` (at least
+    attn_decode_ragged_workspace_bytes bytes) is allocated with torch when not
+    given."""
+    import torch
+
+    bf16 = torch.bfloat16
+    B, _, n_q, d = _cuda_tensor("q", q, (None, 1, None, None), bf16).shape
+    dev = q.device
+    C, n_kv = _cuda_tensor("k", k, (B, None, None, d), bf16, dev).shape[1:3]
+    _cuda_tensor("v", v, tuple(k.shape), bf16, dev)
+    _cuda_tensor("lens", lens, (B,), torch.int32, dev)
+    if weights is not None:
+        _cuda_tensor("weights", weights, (B, n_kv, C), torch.float32, dev)
+    if out is not None:
+        _cuda_tensor("out", out, tuple(q.shape), bf16, dev)
+    if lse is not None:
+        _cuda_tensor("lse", lse, (B, n_q, 1), torch.float32, dev)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    need = attn_decode_ragged_workspace_bytes(B, C, n_q, n_kv, d, weights is not None)
+    if need < 0:
+        raise AttnError(_abi.ATTN_ERR_UNSUPPORTED, "attn_decode_ragged_workspace_bytes")
+    with torch.cuda.device(dev):
+        handle, other = _on_stream(dev, stream)
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            _keep_for(other, workspace)
+        if out is None:
+            out = torch.empty_like(q)
+            _keep_for(other, out)
+        if lse is None:
+            lse = torch.empty((B, n_q, 1), dtype=torch.float32, device=dev)
+            _keep_for(other, lse)
+        nbytes = workspace.numel() * workspace.element_size()
+        st = attn_decode_ragged_fwd(q, k, v, lens, weights, out, lse, workspace, nbytes, B, C, n_q,
+                                    n_kv, d, scale, handle)
+    if st != _abi.ATTN_OK:
+        raise AttnError(st, "attn_decode_ragged_fwd")
+    return out, lse
+
+
+def attn_cache_evict(k, v, weights, lens, k_out, v_out, weights_out, lens_out, index, B, C, C_out,
+                     budget, recent, n_kv, d_h, elem_bytes, stream=None) -> int:
+    """Direct call of the eviction C entry point; returns the raw status code."""
+    lib = _abi.load()
+    return int(lib.attn_cache_evict(_ptr(k), _ptr(v), _ptr(weights), _ptr(lens), _ptr(k_out),
+                                    _ptr(v_out), _ptr(weights_out), _ptr(lens_out), _ptr(index),
+                                    int(B), int(C), int(C_out), int(budget), int(recent),
+                                    int(n_kv), int(d_h), int(elem_bytes),
+                                    _stream_handle(stream)))
+
+
+def attn_evict(k, v, weights, lens, budget, recent=0, *, capacity=None, k_out=None, v_out=None,
+               weights_out=None, lens_out=None, index=None, stream=None):
+    """Brings caches down to ``budget`` positions per sequence and K/V head: the
+    last ``recent`` ones and, of those before them, the ones of largest
+    accumulated weight (ties to the lowest position); shorter caches are kept
+    whole.
+
+    k, v: bf16 or float8_e4m3fn [B, C, n_kv, d_h], d_h 64 or 128; weights fp32
+    [B, n_kv, C] (as attn_key_weights and attn_decode_ragged accumulate it);
+    lens int32 [B]. Returns (k_out, v_out [B, capacity, n_kv, d_h], weights_out
+    [B, n_kv, capacity], lens_out [B], index int32 [B, n_kv, budget]): kept
+    positions in order, weights_out zero and index -1 past lens_out. Rows of
+    k_out and v_out past lens_out are left as they were (unspecified when
+    allocated here). ``capacity`` (that of k_out when given, else ``budget``) is
+    the room of the new caches. Outputs must not overlap the inputs."""
+    import torch
+
+    if not isinstance(k, torch.Tensor) or k.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+        raise TypeError("k must be a bfloat16 or float8_e4m3fn CUDA tensor")
+    B, C, n_kv, d = _cuda_tensor("k", k, (None, None, None, None), k.dtype).shape
+    dev = k.device
+    _cuda_tensor("v", v, tuple(k.shape), k.dtype, dev)
+    _cuda_tensor("weights", weights, (B, n_kv, C), torch.float32, dev)
+    _cuda_tensor("lens", lens, (B,), torch.int32, dev)
+    budget, recent = int(budget), int(recent)
+    if budget < 1 or not 0 <= recent <= budget:
+        raise ValueError("budget must be at least 1 and recent between 0 and budget")
+    if capacity is None:
+        capacity = budget if k_out is None or k_out.dim() != 4 else k_out.shape[1]
+    if capacity < budget:
+        raise ValueError("the new capacity must hold the budget")
+    wanted = {"k_out": (k_out, (B, capacity, n_kv, d), k.dtype),
+              "v_out": (v_out, (B, capacity, n_kv, d), k.dtype),
+              "weights_out": (weights_out, (B, n_kv, capacity), torch.float32),
+              "lens_out": (lens_out, (B,), torch.int32),
+              "index": (index, (B, n_kv, budget), torch.int32)}
+    with torch.cuda.device(dev):
+        handle, other = _on_stream(dev, stream)
+        outs = []
+        for name, (t, shape, dtype) in wanted.items():
+            if t is None:
+                t = torch.empty(shape, dtype=dtype, device=dev)
+                _keep_for(other, t)
+            else:
+                _cuda_tensor(name, t, shape, dtype, dev)
+            outs.append(t)
+        st = attn_cache_evict(k, v, weights, lens, *outs, B, C, capacity, budget, recent, n_kv, d,
+                              k.element_size(), handle)
+    if st != _abi.ATTN_OK:
+        raise AttnError(st, "attn_cache_evict")
+    return tuple(outs)
+
+
 def attn_prefill_bwd_workspace_bytes(B, L, n_q, n_kv, d_h=128) -> int:
     return int(_abi.load().attn_prefill_bwd_workspace_bytes(int(B), int(L), int(n_q), int(n_kv),
                                                             int(d_h)))

@@ -27,6 +27,20 @@
 //                 output and log-sum-exp to the workspace.
 //   combine       one CTA per (b, query head) merges the head's segments
 //                 through their log-sum-exps into bf16 O and fp32 LSE.
+//
+// The ragged step (caches of lens[b] positions in tensors of capacity C) is
+// the same split kernel over n_kv * sum_b ceil(lens[b] / 128) key tiles. The
+// lengths live on the device, so each CTA finds its range itself from their
+// prefix sums; a segment's partial results go to row hd + cta (head and CTA
+// both only grow along the walk, so no two segments share a row), and the
+// segments that hold a head's first and last tile note their CTAs for the
+// combine. Rows of K and V past a sequence's length may hold anything: their
+// scores are masked, and V rows that the tensor cores would multiply by zero
+// weights are overwritten with zeros in shared memory (0 * NaN is NaN).
+// With weights, the split kernel also writes the scores (4 g bytes per
+// position and K/V head beside the 512 of K and V), and CTAs of the combine
+// turn them into softmax weights once the row's log-sum-exp is known, summed
+// over the group's heads.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -75,6 +89,12 @@ struct DecodeParams {
   int G, P_max;          // CTAs and segment slots per CTA
   float c;               // scale * log2(e)
   long long spin_limit;
+  // ragged step only (Lk is the capacity C there, T and W are its bounds)
+  const int* lens;       // [B] cached positions
+  int* ends;             // [B * n_kv][2] CTAs that hold a head's first and last tile
+  float* scores;         // with weights: fp32 [B * n_q, ld] scores * scale * log2(e)
+  long long ld;
+  int B;
 };
 
 struct DecodeCtl {
@@ -86,6 +106,8 @@ struct DecodeCtl {
   int abort;
   float red_m[4][kHeadsPad];
   float red_l[4][kHeadsPad];
+  int start_b, start_u, start_t;    // ragged step: where this CTA's range starts
+  long long tiles;                  // and how many tiles it has
 };
 
 // First global tile of CTA c's range, and the CTA whose range holds tile x.
@@ -191,17 +213,20 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* desc, uint
 }
 
 // One segment of a CTA's tile range: K/V head `hd` (= b * n_kv + kv head),
-// key tiles [t0, t0 + n), written to segment slot `slot` of the CTA.
+// key tiles [t0, t0 + n) of its `len` keys (`tiles` in all), partial results in
+// row `id`.
 struct Segment {
-  int hd, t0, n, slot;
+  int hd, t0, n, len, tiles;
+  long long id;
 };
 
 // Walks CTA c's range segment by segment (every role takes the same walk).
 struct SegmentWalk {
-  long long x, end;
-  int T, slot;
-  __device__ SegmentWalk(const DecodeParams& p, int c)
-      : x(range_start(c, p.W, p.G)), end(range_start(c + 1, p.W, p.G)), T(p.T), slot(0) {}
+  long long x, end, slot;
+  int T, Lk;
+  __device__ SegmentWalk(const DecodeParams& p, const DecodeCtl&, int c)
+      : x(range_start(c, p.W, p.G)), end(range_start(c + 1, p.W, p.G)),
+        slot(static_cast<long long>(c) * p.P_max), T(p.T), Lk(p.Lk) {}
   __device__ bool next(Segment& s) {
     if (x >= end) return false;
     const long long hd = x / T, base = hd * T;
@@ -209,19 +234,111 @@ struct SegmentWalk {
     s.hd = static_cast<int>(hd);
     s.t0 = static_cast<int>(x - base);
     s.n = static_cast<int>(t1 - (x - base));
-    s.slot = slot++;
+    s.len = Lk;
+    s.tiles = T;
+    s.id = slot++;
     x = base + t1;
     return true;
   }
 };
 
-}  // namespace
+// A sequence's length as the kernels use it, and its key tiles.
+__device__ __forceinline__ int clamp_len(int len, int C) { return min(max(len, 0), C); }
+__device__ __forceinline__ int key_tiles(int len) { return (len + kKeys - 1) / kKeys; }
 
-namespace {
+// Where CTA c's range starts, by one warp: each lane sums the tiles of a run
+// of sequences, a warp scan places the runs, and the lane whose run holds the
+// first tile walks it.
+__device__ __forceinline__ void ragged_start(const DecodeParams& p, DecodeCtl& ctl, int c) {
+  const int lane = threadIdx.x & 31;
+  const int run = (p.B + 31) / 32, b0 = min(lane * run, p.B), b1 = min(b0 + run, p.B);
+  long long sum = 0;
+#pragma unroll 4
+  for (int b = b0; b < b1; ++b) sum += key_tiles(clamp_len(p.lens[b], p.Lk));
+  sum *= p.n_kv;
+  long long incl = sum;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const long long n = __shfl_up_sync(0xffffffffu, incl, off);
+    if (lane >= off) incl += n;
+  }
+  const long long W = __shfl_sync(0xffffffffu, incl, 31);
+  const long long G = min(static_cast<long long>(p.G), W);   // every range has a tile
+  if (c >= G) {
+    if (lane == 0) ctl.tiles = 0;
+    return;
+  }
+  const long long x0 = range_start(c, W, G);
+  long long at = incl - sum;
+  if (x0 < at || x0 >= incl) return;
+  for (int b = b0; b < b1; ++b) {
+    const int T = key_tiles(clamp_len(p.lens[b], p.Lk));
+    const long long here = static_cast<long long>(T) * p.n_kv;
+    if (x0 < at + here) {
+      const int off = static_cast<int>(x0 - at);
+      ctl.start_b = b;
+      ctl.start_u = off / T;
+      ctl.start_t = off - (off / T) * T;
+      ctl.tiles = range_start(c + 1, W, G) - x0;
+      return;
+    }
+    at += here;
+  }
+}
+
+// The same walk over the ragged step's tiles, from the start that
+// ragged_start left in `ctl`.
+struct RaggedWalk {
+  const DecodeParams& p;
+  long long left;
+  int cta, b, u, t, len, T;
+  __device__ RaggedWalk(const DecodeParams& params, const DecodeCtl& ctl, int c)
+      : p(params), left(ctl.tiles), cta(c), b(ctl.start_b), u(ctl.start_u), t(ctl.start_t) {
+    if (left > 0) sequence();
+  }
+  __device__ void sequence() {
+    len = clamp_len(p.lens[b], p.Lk);
+    T = key_tiles(len);
+  }
+  __device__ bool next(Segment& s) {
+    if (left <= 0) return false;
+    while (T == 0) {
+      if (++b >= p.B) return false;
+      sequence();
+    }
+    s.hd = b * p.n_kv + u;
+    s.t0 = t;
+    s.n = static_cast<int>(left < T - t ? left : T - t);
+    s.len = len;
+    s.tiles = T;
+    s.id = static_cast<long long>(s.hd) + cta;
+    left -= s.n;
+    t += s.n;
+    if (t == T) {
+      t = 0;
+      if (++u == p.n_kv) {
+        u = 0;
+        if (++b >= p.B) left = 0;
+        else if (left > 0) sequence();
+      }
+    }
+    return true;
+  }
+};
+
+template <bool kRagged>
+struct WalkOf {
+  using type = SegmentWalk;
+};
+template <>
+struct WalkOf<true> {
+  using type = RaggedWalk;
+};
 
 // GP: the group's query heads padded to 4, 8 or 16 (g <= GP); the loops over
-// heads unroll to GP and skip h >= g.
-template <int GP>
+// heads unroll to GP and skip h >= g. kRagged: the ragged step; kWeights: it
+// also writes the scores.
+template <int GP, bool kRagged, bool kWeights>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_decode_split_kernel(const __grid_constant__ CUtensorMap tmQ,
                          const __grid_constant__ CUtensorMap tmK,
@@ -280,10 +397,15 @@ attn_decode_split_kernel(const __grid_constant__ CUtensorMap tmQ,
   // (the previous call's combine, or whatever wrote Q, K and V): the set-up
   // above overlaps it; global memory is touched only after it has completed.
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  using Walk = typename WalkOf<kRagged>::type;
+  if (kRagged) {
+    if (warp == 0) ragged_start(p, ctl, cta);
+    __syncthreads();
+  }
 
   if (warp == kLoadWarp) {
     if (lane == 0) {
-      SegmentWalk walk(p, cta);
+      Walk walk(p, ctl, cta);
       Segment sg;
       uint32_t it = 0;   // ring items issued (K_t and V_t alternate)
       uint32_t qn = 0;   // Q tiles issued (one per segment)
@@ -337,7 +459,7 @@ attn_decode_split_kernel(const __grid_constant__ CUtensorMap tmQ,
     constexpr uint32_t kIdS = idesc_bf16_f32(kKeys, kHeadsPad, false);
     // O^T = V^T P^T: M = 128 dims with V read MN-major (bit 15), B = P K-major.
     constexpr uint32_t kIdO = idesc_bf16_f32(kDim, kHeadsPad, false) | (1u << 15);
-    SegmentWalk walk(p, cta);
+    Walk walk(p, ctl, cta);
     Segment sg;
     uint32_t it = 0, gt = 0, sn = 0;
     bool ok = true;
@@ -413,9 +535,10 @@ attn_decode_split_kernel(const __grid_constant__ CUtensorMap tmQ,
     // where key r of a tile goes in a P buffer: 128-byte swizzled rows of 64
     // keys, chunk r / 64, 16-byte unit (r % 64) / 8 XOR (head % 8)
     const int p_chunk = (r >> 6) * kSmallChunk, p_unit = (r & 63) >> 3, p_byte = (r & 7) * 2;
-    SegmentWalk walk(p, cta);
+    Walk walk(p, ctl, cta);
     Segment sg;
     uint32_t gt = 0, sn = 0;
+    uint32_t it0 = 0;   // ring item of the segment's first K tile (ragged step)
     bool ok = true;
     // Every wait of these four warps ends in a vote over all 128 threads, so
     // they leave together when one of them gives up and none is left alone
@@ -440,13 +563,20 @@ attn_decode_split_kernel(const __grid_constant__ CUtensorMap tmQ,
         uint32_t sv[16];
         tmem_ld16(lane_base + kColS + 16 * (gt & 1), sv);
         tmem_wait_ld16(sv);
-        const bool valid = (sg.t0 + t) * kKeys + r < p.Lk;
+        const int key = (sg.t0 + t) * kKeys + r;
+        const bool valid = key < sg.len;
         float x[GP];
         bool need = false;
 #pragma unroll
         for (int h = 0; h < GP; ++h) {
           x[h] = valid ? __uint_as_float(sv[h]) * p.c : -INFINITY;
           if (h < p.g) need |= x[h] > m_run[h] + kRescale;
+        }
+        if (kWeights && valid) {
+          float* sc = p.scores + static_cast<size_t>(sg.hd) * p.g * p.ld + key;
+#pragma unroll
+          for (int h = 0; h < GP; ++h)
+            if (h < p.g) sc[h * p.ld] = x[h];
         }
         if (bar_softmax_any(need)) {
           // exact maximum of this tile per head, then move the running maxima
@@ -505,11 +635,30 @@ attn_decode_split_kernel(const __grid_constant__ CUtensorMap tmQ,
           *reinterpret_cast<uint16_t*>(pb + h * 128 + ((p_unit ^ (h & 7)) << 4)) =
               static_cast<uint16_t>(pack_bf16x2(e, 0.0f) & 0xFFFFu);
         }
+        if (kRagged && (sg.t0 + t + 1) * kKeys > sg.len) {
+          // a tile that ends past the sequence: zeros over what V holds there
+          // (the tensor cores read V only after this tile's p_full)
+          const uint32_t item = it0 + 2 * t + 1, slot = item % kRing;
+          if (!waited(smem_addr(&ctl.full[slot]), (item / kRing) & 1)) {
+            ok = false;
+            break;
+          }
+          if (!valid) {
+            uint4* row = reinterpret_cast<uint4*>(dyn_smem + (sRing - smem_addr(dyn_smem)) +
+                                                  slot * kTileBytes + r * 128);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              row[e] = make_uint4(0u, 0u, 0u, 0u);
+              row[e + kChunkBytes / 16] = make_uint4(0u, 0u, 0u, 0u);
+            }
+          }
+        }
         fence_proxy_async_smem();
         tc_fence_before_sync();
         mbar_arrive(smem_addr(&ctl.p_full[gt & 1]));
       }
       if (!ok) break;
+      it0 += 2 * sg.n;
       // epilogue: O^T / l and the log-sum-exp of this segment
       if (!waited(smem_addr(&ctl.o_done), sn & 1)) break;
       uint32_t ov[16];
@@ -526,13 +675,19 @@ attn_decode_split_kernel(const __grid_constant__ CUtensorMap tmQ,
         if (lane == 0) ctl.red_l[warp][h] = v;
       }
       bar_softmax();
-      const size_t row0 = (static_cast<size_t>(cta) * p.P_max + sg.slot) * p.g;
+      const size_t row0 = static_cast<size_t>(sg.id) * p.g;
+      if (kRagged && r == 0) {
+        if (sg.t0 == 0) p.ends[2 * sg.hd] = cta;
+        if (sg.t0 + sg.n == sg.tiles) p.ends[2 * sg.hd + 1] = cta;
+      }
 #pragma unroll
       for (int h = 0; h < GP; ++h) {
         if (h >= p.g) break;
         const float l = ctl.red_l[0][h] + ctl.red_l[1][h] + ctl.red_l[2][h] + ctl.red_l[3][h];
         p.part_o[(row0 + h) * kDim + r] = __uint_as_float(ov[h]) / l;
-        if (r == h) p.part_lse[row0 + h] = (m_run[h] + log2f(l)) * 0.69314718055994530942f;
+        if (r == h)
+          p.part_lse[row0 + h] =
+              (m_run[h] + log2f(l)) * (kRagged ? 1.0f : 0.69314718055994530942f);
       }
       ++sn;
     }
@@ -621,6 +776,107 @@ attn_decode_combine_kernel(uint16_t* o, float* lse, const DecodeParams p) {
   }
 }
 
+// The ragged step's combine. The first B * n_q CTAs merge a head's segments,
+// rows hd + first .. hd + last CTA, as above (their log-sum-exps are in log2
+// units); a sequence without a key gets O = 0 and LSE = -inf. With weights,
+// `chunks` CTAs per (b, K/V head) follow, one per kWeightKeys positions: each
+// rebuilds the log-sum-exps of the group's heads and adds
+//   sum_h 2^(score_hj - lse2_h)
+// to the weight of position j.
+constexpr int kWeightKeys = 2048;
+
+__global__ void __launch_bounds__(32 * kCombineWarps)
+attn_decode_ragged_combine_kernel(uint16_t* o, float* lse, float* weights, int chunks,
+                                  const DecodeParams p) {
+  __shared__ float red_m[kCombineWarps], red_w[kCombineWarps];
+  __shared__ float4 red_o[kCombineWarps][32];
+  __shared__ float lse2[kMaxG];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const long long merges = static_cast<long long>(p.B) * p.n_q;
+  const bool merge = blockIdx.x < merges;
+  const long long rest = merge ? 0 : blockIdx.x - merges;
+  const long long hd = merge ? blockIdx.x / p.g : rest / chunks;
+  const int len = clamp_len(p.lens[hd / p.n_kv], p.Lk);
+  const long long c0 = len > 0 ? p.ends[2 * hd] : 0;
+  const int ns = len > 0 ? static_cast<int>(p.ends[2 * hd + 1] - c0 + 1) : 0;
+
+  if (!merge) {
+    const int j0 = static_cast<int>(rest - hd * chunks) * kWeightKeys;
+    if (j0 >= len) return;
+    for (int h = warp; h < p.g; h += kCombineWarps) {
+      float m = -INFINITY;
+      for (int s = lane; s < ns; s += 32) m = fmaxf(m, p.part_lse[(hd + c0 + s) * p.g + h]);
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+      float w = 0.0f;
+      for (int s = lane; s < ns; s += 32) w += exp2f(p.part_lse[(hd + c0 + s) * p.g + h] - m);
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) w += __shfl_xor_sync(0xffffffffu, w, off);
+      if (lane == 0) lse2[h] = m + log2f(w);
+    }
+    __syncthreads();
+    const float* sc = p.scores + hd * p.g * p.ld;
+    float* out = weights + hd * p.Lk;
+    for (int j = j0 + threadIdx.x; j < min(j0 + kWeightKeys, len); j += 32 * kCombineWarps) {
+      float sum = 0.0f;
+#pragma unroll 4
+      for (int h = 0; h < p.g; ++h) sum += ex2_approx(sc[h * p.ld + j] - lse2[h]);
+      out[j] += sum;
+    }
+    return;
+  }
+
+  const long long row = blockIdx.x;                 // b * n_q + query head
+  const int r = static_cast<int>(row - hd * p.g);
+  float m = -INFINITY, wsum = 0.0f;
+  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+  for (int s = warp; s < ns; s += kCombineWarps) {
+    const size_t sr = static_cast<size_t>((hd + c0 + s) * p.g + r);
+    const float ls = p.part_lse[sr];
+    const float4 v = *reinterpret_cast<const float4*>(p.part_o + sr * kDim + 4 * lane);
+    const float mn = fmaxf(m, ls);
+    const float a = (m == -INFINITY) ? 0.0f : exp2f(m - mn);
+    const float w = exp2f(ls - mn);
+    m = mn;
+    wsum = fmaf(wsum, a, w);
+    acc.x = fmaf(w, v.x, acc.x * a);
+    acc.y = fmaf(w, v.y, acc.y * a);
+    acc.z = fmaf(w, v.z, acc.z * a);
+    acc.w = fmaf(w, v.w, acc.w * a);
+  }
+  red_o[warp][lane] = acc;
+  if (lane == 0) {
+    red_m[warp] = m;
+    red_w[warp] = wsum;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    float mx = red_m[0];
+#pragma unroll
+    for (int w = 1; w < kCombineWarps; ++w) mx = fmaxf(mx, red_m[w]);
+    float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float ws = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kCombineWarps; ++w) {
+      const float a = (red_m[w] == -INFINITY) ? 0.0f : exp2f(red_m[w] - mx);
+      const float4 u = red_o[w][lane];
+      t.x = fmaf(a, u.x, t.x);
+      t.y = fmaf(a, u.y, t.y);
+      t.z = fmaf(a, u.z, t.z);
+      t.w = fmaf(a, u.w, t.w);
+      ws = fmaf(a, red_w[w], ws);
+    }
+    const float inv = ns > 0 ? 1.0f / ws : 0.0f;
+    const uint32_t w0 = pack_bf16x2(t.x * inv, t.y * inv);
+    const uint32_t w1 = pack_bf16x2(t.z * inv, t.w * inv);
+    *reinterpret_cast<uint2*>(o + static_cast<size_t>(row) * kDim + 4 * lane) = make_uint2(w0, w1);
+    if (lane == 0) lse[row] = ns > 0 ? (mx + log2f(ws)) * 0.69314718055994530942f : -INFINITY;
+  }
+}
+
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                                    const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
                                    const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
@@ -631,11 +887,27 @@ std::mutex g_decode_mutex;
 bool g_decode_ready[kMaxDevices] = {};
 EncodeTiledFn g_decode_encode = nullptr;
 
-template <int GP>
-bool set_smem() {
-  return cudaFuncSetAttribute(attn_decode_split_kernel<GP>,
+template <int GP, bool kRagged, bool kWeights>
+bool set_smem_of() {
+  return cudaFuncSetAttribute(attn_decode_split_kernel<GP, kRagged, kWeights>,
                               cudaFuncAttributeMaxDynamicSharedMemorySize,
                               kSmemBytes) == cudaSuccess;
+}
+template <int GP>
+bool set_smem() {
+  return set_smem_of<GP, false, false>() && set_smem_of<GP, true, false>() &&
+         set_smem_of<GP, true, true>();
+}
+
+// The split kernel for groups of g query heads.
+template <bool kRagged, bool kWeights>
+cudaError_t launch_split(const cudaLaunchConfig_t& cfg, const CUtensorMap& mq,
+                         const CUtensorMap& mk, const CUtensorMap& mv, const DecodeParams& p) {
+  if (p.g <= 4)
+    return cudaLaunchKernelEx(&cfg, attn_decode_split_kernel<4, kRagged, kWeights>, mq, mk, mv, p);
+  if (p.g <= 8)
+    return cudaLaunchKernelEx(&cfg, attn_decode_split_kernel<8, kRagged, kWeights>, mq, mk, mv, p);
+  return cudaLaunchKernelEx(&cfg, attn_decode_split_kernel<16, kRagged, kWeights>, mq, mk, mv, p);
 }
 
 attn_status_t decode_device_ready(cudaStream_t stream, int** status) {
@@ -712,6 +984,75 @@ DecodeShape decode_shape(int64_t B, int64_t Lk, int32_t n_kv) {
   return s;
 }
 
+// The ragged step's workspace: partial outputs and log-sum-exps of at most
+// B * n_kv + G segments, the heads' first and last CTAs, and the scores.
+struct RaggedShape {
+  int64_t G, ld, lse_at, ends_at, scores_at, bytes;
+};
+RaggedShape ragged_shape(int64_t B, int64_t C, int32_t n_q, int32_t n_kv, bool weighted) {
+  RaggedShape s;
+  const int64_t T = (C + kKeys - 1) / kKeys, most = B * n_kv * T;
+  s.G = most < kDecodeCtas ? most : kDecodeCtas;
+  s.ld = T * kKeys;
+  const int64_t rows = (B * n_kv + s.G) * (n_q / n_kv);
+  auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
+  s.lse_at = up(rows * kDim * 4);
+  s.ends_at = s.lse_at + up(rows * 4);
+  s.scores_at = s.ends_at + up(B * n_kv * 8);
+  s.bytes = s.scores_at + (weighted ? B * n_q * s.ld * 4 : 0);
+  return s;
+}
+
+bool ragged_supported(int64_t B, int64_t C, int32_t n_q, int32_t n_kv, int32_t d_h) {
+  if (d_h != kDim || n_q / n_kv > kMaxG) return false;
+  if (C > (int64_t{1} << 30) || B > (int64_t{1} << 24) || B * n_kv > (int64_t{1} << 24)) return false;
+  const int64_t chunks = (C + kWeightKeys - 1) / kWeightKeys;
+  return B * n_q + B * n_kv * chunks <= INT32_MAX;
+}
+
+// Launches the ragged split kernel (arguments already validated, set-up done);
+// *out gets its parameters, for the combine.
+attn_status_t launch_ragged_split(const void* q, const void* k, const void* v, const int32_t* lens,
+                                  void* workspace, int64_t B, int64_t C, int32_t n_q, int32_t n_kv,
+                                  float scale, bool weighted, cudaStream_t stream, int* status,
+                                  DecodeParams* out) {
+  const RaggedShape s = ragged_shape(B, C, n_q, n_kv, weighted);
+  CUtensorMap mq, mk, mv;
+  if (!encode_q(&mq, q, n_q, B) || !encode_kv(&mk, k, n_kv, C, B) || !encode_kv(&mv, v, n_kv, C, B))
+    return ATTN_ERR_CUDA;
+  char* ws = static_cast<char*>(workspace);
+  DecodeParams p{};
+  p.part_o = reinterpret_cast<float*>(ws);
+  p.part_lse = reinterpret_cast<float*>(ws + s.lse_at);
+  p.ends = reinterpret_cast<int*>(ws + s.ends_at);
+  p.scores = weighted ? reinterpret_cast<float*>(ws + s.scores_at) : nullptr;
+  p.ld = s.ld;
+  p.status = status;
+  p.lens = lens;
+  p.B = static_cast<int>(B);
+  p.Lk = static_cast<int>(C);
+  p.n_q = n_q;
+  p.n_kv = n_kv;
+  p.g = n_q / n_kv;
+  p.G = static_cast<int>(s.G);
+  p.c = scale * 1.4426950408889634f;
+  p.spin_limit = 1ll << 31;   // about a second at 2 GHz
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(s.G));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = weighted ? launch_split<true, true>(cfg, mq, mk, mv, p)
+                                 : launch_split<true, false>(cfg, mq, mk, mv, p);
+  *out = p;
+  return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
 }  // namespace
 
 extern "C" {
@@ -752,7 +1093,7 @@ attn_status_t attn_decode_fwd(const void* q, const void* k, const void* v, void*
   if (!encode_q(&mq, q, n_q, B) || !encode_kv(&mk, k, n_kv, Lk, B) ||
       !encode_kv(&mv, v, n_kv, Lk, B))
     return ATTN_ERR_CUDA;
-  DecodeParams p;
+  DecodeParams p{};
   const int64_t rows = s.G * s.P_max * (n_q / n_kv);
   p.part_o = static_cast<float*>(workspace);
   p.part_lse = p.part_o + rows * kDim;
@@ -781,19 +1122,60 @@ attn_status_t attn_decode_fwd(const void* q, const void* k, const void* v, void*
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaError_t e;
-  if (p.g <= 4)
-    e = cudaLaunchKernelEx(&cfg, attn_decode_split_kernel<4>, mq, mk, mv, p);
-  else if (p.g <= 8)
-    e = cudaLaunchKernelEx(&cfg, attn_decode_split_kernel<8>, mq, mk, mv, p);
-  else
-    e = cudaLaunchKernelEx(&cfg, attn_decode_split_kernel<16>, mq, mk, mv, p);
-  if (e != cudaSuccess) return ATTN_ERR_CUDA;
+  if (launch_split<false, false>(cfg, mq, mk, mv, p) != cudaSuccess) return ATTN_ERR_CUDA;
   cfg.gridDim = dim3(static_cast<unsigned>(B * n_q));
   cfg.blockDim = dim3(32 * kCombineWarps);
   cfg.dynamicSmemBytes = 0;
   uint16_t* o16 = static_cast<uint16_t*>(o);
   if (cudaLaunchKernelEx(&cfg, attn_decode_combine_kernel, o16, lse, p) != cudaSuccess)
+    return ATTN_ERR_CUDA;
+  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+int64_t attn_decode_ragged_workspace_bytes(int64_t B, int64_t C, int32_t n_q, int32_t n_kv,
+                                           int32_t d_h, int32_t weighted) {
+  if (!decode_sizes_ok(B, C, n_q, n_kv, d_h) || (weighted != 0 && weighted != 1)) return -1;
+  if (!ragged_supported(B, C, n_q, n_kv, d_h)) return -1;
+  return ragged_shape(B, C, n_q, n_kv, weighted != 0).bytes;
+}
+
+attn_status_t attn_decode_ragged_fwd(const void* q, const void* k, const void* v,
+                                     const int32_t* lens, float* weights, void* o, float* lse,
+                                     void* workspace, int64_t workspace_bytes, int64_t B, int64_t C,
+                                     int32_t n_q, int32_t n_kv, int32_t d_h, float scale,
+                                     void* stream_ptr) {
+  if (!q || !k || !v || !lens || !o || !lse || !workspace) return ATTN_ERR_INVALID_ARG;
+  if (!decode_sizes_ok(B, C, n_q, n_kv, d_h) || !std::isfinite(scale)) return ATTN_ERR_INVALID_ARG;
+  auto misaligned = [](const void* ptr, uintptr_t a) {
+    return (reinterpret_cast<uintptr_t>(ptr) & (a - 1)) != 0;
+  };
+  if (misaligned(q, 16) || misaligned(k, 16) || misaligned(v, 16) || misaligned(o, 16) ||
+      misaligned(lse, 4) || misaligned(lens, 4) || misaligned(weights, 4) ||
+      misaligned(workspace, 16))
+    return ATTN_ERR_INVALID_ARG;
+  if (!ragged_supported(B, C, n_q, n_kv, d_h)) return ATTN_ERR_UNSUPPORTED;
+  const bool weighted = weights != nullptr;
+  if (workspace_bytes < ragged_shape(B, C, n_q, n_kv, weighted).bytes) return ATTN_ERR_INVALID_ARG;
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
+  int* status = nullptr;
+  attn_status_t st = decode_device_ready(stream, &status);
+  if (st != ATTN_OK) return st;
+  DecodeParams p;
+  st = launch_ragged_split(q, k, v, lens, workspace, B, C, n_q, n_kv, scale, weighted, stream,
+                           status, &p);
+  if (st != ATTN_OK) return st;
+  const int chunks = weighted ? static_cast<int>((C + kWeightKeys - 1) / kWeightKeys) : 0;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(B * n_q + B * n_kv * chunks));
+  cfg.blockDim = dim3(32 * kCombineWarps);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, attn_decode_ragged_combine_kernel, static_cast<uint16_t*>(o), lse,
+                         weights, chunks, p) != cudaSuccess)
     return ATTN_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }

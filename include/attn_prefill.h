@@ -174,6 +174,73 @@ attn_status_t attn_decode_fwd(const void* q, const void* k, const void* v, void*
                               float scale, void* stream);
 
 /*
+ * Ragged decode: attn_decode_fwd for caches of different lengths. The cache
+ * tensors have room for C positions, of which sequence b holds the first
+ * lens[b]; its token attends to those. With `weights`, the step also adds the
+ * attention that every cached position received, summed over the query heads
+ * of the K/V head's group (the weight attn_cache_evict goes by):
+ *
+ *     weights[b,u,j] += sum_{h in group u} exp(s_hj - LSE_h),   j < lens[b]
+ *
+ *   q        bf16 [B, 1, n_q, 128]         k, v  bf16 [B, C, n_kv, 128]
+ *   lens     int32 [B], device memory, read when the kernels run (a captured
+ *            graph follows later values); below 0 counts as 0, above C as C
+ *   weights  fp32 [B, n_kv, C], 4-byte aligned, updated in place; NULL: none.
+ *            Entries at lens[b] and beyond are neither read nor written.
+ *   o        bf16 [B, 1, n_q, 128]         lse   fp32 [B, n_q, 1]
+ *            a sequence of length 0 gets o = 0 and lse = -inf
+ *   workspace  at least attn_decode_ragged_workspace_bytes bytes (`weighted`
+ *            1 with weights, else 0), 16-byte aligned, caller-owned, contents
+ *            on entry ignored and on exit unspecified
+ *   Positions of k and v at lens[b] and beyond may hold anything (NaN
+ *   included). C >= 1; limits, errors and launches (two kernels, programmatic
+ *   dependents) as attn_decode_fwd. No atomics: results are deterministic.
+ */
+int64_t attn_decode_ragged_workspace_bytes(int64_t B, int64_t C, int32_t n_q, int32_t n_kv,
+                                           int32_t d_h, int32_t weighted);   /* -1 as above */
+attn_status_t attn_decode_ragged_fwd(const void* q, const void* k, const void* v,
+                                     const int32_t* lens, float* weights, void* o, float* lse,
+                                     void* workspace, int64_t workspace_bytes, int64_t B, int64_t C,
+                                     int32_t n_q, int32_t n_kv, int32_t d_h, float scale,
+                                     void* stream);
+
+/*
+ * Eviction: brings caches down to a budget, keeping the positions whose
+ * accumulated attention weight is largest and the most recent ones. Per
+ * sequence b and K/V head u, with len = lens[b]:
+ *
+ *     len <= budget   all positions are kept
+ *     len >  budget   the last `recent` positions are kept and, of those before
+ *                     them, the budget - recent of largest weights[b,u,j]; ties
+ *                     go to the lowest position; a NaN weight counts as the
+ *                     lowest, -0 as +0
+ *
+ * Kept positions stay in order; n = min(len, budget) of them go to the first n
+ * rows of caches with room for C_out >= budget positions, ready for
+ * attn_decode_ragged_fwd to go on with.
+ *
+ *   k, v         [B, C, n_kv, d_h] of elem_bytes 2 (bf16) or 1 (e4m3); rows are
+ *                copied as they are
+ *   weights      fp32 [B, n_kv, C]     lens  int32 [B] (clamped to 0 .. C)
+ *   k_out, v_out [B, C_out, n_kv, d_h]   rows 0 .. n-1 written, the others left
+ *                as they were
+ *   weights_out  fp32 [B, n_kv, C_out]   the kept weights, then zeros
+ *   lens_out     int32 [B]               n
+ *   index        int32 [B, n_kv, budget] kept positions in order, then -1
+ *   B, C, budget >= 1; 0 <= recent <= budget <= C_out; d_h 64 or 128 and
+ *   n_kv <= 128 (ATTN_ERR_UNSUPPORTED otherwise); k, v, k_out and v_out 16-byte
+ *   aligned, the rest 4. An output that overlaps an input or another output is
+ *   ATTN_ERR_INVALID_ARG (rows move between positions that other CTAs still
+ *   read). Two kernels, programmatic dependents as in attn_decode_fwd; no
+ *   workspace; deterministic.
+ */
+attn_status_t attn_cache_evict(const void* k, const void* v, const float* weights,
+                               const int32_t* lens, void* k_out, void* v_out, float* weights_out,
+                               int32_t* lens_out, int32_t* index, int64_t B, int64_t C,
+                               int64_t C_out, int64_t budget, int64_t recent, int32_t n_kv,
+                               int32_t d_h, int32_t elem_bytes, void* stream);
+
+/*
  * Backward pass: gradients of attn_prefill_fwd with respect to q, k and v for
  * an upstream gradient dout, computed by rebuilding the score tiles from q, k
  * and the forward's lse instead of storing the L x L table ("Long-Context

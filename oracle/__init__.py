@@ -14,6 +14,9 @@ attention
 backward
     Gradients of the forward (dQ, dK, dV) written out by the chain rule in
     float64, with the row statistic D_i = dO_i . O_i.
+cache
+    The cache operators: key weights, ragged decode, eviction and decode
+    behind a shared prefix, one row or one head at a time.
 flops
     The cost model the pages use: the causal prefill FLOP count
     2*n_q*d_h*L^2, the dense count 4*L^2*d_h*n_q, the K/V byte count and the
@@ -21,14 +24,14 @@ flops
     prefill FLOPs.
 
 Parity status: every function here is pinned (``tests/test_oracle_pins.py``,
-``tests/test_oracle_backward_pins.py``)
+``tests/test_oracle_backward_pins.py``, ``tests/test_cache_ops.py``)
 to values the pages print, closed forms, invariants, brute force and a
 library routine; none is "parity unpinned".
 """
 
 from .attention import attention, attention_rows, kv_head_of
 from .backward import attention_backward, softmax_rowdot
-from . import flops
+from . import cache, flops
 
 __all__ = ["attention", "attention_rows", "attention_backward", "softmax_rowdot", "kv_head_of",
-           "flops"]
+           "cache", "flops"]

@@ -1,0 +1,241 @@
+"""GPU parity of ragged decode against the fp64 oracle, with and without weights.
+
+Tolerances. bf16 P (half a step: 2^-8 of each weight) and bf16 O (2^-8 of the
+result): |O - O_ref| <= 2^-8 (1 + 2^-6) O_abs + 2^-8 |O_ref|, O_abs the oracle's
+output on |V|; the 2^-6 covers the fp32 parts below. A score is a sum of d
+products in fp32, off by at most (d + 2) 2^-24 sum |q_d k_d| scale: E. LSE is off
+by E, by 2^-22 of the exponentials and their sums' logarithm, and by fp32
+roundings of its value: E + 2^-20 + 2^-22 |LSE|. A position's weight exp(s - LSE)
+is off by E + (the same of LSE) of itself, and the sum it is added to rounds
+g + 1 times: (2 E + 2^-19 + 2^-22 |LSE|) added + (g + 1) 2^-24 |W|.
+"""
+
+import numpy as np
+import pytest
+
+import oracle
+from causal_gqa_prefill_gb300 import (ATTN_OK, AttnError, attn_decode, attn_decode_ragged,
+                                      attn_decode_ragged_workspace_bytes, attn_device_check)
+from causal_gqa_prefill_gb300 import workloads as W
+from gpu_common import to_np
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _library():
+    if not torch.cuda.is_available():
+        pytest.fail("GPU tests need a CUDA device")
+    from causal_gqa_prefill_gb300 import build
+    build.build()
+    torch.cuda.set_device(0)
+
+
+def make(B, C, n_q, n_kv, lens, seed=0, weights=True, junk=True):
+    w = W.custom(B, 1, n_q, n_kv, 128, Lk=C)
+    q, k, v = W.make_inputs(w, "cuda", seed=seed)
+    lens = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    if junk:                                  # what lies behind a sequence is anything
+        behind = torch.arange(C, device="cuda")[None] >= lens[:, None]
+        for x, bad in ((k, float("nan")), (v, float("inf"))):
+            x[behind] = bad
+    acc = None
+    if weights:
+        g = torch.Generator(device="cuda").manual_seed(seed + 1)
+        acc = torch.rand(B, n_kv, C, generator=g, device="cuda")
+        if junk:
+            acc[behind[:, None].expand(-1, n_kv, -1)] = float("nan")
+    return q, k, v, lens, acc
+
+
+def check(q, k, v, lens, before, o, lse, after, scale=None, what=""):
+    B, C, n_kv, d = k.shape
+    g = q.shape[2] // n_kv
+    o_r, lse_r, added, o_abs, s_abs = oracle.cache.decode_rows(
+        to_np(q), to_np(k), to_np(v), lens.cpu().numpy(), scale=scale)
+    o, lse = to_np(o), lse.cpu().numpy().astype(np.float64)
+    bound = 2.0 ** -8 * ((1 + 2.0 ** -6) * o_abs + np.abs(o_r))
+    assert (np.abs(o - o_r) <= bound).all(), (what, (np.abs(o - o_r) - bound).max())
+    live = np.isfinite(lse_r)
+    assert (lse[~live] == -np.inf).all(), what
+    E = (d + 2) * 2.0 ** -24 * s_abs
+    size = np.where(live, np.abs(lse_r), 0.0)
+    bound = E + 2.0 ** -20 + 2.0 ** -22 * size
+    off = np.abs(lse[live] - lse_r[live]) - bound[live]
+    assert (off <= 0).all(), (what, off.max())
+    if after is None:
+        return
+    rel = (2 * E + 2.0 ** -19 + 2.0 ** -22 * size)[..., 0].reshape(B, n_kv, g).max(2)[..., None]
+    seen = np.arange(C)[None] < np.clip(lens.cpu().numpy(), 0, C)[:, None]
+    seen = np.broadcast_to(seen[:, None], added.shape)
+    ref = before.cpu().numpy().astype(np.float64) + added
+    bound = rel * added + (g + 1) * 2.0 ** -24 * np.abs(ref)
+    err = np.abs(after.cpu().numpy().astype(np.float64) - ref)
+    assert (err[seen] <= bound[seen]).all(), (what, (err - bound)[seen].max())
+    # entries behind a sequence keep their bits
+    same = before.view(torch.int32).cpu().numpy() == after.view(torch.int32).cpu().numpy()
+    assert same[~seen].all(), what
+
+
+CASES = [
+    # B, C, n_q, n_kv, lens
+    (3, 333, 10, 5, [333, 100, 0]),
+    (1, 1, 4, 1, [1]),
+    (1, 1, 4, 1, [0]),
+    (2, 128, 6, 2, [128, 1]),
+    (5, 300, 4, 4, [127, 128, 129, 256, 257]),            # tile edges, g = 1
+    (4, 2000, 8, 1, [2000, 1, 1999, 640]),                # g = 8
+    (2, 5000, 12, 1, [77, 4999]),                         # g = 12
+    (2, 3000, 32, 2, [3000, 1111]),                       # g = 16
+    (1, 40000, 36, 6, [39999]),                           # every CTA on one sequence
+    (6, 700, 16, 8, [0, 0, 0, 5, 0, 0]),                  # mostly empty
+    (3, 50, 8, 2, [0, 0, 0]),                             # all empty
+    (40, 260, 14, 2, [(37 * i) % 261 for i in range(40)]),    # runs of sequences per lane, g = 7
+    (300, 140, 4, 2, [(53 * i) % 141 for i in range(300)]),
+]
+
+
+@pytest.mark.parametrize("case", CASES, ids=lambda c: "B%d_C%d_q%d_kv%d" % c[:4])
+@pytest.mark.parametrize("weighted", [False, True])
+def test_against_the_oracle(case, weighted):
+    q, k, v, lens, acc = make(*case, seed=sum(case[:4]), weights=weighted)
+    before = acc.clone() if weighted else None
+    o, lse = attn_decode_ragged(q, k, v, lens, weights=acc)
+    assert attn_device_check() == ATTN_OK
+    check(q, k, v, lens, before, o, lse, acc, what=str(case[:4]))
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.3, 2.0])
+def test_other_scales(scale):
+    q, k, v, lens, acc = make(2, 500, 8, 2, [500, 123], seed=9)
+    before = acc.clone()
+    o, lse = attn_decode_ragged(q, k, v, lens, weights=acc, scale=scale)
+    check(q, k, v, lens, before, o, lse, acc, scale=scale, what=str(scale))
+
+
+def test_lengths_out_of_range_are_clamped():
+    q, k, v, _, acc = make(2, 200, 8, 2, [200, 200], seed=5)
+    lens = torch.tensor([100000, -7], dtype=torch.int32, device="cuda")
+    before = acc.clone()
+    o, lse = attn_decode_ragged(q, k, v, lens, weights=acc)
+    check(q, k, v, lens, before, o, lse, acc)
+
+
+def test_full_lengths_match_decode():
+    q, k, v, lens, _ = make(3, 900, 8, 2, [900] * 3, seed=6, weights=False)
+    o, lse = attn_decode_ragged(q, k, v, lens)
+    o2, lse2 = attn_decode(q, k, v)
+    assert (lse - lse2).abs().max().item() <= 1e-5
+    assert (o.float() - o2.float()).abs().max().item() <= 2.0 ** -7 * o2.abs().max().item()
+
+
+def test_same_bits_again_and_one_workspace():
+    ws = torch.full((attn_decode_ragged_workspace_bytes(4, 3000, 8, 2, weighted=True),), 255,
+                    dtype=torch.uint8, device="cuda")
+    q, k, v, lens, acc = make(4, 3000, 8, 2, [3000, 17, 0, 2222], seed=7)
+    runs = []
+    for _ in range(3):
+        mine = acc.clone()
+        o, lse = attn_decode_ragged(q, k, v, lens, weights=mine, workspace=ws)
+        runs.append((o, lse, mine))
+    torch.cuda.synchronize()
+    for o, lse, mine in runs[1:]:
+        assert torch.equal(o, runs[0][0]) and torch.equal(lse, runs[0][1])
+        assert torch.equal(mine.view(torch.int32), runs[0][2].view(torch.int32))
+
+
+def test_graph_follows_lengths_and_cache():
+    """A captured step replayed while the cache grows, against the same eager steps."""
+    B, C, n_q, n_kv = 3, 400, 8, 2
+    q, k, v, lens, acc = make(B, C, n_q, n_kv, [127, 0, 260], seed=8, junk=False)
+    ws = torch.empty(attn_decode_ragged_workspace_bytes(B, C, n_q, n_kv, weighted=True),
+                     dtype=torch.uint8, device="cuda")
+    out, lse = torch.empty_like(q), torch.empty(B, n_q, 1, device="cuda")
+    acc_eager, start = acc.clone(), lens.clone()
+    step = lambda w: attn_decode_ragged(q, k, v, lens, weights=w, workspace=ws, out=out, lse=lse)  # noqa: E731
+    step(acc.clone())
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(acc)
+    eager = []
+    for _ in range(4):
+        step(acc_eager)
+        eager.append((out.clone(), lse.clone()))
+        lens += 1
+    lens.copy_(start)
+    for o_e, l_e in eager:
+        graph.replay()
+        assert torch.equal(out, o_e) and torch.equal(lse, l_e)
+        lens += 1
+    assert torch.equal(acc, acc_eager)
+    assert attn_device_check() == ATTN_OK
+
+
+def test_two_streams_at_once():
+    sets = [make(4, 6000, 8, 2, [6000, 3000 + i, 10, 5999], seed=20 + i) for i in range(2)]
+    alone = []
+    for q, k, v, lens, acc in sets:
+        mine = acc.clone()
+        alone.append((*attn_decode_ragged(q, k, v, lens, weights=mine), mine))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    got = []
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    accs = [x[4].clone() for x in sets]
+    torch.cuda.synchronize()
+    for s, (q, k, v, lens, _), mine in zip(streams, sets, accs):
+        got.append((*attn_decode_ragged(q, k, v, lens, weights=mine, stream=s), mine))
+    torch.cuda.synchronize()
+    for a, b in zip(alone, got):
+        for x, y in zip(a, b):
+            assert torch.equal(x.view(torch.int16), y.view(torch.int16))
+
+
+def test_cache_past_2_to_the_31_elements():
+    """The last sequence's rows start 2.15e9 elements into K and V."""
+    B, C, n_q, n_kv = 3, 350_000, 48, 24
+    k = torch.zeros(B, C, n_kv, 128, dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros_like(k)
+    assert (B - 1) * C * n_kv * 128 > 2 ** 31
+    g = torch.Generator(device="cuda").manual_seed(1)
+    n = 300
+    k[2, :n] = torch.randn(n, n_kv, 128, generator=g, device="cuda").to(torch.bfloat16)
+    v[2, :n] = torch.randn(n, n_kv, 128, generator=g, device="cuda").to(torch.bfloat16)
+    k[2, C - 1], v[2, C - 1] = k[2, 0], v[2, 1]
+    q = torch.randn(B, 1, n_q, 128, generator=g, device="cuda").to(torch.bfloat16)
+    for last in (n, C):
+        lens = torch.tensor([0, 1, last], dtype=torch.int32, device="cuda")
+        acc = torch.zeros(B, n_kv, C, device="cuda")
+        o, lse = attn_decode_ragged(q, k, v, lens, weights=acc)
+        assert attn_device_check() == ATTN_OK
+        for u in (0, n_kv - 1):
+            qs = q[2, 0, 2 * u:2 * u + 2].double()
+            s = qs @ k[2, :last, u].double().T * 128 ** -0.5
+            p = torch.softmax(s, 1)
+            assert ((p @ v[2, :last, u].double()) - o[2, 0, 2 * u:2 * u + 2].double()).abs().max() < 1e-2
+            assert (torch.logsumexp(s, 1) - lse[2, 2 * u:2 * u + 2, 0].double()).abs().max() < 1e-4
+            assert torch.allclose(acc[2, u, :last].double(), p.sum(0), rtol=1e-4, atol=0)
+    del k, v, acc
+    torch.cuda.empty_cache()
+
+
+def test_refusals():
+    q, k, v, lens, acc = make(2, 64, 8, 2, [3, 4], seed=1)
+    with pytest.raises(ValueError):
+        attn_decode_ragged(q, k, v, lens[:1])
+    with pytest.raises(TypeError):
+        attn_decode_ragged(q, k, v, lens.long())
+    with pytest.raises(ValueError):
+        attn_decode_ragged(q, k[:, :32], v[:, :32], lens)          # not contiguous
+    with pytest.raises(ValueError):
+        attn_decode_ragged(q, k, v, lens, weights=acc[:, :1])
+    with pytest.raises(ValueError):
+        attn_decode_ragged(q.repeat(1, 2, 1, 1), k, v, lens)
+    with pytest.raises(AttnError):
+        attn_decode_ragged(q, k, v, lens, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(AttnError):
+        attn_decode_ragged(q[..., :64].contiguous(), k[..., :64].contiguous(),
+                           v[..., :64].contiguous(), lens)
