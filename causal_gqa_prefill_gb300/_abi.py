@@ -50,6 +50,10 @@ _SIGNATURES = {
                                        ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
                                        ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
                                        ctypes.c_float, ctypes.c_void_p]),
+    "attn_key_weights_workspace_bytes": (ctypes.c_int64, [ctypes.c_int64] * 3
+                                         + [ctypes.c_int32] * 3),
+    "attn_key_weights_fwd": (ctypes.c_int, [ctypes.c_void_p] * 5 + [ctypes.c_int64] * 4
+                             + [ctypes.c_int32] * 5 + [ctypes.c_float, ctypes.c_void_p]),
     "attn_decode_ragged_workspace_bytes": (ctypes.c_int64, [ctypes.c_int64, ctypes.c_int64,
                                                             ctypes.c_int32, ctypes.c_int32,
                                                             ctypes.c_int32, ctypes.c_int32]),

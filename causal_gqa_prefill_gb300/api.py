@@ -189,6 +189,66 @@ def _cuda_tensor(name, t, shape, dtype, device=None):
     return t
 
 
+def attn_key_weights_workspace_bytes(B, Lq, Lk, n_q, n_kv, d_h=128) -> int:
+    return int(_abi.load().attn_key_weights_workspace_bytes(int(B), int(Lq), int(Lk), int(n_q),
+                                                            int(n_kv), int(d_h)))
+
+
+def attn_key_weights_fwd(q, k, lse, weights, workspace, workspace_bytes, B, Lq, Lk, n_q, n_kv, d_h,
+                         causal, accumulate, scale, stream=None) -> int:
+    """Direct call of the key weights C entry point; returns the raw status code."""
+    lib = _abi.load()
+    return int(lib.attn_key_weights_fwd(_ptr(q), _ptr(k), _ptr(lse), _ptr(weights),
+                                        _ptr(workspace), int(workspace_bytes), int(B), int(Lq),
+                                        int(Lk), int(n_q), int(n_kv), int(d_h), int(causal),
+                                        int(accumulate), float(scale), _stream_handle(stream)))
+
+
+def attn_key_weights(q, k, lse, *, causal=True, scale=None, weights=None, accumulate=False,
+                     workspace=None, stream=None):
+    """How much attention every key received: fp32 [B, n_kv, Lk], the softmax
+    weights of a prefill summed over the rows that see the key and over its
+    group's query heads.
+
+    q bf16 [B, Lq, n_q, d], k bf16 [B, Lk, n_kv, d] (d 64 or 128, rows the last
+    Lq of the Lk positions), lse fp32 [B, n_q, Lq] as attn_prefill returned it
+    for the same causal and scale. ``weights`` receives the result, or with
+    ``accumulate`` is added to (chunk after chunk of one prompt: pass the part
+    of the tensor's positions that exist as its own contiguous tensor)."""
+    import torch
+
+    bf16 = torch.bfloat16
+    B, Lq, n_q, d = _cuda_tensor("q", q, (None, None, None, None), bf16).shape
+    dev = q.device
+    Lk, n_kv = _cuda_tensor("k", k, (B, None, None, d), bf16, dev).shape[1:3]
+    if Lk < Lq:
+        raise ValueError("k must hold at least as many positions as q has rows")
+    _cuda_tensor("lse", lse, (B, n_q, Lq), torch.float32, dev)
+    if weights is not None:
+        _cuda_tensor("weights", weights, (B, n_kv, Lk), torch.float32, dev)
+    elif accumulate:
+        raise ValueError("accumulate needs the weights to add to")
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    need = attn_key_weights_workspace_bytes(B, Lq, Lk, n_q, n_kv, d)
+    if need < 0:
+        raise AttnError(_abi.ATTN_ERR_UNSUPPORTED, "attn_key_weights_workspace_bytes")
+    with torch.cuda.device(dev):
+        handle, other = _on_stream(dev, stream)
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            _keep_for(other, workspace)
+        if weights is None:
+            weights = torch.empty((B, n_kv, Lk), dtype=torch.float32, device=dev)
+            _keep_for(other, weights)
+        nbytes = workspace.numel() * workspace.element_size()
+        st = attn_key_weights_fwd(q, k, lse, weights, workspace, nbytes, B, Lq, Lk, n_q, n_kv, d,
+                                  int(bool(causal)), int(bool(accumulate)), scale, handle)
+    if st != _abi.ATTN_OK:
+        raise AttnError(st, "attn_key_weights_fwd")
+    return weights
+
+
 def attn_decode_ragged_workspace_bytes(B, C, n_q, n_kv, d_h=128, weighted=False) -> int:
     return int(_abi.load().attn_decode_ragged_workspace_bytes(
         int(B), int(C), int(n_q), int(n_kv), int(d_h), int(bool(weighted))))

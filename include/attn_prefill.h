@@ -174,6 +174,35 @@ attn_status_t attn_decode_fwd(const void* q, const void* k, const void* v, void*
                               float scale, void* stream);
 
 /*
+ * Key weights: the attention that every key of a prefill received, summed over
+ * the query rows that see it and over the query heads of its group, rebuilt
+ * from q, k and the forward's lse (the weight attn_cache_evict goes by):
+ *
+ *     weights[b,u,j] (+)= sum_{h in group u} sum_{i sees j} exp(s_ij - LSE[b,h,i])
+ *
+ * Rows are the last Lq positions of the Lk keys, as in attn_prefill_fwd_chunk:
+ * the whole prompt (Lq = Lk), a chunk added to the earlier chunks' weights
+ * (accumulate = 1), or only a prompt's last rows.
+ *
+ *   q        bf16 [B, Lq, n_q, d_h]        k    bf16 [B, Lk, n_kv, d_h]
+ *   lse      fp32 [B, n_q, Lq], of the same q, k, causal and scale; a row whose
+ *            lse is -inf (one without keys) adds nothing
+ *   weights  fp32 [B, n_kv, Lk], 4-byte aligned; accumulate = 0: written,
+ *            1: added to
+ *   workspace  at least attn_key_weights_workspace_bytes bytes, 16-byte aligned,
+ *            caller-owned, contents on entry ignored and on exit unspecified
+ *   d_h 64 or 128, n_q / n_kv <= 128 (ATTN_ERR_UNSUPPORTED otherwise). Everything
+ *   else as attn_prefill_fwd_chunk; one or two kernels, programmatic dependents
+ *   as in attn_decode_fwd. No atomics: results are deterministic.
+ */
+int64_t attn_key_weights_workspace_bytes(int64_t B, int64_t Lq, int64_t Lk, int32_t n_q,
+                                         int32_t n_kv, int32_t d_h);   /* -1 as above */
+attn_status_t attn_key_weights_fwd(const void* q, const void* k, const float* lse, float* weights,
+                                   void* workspace, int64_t workspace_bytes, int64_t B, int64_t Lq,
+                                   int64_t Lk, int32_t n_q, int32_t n_kv, int32_t d_h,
+                                   int32_t causal, int32_t accumulate, float scale, void* stream);
+
+/*
  * Ragged decode: attn_decode_fwd for caches of different lengths. The cache
  * tensors have room for C positions, of which sequence b holds the first
  * lens[b]; its token attends to those. With `weights`, the step also adds the

@@ -31,6 +31,36 @@ def _call(fn, order, base, change):
     return fn(*[a[n] for n in order], stream=0)
 
 
+# --------------------------------------------------------------- key weights
+
+WEIGHTS_ORDER = ("q k lse weights workspace workspace_bytes B Lq Lk n_q n_kv d_h causal accumulate "
+                 "scale").split()
+WEIGHTS_BASE = dict(q=_at(0), k=_at(1), lse=_at(2), weights=_at(3), workspace=_at(4),
+                    workspace_bytes=1 << 20, B=2, Lq=300, Lk=500, n_q=8, n_kv=2, d_h=128, causal=1,
+                    accumulate=0, scale=0.1)
+
+
+@pytest.mark.parametrize("change,expect", [
+    (dict(q=0), BAD), (dict(k=0), BAD), (dict(lse=0), BAD), (dict(weights=0), BAD),
+    (dict(workspace=0), BAD), (dict(workspace_bytes=1000), BAD), (dict(B=0), BAD),
+    (dict(Lq=0), BAD), (dict(Lq=501), BAD), (dict(n_q=7), BAD), (dict(n_kv=0), BAD),
+    (dict(causal=2), BAD), (dict(accumulate=-1), BAD), (dict(scale=math.nan), BAD),
+    (dict(q=_at(0) + 8), BAD), (dict(lse=_at(2) + 2), BAD), (dict(workspace=_at(4) + 4), BAD),
+    (dict(d_h=96), UNSUP), (dict(n_q=258), UNSUP), (dict(Lk=1 << 31), UNSUP),
+    (dict(Lq=1 << 30, Lk=1 << 30), UNSUP),
+], ids=str)
+def test_key_weights_refuse(change, expect):
+    assert _call(cg.attn_key_weights_fwd, WEIGHTS_ORDER, WEIGHTS_BASE, change) == expect
+
+
+def test_key_weights_workspace():
+    size = cg.attn_key_weights_workspace_bytes
+    assert size(1, 100, 100, 8, 2) == size(3, 1, 100000, 128, 1, 64) > 0
+    for bad in ((0, 1, 1, 1, 1), (1, 2, 1, 1, 1), (1, 1, 1, 3, 2), (1, 1, 1, 129, 1),
+                (1, 1, 1, 1, 1, 32)):
+        assert size(*bad) == -1, bad
+
+
 # ------------------------------------------------------------- ragged decode
 
 RAGGED_ORDER = ("q k v lens weights o lse workspace workspace_bytes B C n_q n_kv d_h "
