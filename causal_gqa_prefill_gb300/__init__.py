@@ -11,6 +11,7 @@ from ._abi import (ATTN_OK, ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED, ATTN_ERR
                    status_string)
 from .api import (AttnError, attn_cache_evict, attn_decode, attn_decode_fwd, attn_decode_ragged,
                   attn_decode_ragged_fwd, attn_decode_ragged_workspace_bytes,
+                  attn_decode_shared, attn_decode_shared_fwd, attn_decode_shared_workspace_bytes,
                   attn_decode_workspace_bytes, attn_evict,
                   attn_key_weights, attn_key_weights_fwd, attn_key_weights_workspace_bytes,
                   attn_prefill, attn_prefill_fp8, attn_prefill_fwd, attn_prefill_fwd_chunk,
@@ -25,7 +26,8 @@ __all__ = [
     "ATTN_ERR_TIMEOUT", "ATTN_ERR_CHECK", "AttnError", "attn_prefill", "attn_prefill_fwd", "attn_prefill_fwd_chunk",
     "attn_prefill_fp8", "attn_prefill_fwd_fp8", "attn_decode", "attn_decode_fwd",
     "attn_decode_workspace_bytes", "attn_decode_ragged", "attn_decode_ragged_fwd",
-    "attn_decode_ragged_workspace_bytes", "attn_evict", "attn_cache_evict", "attn_key_weights",
+    "attn_decode_ragged_workspace_bytes", "attn_decode_shared", "attn_decode_shared_fwd",
+    "attn_decode_shared_workspace_bytes", "attn_evict", "attn_cache_evict", "attn_key_weights",
     "attn_key_weights_fwd", "attn_key_weights_workspace_bytes", "attn_device_check", "attn_prefill_backward",
     "attn_prefill_bwd", "attn_prefill_bwd_workspace_bytes", "attn_selftest_wait_timeout",
     "attn_selftest_wait_timeout_noalloc", "attn_prefill_fwd_host", "attn_prefill_host_staging_bytes",

@@ -61,6 +61,10 @@ _SIGNATURES = {
                                + [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int32,
                                   ctypes.c_int32, ctypes.c_int32, ctypes.c_float,
                                   ctypes.c_void_p]),
+    "attn_decode_shared_workspace_bytes": (ctypes.c_int64, [ctypes.c_int64] * 3
+                                           + [ctypes.c_int32] * 3),
+    "attn_decode_shared_fwd": (ctypes.c_int, [ctypes.c_void_p] * 9 + [ctypes.c_int64] * 4
+                               + [ctypes.c_int32] * 3 + [ctypes.c_float, ctypes.c_void_p]),
     "attn_cache_evict": (ctypes.c_int, [ctypes.c_void_p] * 9
                          + [ctypes.c_int64] * 5 + [ctypes.c_int32] * 3 + [ctypes.c_void_p]),
     "attn_prefill_bwd_workspace_bytes": (ctypes.c_int64, [ctypes.c_int64, ctypes.c_int64,

@@ -315,6 +315,70 @@ def attn_decode_ragged(q, k, v, lens, *, weights=None, scale=None, workspace=Non
     return out, lse
 
 
+def attn_decode_shared_workspace_bytes(B, P, C, n_q, n_kv, d_h=128) -> int:
+    return int(_abi.load().attn_decode_shared_workspace_bytes(int(B), int(P), int(C), int(n_q),
+                                                              int(n_kv), int(d_h)))
+
+
+def attn_decode_shared_fwd(q, prefix_k, prefix_v, k, v, lens, o, lse, workspace, workspace_bytes, B,
+                           P, C, n_q, n_kv, d_h, scale, stream=None) -> int:
+    """Direct call of the shared-prefix decode C entry point; returns the raw status code."""
+    lib = _abi.load()
+    return int(lib.attn_decode_shared_fwd(_ptr(q), _ptr(prefix_k), _ptr(prefix_v), _ptr(k), _ptr(v),
+                                          _ptr(lens), _ptr(o), _ptr(lse), _ptr(workspace),
+                                          int(workspace_bytes), int(B), int(P), int(C), int(n_q),
+                                          int(n_kv), int(d_h), float(scale),
+                                          _stream_handle(stream)))
+
+
+def attn_decode_shared(q, prefix_k, prefix_v, k, v, lens, *, scale=None, workspace=None, out=None,
+                       lse=None, stream=None):
+    """One decode step of a batch behind a shared prefix: q bf16 [B, 1, n_q, 128]
+    attends to prefix_k/prefix_v bf16 [1, P, n_kv, 128], which all sequences share,
+    and to the first lens[b] positions of its own k/v bf16 [B, C, n_kv, 128]
+    (lens: int32 CUDA tensor [B], 0 allowed), in one softmax.
+
+    Returns (o bf16 [B, 1, n_q, 128], lse fp32 [B, n_q, 1]). ``workspace`` (at
+    least attn_decode_shared_workspace_bytes bytes) is allocated with torch when
+    not given."""
+    import torch
+
+    bf16 = torch.bfloat16
+    B, _, n_q, d = _cuda_tensor("q", q, (None, 1, None, None), bf16).shape
+    dev = q.device
+    P, n_kv = _cuda_tensor("prefix_k", prefix_k, (1, None, None, d), bf16, dev).shape[1:3]
+    _cuda_tensor("prefix_v", prefix_v, tuple(prefix_k.shape), bf16, dev)
+    C = _cuda_tensor("k", k, (B, None, n_kv, d), bf16, dev).shape[1]
+    _cuda_tensor("v", v, tuple(k.shape), bf16, dev)
+    _cuda_tensor("lens", lens, (B,), torch.int32, dev)
+    if out is not None:
+        _cuda_tensor("out", out, tuple(q.shape), bf16, dev)
+    if lse is not None:
+        _cuda_tensor("lse", lse, (B, n_q, 1), torch.float32, dev)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    need = attn_decode_shared_workspace_bytes(B, P, C, n_q, n_kv, d)
+    if need < 0:
+        raise AttnError(_abi.ATTN_ERR_UNSUPPORTED, "attn_decode_shared_workspace_bytes")
+    with torch.cuda.device(dev):
+        handle, other = _on_stream(dev, stream)
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            _keep_for(other, workspace)
+        if out is None:
+            out = torch.empty_like(q)
+            _keep_for(other, out)
+        if lse is None:
+            lse = torch.empty((B, n_q, 1), dtype=torch.float32, device=dev)
+            _keep_for(other, lse)
+        nbytes = workspace.numel() * workspace.element_size()
+        st = attn_decode_shared_fwd(q, prefix_k, prefix_v, k, v, lens, out, lse, workspace, nbytes,
+                                    B, P, C, n_q, n_kv, d, scale, handle)
+    if st != _abi.ATTN_OK:
+        raise AttnError(st, "attn_decode_shared_fwd")
+    return out, lse
+
+
 def attn_cache_evict(k, v, weights, lens, k_out, v_out, weights_out, lens_out, index, B, C, C_out,
                      budget, recent, n_kv, d_h, elem_bytes, stream=None) -> int:
     """Direct call of the eviction C entry point; returns the raw status code."""

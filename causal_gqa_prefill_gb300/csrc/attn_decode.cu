@@ -49,6 +49,7 @@
 #include <mutex>
 
 #include "attn_prefill.h"
+#include "decode_parts.h"
 #include "sm103_ptx.cuh"
 
 namespace gb300_host {
@@ -95,6 +96,7 @@ struct DecodeParams {
   float* scores;         // with weights: fp32 [B * n_q, ld] scores * scale * log2(e)
   long long ld;
   int B;
+  int beside;            // 1: wait for the kernel before only at the end (decode_parts.h)
 };
 
 struct DecodeCtl {
@@ -182,12 +184,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       : "memory");
 }
 
-// Generic-proxy shared-memory writes of this thread become visible to the
-// tensor cores (async proxy).
-__device__ __forceinline__ void fence_proxy_async_smem() {
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-
 // Named barrier 1 over the 128 softmax threads; the OR of `v` over them.
 __device__ __forceinline__ void bar_softmax() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 __device__ __forceinline__ bool bar_softmax_any(bool v) {
@@ -201,15 +197,6 @@ __device__ __forceinline__ bool bar_softmax_any(bool v) {
       : "r"(static_cast<uint32_t>(v))
       : "memory");
   return r != 0;
-}
-
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* desc, uint32_t bar, int c0,
-                                            int c1, int c2) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%3, %4, %5}], [%2];"
-      ::"r"(dst), "l"(desc), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
-      : "memory");
 }
 
 // One segment of a CTA's tile range: K/V head `hd` (= b * n_kv + kv head),
@@ -396,7 +383,7 @@ attn_decode_split_kernel(const __grid_constant__ CUtensorMap tmQ,
   // Launched as the programmatic dependent of the stream's previous kernel
   // (the previous call's combine, or whatever wrote Q, K and V): the set-up
   // above overlaps it; global memory is touched only after it has completed.
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!kRagged || !p.beside) asm volatile("griddepcontrol.wait;" ::: "memory");
   using Walk = typename WalkOf<kRagged>::type;
   if (kRagged) {
     if (warp == 0) ragged_start(p, ctl, cta);
@@ -699,6 +686,7 @@ attn_decode_split_kernel(const __grid_constant__ CUtensorMap tmQ,
     tc_fence_after_sync();
     tmem_dealloc(tmem, kTmemCols);
   }
+  if (kRagged && p.beside) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // One CTA of kCombineWarps warps per (b, query head): O = sum_s w_s O_s,
@@ -1014,8 +1002,8 @@ bool ragged_supported(int64_t B, int64_t C, int32_t n_q, int32_t n_kv, int32_t d
 // *out gets its parameters, for the combine.
 attn_status_t launch_ragged_split(const void* q, const void* k, const void* v, const int32_t* lens,
                                   void* workspace, int64_t B, int64_t C, int32_t n_q, int32_t n_kv,
-                                  float scale, bool weighted, cudaStream_t stream, int* status,
-                                  DecodeParams* out) {
+                                  float scale, bool weighted, bool beside, cudaStream_t stream,
+                                  int* status, DecodeParams* out) {
   const RaggedShape s = ragged_shape(B, C, n_q, n_kv, weighted);
   CUtensorMap mq, mk, mv;
   if (!encode_q(&mq, q, n_q, B) || !encode_kv(&mk, k, n_kv, C, B) || !encode_kv(&mv, v, n_kv, C, B))
@@ -1027,6 +1015,7 @@ attn_status_t launch_ragged_split(const void* q, const void* k, const void* v, c
   p.ends = reinterpret_cast<int*>(ws + s.ends_at);
   p.scores = weighted ? reinterpret_cast<float*>(ws + s.scores_at) : nullptr;
   p.ld = s.ld;
+  p.beside = beside ? 1 : 0;
   p.status = status;
   p.lens = lens;
   p.B = static_cast<int>(B);
@@ -1054,6 +1043,30 @@ attn_status_t launch_ragged_split(const void* q, const void* k, const void* v, c
 }
 
 }  // namespace
+
+namespace gb300_host {
+
+attn_status_t decode_ready(cudaStream_t stream, int** status) {
+  return decode_device_ready(stream, status);
+}
+
+int64_t ragged_split_bytes(int64_t B, int64_t C, int32_t n_q, int32_t n_kv, int32_t d_h) {
+  if (!decode_sizes_ok(B, C, n_q, n_kv, d_h) || !ragged_supported(B, C, n_q, n_kv, d_h)) return -1;
+  return ragged_shape(B, C, n_q, n_kv, false).bytes;
+}
+
+attn_status_t ragged_split_beside(const void* q, const void* k, const void* v, const int32_t* lens,
+                                  void* workspace, int64_t B, int64_t C, int32_t n_q, int32_t n_kv,
+                                  float scale, cudaStream_t stream, int* status,
+                                  RaggedParts* parts) {
+  DecodeParams p;
+  const attn_status_t st = launch_ragged_split(q, k, v, lens, workspace, B, C, n_q, n_kv, scale,
+                                               false, true, stream, status, &p);
+  *parts = {p.part_o, p.part_lse, p.ends};
+  return st;
+}
+
+}  // namespace gb300_host
 
 extern "C" {
 
@@ -1161,8 +1174,8 @@ attn_status_t attn_decode_ragged_fwd(const void* q, const void* k, const void* v
   attn_status_t st = decode_device_ready(stream, &status);
   if (st != ATTN_OK) return st;
   DecodeParams p;
-  st = launch_ragged_split(q, k, v, lens, workspace, B, C, n_q, n_kv, scale, weighted, stream,
-                           status, &p);
+  st = launch_ragged_split(q, k, v, lens, workspace, B, C, n_q, n_kv, scale, weighted, false,
+                           stream, status, &p);
   if (st != ATTN_OK) return st;
   const int chunks = weighted ? static_cast<int>((C + kWeightKeys - 1) / kWeightKeys) : 0;
   cudaLaunchAttribute attr[1];

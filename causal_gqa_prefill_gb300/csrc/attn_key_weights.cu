@@ -241,7 +241,7 @@ key_weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     uint4* z = reinterpret_cast<uint4*>(generic + (sQ - base));
     for (int i = threadIdx.x; i < G::kQStages * G::kTileBytes / 16; i += 256)
       z[i] = make_uint4(0u, 0u, 0u, 0u);
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    fence_proxy_async_smem();
   }
   tc_fence_before_sync();
   __syncthreads();

@@ -234,6 +234,37 @@ attn_status_t attn_decode_ragged_fwd(const void* q, const void* k, const void* v
                                      void* stream);
 
 /*
+ * Decode behind a shared prefix: one new token per sequence attends to P
+ * positions that the whole batch shares (a system prompt, a document; stored
+ * once) and to the first lens[b] positions of its own cache, in one softmax:
+ *
+ *     O[b,h,:]  over the keys  prefix_k[0 .. P-1], k[b, 0 .. lens[b]-1]
+ *
+ *   q         bf16 [B, 1, n_q, 128]
+ *   prefix_k, prefix_v   bf16 [P, n_kv, 128], P >= 1
+ *   k, v      bf16 [B, C, n_kv, 128], C >= 1; positions at lens[b] and beyond
+ *             may hold anything
+ *   lens      int32 [B], device memory, 0 allowed, clamped to 0 .. C
+ *   o         bf16 [B, 1, n_q, 128]         lse   fp32 [B, n_q, 1]
+ *   workspace at least attn_decode_shared_workspace_bytes bytes, 16-byte
+ *             aligned, caller-owned, contents on entry ignored and on exit
+ *             unspecified
+ *   d_h = 128 and n_q / n_kv <= 16 (ATTN_ERR_UNSUPPORTED otherwise). Everything
+ *   else as attn_decode_ragged_fwd.
+ *
+ * Three kernels: the prefix's (a programmatic dependent of the kernel before
+ * the call), the own positions', which runs beside it, and the merge, which
+ * waits for both. Everything is complete when the merge is.
+ */
+int64_t attn_decode_shared_workspace_bytes(int64_t B, int64_t P, int64_t C, int32_t n_q,
+                                           int32_t n_kv, int32_t d_h);   /* -1 as above */
+attn_status_t attn_decode_shared_fwd(const void* q, const void* prefix_k, const void* prefix_v,
+                                     const void* k, const void* v, const int32_t* lens, void* o,
+                                     float* lse, void* workspace, int64_t workspace_bytes, int64_t B,
+                                     int64_t P, int64_t C, int32_t n_q, int32_t n_kv, int32_t d_h,
+                                     float scale, void* stream);
+
+/*
  * Eviction: brings caches down to a budget, keeping the positions whose
  * accumulated attention weight is largest and the most recent ones. Per
  * sequence b and K/V head u, with len = lens[b]:

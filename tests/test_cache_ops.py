@@ -98,6 +98,42 @@ def test_ragged_decode_workspace():
         assert size(*bad) == -1, bad
 
 
+# -------------------------------------------------------------- shared prefix
+
+SHARED_ORDER = ("q prefix_k prefix_v k v lens o lse workspace workspace_bytes B P C n_q n_kv d_h "
+                "scale").split()
+
+
+def _shared_base():
+    need = cg.attn_decode_shared_workspace_bytes(40, 1000, 300, 8, 2)
+    return dict(q=_at(0), prefix_k=_at(1), prefix_v=_at(2), k=_at(3), v=_at(4), lens=_at(5),
+                o=_at(6), lse=_at(7), workspace=_at(8), workspace_bytes=need, B=40, P=1000, C=300,
+                n_q=8, n_kv=2, d_h=128, scale=0.1)
+
+
+@pytest.mark.parametrize("change,expect", [
+    (dict(q=0), BAD), (dict(prefix_k=0), BAD), (dict(prefix_v=0), BAD), (dict(k=0), BAD),
+    (dict(v=0), BAD), (dict(lens=0), BAD), (dict(o=0), BAD), (dict(lse=0), BAD),
+    (dict(workspace=0), BAD), (dict(B=0), BAD), (dict(P=0), BAD), (dict(C=0), BAD),
+    (dict(n_q=9), BAD), (dict(n_kv=-1), BAD), (dict(scale=math.inf), BAD),
+    (dict(prefix_k=_at(1) + 8), BAD), (dict(lens=_at(5) + 1), BAD),
+    (dict(workspace=_at(8) + 8), BAD), (dict(d_h=64), UNSUP), (dict(n_q=34), UNSUP),
+    (dict(P=1 << 31), UNSUP), (dict(C=1 << 31), UNSUP), (dict(B=1 << 25), UNSUP),
+], ids=str)
+def test_shared_decode_refuses(change, expect):
+    assert _call(cg.attn_decode_shared_fwd, SHARED_ORDER, _shared_base(), change) == expect
+
+
+def test_shared_decode_workspace():
+    base = _shared_base()
+    small = dict(workspace_bytes=base["workspace_bytes"] - 1)
+    assert _call(cg.attn_decode_shared_fwd, SHARED_ORDER, base, small) == BAD
+    size = cg.attn_decode_shared_workspace_bytes
+    for bad in ((0, 1, 1, 1, 1), (1, 0, 1, 1, 1), (1, 1, 0, 1, 1), (1, 1, 1, 3, 2),
+                (1, 1, 1, 17, 1), (1, 1, 1, 1, 1, 64)):
+        assert size(*bad) == -1, bad
+
+
 # ------------------------------------------------------------------ eviction
 
 EVICT_ORDER = ("k v weights lens k_out v_out weights_out lens_out index B C C_out budget recent "
