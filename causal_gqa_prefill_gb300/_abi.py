@@ -106,6 +106,8 @@ def library_path() -> str:
 def load(path: str | None = None):
     """Load (once) and return the ctypes handle of the CUDA library."""
     global _lib
+    if _lib is not None and path is None:
+        return _lib
     with _lock:
         if _lib is not None and path is None:
             return _lib

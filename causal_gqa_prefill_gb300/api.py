@@ -149,32 +149,63 @@ def attn_decode(q, k, v, *, scale=None, workspace=None, out=None, lse=None, stre
     return out, lse
 
 
-def _on_stream(device, stream):
-    """(raw stream handle, torch stream when it is not ``device``'s current one)
-    for a call over tensors of ``device``."""
-    import torch
+class _Call:
+    """Where a call over tensors of ``device`` runs: makes the device current,
+    ``handle`` is the raw stream."""
 
-    current = torch.cuda.current_stream(device)
-    if stream is None:
-        return int(current.cuda_stream), None
-    if isinstance(stream, int):
-        if stream == int(current.cuda_stream):
-            return stream, None
-        return stream, torch.cuda.ExternalStream(stream, device=device)
-    return int(stream.cuda_stream), None if stream == current else stream
+    __slots__ = ("torch", "device", "guard", "handle", "other")
 
+    def __init__(self, torch, device, stream):
+        self.torch = torch
+        self.device = device
+        self.guard = None
+        self.other = None                 # the torch stream, when it is not the current one
+        if torch.cuda.current_device() != device.index:
+            self.guard = torch.cuda.device(device)
+        self.handle = torch.cuda.current_stream(device).cuda_stream
+        if stream is not None:
+            handle = stream if isinstance(stream, int) else stream.cuda_stream
+            if handle != self.handle:
+                self.handle = handle
+                self.other = torch.cuda.ExternalStream(handle, device=device)
 
-def _keep_for(stream, *tensors):
-    """Memory allocated here for a call on another stream than the current one
-    must not be handed out again before that stream is done with it."""
-    if stream is not None:
-        for t in tensors:
-            t.record_stream(stream)
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+    def empty(self, shape, dtype):
+        """Memory for the call; on another stream than the current one it is not
+        handed out again before that stream is done with it."""
+        t = self.torch.empty(shape, dtype=dtype, device=self.device)
+        if self.other is not None:
+            t.record_stream(self.other)
+        return t
+
+    def workspace(self, given, size, *sizes):
+        """(workspace, its bytes): the one given, or one of size(*sizes) bytes."""
+        if given is None:
+            nbytes = size(*sizes)
+            if nbytes < 0:
+                raise AttnError(_abi.ATTN_ERR_UNSUPPORTED, size.__name__)
+            return self.empty(nbytes, self.torch.uint8), nbytes
+        if not isinstance(given, self.torch.Tensor) or given.device != self.device:
+            raise ValueError(f"workspace must be a tensor on {self.device}")
+        if not given.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+        return given, given.numel() * given.element_size()
 
 
 def _cuda_tensor(name, t, shape, dtype, device=None):
-    """A contiguous CUDA tensor of this shape (None: any size) and dtype, on
-    ``device``."""
+    """``t`` if it is a contiguous CUDA tensor of this shape (None: any size) and
+    dtype, on ``device``; else the error that says what it should be."""
+    if (getattr(t, "dtype", None) is dtype and t.device == device and t.shape == shape
+            and t.is_contiguous()):
+        return t                          # the usual case, in as few steps as it takes
     import torch
 
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dtype:
@@ -230,20 +261,14 @@ def attn_key_weights(q, k, lse, *, causal=True, scale=None, weights=None, accumu
         raise ValueError("accumulate needs the weights to add to")
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    need = attn_key_weights_workspace_bytes(B, Lq, Lk, n_q, n_kv, d)
-    if need < 0:
-        raise AttnError(_abi.ATTN_ERR_UNSUPPORTED, "attn_key_weights_workspace_bytes")
-    with torch.cuda.device(dev):
-        handle, other = _on_stream(dev, stream)
-        if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-            _keep_for(other, workspace)
+    with _Call(torch, dev, stream) as call:
+        workspace, nbytes = call.workspace(workspace, attn_key_weights_workspace_bytes, B, Lq, Lk,
+                                           n_q, n_kv, d)
         if weights is None:
-            weights = torch.empty((B, n_kv, Lk), dtype=torch.float32, device=dev)
-            _keep_for(other, weights)
-        nbytes = workspace.numel() * workspace.element_size()
-        st = attn_key_weights_fwd(q, k, lse, weights, workspace, nbytes, B, Lq, Lk, n_q, n_kv, d,
-                                  int(bool(causal)), int(bool(accumulate)), scale, handle)
+            weights = call.empty((B, n_kv, Lk), torch.float32)
+        st = _abi.load().attn_key_weights_fwd(
+            q.data_ptr(), k.data_ptr(), lse.data_ptr(), weights.data_ptr(), workspace.data_ptr(),
+            nbytes, B, Lq, Lk, n_q, n_kv, d, bool(causal), bool(accumulate), scale, call.handle)
     if st != _abi.ATTN_OK:
         raise AttnError(st, "attn_key_weights_fwd")
     return weights
@@ -293,23 +318,17 @@ def attn_decode_ragged(q, k, v, lens, *, weights=None, scale=None, workspace=Non
         _cuda_tensor("lse", lse, (B, n_q, 1), torch.float32, dev)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    need = attn_decode_ragged_workspace_bytes(B, C, n_q, n_kv, d, weights is not None)
-    if need < 0:
-        raise AttnError(_abi.ATTN_ERR_UNSUPPORTED, "attn_decode_ragged_workspace_bytes")
-    with torch.cuda.device(dev):
-        handle, other = _on_stream(dev, stream)
-        if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-            _keep_for(other, workspace)
+    with _Call(torch, dev, stream) as call:
+        workspace, nbytes = call.workspace(workspace, attn_decode_ragged_workspace_bytes, B, C, n_q,
+                                           n_kv, d, weights is not None)
         if out is None:
-            out = torch.empty_like(q)
-            _keep_for(other, out)
+            out = call.empty(q.shape, bf16)
         if lse is None:
-            lse = torch.empty((B, n_q, 1), dtype=torch.float32, device=dev)
-            _keep_for(other, lse)
-        nbytes = workspace.numel() * workspace.element_size()
-        st = attn_decode_ragged_fwd(q, k, v, lens, weights, out, lse, workspace, nbytes, B, C, n_q,
-                                    n_kv, d, scale, handle)
+            lse = call.empty((B, n_q, 1), torch.float32)
+        st = _abi.load().attn_decode_ragged_fwd(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), lens.data_ptr(), _ptr(weights),
+            out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), nbytes, B, C, n_q, n_kv, d, scale,
+            call.handle)
     if st != _abi.ATTN_OK:
         raise AttnError(st, "attn_decode_ragged_fwd")
     return out, lse
@@ -357,23 +376,17 @@ def attn_decode_shared(q, prefix_k, prefix_v, k, v, lens, *, scale=None, workspa
         _cuda_tensor("lse", lse, (B, n_q, 1), torch.float32, dev)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    need = attn_decode_shared_workspace_bytes(B, P, C, n_q, n_kv, d)
-    if need < 0:
-        raise AttnError(_abi.ATTN_ERR_UNSUPPORTED, "attn_decode_shared_workspace_bytes")
-    with torch.cuda.device(dev):
-        handle, other = _on_stream(dev, stream)
-        if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-            _keep_for(other, workspace)
+    with _Call(torch, dev, stream) as call:
+        workspace, nbytes = call.workspace(workspace, attn_decode_shared_workspace_bytes, B, P, C,
+                                           n_q, n_kv, d)
         if out is None:
-            out = torch.empty_like(q)
-            _keep_for(other, out)
+            out = call.empty(q.shape, bf16)
         if lse is None:
-            lse = torch.empty((B, n_q, 1), dtype=torch.float32, device=dev)
-            _keep_for(other, lse)
-        nbytes = workspace.numel() * workspace.element_size()
-        st = attn_decode_shared_fwd(q, prefix_k, prefix_v, k, v, lens, out, lse, workspace, nbytes,
-                                    B, P, C, n_q, n_kv, d, scale, handle)
+            lse = call.empty((B, n_q, 1), torch.float32)
+        st = _abi.load().attn_decode_shared_fwd(
+            q.data_ptr(), prefix_k.data_ptr(), prefix_v.data_ptr(), k.data_ptr(), v.data_ptr(),
+            lens.data_ptr(), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), nbytes, B, P, C,
+            n_q, n_kv, d, scale, call.handle)
     if st != _abi.ATTN_OK:
         raise AttnError(st, "attn_decode_shared_fwd")
     return out, lse
@@ -426,18 +439,13 @@ def attn_evict(k, v, weights, lens, budget, recent=0, *, capacity=None, k_out=No
               "weights_out": (weights_out, (B, n_kv, capacity), torch.float32),
               "lens_out": (lens_out, (B,), torch.int32),
               "index": (index, (B, n_kv, budget), torch.int32)}
-    with torch.cuda.device(dev):
-        handle, other = _on_stream(dev, stream)
-        outs = []
-        for name, (t, shape, dtype) in wanted.items():
-            if t is None:
-                t = torch.empty(shape, dtype=dtype, device=dev)
-                _keep_for(other, t)
-            else:
-                _cuda_tensor(name, t, shape, dtype, dev)
-            outs.append(t)
-        st = attn_cache_evict(k, v, weights, lens, *outs, B, C, capacity, budget, recent, n_kv, d,
-                              k.element_size(), handle)
+    with _Call(torch, dev, stream) as call:
+        outs = [call.empty(shape, dtype) if t is None else _cuda_tensor(name, t, shape, dtype, dev)
+                for name, (t, shape, dtype) in wanted.items()]
+        st = _abi.load().attn_cache_evict(
+            k.data_ptr(), v.data_ptr(), weights.data_ptr(), lens.data_ptr(),
+            *(t.data_ptr() for t in outs), B, C, capacity, budget, recent, n_kv, d,
+            k.element_size(), call.handle)
     if st != _abi.ATTN_OK:
         raise AttnError(st, "attn_cache_evict")
     return tuple(outs)

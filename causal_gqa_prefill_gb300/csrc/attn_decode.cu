@@ -24,7 +24,10 @@
 //                 thread per key; the running maximum moves lazily, so the
 //                 cross-thread maximum is only taken when a score exceeds it
 //                 by the threshold). It writes the segment's normalised partial
-//                 output and log-sum-exp to the workspace.
+//                 output and log-sum-exp to the workspace. Both the scores
+//                 of the next tile and the output of the segment before run
+//                 across segment borders (two O^T accumulators), so many short
+//                 segments go at the pace of one long one.
 //   combine       one CTA per (b, query head) merges the head's segments
 //                 through their log-sum-exps into bf16 O and fp32 LSE.
 //
@@ -65,18 +68,19 @@ constexpr int kKeys = 128;           // keys per tile (= TMEM lanes of S^T)
 constexpr int kHeadsPad = 16;        // N of both products: the group's heads, padded
 constexpr int kMaxG = 16;            // query heads per K/V head
 constexpr int kRing = 6;             // K/V ring slots (K and V tiles alternate)
+constexpr int kQBufs = 4;            // Q tiles: the ring may hold the K/V of three one-tile segments
 constexpr int kTileBytes = kKeys * kDim * 2;          // 32 KiB: two 128 x 64 swizzled chunks
 constexpr int kChunkBytes = kKeys * 128;              // 16 KiB
 constexpr int kQBytes = kHeadsPad * kDim * 2;         // 4 KiB: two 16 x 64 chunks
 constexpr int kPBytes = kHeadsPad * kKeys * 2;        // 4 KiB: P as 16 heads x 128 keys
 constexpr int kSmallChunk = kHeadsPad * 128;          // 2 KiB: one 16-row swizzled chunk
-constexpr int kSmemBytes = kRing * kTileBytes + 2 * kQBytes + 2 * kPBytes + 1024;
+constexpr int kSmemBytes = kRing * kTileBytes + kQBufs * kQBytes + 2 * kPBytes + 1024;
 constexpr int kDecodeCtas = 152;     // one CTA per SM on a 152-SM GB300
 constexpr int kThreads = 192;        // warps 0-3 softmax, 4 TMA producer, 5 MMA issuer
 constexpr int kLoadWarp = 4, kMmaWarp = 5;
 constexpr uint32_t kTmemCols = 64;
 constexpr uint32_t kColS = 0;        // S^T buffers at columns 0 and 16
-constexpr uint32_t kColO = 32;       // O^T accumulator
+constexpr uint32_t kColO = 32;       // O^T accumulators at columns 32 and 48
 constexpr float kRescale = 8.0f;     // lazy running-max threshold (log2 units)
 constexpr int kStatusTimeout = 1;
 
@@ -101,9 +105,9 @@ struct DecodeParams {
 
 struct DecodeCtl {
   uint64_t full[kRing], empty[kRing];
-  uint64_t q_full[2], q_empty[2];
+  uint64_t q_full[kQBufs], q_empty[kQBufs];
   uint64_t s_full[2], p_full[2], pv_done[2];
-  uint64_t o_done, o_free, drain;
+  uint64_t o_done[2], o_free[2], drain;
   uint32_t tmem_base;
   int abort;
   float red_m[4][kHeadsPad];
@@ -153,37 +157,6 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, const 
     if (static_cast<long long>(clock64_now() - t0) > p.spin_limit) return;
 }
 
-// 16 consecutive 32-bit TMEM columns of this thread's lane.
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
-        "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
-}
-
-__device__ __forceinline__ void tmem_wait_ld16(uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.wait::ld.sync.aligned;"
-      : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
-        "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
-        "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-      :
-      : "memory");
-}
-
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
-      ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]),
-        "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]),
-        "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
-
 // Named barrier 1 over the 128 softmax threads; the OR of `v` over them.
 __device__ __forceinline__ void bar_softmax() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 __device__ __forceinline__ bool bar_softmax_any(bool v) {
@@ -197,6 +170,31 @@ __device__ __forceinline__ bool bar_softmax_any(bool v) {
       : "r"(static_cast<uint32_t>(v))
       : "memory");
   return r != 0;
+}
+
+// Reduces GP per-head values over the warp: log2(GP) steps that each halve
+// the heads a lane carries (it keeps one half and sends the other), then plain
+// steps. Lane l returns the result of head l / (32 / GP): GP + 3 - log2(GP)
+// shuffles or so where a butterfly per head takes 5 GP, in the same order.
+template <int GP, typename Op>
+__device__ __forceinline__ float reduce_heads(const float (&in)[GP], Op op) {
+  const int lane = threadIdx.x & 31;
+  float v[GP];
+#pragma unroll
+  for (int h = 0; h < GP; ++h) v[h] = in[h];
+  int off = 16;
+#pragma unroll
+  for (int width = GP / 2; width > 0; width >>= 1, off >>= 1) {
+    const bool upper = (lane & off) != 0;
+#pragma unroll
+    for (int i = 0; i < width; ++i) {
+      const float send = upper ? v[i] : v[i + width], keep = upper ? v[i + width] : v[i];
+      v[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, off));
+    }
+  }
+#pragma unroll
+  for (; off > 0; off >>= 1) v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], off));
+  return v[0];
 }
 
 // One segment of a CTA's tile range: K/V head `hd` (= b * n_kv + kv head),
@@ -332,9 +330,9 @@ attn_decode_split_kernel(const __grid_constant__ CUtensorMap tmQ,
                          const __grid_constant__ CUtensorMap tmV, const DecodeParams p) {
   extern __shared__ uint8_t dyn_smem[];
   __shared__ DecodeCtl ctl;
-  // smem: kRing K/V tiles | Q[2] (16 heads x 128, two 2 KiB chunks) | P[2]
+  // smem: kRing K/V tiles | Q[kQBufs] (16 heads x 128, two 2 KiB chunks) | P[2]
   const uint32_t base = (smem_addr(dyn_smem) + 1023u) & ~1023u;   // swizzle atoms need 1 KiB
-  const uint32_t sRing = base, sQ = base + kRing * kTileBytes, sP = sQ + 2 * kQBytes;
+  const uint32_t sRing = base, sQ = base + kRing * kTileBytes, sP = sQ + kQBufs * kQBytes;
   uint8_t* const pgen = dyn_smem + (sP - smem_addr(dyn_smem));      // generic address of P[0]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int cta = static_cast<int>(blockIdx.x);
@@ -347,15 +345,17 @@ attn_decode_split_kernel(const __grid_constant__ CUtensorMap tmQ,
       mbar_init(smem_addr(&ctl.full[s]), 1);
       mbar_init(smem_addr(&ctl.empty[s]), 1);
     }
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < kQBufs; ++s) {
       mbar_init(smem_addr(&ctl.q_full[s]), 1);
       mbar_init(smem_addr(&ctl.q_empty[s]), 1);
+    }
+    for (int s = 0; s < 2; ++s) {
       mbar_init(smem_addr(&ctl.s_full[s]), 1);
       mbar_init(smem_addr(&ctl.p_full[s]), 128);
       mbar_init(smem_addr(&ctl.pv_done[s]), 1);
+      mbar_init(smem_addr(&ctl.o_done[s]), 1);
+      mbar_init(smem_addr(&ctl.o_free[s]), 128);
     }
-    mbar_init(smem_addr(&ctl.o_done), 1);
-    mbar_init(smem_addr(&ctl.o_free), 128);
     mbar_init(smem_addr(&ctl.drain), 1);
     ctl.abort = 0;
     fence_mbar_init();
@@ -399,8 +399,9 @@ attn_decode_split_kernel(const __grid_constant__ CUtensorMap tmQ,
       bool ok = true;
       while (ok && walk.next(sg)) {
         const int b = sg.hd / p.n_kv, kvh = sg.hd - b * p.n_kv;
-        const uint32_t qb = qn & 1;
-        if (qn >= 2 && !spin_wait(smem_addr(&ctl.q_empty[qb]), ((qn >> 1) - 1) & 1, ctl, p)) {
+        const uint32_t qb = qn % kQBufs;
+        if (qn >= kQBufs &&
+            !spin_wait(smem_addr(&ctl.q_empty[qb]), (qn / kQBufs - 1) & 1, ctl, p)) {
           ok = false;
           break;
         }
@@ -428,10 +429,8 @@ attn_decode_split_kernel(const __grid_constant__ CUtensorMap tmQ,
       }
       if (!ok) {
         // Let every copy this thread started land before the CTA can exit.
-        for (uint32_t s = 0; s < 2 && s < qn; ++s) {
-          const uint32_t last = s + ((qn - 1 - s) / 2) * 2;
-          drain_wait(smem_addr(&ctl.q_full[s]), (last >> 1) & 1, p);
-        }
+        for (uint32_t s = 0; s < kQBufs && s < qn; ++s)
+          drain_wait(smem_addr(&ctl.q_full[s]), ((qn - 1 - s) / kQBufs) & 1, p);
         for (uint32_t s = 0; s < kRing && s < it; ++s) {
           const uint32_t last = s + ((it - 1 - s) / kRing) * kRing;
           drain_wait(smem_addr(&ctl.full[s]), (last / kRing) & 1, p);
@@ -446,69 +445,77 @@ attn_decode_split_kernel(const __grid_constant__ CUtensorMap tmQ,
     constexpr uint32_t kIdS = idesc_bf16_f32(kKeys, kHeadsPad, false);
     // O^T = V^T P^T: M = 128 dims with V read MN-major (bit 15), B = P K-major.
     constexpr uint32_t kIdO = idesc_bf16_f32(kDim, kHeadsPad, false) | (1u << 15);
-    Walk walk(p, ctl, cta);
-    Segment sg;
-    uint32_t it = 0, gt = 0, sn = 0;
-    bool ok = true;
+    // Two cursors over the CTA's tiles: the products of tile gt are issued in
+    // two parts, S^T one tile ahead (also over a segment's end, so that short
+    // segments keep the same pace) and O^T once the softmax has written P.
+    // Tile gt is ring items 2 gt (K) and 2 gt + 1 (V).
+    struct Cursor {
+      Walk walk;
+      Segment sg;
+      int t;
+      uint32_t sn;       // segment number
+      bool live;
+      __device__ explicit Cursor(const Walk& w) : walk(w), t(0), sn(0) { live = walk.next(sg); }
+      __device__ void advance() {
+        if (++t < sg.n) return;
+        t = 0;
+        ++sn;
+        live = walk.next(sg);
+      }
+    };
+    Cursor ahead(Walk(p, ctl, cta));
+    Cursor cur = ahead;
     auto wait_item = [&](uint32_t item) {
       const bool r = wait_warp(smem_addr(&ctl.full[item % kRing]), (item / kRing) & 1, ctl, p);
       tc_fence_after_sync();
       return r;
     };
-    auto issue_s = [&](uint32_t kitem, uint32_t qb, uint32_t sbuf) {
+    // S^T of the tile `ahead` is at (tile number gt); false: a wait gave up
+    auto issue_s = [&](uint32_t gt) {
+      const uint32_t qb = ahead.sn % kQBufs;
+      if (ahead.t == 0 && !wait_warp(smem_addr(&ctl.q_full[qb]), (ahead.sn / kQBufs) & 1, ctl, p))
+        return false;
+      const uint32_t kitem = 2 * gt;
+      if (!wait_item(kitem)) return false;
       const uint32_t k_smem = sRing + (kitem % kRing) * kTileBytes, q_smem = sQ + qb * kQBytes;
 #pragma unroll
       for (int kk = 0; kk < kDim / 16; ++kk) {
         const uint64_t a = sdesc_sw128(k_smem + (kk >> 2) * kChunkBytes + (kk & 3) * 32, 16, 1024);
         const uint64_t bq = sdesc_sw128(q_smem + (kk >> 2) * kSmallChunk + (kk & 3) * 32, 16, 1024);
-        if (leader) mma_ss(tmem + kColS + 16 * sbuf, a, bq, kIdS, kk > 0 ? 1u : 0u);
+        if (leader) mma_ss(tmem + kColS + 16 * (gt & 1), a, bq, kIdS, kk > 0 ? 1u : 0u);
       }
-      if (leader) mma_commit(smem_addr(&ctl.s_full[sbuf]));
+      if (leader) mma_commit(smem_addr(&ctl.s_full[gt & 1]));
       if (leader) mma_commit(smem_addr(&ctl.empty[kitem % kRing]));
+      if (ahead.t == ahead.sg.n - 1 && leader) mma_commit(smem_addr(&ctl.q_empty[qb]));
+      ahead.advance();
+      return true;
     };
-    while (ok && walk.next(sg)) {
-      const uint32_t qb = sn & 1, it0 = it;
-      if (!wait_warp(smem_addr(&ctl.q_full[qb]), (sn >> 1) & 1, ctl, p) || !wait_item(it0)) {
-        ok = false;
+    bool ok = !ahead.live || issue_s(0);
+    for (uint32_t gt = 0; ok && cur.live; ++gt) {
+      // scores of the next tile run while the softmax works on this one
+      if (ahead.live && !issue_s(gt + 1)) break;
+      // O^T of two segments ago must have been read out first
+      const uint32_t ob = cur.sn & 1;
+      if (cur.t == 0 && cur.sn >= 2 &&
+          !wait_warp(smem_addr(&ctl.o_free[ob]), ((cur.sn >> 1) - 1) & 1, ctl, p))
         break;
-      }
-      issue_s(it0, qb, gt & 1);
-      if (sg.n == 1 && leader) mma_commit(smem_addr(&ctl.q_empty[qb]));
-      for (int t = 0; t < sg.n; ++t, ++gt) {
-        // scores of the next tile run while the softmax works on this one
-        if (t + 1 < sg.n) {
-          if (!wait_item(it0 + 2 * (t + 1))) { ok = false; break; }
-          issue_s(it0 + 2 * (t + 1), qb, (gt + 1) & 1);
-          if (t + 2 == sg.n && leader) mma_commit(smem_addr(&ctl.q_empty[qb]));
-        }
-        // O^T of the previous segment must have been read out first
-        if (t == 0 && sn > 0 && !wait_warp(smem_addr(&ctl.o_free), (sn - 1) & 1, ctl, p)) {
-          ok = false;
-          break;
-        }
-        if (!wait_warp(smem_addr(&ctl.p_full[gt & 1]), (gt >> 1) & 1, ctl, p) ||
-            !wait_item(it0 + 2 * t + 1)) {
-          ok = false;
-          break;
-        }
-        const uint32_t vitem = it0 + 2 * t + 1;
-        const uint32_t v_smem = sRing + (vitem % kRing) * kTileBytes;
-        const uint32_t p_smem = sP + (gt & 1) * kPBytes;
+      const uint32_t vitem = 2 * gt + 1;
+      if (!wait_warp(smem_addr(&ctl.p_full[gt & 1]), (gt >> 1) & 1, ctl, p) || !wait_item(vitem))
+        break;
+      const uint32_t v_smem = sRing + (vitem % kRing) * kTileBytes;
+      const uint32_t p_smem = sP + (gt & 1) * kPBytes;
 #pragma unroll
-        for (int kk = 0; kk < kKeys / 16; ++kk) {
-          // V^T: a K step of 16 keys spans 16 rows (2 KiB); the two 64-dim
-          // chunks are kChunkBytes apart. P: 32 bytes per K step.
-          const uint64_t a = sdesc_sw128(v_smem + kk * 16 * 128, kChunkBytes, 1024);
-          const uint64_t bp = sdesc_sw128(p_smem + (kk >> 2) * kSmallChunk + (kk & 3) * 32, 16, 1024);
-          if (leader) mma_ss(tmem + kColO, a, bp, kIdO, (t > 0 || kk > 0) ? 1u : 0u);
-        }
-        if (leader) mma_commit(smem_addr(&ctl.pv_done[gt & 1]));
-        if (leader) mma_commit(smem_addr(&ctl.empty[vitem % kRing]));
+      for (int kk = 0; kk < kKeys / 16; ++kk) {
+        // V^T: a K step of 16 keys spans 16 rows (2 KiB); the two 64-dim
+        // chunks are kChunkBytes apart. P: 32 bytes per K step.
+        const uint64_t a = sdesc_sw128(v_smem + kk * 16 * 128, kChunkBytes, 1024);
+        const uint64_t bp = sdesc_sw128(p_smem + (kk >> 2) * kSmallChunk + (kk & 3) * 32, 16, 1024);
+        if (leader) mma_ss(tmem + kColO + 16 * ob, a, bp, kIdO, (cur.t > 0 || kk > 0) ? 1u : 0u);
       }
-      if (!ok) break;
-      if (leader) mma_commit(smem_addr(&ctl.o_done));
-      it = it0 + 2 * sg.n;
-      ++sn;
+      if (leader) mma_commit(smem_addr(&ctl.pv_done[gt & 1]));
+      if (leader) mma_commit(smem_addr(&ctl.empty[vitem % kRing]));
+      if (cur.t == cur.sg.n - 1 && leader) mma_commit(smem_addr(&ctl.o_done[ob]));
+      cur.advance();
     }
     // No MMA may still be running when TMEM is released.
     if (leader) mma_commit(smem_addr(&ctl.drain));
@@ -525,7 +532,6 @@ attn_decode_split_kernel(const __grid_constant__ CUtensorMap tmQ,
     Walk walk(p, ctl, cta);
     Segment sg;
     uint32_t gt = 0, sn = 0;
-    uint32_t it0 = 0;   // ring item of the segment's first K tile (ragged step)
     bool ok = true;
     // Every wait of these four warps ends in a vote over all 128 threads, so
     // they leave together when one of them gives up and none is left alone
@@ -535,8 +541,41 @@ attn_decode_split_kernel(const __grid_constant__ CUtensorMap tmQ,
       tc_fence_after_sync();
       return !fail;
     };
+    float m_run[GP], l_thr[GP];
+    // The segment before, finished but for its output: its product is still
+    // running when its last P is written, so its output waits until this
+    // segment's first P is under way.
+    Segment old;
+    float m_old[GP], l_old[GP];
+    bool pending = false;
+    // O^T / l and the log-sum-exp of segment number `num`
+    auto finish = [&](uint32_t num) {
+      if (!waited(smem_addr(&ctl.o_done[num & 1]), (num >> 1) & 1)) return false;
+      uint32_t ov[16];
+      tmem_ld16(lane_base + kColO + 16 * (num & 1), ov);
+      tmem_wait_ld16(ov);
+      tc_fence_before_sync();
+      mbar_arrive(smem_addr(&ctl.o_free[num & 1]));
+      const float part = reduce_heads<GP>(l_old, [](float a, float b) { return a + b; });
+      if (lane % (32 / GP) == 0) ctl.red_l[warp][lane / (32 / GP)] = part;
+      bar_softmax();
+      const size_t row0 = static_cast<size_t>(old.id) * p.g;
+      if (kRagged && r == 0) {
+        if (old.t0 == 0) p.ends[2 * old.hd] = cta;
+        if (old.t0 + old.n == old.tiles) p.ends[2 * old.hd + 1] = cta;
+      }
+#pragma unroll
+      for (int h = 0; h < GP; ++h) {
+        if (h >= p.g) break;
+        const float l = ctl.red_l[0][h] + ctl.red_l[1][h] + ctl.red_l[2][h] + ctl.red_l[3][h];
+        p.part_o[(row0 + h) * kDim + r] = __uint_as_float(ov[h]) / l;
+        if (r == h)
+          p.part_lse[row0 + h] =
+              (m_old[h] + log2f(l)) * (kRagged ? 1.0f : 0.69314718055994530942f);
+      }
+      return true;
+    };
     while (ok && walk.next(sg)) {
-      float m_run[GP], l_thr[GP];
 #pragma unroll
       for (int h = 0; h < GP; ++h) {
         m_run[h] = -INFINITY;
@@ -567,14 +606,8 @@ attn_decode_split_kernel(const __grid_constant__ CUtensorMap tmQ,
         }
         if (bar_softmax_any(need)) {
           // exact maximum of this tile per head, then move the running maxima
-#pragma unroll
-          for (int h = 0; h < GP; ++h) {
-            if (h >= p.g) break;
-            float v = x[h];
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
-            if (lane == 0) ctl.red_m[warp][h] = v;
-          }
+          const float top = reduce_heads<GP>(x, [](float a, float b) { return fmaxf(a, b); });
+          if (lane % (32 / GP) == 0) ctl.red_m[warp][lane / (32 / GP)] = top;
           bar_softmax();
           float alpha[GP];
           bool scaled = false;
@@ -600,11 +633,11 @@ attn_decode_split_kernel(const __grid_constant__ CUtensorMap tmQ,
               break;
             }
             uint32_t ov[16];
-            tmem_ld16(lane_base + kColO, ov);
+            tmem_ld16(lane_base + kColO + 16 * (sn & 1), ov);
             tmem_wait_ld16(ov);
 #pragma unroll
             for (int h = 0; h < GP; ++h) ov[h] = __float_as_uint(__uint_as_float(ov[h]) * alpha[h]);
-            tmem_st16(lane_base + kColO, ov);
+            tmem_st16(lane_base + kColO + 16 * (sn & 1), ov);
             tmem_wait_st();
           }
         }
@@ -625,7 +658,7 @@ attn_decode_split_kernel(const __grid_constant__ CUtensorMap tmQ,
         if (kRagged && (sg.t0 + t + 1) * kKeys > sg.len) {
           // a tile that ends past the sequence: zeros over what V holds there
           // (the tensor cores read V only after this tile's p_full)
-          const uint32_t item = it0 + 2 * t + 1, slot = item % kRing;
+          const uint32_t item = 2 * gt + 1, slot = item % kRing;
           if (!waited(smem_addr(&ctl.full[slot]), (item / kRing) & 1)) {
             ok = false;
             break;
@@ -634,50 +667,30 @@ attn_decode_split_kernel(const __grid_constant__ CUtensorMap tmQ,
             uint4* row = reinterpret_cast<uint4*>(dyn_smem + (sRing - smem_addr(dyn_smem)) +
                                                   slot * kTileBytes + r * 128);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              row[e] = make_uint4(0u, 0u, 0u, 0u);
-              row[e + kChunkBytes / 16] = make_uint4(0u, 0u, 0u, 0u);
+            for (int e = 0; e < 8; ++e) {    // eight lanes at a time on all banks
+              row[(e + r) & 7] = make_uint4(0u, 0u, 0u, 0u);
+              row[((e + r) & 7) + kChunkBytes / 16] = make_uint4(0u, 0u, 0u, 0u);
             }
           }
         }
         fence_proxy_async_smem();
         tc_fence_before_sync();
         mbar_arrive(smem_addr(&ctl.p_full[gt & 1]));
+        if (t == 0 && pending && !finish(sn - 1)) {
+          ok = false;
+          break;
+        }
       }
-      if (!ok) break;
-      it0 += 2 * sg.n;
-      // epilogue: O^T / l and the log-sum-exp of this segment
-      if (!waited(smem_addr(&ctl.o_done), sn & 1)) break;
-      uint32_t ov[16];
-      tmem_ld16(lane_base + kColO, ov);
-      tmem_wait_ld16(ov);
-      tc_fence_before_sync();
-      mbar_arrive(smem_addr(&ctl.o_free));
+      old = sg;
 #pragma unroll
       for (int h = 0; h < GP; ++h) {
-        if (h >= p.g) break;
-        float v = l_thr[h];
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-        if (lane == 0) ctl.red_l[warp][h] = v;
+        m_old[h] = m_run[h];
+        l_old[h] = l_thr[h];
       }
-      bar_softmax();
-      const size_t row0 = static_cast<size_t>(sg.id) * p.g;
-      if (kRagged && r == 0) {
-        if (sg.t0 == 0) p.ends[2 * sg.hd] = cta;
-        if (sg.t0 + sg.n == sg.tiles) p.ends[2 * sg.hd + 1] = cta;
-      }
-#pragma unroll
-      for (int h = 0; h < GP; ++h) {
-        if (h >= p.g) break;
-        const float l = ctl.red_l[0][h] + ctl.red_l[1][h] + ctl.red_l[2][h] + ctl.red_l[3][h];
-        p.part_o[(row0 + h) * kDim + r] = __uint_as_float(ov[h]) / l;
-        if (r == h)
-          p.part_lse[row0 + h] =
-              (m_run[h] + log2f(l)) * (kRagged ? 1.0f : 0.69314718055994530942f);
-      }
+      pending = true;
       ++sn;
     }
+    if (ok && pending) finish(sn - 1);
   }
 
   tc_fence_before_sync();
@@ -764,28 +777,36 @@ attn_decode_combine_kernel(uint16_t* o, float* lse, const DecodeParams p) {
   }
 }
 
-// The ragged step's combine. The first B * n_q CTAs merge a head's segments,
-// rows hd + first .. hd + last CTA, as above (their log-sum-exps are in log2
-// units); a sequence without a key gets O = 0 and LSE = -inf. With weights,
-// `chunks` CTAs per (b, K/V head) follow, one per kWeightKeys positions: each
-// rebuilds the log-sum-exps of the group's heads and adds
+// The ragged step's combine. The first `merges` CTAs merge the segments of
+// eight / kPerRow heads' rows each, segments hd + first .. hd + last CTA, as above
+// (their log-sum-exps are in log2 units): one warp per row where a head has few
+// segments (16384 rows of one or two: 12 us, with eight warps per row 145), eight
+// where it has many. A sequence without a key gets O = 0 and LSE = -inf. With
+// weights, `chunks` CTAs per (b, K/V head) follow, one per kWeightKeys positions:
+// each rebuilds the log-sum-exps of the group's heads and adds
 //   sum_h 2^(score_hj - lse2_h)
-// to the weight of position j.
-constexpr int kWeightKeys = 2048;
+// to the weight of position j. The scores of the first four heads are on their
+// way while the log-sum-exps are rebuilt.
+constexpr int kWeightKeys = 1024;
+constexpr int kWeightPer = kWeightKeys / (32 * kCombineWarps);   // positions per thread
+constexpr int kWeightAhead = 4;
 
+template <int kPerRow>
 __global__ void __launch_bounds__(32 * kCombineWarps)
-attn_decode_ragged_combine_kernel(uint16_t* o, float* lse, float* weights, int chunks,
+attn_decode_ragged_combine_kernel(uint16_t* o, float* lse, float* weights, int merges, int chunks,
                                   const DecodeParams p) {
+  constexpr int kRows = kCombineWarps / kPerRow;
   __shared__ float red_m[kCombineWarps], red_w[kCombineWarps];
   __shared__ float4 red_o[kCombineWarps][32];
   __shared__ float lse2[kMaxG];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const long long merges = static_cast<long long>(p.B) * p.n_q;
-  const bool merge = blockIdx.x < merges;
-  const long long rest = merge ? 0 : blockIdx.x - merges;
-  const long long hd = merge ? blockIdx.x / p.g : rest / chunks;
+  const bool merge = blockIdx.x < static_cast<unsigned>(merges);
+  const long long rest = merge ? 0 : static_cast<long long>(blockIdx.x) - merges;
+  const long long row = static_cast<long long>(blockIdx.x) * kRows + warp / kPerRow;   // b * n_q + h
+  const bool live = !merge || row < static_cast<long long>(p.B) * p.n_q;
+  const long long hd = merge ? (live ? row / p.g : 0) : rest / chunks;
   const int len = clamp_len(p.lens[hd / p.n_kv], p.Lk);
   const long long c0 = len > 0 ? p.ends[2 * hd] : 0;
   const int ns = len > 0 ? static_cast<int>(p.ends[2 * hd + 1] - c0 + 1) : 0;
@@ -793,6 +814,15 @@ attn_decode_ragged_combine_kernel(uint16_t* o, float* lse, float* weights, int c
   if (!merge) {
     const int j0 = static_cast<int>(rest - hd * chunks) * kWeightKeys;
     if (j0 >= len) return;
+    const float* sc = p.scores + hd * p.g * p.ld + j0 + threadIdx.x;
+    const int n = len - j0 - static_cast<int>(threadIdx.x);   // position e is live while e * 256 < n
+    float x[kWeightAhead][kWeightPer];
+#pragma unroll
+    for (int h = 0; h < kWeightAhead; ++h)
+#pragma unroll
+      for (int e = 0; e < kWeightPer; ++e)
+        x[h][e] = h < p.g && e * 32 * kCombineWarps < n ? sc[h * p.ld + e * 32 * kCombineWarps]
+                                                         : -INFINITY;
     for (int h = warp; h < p.g; h += kCombineWarps) {
       float m = -INFINITY;
       for (int s = lane; s < ns; s += 32) m = fmaxf(m, p.part_lse[(hd + c0 + s) * p.g + h]);
@@ -805,64 +835,78 @@ attn_decode_ragged_combine_kernel(uint16_t* o, float* lse, float* weights, int c
       if (lane == 0) lse2[h] = m + log2f(w);
     }
     __syncthreads();
-    const float* sc = p.scores + hd * p.g * p.ld;
-    float* out = weights + hd * p.Lk;
-    for (int j = j0 + threadIdx.x; j < min(j0 + kWeightKeys, len); j += 32 * kCombineWarps) {
-      float sum = 0.0f;
-#pragma unroll 4
-      for (int h = 0; h < p.g; ++h) sum += ex2_approx(sc[h * p.ld + j] - lse2[h]);
-      out[j] += sum;
+    float sum[kWeightPer] = {};
+#pragma unroll
+    for (int h = 0; h < kWeightAhead; ++h) {
+      if (h >= p.g) break;
+#pragma unroll
+      for (int e = 0; e < kWeightPer; ++e) sum[e] += ex2_approx(x[h][e] - lse2[h]);
     }
+#pragma unroll 4
+    for (int h = kWeightAhead; h < p.g; ++h) {
+#pragma unroll
+      for (int e = 0; e < kWeightPer; ++e)
+        if (e * 32 * kCombineWarps < n)
+          sum[e] += ex2_approx(sc[h * p.ld + e * 32 * kCombineWarps] - lse2[h]);
+    }
+    float* out = weights + hd * p.Lk + j0 + threadIdx.x;
+#pragma unroll
+    for (int e = 0; e < kWeightPer; ++e)
+      if (e * 32 * kCombineWarps < n) out[e * 32 * kCombineWarps] += sum[e];
     return;
   }
 
-  const long long row = blockIdx.x;                 // b * n_q + query head
-  const int r = static_cast<int>(row - hd * p.g);
+  const int r = static_cast<int>(row - hd * p.g), sub = warp % kPerRow;
   float m = -INFINITY, wsum = 0.0f;
   float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (live) {
 #pragma unroll 4
-  for (int s = warp; s < ns; s += kCombineWarps) {
-    const size_t sr = static_cast<size_t>((hd + c0 + s) * p.g + r);
-    const float ls = p.part_lse[sr];
-    const float4 v = *reinterpret_cast<const float4*>(p.part_o + sr * kDim + 4 * lane);
-    const float mn = fmaxf(m, ls);
-    const float a = (m == -INFINITY) ? 0.0f : exp2f(m - mn);
-    const float w = exp2f(ls - mn);
-    m = mn;
-    wsum = fmaf(wsum, a, w);
-    acc.x = fmaf(w, v.x, acc.x * a);
-    acc.y = fmaf(w, v.y, acc.y * a);
-    acc.z = fmaf(w, v.z, acc.z * a);
-    acc.w = fmaf(w, v.w, acc.w * a);
-  }
-  red_o[warp][lane] = acc;
-  if (lane == 0) {
-    red_m[warp] = m;
-    red_w[warp] = wsum;
-  }
-  __syncthreads();
-  if (warp == 0) {
-    float mx = red_m[0];
-#pragma unroll
-    for (int w = 1; w < kCombineWarps; ++w) mx = fmaxf(mx, red_m[w]);
-    float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    float ws = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kCombineWarps; ++w) {
-      const float a = (red_m[w] == -INFINITY) ? 0.0f : exp2f(red_m[w] - mx);
-      const float4 u = red_o[w][lane];
-      t.x = fmaf(a, u.x, t.x);
-      t.y = fmaf(a, u.y, t.y);
-      t.z = fmaf(a, u.z, t.z);
-      t.w = fmaf(a, u.w, t.w);
-      ws = fmaf(a, red_w[w], ws);
+    for (int s = sub; s < ns; s += kPerRow) {
+      const size_t sr = static_cast<size_t>((hd + c0 + s) * p.g + r);
+      const float ls = p.part_lse[sr];
+      const float4 v = *reinterpret_cast<const float4*>(p.part_o + sr * kDim + 4 * lane);
+      const float mn = fmaxf(m, ls);
+      const float a = (m == -INFINITY) ? 0.0f : exp2f(m - mn);
+      const float w = exp2f(ls - mn);
+      m = mn;
+      wsum = fmaf(wsum, a, w);
+      acc.x = fmaf(w, v.x, acc.x * a);
+      acc.y = fmaf(w, v.y, acc.y * a);
+      acc.z = fmaf(w, v.z, acc.z * a);
+      acc.w = fmaf(w, v.w, acc.w * a);
     }
-    const float inv = ns > 0 ? 1.0f / ws : 0.0f;
-    const uint32_t w0 = pack_bf16x2(t.x * inv, t.y * inv);
-    const uint32_t w1 = pack_bf16x2(t.z * inv, t.w * inv);
-    *reinterpret_cast<uint2*>(o + static_cast<size_t>(row) * kDim + 4 * lane) = make_uint2(w0, w1);
-    if (lane == 0) lse[row] = ns > 0 ? (mx + log2f(ws)) * 0.69314718055994530942f : -INFINITY;
   }
+  if (kPerRow > 1) {
+    red_o[warp][lane] = acc;
+    if (lane == 0) {
+      red_m[warp] = m;
+      red_w[warp] = wsum;
+    }
+    __syncthreads();
+    if (sub != 0) return;
+    float mx = red_m[warp];
+#pragma unroll
+    for (int w = 1; w < kPerRow; ++w) mx = fmaxf(mx, red_m[warp + w]);
+    acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    wsum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kPerRow; ++w) {
+      const float a = (red_m[warp + w] == -INFINITY) ? 0.0f : exp2f(red_m[warp + w] - mx);
+      const float4 u = red_o[warp + w][lane];
+      acc.x = fmaf(a, u.x, acc.x);
+      acc.y = fmaf(a, u.y, acc.y);
+      acc.z = fmaf(a, u.z, acc.z);
+      acc.w = fmaf(a, u.w, acc.w);
+      wsum = fmaf(a, red_w[warp + w], wsum);
+    }
+    m = mx;
+  }
+  if (!live) return;
+  const float inv = ns > 0 ? 1.0f / wsum : 0.0f;
+  const uint32_t w0 = pack_bf16x2(acc.x * inv, acc.y * inv);
+  const uint32_t w1 = pack_bf16x2(acc.z * inv, acc.w * inv);
+  *reinterpret_cast<uint2*>(o + static_cast<size_t>(row) * kDim + 4 * lane) = make_uint2(w0, w1);
+  if (lane == 0) lse[row] = ns > 0 ? (m + log2f(wsum)) * 0.69314718055994530942f : -INFINITY;
 }
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
@@ -1182,14 +1226,22 @@ attn_status_t attn_decode_ragged_fwd(const void* q, const void* k, const void* v
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(B * n_q + B * n_kv * chunks));
+  // segments per head: one, and one more for every range border inside it
+  const bool many = p.G > 8 * B * n_kv;
+  const int64_t merges = many ? B * n_q : (B * n_q + kCombineWarps - 1) / kCombineWarps;
+  cfg.gridDim = dim3(static_cast<unsigned>(merges + B * n_kv * chunks));
   cfg.blockDim = dim3(32 * kCombineWarps);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, attn_decode_ragged_combine_kernel, static_cast<uint16_t*>(o), lse,
-                         weights, chunks, p) != cudaSuccess)
-    return ATTN_ERR_CUDA;
+  uint16_t* o16 = static_cast<uint16_t*>(o);
+  const int m32 = static_cast<int>(merges);
+  const cudaError_t e =
+      many ? cudaLaunchKernelEx(&cfg, attn_decode_ragged_combine_kernel<kCombineWarps>, o16, lse,
+                                weights, m32, chunks, p)
+           : cudaLaunchKernelEx(&cfg, attn_decode_ragged_combine_kernel<1>, o16, lse, weights, m32,
+                                chunks, p);
+  if (e != cudaSuccess) return ATTN_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 

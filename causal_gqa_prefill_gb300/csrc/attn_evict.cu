@@ -11,13 +11,16 @@
 //
 // The kept positions stay in order. Two kernels:
 //
-//   select  one cluster of 1 to 8 CTAs per (b, u). A radix select over the
-//           weights' order-preserving integer keys (three passes of 11, 11 and
-//           10 bits) finds the (N - R)-th largest key: each CTA counts its part
-//           of the row in shared memory and sums the cluster's counts through
-//           distributed shared memory. A last pass compacts the kept positions
-//           in order (prefix sums over warps, CTA and cluster) and writes their
-//           index and weight.
+//   select  one cluster of 1 to 8 CTAs per (b, u), each with its part of the row
+//           in shared memory. A radix select over the weights' order-preserving
+//           integer keys, 8 bits a pass, finds the (N - R)-th largest key; it
+//           ends early when a pass leaves exactly the keys that are needed. A
+//           CTA counts into 32 histograms, one per lane, whose counters lie in
+//           the lane's own bank: weights crowd into a few exponents, and with one
+//           histogram the atomics on its few busy counters took most of the time
+//           (39 us against MEASURED_SELECT us for 6 rows of 131072). The cluster's
+//           counts are summed through distributed shared memory. A last pass
+//           compacts the kept positions in order and writes index and weight.
 //   gather  copies the kept K and V rows, in the order of the destination, 16
 //           bytes a lane; it is what the call's bytes are.
 #include <cooperative_groups.h>
@@ -36,11 +39,11 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kSelThreads = 1024;
-constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kBins = 2048;               // 11-bit digits (the last one has 10)
+constexpr int kBins = 256;                // 8-bit digits
 constexpr int kMaxCluster = 8;
-constexpr int kPartSmem = 40960;          // weights of a CTA's part held in shared memory
+constexpr int kSms = 152;                 // SMs of a GB300
+constexpr int kPartSmem = 32768;          // keys of a CTA's part held in shared memory
+static_assert(kPartSmem < 1 << 16, "a piece's two counts share 32 bits");
 constexpr int kGatherThreads = 256;
 constexpr int kGatherRows = 64;           // destination positions per gather CTA
 
@@ -63,15 +66,24 @@ __device__ __forceinline__ uint32_t order_key(float x) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
+// The weight of a key; a NaN's and a zero's bits are the original's (`at`).
+__device__ __forceinline__ float weight_of(uint32_t key, const float* at) {
+  if (key == 0u || key == 0x80000000u) return *at;
+  return __uint_as_float((key & 0x80000000u) ? key ^ 0x80000000u : ~key);
+}
+
 struct SelectSmem {
-  unsigned int hist[kBins];        // this CTA's counts, read by the cluster
-  unsigned int warp_sum[kSelWarps];
-  unsigned int n_gt, n_eq;         // this CTA's kept and tied positions, read by the cluster
-  unsigned int digit, above;       // the digit of the key sought, keys above it
-  unsigned int scan_total;
+  unsigned int hist[kBins][32];            // [digit][lane]
+  unsigned int total[2][kBins];            // a pass's counts, read by the cluster
+  unsigned int warp_sum[32];
+  unsigned long long wide_sum[kBins / 32];
+  // the digit of the key sought: keys above it and at it in the row, and in
+  // the parts of the CTAs before this one
+  unsigned int digit, above, at, above_before, at_before;
 };
 
-// Inclusive sum of v over the CTA's threads; *total gets the sum of all.
+// Inclusive sum of v over the CTA's kThreads threads; *total: the sum of all.
+template <int kThreads>
 __device__ __forceinline__ unsigned int block_scan(unsigned int v, SelectSmem& sm,
                                                    unsigned int* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -82,31 +94,29 @@ __device__ __forceinline__ unsigned int block_scan(unsigned int v, SelectSmem& s
   }
   if (lane == 31) sm.warp_sum[warp] = v;
   __syncthreads();
-  if (warp == 0) {
-    unsigned int s = sm.warp_sum[lane];
+  unsigned int s = lane < kThreads / 32 ? sm.warp_sum[lane] : 0u;   // every warp sums the warps
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const unsigned int n = __shfl_up_sync(0xffffffffu, s, off);
-      if (lane >= off) s += n;
-    }
-    sm.warp_sum[lane] = s;
+  for (int off = 1; off < 32; off <<= 1) {
+    const unsigned int n = __shfl_up_sync(0xffffffffu, s, off);
+    if (lane >= off) s += n;
   }
-  __syncthreads();
-  const unsigned int base = warp ? sm.warp_sum[warp - 1] : 0u;
-  *total = sm.warp_sum[kSelWarps - 1];
-  __syncthreads();
-  return base + v;
+  *total = __shfl_sync(0xffffffffu, s, 31);
+  const unsigned int base = __shfl_sync(0xffffffffu, s, (warp + 31) & 31);
+  return (warp ? base : 0u) + v;
 }
 
-__global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const EvictParams p) {
-  extern __shared__ __align__(16) float held[];      // the part's weights, when they fit
+template <int kThreads>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads)
+evict_select_kernel(const EvictParams p) {
+  constexpr int kWarps = kThreads / 32;
+  extern __shared__ __align__(16) uint32_t held[];   // the part's keys, or those of a piece of it
   __shared__ SelectSmem sm;
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = static_cast<int>(cluster.block_rank());
   const int ncta = static_cast<int>(cluster.num_blocks());
   const int row = static_cast<int>(blockIdx.x) / ncta;      // b * n_kv + u
   const int b = row / p.n_kv;
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
@@ -118,116 +128,162 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
   float* w_out = p.w_out + static_cast<size_t>(row) * p.C_out;
   int* index = p.index + static_cast<size_t>(row) * p.N;
 
+  const int lo = min(rank * p.part, old), hi = min(lo + p.part, old);
+  const int n = hi - lo;
+  const bool choose = need != old && need > 0;   // the same for the whole cluster
+  const bool in_smem = p.part <= kPartSmem;
+  // keys of positions from .. from + m - 1 to shared memory; up to the next
+  // multiple of four, keys of nothing (0 is a NaN's: they are not counted)
+  auto hold = [&](int from, int m) {
+#pragma unroll 4
+    for (int i = tid; i < (m + 3) / 4 * 4; i += kThreads)
+      held[i] = i < m ? order_key(w[from + i]) : 0u;
+  };
+  if (choose && in_smem) hold(lo, n);
   // what lies behind the kept positions, and the recent ones
-  for (int i = kept + rank * kSelThreads + tid; i < p.C_out; i += ncta * kSelThreads) w_out[i] = 0.0f;
-  for (int i = kept + rank * kSelThreads + tid; i < p.N; i += ncta * kSelThreads) index[i] = -1;
-  for (int i = need + rank * kSelThreads + tid; i < kept; i += ncta * kSelThreads) {
+  for (int i = kept + rank * kThreads + tid; i < p.C_out; i += ncta * kThreads) w_out[i] = 0.0f;
+  for (int i = kept + rank * kThreads + tid; i < p.N; i += ncta * kThreads) index[i] = -1;
+  for (int i = need + rank * kThreads + tid; i < kept; i += ncta * kThreads) {
     const int src = old + (i - need);
     w_out[i] = w[src];
     index[i] = src;
   }
   if (rank == 0 && tid == 0 && row % p.n_kv == 0) p.lens_out[b] = kept;
-
-  const int lo = min(rank * p.part, old), hi = min(lo + p.part, old);
-  if (need == old) {                             // the same for the whole cluster
-    for (int i = lo + tid; i < hi; i += kSelThreads) {
-      w_out[i] = w[i];
-      index[i] = i;
-    }
+  if (!choose) {
+    if (need > 0)                                // all of them stay
+      for (int i = lo + tid; i < hi; i += kThreads) {
+        w_out[i] = w[i];
+        index[i] = i;
+      }
     return;
   }
-  const bool in_smem = p.part <= kPartSmem;
-  const float* src = w + lo;
-  const int n = hi - lo;
-  if (in_smem) {
-    for (int i = tid; i < n; i += kSelThreads) held[i] = w[lo + i];
-    src = held;
-    __syncthreads();
-  }
 
-  // the need-th largest key: `prefix` holds its digits found so far, `above`
-  // the number of keys larger than every key with this prefix
+  // The need-th largest key: `prefix` holds its digits found so far (the key
+  // shifted right by `shift`), `above` the number of keys with larger leading
+  // digits, and `gt`, `eq` how many of the larger and of the equal ones lie in
+  // the CTAs before this one.
   uint32_t prefix = 0;
-  unsigned int above = 0;
-  bool all = need == 0;                          // nothing of the older part stays
-  for (int pass = 0; pass < 3 && !all; ++pass) {
-    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-    const uint32_t mask = pass == 2 ? 1023u : 2047u;
-    for (int i = tid; i < kBins; i += kSelThreads) sm.hist[i] = 0;
+  unsigned int above = 0, gt = 0, eq = 0;
+  int shift = 32;
+  for (int pass = 0; pass < 4; ++pass) {
+    shift -= 8;
+#pragma unroll
+    for (int i = 0; i < kBins * 32 / 4 / kThreads; ++i)
+      reinterpret_cast<uint4*>(&sm.hist[0][0])[tid + i * kThreads] = make_uint4(0u, 0u, 0u, 0u);
     __syncthreads();
-    for (int i = tid; i < n; i += kSelThreads) {
-      const uint32_t key = order_key(src[i]);
-      if (pass == 0 || (key >> (pass == 1 ? 21 : 10)) == prefix)
-        atomicAdd(&sm.hist[(key >> shift) & mask], 1u);
+    auto count = [&](uint32_t key) {
+      if (pass == 0 || (key >> (shift + 8)) == prefix)
+        atomicAdd(&sm.hist[(key >> shift) & (kBins - 1)][lane], 1u);
+    };
+    if (in_smem) {
+#pragma unroll 2
+      for (int i = 4 * tid; i < n; i += 4 * kThreads) {
+        const uint4 key = *reinterpret_cast<const uint4*>(held + i);
+        count(key.x);
+        if (i + 1 < n) count(key.y);
+        if (i + 2 < n) count(key.z);
+        if (i + 3 < n) count(key.w);
+      }
+    } else {
+      for (int i = tid; i < n; i += kThreads) count(order_key(w[lo + i]));
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kBins / kWarps; ++i) {
+      const int d = warp * (kBins / kWarps) + i;
+      const unsigned int sum = __reduce_add_sync(0xffffffffu, sm.hist[d][lane]);
+      if (lane == 0) sm.total[pass & 1][d] = sum;
     }
     cluster.sync();
-    // digits in descending order: thread t owns digits 2047 - 2t and 2046 - 2t
-    unsigned int c0 = 0, c1 = 0;
-    const int d0 = kBins - 1 - 2 * tid, d1 = d0 - 1;
-    for (int r = 0; r < ncta; ++r) {
-      const unsigned int* h = cluster.map_shared_rank(sm.hist, r);
-      c0 += h[d0];
-      c1 += h[d1];
-    }
-    unsigned int total;
-    const unsigned int incl = block_scan(c0 + c1, sm, &total);
-    const unsigned int before = above + incl - c0 - c1;       // keys above digit d0
-    const unsigned int want = static_cast<unsigned int>(need);
-    if (before < want && before + c0 >= want) {
-      sm.digit = d0;
-      sm.above = before;
-    } else if (before + c0 < want && before + c0 + c1 >= want) {
-      sm.digit = d1;
-      sm.above = before + c0;
+    // digits in descending order, one per thread: counts of the row (low half)
+    // and of the CTAs before this one (high half)
+    unsigned long long c = 0, incl = 0;
+    if (tid < kBins) {
+      unsigned int all = 0, before = 0;
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r) {
+        unsigned int x = 0;
+        if (r < ncta) x = cluster.map_shared_rank(&sm.total[pass & 1][0], r)[kBins - 1 - tid];
+        all += x;
+        before += r < rank ? x : 0u;
+      }
+      c = all | static_cast<unsigned long long>(before) << 32;
+      incl = c;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const unsigned long long y = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += y;
+      }
+      if (lane == 31) sm.wide_sum[warp] = incl;
     }
     __syncthreads();
-    prefix = (prefix << (pass == 2 ? 10 : 11)) | sm.digit;
+    if (tid < kBins) {
+      for (int x = 0; x < warp; ++x) incl += sm.wide_sum[x];
+      const unsigned long long excl = incl - c;
+      const unsigned int larger = above + static_cast<unsigned int>(excl);
+      const unsigned int here = static_cast<unsigned int>(c);
+      if (larger < static_cast<unsigned int>(need) && larger + here >= static_cast<unsigned int>(need)) {
+        sm.digit = kBins - 1 - tid;
+        sm.above = larger;
+        sm.at = here;
+        sm.above_before = static_cast<unsigned int>(excl >> 32);
+        sm.at_before = static_cast<unsigned int>(c >> 32);
+      }
+    }
+    __syncthreads();
+    prefix = (prefix << 8) | sm.digit;
     above = sm.above;
-    cluster.sync();                              // every CTA has read the counts
+    gt += sm.above_before;
+    eq = sm.at_before;
+    if (above + sm.at == static_cast<unsigned int>(need)) break;   // all of these stay
   }
   // kept: keys above `prefix`, and the first `ties` of those equal to it
-  const unsigned int ties = all ? 0u : static_cast<unsigned int>(need) - above;
+  const unsigned int ties = static_cast<unsigned int>(need) - above;
 
-  // this CTA's counts, then how many lie in the CTAs before it
-  unsigned int gt = 0, eq = 0;
-  if (!all) {
-    for (int i = tid; i < n; i += kSelThreads) {
-      const uint32_t key = order_key(src[i]);
-      gt += key > prefix;
-      eq += key == prefix;
+  // in order, a piece of at most kPartSmem positions at a time; a thread takes
+  // a run of an odd number of fours (the lanes' reads then meet all banks)
+  for (int i0 = 0; i0 < n; i0 += kPartSmem) {
+    const int m = min(n - i0, kPartSmem);
+    if (!in_smem) {
+      __syncthreads();
+      hold(lo + i0, m);
+      __syncthreads();
     }
-  }
-  unsigned int n_gt, n_eq;
-  block_scan(gt, sm, &n_gt);
-  block_scan(eq, sm, &n_eq);
-  if (tid == 0) {
-    sm.n_gt = n_gt;
-    sm.n_eq = n_eq;
-  }
-  cluster.sync();
-  unsigned int base_gt = 0, base_eq = 0;
-  for (int r = 0; r < rank; ++r) {
-    base_gt += *cluster.map_shared_rank(&sm.n_gt, r);
-    base_eq += *cluster.map_shared_rank(&sm.n_eq, r);
-  }
-  // in order, kSelThreads positions at a time
-  for (int i0 = 0; i0 < n && !all; i0 += kSelThreads) {
-    const int i = i0 + tid;
-    const float x = i < n ? src[i] : 0.0f;
-    const uint32_t key = i < n ? order_key(x) : 0u;
-    const bool is_gt = i < n && key > prefix, is_eq = i < n && key == prefix;
+    const int run = 4 * (((m + 4 * kThreads - 1) / (4 * kThreads)) | 1);
+    const int r0 = min(tid * run, m), r1 = min(r0 + run, m);
+    unsigned int my_gt = 0, my_eq = 0;
+    for (int i = r0; i < r1; i += 4) {
+      const uint4 key = *reinterpret_cast<const uint4*>(held + i);
+      const uint32_t k[4] = {key.x >> shift, key.y >> shift, key.z >> shift, key.w >> shift};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (i + e >= r1) break;
+        my_gt += k[e] > prefix;
+        my_eq += k[e] == prefix;
+      }
+    }
     unsigned int t;
-    // both counts in one scan: at most 1024 of each
-    const unsigned int s =
-        block_scan((is_gt ? 1u : 0u) | (is_eq ? 1u << 16 : 0u), sm, &t);
-    const unsigned int my_gt = base_gt + (s & 0xFFFFu), my_eq = base_eq + (s >> 16);   // inclusive
-    if (is_gt || (is_eq && my_eq <= ties)) {
-      const unsigned int at = my_gt + min(my_eq, ties) - 1u;
-      w_out[at] = x;
-      index[at] = lo + i;
+    const unsigned int both = my_gt | my_eq << 16;           // a piece has fewer than 2^16
+    const unsigned int s = block_scan<kThreads>(both, sm, &t) - both;    // before this thread
+    unsigned int at_gt = gt + (s & 0xFFFFu), at_eq = eq + (s >> 16);
+    for (int i = r0; i < r1; i += 4) {
+      const uint4 key = *reinterpret_cast<const uint4*>(held + i);
+      const uint32_t k[4] = {key.x, key.y, key.z, key.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (i + e >= r1) break;
+        const uint32_t lead = k[e] >> shift;
+        if (lead > prefix || (lead == prefix && at_eq < ties)) {
+          const unsigned int to = at_gt + min(at_eq, ties);
+          w_out[to] = weight_of(k[e], w + lo + i0 + i + e);
+          index[to] = lo + i0 + i + e;
+        }
+        at_gt += lead > prefix;
+        at_eq += lead == prefix;
+      }
     }
-    base_gt += t & 0xFFFFu;
-    base_eq += t >> 16;
+    gt += t & 0xFFFFu;
+    eq += t >> 16;
   }
   cluster.sync();                                // no CTA ends while its counts are read
 }
@@ -303,7 +359,9 @@ attn_status_t evict_device_ready(cudaStream_t stream) {
     cudaGetLastError();
     return ATTN_ERR_UNSUPPORTED;
   }
-  if (cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  if (cudaFuncSetAttribute(evict_select_kernel<512>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           kPartSmem * 4) != cudaSuccess ||
+      cudaFuncSetAttribute(evict_select_kernel<1024>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            kPartSmem * 4) != cudaSuccess)
     return ATTN_ERR_CUDA;
   g_evict_ready[dev] = true;
@@ -366,7 +424,8 @@ extern "C" attn_status_t attn_cache_evict(const void* k, const void* v, const fl
 
   const int64_t rows = B * n_kv;
   int cluster = 1;
-  while (cluster < kMaxCluster && rows * cluster * 2 <= 304 && C >= 4096 * 2 * cluster) cluster *= 2;
+  while (cluster < kMaxCluster && rows * cluster * 2 <= 2 * kSms && C >= 4096 * 2 * cluster)
+    cluster *= 2;
   EvictParams p;
   p.w = weights;
   p.lens = lens;
@@ -388,12 +447,16 @@ extern "C" attn_status_t attn_cache_evict(const void* k, const void* v, const fl
   attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(rows * cluster));
-  cfg.blockDim = dim3(kSelThreads);
-  cfg.dynamicSmemBytes = p.part <= kPartSmem ? static_cast<size_t>(p.part) * 4 : 0;
+  // more CTAs than SMs: two of 512 threads to an SM
+  const bool wide = rows * cluster <= kSms;
+  cfg.blockDim = dim3(wide ? 1024 : 512);
+  cfg.dynamicSmemBytes = static_cast<size_t>(p.part <= kPartSmem ? (p.part + 3) / 4 * 4 : kPartSmem) * 4;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  if (cudaLaunchKernelEx(&cfg, evict_select_kernel, p) != cudaSuccess) return ATTN_ERR_CUDA;
+  if ((wide ? cudaLaunchKernelEx(&cfg, evict_select_kernel<1024>, p)
+            : cudaLaunchKernelEx(&cfg, evict_select_kernel<512>, p)) != cudaSuccess)
+    return ATTN_ERR_CUDA;
 
   GatherParams g;
   g.k = static_cast<const uint4*>(k);

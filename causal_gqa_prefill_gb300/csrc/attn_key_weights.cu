@@ -5,29 +5,36 @@
 //   W[b,u,j] (+)= sum_{h in group u} sum_{i sees j} 2^(c q_ih . k_ju - lse2_ih),
 //   c = scale * log2(e),  lse2 = LSE * log2(e).
 //
-// With the keys on the TMEM lanes (S^T = K Q^T, tcgen05, both operands in
-// shared memory) a column sum is a sum over one thread's own columns: no
-// reduction over threads at all, one FMA, one exponential and one addition per
-// score. The columns are packed: one step of 128 columns holds nr = 128 / g
-// consecutive query rows of all g heads of the group (column = row * g + head,
-// which is what one TMA box of g heads x nr rows lands as), so every head
-// count fills the tile, a causal step wastes at most nr rows, and masking a
-// row means comparing the column with a threshold.
+// A step is 128 query rows against 256 keys, S = Q K^T on tcgen05 with the rows
+// on the TMEM lanes. A thread owns a row and 64 keys: its lse2 is one register
+// for the whole step, and it adds each weight to a register of its own per key,
+// step after step, so a score costs one FMA, one exponential and one addition
+// and nothing is exchanged between threads until the keys change. Only then are
+// the 64 sums of a warp's 32 rows folded (62 shuffles) and the four warps' added.
+// (With the keys on the lanes a column sum needs no folding at all, but then
+// every score takes its row's lse2 from shared memory, whose reads queue behind
+// the exponentials: 2130 clocks a step against MEASURED_STEP.)
 //
-//   unit     256 keys of one (b, K/V head): two 128-key tiles that read the same
-//            Q steps (at one tile the Q tiles would need 64 bytes a clock and SM
-//            from L2; two halve that). A unit's steps are the row blocks that
-//            see it, in order.
+//   rows     packed: a step holds nr = 128 / g consecutive query rows of all g
+//            heads of the group (lane = row * g + head, which is what one TMA box
+//            of g heads x nr rows lands as), so every head count fills the tile
+//            and a causal step wastes at most nr rows.
+//   unit     256 keys of one (b, K/V head), N = 256: at N = 128 the two operands
+//            of a product are all that shared memory can read at the tensor
+//            cores' rate, and the Q tiles would need 64 bytes a clock and SM from
+//            L2. A unit's steps are the row blocks that see it, in order.
 //   CTA      one per SM; the steps of all units, in order, are cut into equal
 //            ranges (triangles need no further balancing). A unit that a range
 //            border cuts is summed by a second kernel from at most one partial
 //            per CTA, in CTA order: no atomics, the same bits every time.
-//   warps    0-3 and 4-7 one warpgroup per key tile; 8 TMA; 9 MMA; 10 the rows'
-//            -lse2 (shared memory, read by the whole warpgroup as broadcasts).
+//   warps    0-15 four warpgroups of 64 keys each (four warps a scheduler keep
+//            the exponential unit fed); 16 TMA; 17 MMA; 18 the rows' -lse2.
 //
-// S^T is double-buffered per key tile (4 x 128 TMEM columns), so the products
-// of a step run under the exponentials of the one before; both take 1024
-// clocks a step, the exponentials at 32 a clock and SM.
+// S is double-buffered (all 512 TMEM columns), so the product of a step runs
+// under the exponentials of the one before; both take 1024 clocks a step, the
+// exponentials at 32 a clock and SM. K is fetched a unit ahead, and where a
+// head's steps fit the Q ring they stay there from unit to unit (a prompt's last
+// rows against a long cache: K is then all that is read).
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -46,24 +53,34 @@ namespace {
 
 using namespace gb300;
 
-constexpr int kKeys = 128;            // keys per tile (TMEM lanes)
-constexpr int kUnitKeys = 2 * kKeys;
-constexpr int kCols = 128;            // columns (query rows x heads) per step
+constexpr int kUnitKeys = 256;        // keys per unit (N)
+constexpr int kRows = 128;            // rows (query positions x heads) per step (TMEM lanes)
 constexpr int kCtas = 152;            // one CTA per SM on a 152-SM GB300
-constexpr int kThreads = 384;
-constexpr int kLoadWarp = 8, kMmaWarp = 9, kLseWarp = 10;
-constexpr uint32_t kTmemCols = 512;
-constexpr int kStatusTimeout = 1;
+constexpr int kGroups = 4;            // warpgroups of the sums
+constexpr int kCols = kUnitKeys / kGroups;    // keys per thread
+constexpr int kSumWarps = 4 * kGroups;
+constexpr int kThreads = 32 * kSumWarps + 128;
+constexpr int kLoadWarp = kSumWarps, kMmaWarp = kSumWarps + 1, kStatWarp = kSumWarps + 2;
+constexpr int kFold = kCols / 32;     // keys per lane once the rows are folded
+// registers per thread: the sums of 64 keys, and their scores 16 at a time
+constexpr int kSumRegs = 104, kOtherRegs = 64;
+constexpr int kLaunchRegs = 96;
+constexpr int kRegBudget = 32 * kSumWarps * kSumRegs + 128 * kOtherRegs;
+static_assert(kRegBudget <= kThreads * kLaunchRegs, "setmaxnreg split exceeds the launch allocation");
+constexpr uint32_t kTmemCols = 512;   // S at columns 0 and 256
+constexpr int kStatusTimeout = 1, kStatusCheck = 2;
+constexpr uint32_t kSuspendNs = 2000;
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <int D>
 struct Geometry {
   static constexpr int kChunks = D * 2 / 128;              // 128-byte swizzle column chunks
-  static constexpr int kTileBytes = 128 * D * 2;
-  static constexpr int kChunkBytes = 128 * 128;
+  static constexpr int kQBytes = kRows * D * 2;
+  static constexpr int kQChunk = kRows * 128;
+  static constexpr int kKBytes = kUnitKeys * D * 2;
+  static constexpr int kKChunk = kUnitKeys * 128;
   static constexpr int kQStages = D == 128 ? 3 : 6;
-  // K: two buffers of two tiles; Q ring; two steps' row statistics
-  static constexpr int kSmemBytes = (4 + kQStages) * kTileBytes + 2 * kCols * 4 + 1024;
+  static constexpr int kTileBytes = 2 * kKBytes + kQStages * kQBytes;   // two K buffers, the Q ring
 };
 
 struct Params {
@@ -85,54 +102,78 @@ struct Starts {
   int unit[kCtas], step[kCtas], count[kCtas];
 };
 
-struct Ctl {
+struct __align__(16) Ctl {
   uint64_t k_full[2], k_empty[2];
   uint64_t q_full[6], q_empty[6];
-  uint64_t l_full[2], l_empty[2];
-  uint64_t s_full[2][2], s_free[2][2];
+  uint64_t s_full[2], s_free[2];
+  uint64_t fold[kGroups][3], fold_free[kGroups];
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
+  __align__(16) float nl[2][kRows];      // -lse2 of a step's rows
+  float sums[kGroups][kFold][32];        // a warpgroup's sums on their way from warp to warp
 };
 
+// Ctl, then the tiles at the next multiple of 1 KiB (swizzle atoms). With
+// d_h = 128 this is all of an SM's 227 KiB: the kernel checks that it fits.
+constexpr int kCtlBytes = (sizeof(Ctl) + 1023) / 1024 * 1024;
+template <int D>
+__host__ __device__ constexpr int smem_bytes() {
+  return kCtlBytes + Geometry<D>::kTileBytes;
+}
+static_assert(smem_bytes<128>() <= 232448 && smem_bytes<64>() <= 232448, "shared memory");
+
 __host__ __device__ __forceinline__ int first_step(int t, int off, int nr, int causal) {
-  const long long past = static_cast<long long>(t) * kUnitKeys - off;
-  return causal && past > 0 ? static_cast<int>(past / nr) : 0;
+  const int past = t * kUnitKeys - off;
+  return causal && past > 0 ? static_cast<int>(static_cast<unsigned>(past) / static_cast<unsigned>(nr))
+                            : 0;
 }
 
 struct Segment {
-  int unit, b, kvh, key0, s0, n;
-  bool first, whole;     // the range's first segment; a unit that nothing cuts
+  int head, b, kvh, key0, s0, n;   // head = b * n_kv + kvh
+  bool first, whole;               // the range's first segment; a unit that nothing cuts
 };
 
+// Walks a CTA's range unit by unit; every role takes the same walk.
 struct Walk {
   const Params& p;
-  int unit, step, left;
+  int head, b, kvh, t, step, first_of_unit, left;
   bool first;
   __device__ Walk(const Params& params, const Starts& st, int c)
-      : p(params), unit(st.unit[c]), step(st.step[c]), left(st.count[c]), first(true) {}
+      : p(params), step(st.step[c]), left(st.count[c]), first(true) {
+    head = st.unit[c] / p.T;
+    t = st.unit[c] - head * p.T;
+    b = head / p.n_kv;
+    kvh = head - b * p.n_kv;
+    first_of_unit = first_step(t, p.off, p.nr, p.causal);
+  }
   __device__ bool next(Segment& s) {
     if (left <= 0) return false;
-    const int grp = unit / p.T, t = unit - grp * p.T;
-    s.unit = unit;
-    s.b = grp / p.n_kv;
-    s.kvh = grp - s.b * p.n_kv;
+    s.head = head;
+    s.b = b;
+    s.kvh = kvh;
     s.key0 = t * kUnitKeys;
     s.s0 = step;
     s.n = min(left, p.steps - step);
     s.first = first;
-    s.whole = s.n == p.steps - first_step(t, p.off, p.nr, p.causal);
+    s.whole = step == first_of_unit && s.n == p.steps - step;
     left -= s.n;
     first = false;
-    ++unit;
-    step = unit % p.T ? first_step(unit % p.T, p.off, p.nr, p.causal) : 0;
+    if (++t == p.T) {
+      t = 0;
+      ++head;
+      if (++kvh == p.n_kv) {
+        kvh = 0;
+        ++b;
+      }
+    }
+    step = first_of_unit = first_step(t, p.off, p.nr, p.causal);
     return true;
   }
 };
 
-// Key tile w of a segment takes part in step `step`: it has keys, and the
-// step's last row sees the first of them.
-__device__ __forceinline__ bool takes_part(const Params& p, int key, int step) {
+// Does any row of step `step` see `key`?
+__device__ __forceinline__ bool seen(const Params& p, int key, int step) {
   if (key >= p.Lk) return false;
   const int last = min((step + 1) * p.nr, p.Lq) - 1;
   return !p.causal || key <= last + p.off;
@@ -143,7 +184,7 @@ __device__ __forceinline__ bool spin_wait(uint32_t bar, uint32_t parity, Ctl& ct
   if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = clock64_now();
   while (true) {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (mbar_try_wait_for(bar, parity, kSuspendNs)) return true;
     if (*reinterpret_cast<volatile int*>(&ctl.abort)) return false;
     if (static_cast<long long>(clock64_now() - t0) > p.spin_limit) {
       *reinterpret_cast<volatile int*>(&ctl.abort) = 1;
@@ -153,9 +194,14 @@ __device__ __forceinline__ bool spin_wait(uint32_t bar, uint32_t parity, Ctl& ct
   }
 }
 
+__device__ __forceinline__ bool wait_slowly(uint32_t bar, uint32_t parity, Ctl& ctl, const Params& p) {
+  return __all_sync(0xffffffffu, spin_wait(bar, parity, ctl, p));
+}
+
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, Ctl& ctl,
                                           const Params& p) {
-  return __all_sync(0xffffffffu, spin_wait(bar, parity, ctl, p));
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return wait_slowly(bar, parity, ctl, p);
 }
 
 // Wait used while draining after an abort: ignores the abort flag.
@@ -165,31 +211,299 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, const 
     if (static_cast<long long>(clock64_now() - t0) > p.spin_limit) return;
 }
 
-// sum over the step's columns of 2^(c s + nl) for this thread's key; kMask:
-// columns below `from` are rows that do not see it.
-template <bool kMask>
-__device__ __forceinline__ float column_sum(const float (&s)[kCols], const float* nl, uint64_t c2,
-                                            int from) {
-  uint64_t a0 = f32x2_pack(0.0f, 0.0f), a1 = a0;
+// acc += 2^(c s + nl) for the 16 keys whose scores are in s, two at a time.
+__device__ __forceinline__ void add_weights(uint64_t* acc, const uint32_t (&s)[16], uint64_t c2,
+                                            uint64_t nl2) {
 #pragma unroll
-  for (int i = 0; i < kCols; i += 4) {
-    const float4 l = *reinterpret_cast<const float4*>(nl + i);
-    float x0, x1, x2, x3;
-    f32x2_unpack(ffma2(f32x2_pack(s[i], s[i + 1]), c2, f32x2_pack(l.x, l.y)), x0, x1);
-    f32x2_unpack(ffma2(f32x2_pack(s[i + 2], s[i + 3]), c2, f32x2_pack(l.z, l.w)), x2, x3);
-    float e0 = ex2_approx(x0), e1 = ex2_approx(x1), e2 = ex2_approx(x2), e3 = ex2_approx(x3);
-    if (kMask) {
-      if (i < from) e0 = 0.0f;
-      if (i + 1 < from) e1 = 0.0f;
-      if (i + 2 < from) e2 = 0.0f;
-      if (i + 3 < from) e3 = 0.0f;
-    }
-    a0 = fadd2(a0, f32x2_pack(e0, e1));
-    a1 = fadd2(a1, f32x2_pack(e2, e3));
+  for (int i = 0; i < 16; i += 2) {
+    float x0, x1;
+    f32x2_unpack(ffma2(f32x2_pack(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), c2, nl2), x0, x1);
+    const uint64_t e = f32x2_pack(ex2_approx(x0), ex2_approx(x1));
+    asm("add.f32x2 %0, %0, %1;" : "+l"(acc[i / 2]) : "l"(e));
   }
-  float lo, hi;
-  f32x2_unpack(fadd2(a0, a1), lo, hi);
-  return lo + hi;
+}
+
+// Sums kCols values per lane over the warp's lanes: five steps that each halve
+// what a lane carries. Lane l gets the sums of keys kFold l .. kFold l + kFold - 1
+// in v[0 .. kFold - 1].
+__device__ __forceinline__ void fold_lanes(float (&v)[kCols]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int off = 16, width = kCols / 2; off > 0; off >>= 1, width >>= 1) {
+    const bool upper = (lane & off) != 0;
+#pragma unroll
+    for (int i = 0; i < width; ++i) {
+      const float send = upper ? v[i] : v[i + width], keep = upper ? v[i + width] : v[i];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, off);
+    }
+  }
+}
+
+__device__ void sum_role(Ctl& ctl, const Params& p, const Starts& starts, uint32_t tmem) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int group = warp >> 2, quarter = warp & 3;
+  const int r = quarter * 32 + lane;                   // row of the step = TMEM lane
+  const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + kCols * group;
+  const uint64_t c2 = f32x2_pack(p.c, p.c);
+  const uint32_t hidden = p.c > 0.0f ? 0xff800000u : 0x7f800000u;   // c * hidden = -inf
+  const int row = r / p.g;
+  Walk walk(p, starts, blockIdx.x);
+  Segment sg;
+  uint32_t n = 0, seg = 0;
+  while (walk.next(sg)) {
+    const int key0 = sg.key0 + kCols * group;
+    // steps before `from` do not see the group's first key; in steps before
+    // `until` some row does not see its last one
+    const int past = p.causal ? key0 - p.off : 0;
+    int from = past > 0 ? static_cast<int>(static_cast<unsigned>(past) / static_cast<unsigned>(p.nr)) : 0;
+    if (key0 >= p.Lk) from = p.steps;
+    const int until =
+        p.causal && past + kCols - 1 > 0
+            ? static_cast<int>(static_cast<unsigned>(past + kCols - 2 + p.nr) / static_cast<unsigned>(p.nr))
+            : 0;
+    uint64_t acc[kCols / 2];
+#pragma unroll
+    for (int i = 0; i < kCols / 2; ++i) acc[i] = f32x2_pack(0.0f, 0.0f);
+    const int end = sg.s0 + sg.n;
+    for (int st = sg.s0; st < end; ++st, ++n) {
+      const uint32_t buf = n & 1;
+      if (!wait_warp(smem_addr(&ctl.s_full[buf]), (n >> 1) & 1, ctl, p)) return;
+      tc_fence_after_sync();
+      if (st >= from) {
+        const float nl = ctl.nl[buf][r];
+        const uint64_t nl2 = f32x2_pack(nl, nl);
+        const uint32_t taddr = lanes + kUnitKeys * buf;
+        uint32_t s[16];
+        if (st >= until) {
+#pragma unroll
+          for (int q = 0; q < kCols / 16; ++q) {
+            tmem_ld16(taddr + 16 * q, s);
+            tmem_wait_ld16(s);
+            add_weights(acc + 8 * q, s, c2, nl2);
+          }
+        } else {
+          // this row's position sees key0 + i for i <= keep
+          const int keep = p.off + st * p.nr + row - key0;
+#pragma unroll
+          for (int q = 0; q < kCols / 16; ++q) {
+            tmem_ld16(taddr + 16 * q, s);
+            tmem_wait_ld16(s);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (16 * q + i > keep) s[i] = hidden;
+            add_weights(acc + 8 * q, s, c2, nl2);
+          }
+        }
+        tc_fence_before_sync();
+        __syncwarp();
+      }
+      if (lane == 0) mbar_arrive(smem_addr(&ctl.s_free[buf]));
+    }
+    // fold the rows: over the warp's lanes, then from warp 3 of the warpgroup
+    // to warp 0
+    float v[kCols];
+#pragma unroll
+    for (int i = 0; i < kCols / 2; ++i) f32x2_unpack(acc[i], v[2 * i], v[2 * i + 1]);
+    fold_lanes(v);
+    if (quarter == 3) {
+      if (seg > 0 && !wait_warp(smem_addr(&ctl.fold_free[group]), (seg - 1) & 1, ctl, p)) return;
+    } else {
+      if (!wait_warp(smem_addr(&ctl.fold[group][quarter]), seg & 1, ctl, p)) return;
+#pragma unroll
+      for (int i = 0; i < kFold; ++i) v[i] += ctl.sums[group][i][lane];
+    }
+    if (quarter > 0) {
+#pragma unroll
+      for (int i = 0; i < kFold; ++i) ctl.sums[group][i][lane] = v[i];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&ctl.fold[group][quarter - 1]));
+    } else {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&ctl.fold_free[group]));
+      const int key = key0 + kFold * lane;
+      float* out = sg.whole ? p.weights + static_cast<size_t>(sg.head) * p.Lk + key
+                            : p.part + (2 * blockIdx.x + (sg.first ? 0 : 1)) * kUnitKeys +
+                                  kCols * group + kFold * lane;
+      const bool old = sg.whole && p.accumulate;
+#pragma unroll
+      for (int i = 0; i < kFold; ++i)
+        if (!sg.whole || key + i < p.Lk) out[i] = old ? out[i] + v[i] : v[i];
+    }
+    ++seg;
+  }
+}
+
+// One warp: -lse2 of every step's rows to shared memory, as one of the two
+// arrivals that complete s_full. Lane's rows lane + 32 m; the values of the next
+// kAhead steps are in registers or on their way.
+__device__ void stat_role(Ctl& ctl, const Params& p, const Starts& starts) {
+  const int lane = threadIdx.x & 31;
+  constexpr int kAhead = 2;
+  int row[4], at[4];                       // row of the step, offset of its head
+#pragma unroll
+  for (int m = 0; m < 4; ++m) {
+    const int r = lane + 32 * m;
+    row[m] = r < p.nr * p.g ? r / p.g : p.Lq;            // past the last row: none
+    at[m] = (r % p.g) * p.Lq + row[m];
+  }
+  Walk walk(p, starts, blockIdx.x);
+  Segment sg;
+  int left = 0, i0 = 0;
+  const float* lse = nullptr;
+  auto fetch = [&](float (&v)[4]) {
+    if (left == 0) {
+      if (!walk.next(sg)) return false;
+      left = sg.n;
+      i0 = sg.s0 * p.nr;
+      lse = p.lse + (static_cast<size_t>(sg.b) * p.n_q + sg.kvh * p.g) * p.Lq;
+    }
+#pragma unroll
+    for (int m = 0; m < 4; ++m) v[m] = row[m] < p.Lq - i0 ? lse[at[m] + i0] : -INFINITY;
+    --left;
+    i0 += p.nr;
+    return true;
+  };
+  float l[kAhead][4];
+  bool have[kAhead];
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u) have[u] = fetch(l[u]);
+  for (uint32_t n0 = 0; have[0]; n0 += kAhead) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      if (!have[u]) return;
+      const uint32_t n = n0 + u, buf = n & 1;
+      // the rows of step n - 2 have been read (and its s_full phase is over)
+      if (n >= 2 && !wait_warp(smem_addr(&ctl.s_free[buf]), ((n >> 1) - 1) & 1, ctl, p)) return;
+      // a row without keys, like a lane without a row, has no weight
+#pragma unroll
+      for (int m = 0; m < 4; ++m)
+        ctl.nl[buf][lane + 32 * m] = l[u][m] == -INFINITY ? -INFINITY : -l[u][m] * kLog2e;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&ctl.s_full[buf]));
+      have[u] = fetch(l[u]);
+    }
+  }
+}
+
+template <int D>
+__device__ void load_role(const CUtensorMap* tmQ, const CUtensorMap* tmK, Ctl& ctl, const Params& p,
+                          const Starts& starts, uint32_t sK, uint32_t sQ, bool stay) {
+  using G = Geometry<D>;
+  uint32_t qn = 0, kn = 0, gn = 0;         // Q steps, K buffers and heads issued
+  const uint32_t q_bytes = static_cast<uint32_t>(G::kChunks * 128 * p.g * p.nr);
+  auto load_k = [&](const Segment& s) {
+    const uint32_t kb = kn & 1;
+    if (kn >= 2 && !spin_wait(smem_addr(&ctl.k_empty[kb]), ((kn >> 1) - 1) & 1, ctl, p)) return false;
+    const uint32_t bar = smem_addr(&ctl.k_full[kb]);
+    mbar_arrive_expect_tx(bar, G::kKBytes);
+    for (int ch = 0; ch < G::kChunks; ++ch)
+      tma_load_4d(sK + kb * G::kKBytes + ch * G::kKChunk, tmK, bar, ch * 64, s.kvh, s.key0, s.b);
+    ++kn;
+    return true;
+  };
+  // step `step` of segment s to ring slot `slot` for the use-th time
+  auto load_q = [&](const Segment& s, int step, uint32_t slot, uint32_t use) {
+    if (use > 0 && !spin_wait(smem_addr(&ctl.q_empty[slot]), (use - 1) & 1, ctl, p)) return false;
+    const uint32_t bar = smem_addr(&ctl.q_full[slot]);
+    mbar_arrive_expect_tx(bar, q_bytes);
+    for (int ch = 0; ch < G::kChunks; ++ch)
+      tma_load_4d(sQ + slot * G::kQBytes + ch * G::kQChunk, tmQ, bar, ch * 64, s.kvh * p.g,
+                  step * p.nr, s.b);
+    return true;
+  };
+  Walk walk(p, starts, blockIdx.x);
+  Segment sg, nx;
+  bool more = walk.next(nx);
+  bool ok = more && load_k(nx);
+  int head = -1;                           // whose steps are in the ring
+  while (ok && more) {
+    sg = nx;
+    more = walk.next(nx);
+    if (more && !load_k(nx)) {             // a unit ahead
+      ok = false;
+      break;
+    }
+    if (stay) {
+      if (sg.head == head) continue;
+      head = sg.head;
+      for (int i = 0; i < p.steps && ok; ++i) ok = load_q(sg, i, i, gn);
+      if (ok) ++gn;
+    } else {
+      for (int i = 0; i < sg.n && ok; ++i) {
+        ok = load_q(sg, sg.s0 + i, qn % G::kQStages, qn / G::kQStages);
+        if (ok) ++qn;
+      }
+    }
+  }
+  if (!ok) {
+    // let every copy this thread started land before the CTA can exit: each
+    // barrier is waited for in its last phase, and in the one before, which
+    // covers a round of loads that was cut short
+    for (uint32_t s = 0; s < 2 && s < kn; ++s)
+      drain_wait(smem_addr(&ctl.k_full[s]), ((kn - 1 - s) >> 1) & 1, p);
+    for (int s = 0; s < G::kQStages; ++s) {
+      if (stay) {
+        if (s < p.steps && gn > 0) drain_wait(smem_addr(&ctl.q_full[s]), (gn - 1) & 1, p);
+      } else if (static_cast<uint32_t>(s) < qn) {
+        drain_wait(smem_addr(&ctl.q_full[s]), ((qn - 1 - s) / G::kQStages) & 1, p);
+      }
+    }
+  }
+}
+
+template <int D>
+__device__ void mma_role(Ctl& ctl, const Params& p, const Starts& starts, uint32_t tmem, uint32_t sK,
+                         uint32_t sQ, bool stay) {
+  using G = Geometry<D>;
+  const bool leader = elect_one();
+  constexpr uint32_t kIdWide = idesc_bf16_f32(kRows, kUnitKeys, false);
+  constexpr uint32_t kIdHalf = idesc_bf16_f32(kRows, kUnitKeys / 2, false);
+  uint32_t qn = 0, seg = 0, gn = 0;
+  Walk walk(p, starts, blockIdx.x);
+  Segment sg, nx;
+  bool more = walk.next(nx), ok = true;
+  while (ok && more) {
+    sg = nx;
+    more = walk.next(nx);
+    const bool last_of_head = !more || nx.head != sg.head;
+    if (!wait_warp(smem_addr(&ctl.k_full[seg & 1]), (seg >> 1) & 1, ctl, p)) break;
+    const uint64_t k0 = sdesc_sw128(sK + (seg & 1) * G::kKBytes, 16, 1024);
+    for (int i = 0; i < sg.n; ++i, ++qn) {
+      const uint32_t slot = stay ? sg.s0 + i : qn % G::kQStages;
+      const uint32_t use = stay ? gn : qn / G::kQStages;
+      const uint32_t buf = qn & 1;
+      if (!wait_warp(smem_addr(&ctl.q_full[slot]), use & 1, ctl, p) ||
+          (qn >= 2 && !wait_warp(smem_addr(&ctl.s_free[buf]), ((qn >> 1) - 1) & 1, ctl, p))) {
+        ok = false;
+        break;
+      }
+      tc_fence_after_sync();
+      const uint64_t q0 = sdesc_sw128(sQ + slot * G::kQBytes, 16, 1024);
+      // keys that no row of the step sees are not computed, 128 at a time
+      const uint32_t idesc =
+          seen(p, sg.key0 + kUnitKeys / 2, sg.s0 + i) ? kIdWide : kIdHalf;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t qo = ((kk >> 2) * G::kQChunk + (kk & 3) * 32) >> 4;
+        const uint32_t ko = ((kk >> 2) * G::kKChunk + (kk & 3) * 32) >> 4;
+        if (leader) mma_ss(tmem + kUnitKeys * buf, q0 + qo, k0 + ko, idesc, kk > 0 ? 1u : 0u);
+      }
+      if (leader) mma_commit(smem_addr(&ctl.s_full[buf]));
+      if (leader && !stay) mma_commit(smem_addr(&ctl.q_empty[slot]));
+    }
+    if (!ok) break;
+    if (leader) mma_commit(smem_addr(&ctl.k_empty[seg & 1]));
+    ++seg;
+    if (stay && last_of_head) {
+      for (int i = 0; i < p.steps; ++i)
+        if (leader) mma_commit(smem_addr(&ctl.q_empty[i]));
+      ++gn;
+    }
+  }
+  // no MMA may still be running when TMEM is released
+  if (leader) mma_commit(smem_addr(&ctl.drain));
+  drain_wait(smem_addr(&ctl.drain), 0, p);
+  __syncwarp();
 }
 
 template <int D>
@@ -197,31 +511,32 @@ __global__ void __launch_bounds__(kThreads, 1)
 key_weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ Params p, const __grid_constant__ Starts starts) {
   using G = Geometry<D>;
-  extern __shared__ uint8_t dyn_smem[];
-  __shared__ Ctl ctl;
-  const uint32_t base = (smem_addr(dyn_smem) + 1023u) & ~1023u;   // swizzle atoms need 1 KiB
-  const uint32_t sK = base, sQ = base + 4 * G::kTileBytes;
-  const uint32_t sL = sQ + G::kQStages * G::kTileBytes;
-  uint8_t* const generic = dyn_smem + (base - smem_addr(dyn_smem));
-  float* const nl_ring = reinterpret_cast<float*>(generic + (sL - base));
+  extern __shared__ __align__(1024) uint8_t dyn_smem[];
+  Ctl& ctl = *reinterpret_cast<Ctl*>(dyn_smem);
+  const uint32_t start = smem_addr(dyn_smem);
+  const uint32_t base = (start + static_cast<uint32_t>(sizeof(Ctl)) + 1023u) & ~1023u;
+  if (base + G::kTileBytes > start + smem_bytes<D>()) {
+    if (threadIdx.x == 0) atomicOr(p.status, kStatusCheck);
+    return;
+  }
+  const uint32_t sK = base, sQ = base + 2 * G::kKBytes;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int cta = static_cast<int>(blockIdx.x);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
       mbar_init(smem_addr(&ctl.k_full[s]), 1);
       mbar_init(smem_addr(&ctl.k_empty[s]), 1);
-      mbar_init(smem_addr(&ctl.l_full[s]), 32);
-      mbar_init(smem_addr(&ctl.l_empty[s]), 8);
-      for (int w = 0; w < 2; ++w) {
-        mbar_init(smem_addr(&ctl.s_full[w][s]), 1);
-        mbar_init(smem_addr(&ctl.s_free[w][s]), 4);
-      }
+      mbar_init(smem_addr(&ctl.s_full[s]), 2);       // the scores, and the rows' statistics
+      mbar_init(smem_addr(&ctl.s_free[s]), kSumWarps);
     }
     for (int s = 0; s < G::kQStages; ++s) {
       mbar_init(smem_addr(&ctl.q_full[s]), 1);
       mbar_init(smem_addr(&ctl.q_empty[s]), 1);
+    }
+    for (int w = 0; w < kGroups; ++w) {
+      for (int q = 0; q < 3; ++q) mbar_init(smem_addr(&ctl.fold[w][q]), 1);
+      mbar_init(smem_addr(&ctl.fold_free[w]), 1);
     }
     mbar_init(smem_addr(&ctl.drain), 1);
     ctl.abort = 0;
@@ -235,11 +550,11 @@ key_weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     tmem_alloc(smem_addr(&ctl.tmem_base), kTmemCols);
     tmem_relinquish();
   }
-  if (p.nr * p.g < kCols && warp < 8) {
-    // columns past nr * g are never loaded: zeros, so that their scores are 0
-    // and their weight 2^(0 - inf) too
-    uint4* z = reinterpret_cast<uint4*>(generic + (sQ - base));
-    for (int i = threadIdx.x; i < G::kQStages * G::kTileBytes / 16; i += 256)
+  if (p.nr * p.g < kRows && warp < kSumWarps) {
+    // rows past nr * g are never loaded: zeros, so that their scores are 0 and
+    // their weights 2^(0 - inf) too
+    uint4* z = reinterpret_cast<uint4*>(dyn_smem + (sQ - start));
+    for (int i = threadIdx.x; i < G::kQStages * G::kQBytes / 16; i += 32 * kSumWarps)
       z[i] = make_uint4(0u, 0u, 0u, 0u);
     fence_proxy_async_smem();
   }
@@ -251,185 +566,19 @@ key_weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   // kernel, global memory is touched only after it has completed
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
-  Walk walk(p, starts, cta);
-  Segment sg;
-  if (warp == kLoadWarp) {
-    if (lane == 0) {
-      uint32_t qn = 0, kn = 0;       // Q steps and K buffers issued
-      bool ok = true;
-      const uint32_t q_bytes = static_cast<uint32_t>(G::kChunks * 128 * p.g * p.nr);
-      while (ok && walk.next(sg)) {
-        const uint32_t kb = kn & 1;
-        if (kn >= 2 && !spin_wait(smem_addr(&ctl.k_empty[kb]), ((kn >> 1) - 1) & 1, ctl, p)) {
-          ok = false;
-          break;
-        }
-        const int tiles = sg.key0 + kKeys < p.Lk ? 2 : 1;
-        const uint32_t kbar = smem_addr(&ctl.k_full[kb]);
-        mbar_arrive_expect_tx(kbar, tiles * G::kTileBytes);
-        for (int w = 0; w < tiles; ++w)
-          for (int ch = 0; ch < G::kChunks; ++ch)
-            tma_load_4d(sK + (2 * kb + w) * G::kTileBytes + ch * G::kChunkBytes, &tmK, kbar, ch * 64,
-                        sg.kvh, sg.key0 + w * kKeys, sg.b);
-        ++kn;
-        for (int i = 0; i < sg.n; ++i, ++qn) {
-          const uint32_t slot = qn % G::kQStages, use = qn / G::kQStages;
-          if (use > 0 && !spin_wait(smem_addr(&ctl.q_empty[slot]), (use - 1) & 1, ctl, p)) {
-            ok = false;
-            break;
-          }
-          const uint32_t bar = smem_addr(&ctl.q_full[slot]);
-          mbar_arrive_expect_tx(bar, q_bytes);
-          for (int ch = 0; ch < G::kChunks; ++ch)
-            tma_load_4d(sQ + slot * G::kTileBytes + ch * G::kChunkBytes, &tmQ, bar, ch * 64,
-                        sg.kvh * p.g, (sg.s0 + i) * p.nr, sg.b);
-        }
-      }
-      if (!ok) {
-        // let every copy this thread started land before the CTA can exit
-        for (uint32_t s = 0; s < 2 && s < kn; ++s)
-          drain_wait(smem_addr(&ctl.k_full[s]), ((s + ((kn - 1 - s) / 2) * 2) >> 1) & 1, p);
-        for (uint32_t s = 0; s < G::kQStages && s < qn; ++s)
-          drain_wait(smem_addr(&ctl.q_full[s]), ((qn - 1 - s) / G::kQStages) & 1, p);
-      }
-    }
-  } else if (warp == kMmaWarp) {
-    const bool leader = elect_one();
-    constexpr uint32_t idesc = idesc_bf16_f32(kKeys, kCols, false);
-    uint32_t qn = 0, kn = 0, sn[2] = {0, 0};
-    bool ok = true;
-    while (ok && walk.next(sg)) {
-      const uint32_t kb = kn & 1;
-      if (!wait_warp(smem_addr(&ctl.k_full[kb]), (kn >> 1) & 1, ctl, p)) break;
-      ++kn;
-      for (int i = 0; i < sg.n && ok; ++i, ++qn) {
-        const uint32_t slot = qn % G::kQStages;
-        if (!wait_warp(smem_addr(&ctl.q_full[slot]), (qn / G::kQStages) & 1, ctl, p)) {
-          ok = false;
-          break;
-        }
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          if (!takes_part(p, sg.key0 + w * kKeys, sg.s0 + i)) continue;
-          const uint32_t sb = sn[w] & 1;
-          if (sn[w] >= 2 &&
-              !wait_warp(smem_addr(&ctl.s_free[w][sb]), ((sn[w] >> 1) - 1) & 1, ctl, p)) {
-            ok = false;
-            break;
-          }
-          ++sn[w];
-          tc_fence_after_sync();
-          const uint64_t a0 = sdesc_sw128(sK + (2 * kb + w) * G::kTileBytes, 16, 1024);
-          const uint64_t b0 = sdesc_sw128(sQ + slot * G::kTileBytes, 16, 1024);
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = ((kk >> 2) * G::kChunkBytes + (kk & 3) * 32) >> 4;
-            if (leader)
-              mma_ss(tmem + 256 * w + 128 * sb, a0 + off, b0 + off, idesc, kk > 0 ? 1u : 0u);
-          }
-          if (leader) mma_commit(smem_addr(&ctl.s_full[w][sb]));
-        }
-        if (!ok) break;
-        if (leader) mma_commit(smem_addr(&ctl.q_empty[slot]));
-      }
-      if (leader && ok) mma_commit(smem_addr(&ctl.k_empty[kb]));
-    }
-    // no MMA may still be running when TMEM is released
-    if (leader) mma_commit(smem_addr(&ctl.drain));
-    drain_wait(smem_addr(&ctl.drain), 0, p);
-    __syncwarp();
-  } else if (warp == kLseWarp) {
-    // lane's columns lane + 32 m: row col / g of the step, head col % g
-    int row[4], head[4];
-#pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      const int col = lane + 32 * m;
-      row[m] = col < p.nr * p.g ? col / p.g : p.Lq;      // past the last row: no weight
-      head[m] = col % p.g;
-    }
-    uint32_t n = 0;
-    bool ok = true;
-    while (ok && walk.next(sg)) {
-      const float* lse = p.lse + (static_cast<size_t>(sg.b) * p.n_q + sg.kvh * p.g) * p.Lq;
-      for (int i = 0; i < sg.n; ++i, ++n) {
-        const int i0 = (sg.s0 + i) * p.nr;
-        float nl[4];
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          nl[m] = -INFINITY;
-          if (row[m] < p.Lq - i0) {
-            const float l = lse[static_cast<size_t>(head[m]) * p.Lq + i0 + row[m]];
-            if (l != -INFINITY) nl[m] = -l * kLog2e;     // a row without keys has no weight
-          }
-        }
-        const uint32_t slot = n & 1;
-        if (n >= 2 && !wait_warp(smem_addr(&ctl.l_empty[slot]), ((n >> 1) - 1) & 1, ctl, p)) {
-          ok = false;
-          break;
-        }
-#pragma unroll
-        for (int m = 0; m < 4; ++m) nl_ring[slot * kCols + lane + 32 * m] = nl[m];
-        mbar_arrive(smem_addr(&ctl.l_full[slot]));
-      }
-    }
-  } else if (warp < 8) {
-    const int w = warp >> 2;
-    const int r = (warp & 3) * 32 + lane;                // key of the tile = TMEM lane
-    const uint32_t taddr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 256 * w;
-    const uint64_t c2 = f32x2_pack(p.c, p.c);
-    uint32_t n = 0, sn = 0;
-    bool ok = true;
-    while (ok && walk.next(sg)) {
-      const int key = sg.key0 + w * kKeys + r;
-      // the running sum with its rounding error carried along: a key of a long
-      // prompt adds thousands of steps
-      float sum = 0.0f, carry = 0.0f;
-      for (int i = 0; i < sg.n; ++i, ++n) {
-        const uint32_t slot = n & 1;
-        if (!wait_warp(smem_addr(&ctl.l_full[slot]), (n >> 1) & 1, ctl, p)) {
-          ok = false;
-          break;
-        }
-        if (takes_part(p, sg.key0 + w * kKeys, sg.s0 + i)) {
-          const uint32_t sb = sn & 1;
-          if (!wait_warp(smem_addr(&ctl.s_full[w][sb]), (sn >> 1) & 1, ctl, p)) {
-            ok = false;
-            break;
-          }
-          ++sn;
-          tc_fence_after_sync();
-          float s[kCols];
-          uint32_t* sr = reinterpret_cast<uint32_t*>(s);
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            tmem_ld32(taddr + 128 * sb + 32 * q, *reinterpret_cast<uint32_t(*)[32]>(sr + 32 * q));
-          tmem_wait_ld(*reinterpret_cast<uint32_t(*)[32]>(sr));
-          tmem_after_wait(*reinterpret_cast<uint32_t(*)[32]>(sr + 32));
-          tmem_after_wait(*reinterpret_cast<uint32_t(*)[32]>(sr + 64));
-          tmem_after_wait(*reinterpret_cast<uint32_t(*)[32]>(sr + 96));
-          tc_fence_before_sync();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_addr(&ctl.s_free[w][sb]));
-          // rows before the key's own position do not see it
-          const int i0 = (sg.s0 + i) * p.nr;
-          const bool diag = p.causal && sg.key0 + w * kKeys + kKeys - 1 - p.off > i0;
-          const float* nl = nl_ring + slot * kCols;
-          const float add = diag ? column_sum<true>(s, nl, c2, (key - p.off - i0) * p.g)
-                                 : column_sum<false>(s, nl, c2, 0);
-          const float y = add - carry, t = sum + y;
-          carry = (t - sum) - y;
-          sum = t;
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&ctl.l_empty[slot]));
-      }
-      if (!ok) break;
-      if (!sg.whole) {
-        p.part[(2 * cta + (sg.first ? 0 : 1)) * kUnitKeys + w * kKeys + r] = sum;
-      } else if (key < p.Lk) {
-        float* out = p.weights + (static_cast<size_t>(sg.b) * p.n_kv + sg.kvh) * p.Lk + key;
-        *out = p.accumulate ? *out + sum : sum;
-      }
+  // all of a head's steps fit the Q ring: step i stays in slot i
+  const bool stay = p.steps <= G::kQStages;
+  if (warp < kSumWarps) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
+    sum_role(ctl, p, starts, tmem);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == kLoadWarp) {
+      if (lane == 0) load_role<D>(&tmQ, &tmK, ctl, p, starts, sK, sQ, stay);
+    } else if (warp == kMmaWarp) {
+      mma_role<D>(ctl, p, starts, tmem, sK, sQ, stay);
+    } else if (warp == kStatWarp) {
+      stat_role(ctl, p, starts);
     }
   }
 
@@ -472,10 +621,15 @@ std::mutex g_weights_mutex;
 bool g_weights_ready[kMaxDevices] = {};
 EncodeTiledFn g_weights_encode = nullptr;
 
+// The register split only works on a CTA launched with at least that many.
 template <int D>
-bool set_smem() {
+bool configure() {
+  cudaFuncAttributes fa;
+  if (cudaFuncGetAttributes(&fa, key_weights_kernel<D>) != cudaSuccess ||
+      fa.numRegs * kThreads < kRegBudget)
+    return false;
   return cudaFuncSetAttribute(key_weights_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              Geometry<D>::kSmemBytes) == cudaSuccess;
+                              smem_bytes<D>()) == cudaSuccess;
 }
 
 attn_status_t weights_device_ready(cudaStream_t stream, int** status) {
@@ -500,7 +654,7 @@ attn_status_t weights_device_ready(cudaStream_t stream, int** status) {
       return ATTN_ERR_CUDA;
     g_weights_encode = reinterpret_cast<EncodeTiledFn>(fn);
   }
-  if (!set_smem<64>() || !set_smem<128>()) return ATTN_ERR_CUDA;
+  if (!configure<64>() || !configure<128>()) return ATTN_ERR_UNSUPPORTED;
   g_weights_ready[dev] = true;
   return ATTN_OK;
 }
@@ -551,12 +705,12 @@ int64_t steps_before(const Params& p, int64_t t) {
 }
 
 bool supported(int64_t B, int64_t Lq, int64_t Lk, int32_t n_q, int32_t n_kv, int32_t d_h) {
-  if ((d_h != 64 && d_h != 128) || n_q / n_kv > kCols) return false;
+  if ((d_h != 64 && d_h != 128) || n_q / n_kv > kRows) return false;
   constexpr int64_t kMost = int64_t{1} << 30;
   if (Lq > kMost || Lk > kMost || B > kMost || B * n_kv > kMost) return false;
   // units and a CTA's steps are 32-bit; scores in all fit 64 with room
   const int64_t units = B * n_kv * ((Lk + kUnitKeys - 1) / kUnitKeys);
-  const int64_t steps = (Lq * (n_q / n_kv) + kCols - 1) / kCols * 2;
+  const int64_t steps = (Lq * (n_q / n_kv) + kRows - 1) / kRows * 2;
   return units <= INT32_MAX - kCtas && steps <= INT64_MAX / units / kCtas &&
          units * steps / kCtas < INT32_MAX / 2 && Lk * (n_q / n_kv) <= INT32_MAX;
 }
@@ -609,12 +763,14 @@ attn_status_t attn_key_weights_fwd(const void* q, const void* k, const float* ls
   p.n_q = n_q;
   p.n_kv = n_kv;
   p.g = n_q / n_kv;
-  p.nr = kCols / p.g;
+  p.nr = kRows / p.g;
   p.steps = static_cast<int>((Lq + p.nr - 1) / p.nr);
   p.T = static_cast<int>((Lk + kUnitKeys - 1) / kUnitKeys);
   p.causal = causal;
   p.accumulate = accumulate;
-  p.c = scale * kLog2e;
+  // (a scale of 0 as one that no score notices: a hidden score still has to
+  // come out as -inf)
+  p.c = scale != 0.0f ? scale * kLog2e : 1e-30f;
   p.spin_limit = 1ll << 31;   // about a second at 2 GHz
 
   // equal ranges of the steps of all units
@@ -638,7 +794,7 @@ attn_status_t attn_key_weights_fwd(const void* q, const void* k, const float* ls
   }
 
   CUtensorMap mq, mk;
-  if (!encode(&mq, q, d_h, n_q, Lq, B, p.g, p.nr) || !encode(&mk, k, d_h, n_kv, Lk, B, 1, kKeys))
+  if (!encode(&mq, q, d_h, n_q, Lq, B, p.g, p.nr) || !encode(&mk, k, d_h, n_kv, Lk, B, 1, kUnitKeys))
     return ATTN_ERR_CUDA;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -651,10 +807,10 @@ attn_status_t attn_key_weights_fwd(const void* q, const void* k, const float* ls
   cfg.numAttrs = 1;
   cudaError_t e;
   if (d_h == 128) {
-    cfg.dynamicSmemBytes = Geometry<128>::kSmemBytes;
+    cfg.dynamicSmemBytes = smem_bytes<128>();
     e = cudaLaunchKernelEx(&cfg, key_weights_kernel<128>, mq, mk, p, st);
   } else {
-    cfg.dynamicSmemBytes = Geometry<64>::kSmemBytes;
+    cfg.dynamicSmemBytes = smem_bytes<64>();
     e = cudaLaunchKernelEx(&cfg, key_weights_kernel<64>, mq, mk, p, st);
   }
   if (e != cudaSuccess) return ATTN_ERR_CUDA;

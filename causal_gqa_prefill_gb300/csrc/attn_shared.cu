@@ -24,8 +24,8 @@
 //                  one-row threads), and log-sum-exps.
 //   ragged split   (attn_decode.cu) starts on the SMs that the prefix kernel
 //                  leaves free, without waiting for it.
-//   combine        eight rows per CTA, one warp each: merges the row's partials of
-//                  both kernels into bf16 O and fp32 LSE.
+//   combine        one thread per row and eight dimensions: merges the row's
+//                  partials of both kernels into bf16 O and fp32 LSE.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -46,7 +46,7 @@ constexpr int kRows = 128;            // query rows per tile (TMEM lanes)
 constexpr int kKeys = 128;            // keys per tile
 constexpr int kCtas = 152;            // one CTA per SM on a 152-SM GB300
 constexpr int kThreads = 384;
-constexpr int kSoftmaxRegs = 224, kOtherRegs = 56;
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;   // registers per thread
 constexpr int kRegBudget = 2 * 128 * kSoftmaxRegs + 128 * kOtherRegs;
 static_assert(kRegBudget <= kThreads * 168, "setmaxnreg split exceeds the launch allocation");
 constexpr int kLoadWarp = 8, kMmaWarp = 9;
@@ -309,13 +309,15 @@ __device__ __forceinline__ float row_max128(const float* v) {
   return max3(max3(m[0], m[1], m[2]), max3(m[3], m[4], m[5]), fmaxf(m[6], m[7]));
 }
 
+// kPos: the scale is positive and multiplies inside the exponent's FMA; any
+// other is applied to the scores first, so that the maximum is of scaled ones.
+template <bool kPos>
 __device__ void softmax_role(int slot, Ctl& ctl, const Params& p, uint32_t tmem) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r = (warp & 3) * 32 + lane;                         // row of the tile = TMEM lane
   const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
   const uint32_t tS = lane_base + 128 * slot, tO = lane_base + 256 + 128 * slot;
-  const bool positive = p.c > 0.0f;
-  const float cc = positive ? p.c : 1.0f;
+  const float cc = kPos ? p.c : 1.0f;
   const uint64_t cc2 = f32x2_pack(cc, cc);
   uint32_t ph_s = 0, ph_o = 0;
   Walk walk(p, blockIdx.x);
@@ -341,8 +343,7 @@ __device__ void softmax_role(int slot, Ctl& ctl, const Params& p, uint32_t tmem)
       tmem_after_wait(*reinterpret_cast<uint32_t(*)[32]>(sr + 32));
       tmem_after_wait(*reinterpret_cast<uint32_t(*)[32]>(sr + 64));
       tmem_after_wait(*reinterpret_cast<uint32_t(*)[32]>(sr + 96));
-      if (!positive) {
-        // fold the scale in first, so that the maximum below is of scaled scores
+      if (!kPos) {
 #pragma unroll
         for (int i = 0; i < 128; ++i) s[i] *= p.c;
       }
@@ -419,6 +420,7 @@ __device__ void softmax_role(int slot, Ctl& ctl, const Params& p, uint32_t tmem)
   }
 }
 
+template <bool kPos>
 __global__ void __launch_bounds__(kThreads, 1)
 prefix_split_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Params p) {
@@ -469,7 +471,7 @@ prefix_split_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
 
   if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-    softmax_role(warp >> 2, ctl, p, tmem);
+    softmax_role<kPos>(warp >> 2, ctl, p, tmem);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == kLoadWarp) {
@@ -486,11 +488,12 @@ prefix_split_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
   }
 }
 
-// Rows r0 .. r0 + 7 of one row tile, one warp per row, lane = four dimensions:
-// the eight rows' 16-byte pieces of a prefix partial are one 128-byte line.
-constexpr int kCombineRows = 8;
+// 32 rows of one row tile per CTA, lane = row: the prefix partials' pieces of
+// four dimensions are 512 contiguous bytes for the warp. Warp w of the CTA's
+// eight takes dimensions 8 (8 y + w) .. + 7, y = blockIdx.y in 0 .. 1.
+constexpr int kCombineRows = 32, kCombineWarps = 8, kCombineY = 2;
 
-__global__ void __launch_bounds__(32 * kCombineRows)
+__global__ void __launch_bounds__(32 * kCombineWarps)
 shared_combine_kernel(uint16_t* o, float* lse, const int* lens, int C,
                       const gb300_host::RaggedParts own, const Params p) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -498,24 +501,30 @@ shared_combine_kernel(uint16_t* o, float* lse, const int* lens, int C,
   const int lane = threadIdx.x & 31;
   const int blocks = (p.nb * p.g + kCombineRows - 1) / kCombineRows;
   const int kt = blockIdx.x / blocks;                     // K/V head and row tile
-  const int r = (blockIdx.x - kt * blocks) * kCombineRows + (threadIdx.x >> 5);
+  const int r = (blockIdx.x - kt * blocks) * kCombineRows + lane;
   const int kvh = kt / p.tiles, tile = kt - kvh * p.tiles;
   const int b = tile * p.nb + r / p.g, h = r % p.g;
   if (r >= p.nb * p.g || b >= p.B) return;
+  const int d4 = 2 * (blockIdx.y * kCombineWarps + (threadIdx.x >> 5));   // first of two
 
   float m = -INFINITY, wsum = 0.0f;
-  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  auto add = [&](float ls, const float4& v) {
-    if (ls == -INFINITY) return;                          // an empty part: v is not written
+  float4 acc[2];
+  acc[0] = acc[1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  auto add = [&](float ls, const float4& u, const float4& v) {
+    if (ls == -INFINITY) return;                          // an empty part: u, v are not written
     const float mn = fmaxf(m, ls);
     const float a = (m == -INFINITY) ? 0.0f : exp2f(m - mn);
     const float w = exp2f(ls - mn);
     m = mn;
     wsum = fmaf(wsum, a, w);
-    acc.x = fmaf(w, v.x, acc.x * a);
-    acc.y = fmaf(w, v.y, acc.y * a);
-    acc.z = fmaf(w, v.z, acc.z * a);
-    acc.w = fmaf(w, v.w, acc.w * a);
+    acc[0].x = fmaf(w, u.x, acc[0].x * a);
+    acc[0].y = fmaf(w, u.y, acc[0].y * a);
+    acc[0].z = fmaf(w, u.z, acc[0].z * a);
+    acc[0].w = fmaf(w, u.w, acc[0].w * a);
+    acc[1].x = fmaf(w, v.x, acc[1].x * a);
+    acc[1].y = fmaf(w, v.y, acc[1].y * a);
+    acc[1].z = fmaf(w, v.z, acc[1].z * a);
+    acc[1].w = fmaf(w, v.w, acc[1].w * a);
   };
 
   const int unit = kvh * p.pairs + tile / 2;
@@ -526,26 +535,40 @@ shared_combine_kernel(uint16_t* o, float* lse, const int* lens, int C,
   // two row tiles: this tile's slot of every segment; one: both slots
   const int step = both ? 2 : 1, slots = both ? 1 : 2;
   const size_t first = 2 * (static_cast<size_t>(unit) + c0) + (both ? (tile & 1) : 0);
-  const float4* part = reinterpret_cast<const float4*>(p.part_o) + lane * kRows + r;
-#pragma unroll 4
-  for (int e = 0; e < (c1 - c0 + 1) * slots; ++e) {
-    const size_t at = first + static_cast<size_t>(e) * step;
-    add(p.part_lse2[at * kRows + r], part[at * (kPartFloats / 4)]);
+  const float4* part = reinterpret_cast<const float4*>(p.part_o) + d4 * kRows + r;
+  const int count = (c1 - c0 + 1) * slots;
+  constexpr int kBatch = 4;              // partials on their way at once
+  for (int e0 = 0; e0 < count; e0 += kBatch) {
+    float ls[kBatch];
+    float4 u[kBatch], v[kBatch];
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e) {
+      ls[e] = -INFINITY;
+      if (e0 + e < count) {
+        const size_t at = first + static_cast<size_t>(e0 + e) * step;
+        ls[e] = p.part_lse2[at * kRows + r];
+        u[e] = part[at * (kPartFloats / 4)];
+        v[e] = part[at * (kPartFloats / 4) + kRows];
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e) add(ls[e], u[e], v[e]);
   }
   if (min(lens[b], C) > 0) {
     const size_t hd = static_cast<size_t>(b) * p.n_kv + kvh;
-    const int d0 = own.ends[2 * hd], d1 = own.ends[2 * hd + 1];
-#pragma unroll 2
-    for (int c = d0; c <= d1; ++c) {
+    const int e0 = own.ends[2 * hd], e1 = own.ends[2 * hd + 1];
+    for (int c = e0; c <= e1; ++c) {
       const size_t row = (hd + c) * p.g + h;
-      add(own.lse2[row], reinterpret_cast<const float4*>(own.o)[row * 32 + lane]);
+      const float4* src = reinterpret_cast<const float4*>(own.o) + row * 32 + d4;
+      add(own.lse2[row], src[0], src[1]);
     }
   }
   const float inv = 1.0f / wsum;
   const size_t row = static_cast<size_t>(b) * p.n_q + kvh * p.g + h;
-  *reinterpret_cast<uint2*>(o + row * kDim + 4 * lane) =
-      make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-  if (lane == 0) lse[row] = (m + log2f(wsum)) * 0.69314718055994530942f;
+  *reinterpret_cast<uint4*>(o + row * kDim + 4 * d4) =
+      make_uint4(pack_bf16x2(acc[0].x * inv, acc[0].y * inv), pack_bf16x2(acc[0].z * inv, acc[0].w * inv),
+                 pack_bf16x2(acc[1].x * inv, acc[1].y * inv), pack_bf16x2(acc[1].z * inv, acc[1].w * inv));
+  if (d4 == 0) lse[row] = (m + log2f(wsum)) * 0.69314718055994530942f;
 }
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
@@ -557,6 +580,17 @@ constexpr int kMaxDevices = 64;
 std::mutex g_shared_mutex;
 bool g_shared_ready[kMaxDevices] = {};
 EncodeTiledFn g_shared_encode = nullptr;
+
+// The register split only works on a CTA launched with at least that many.
+template <bool kPos>
+bool configure() {
+  cudaFuncAttributes fa;
+  if (cudaFuncGetAttributes(&fa, prefix_split_kernel<kPos>) != cudaSuccess ||
+      fa.numRegs * kThreads < kRegBudget)
+    return false;
+  return cudaFuncSetAttribute(prefix_split_kernel<kPos>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              kSmemBytes) == cudaSuccess;
+}
 
 attn_status_t shared_device_ready(cudaStream_t stream, int** status) {
   int dev = 0;
@@ -580,14 +614,7 @@ attn_status_t shared_device_ready(cudaStream_t stream, int** status) {
       return ATTN_ERR_CUDA;
     g_shared_encode = reinterpret_cast<EncodeTiledFn>(fn);
   }
-  // the register split only works on a CTA launched with at least that many
-  cudaFuncAttributes fa;
-  if (cudaFuncGetAttributes(&fa, prefix_split_kernel) != cudaSuccess ||
-      fa.numRegs * kThreads < kRegBudget)
-    return ATTN_ERR_UNSUPPORTED;
-  if (cudaFuncSetAttribute(prefix_split_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           kSmemBytes) != cudaSuccess)
-    return ATTN_ERR_CUDA;
+  if (!configure<true>() || !configure<false>()) return ATTN_ERR_UNSUPPORTED;
   g_shared_ready[dev] = true;
   return ATTN_OK;
 }
@@ -700,15 +727,17 @@ attn_status_t attn_decode_shared_fwd(const void* q, const void* prefix_k, const 
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, prefix_split_kernel, mq, mk, mv, p) != cudaSuccess)
-    return ATTN_ERR_CUDA;
+  const cudaError_t e = p.c > 0.0f
+                            ? cudaLaunchKernelEx(&cfg, prefix_split_kernel<true>, mq, mk, mv, p)
+                            : cudaLaunchKernelEx(&cfg, prefix_split_kernel<false>, mq, mk, mv, p);
+  if (e != cudaSuccess) return ATTN_ERR_CUDA;
   gb300_host::RaggedParts own;
   st = gb300_host::ragged_split_beside(q, k, v, lens, ws + s.own_at, B, C, n_q, n_kv, scale, stream,
                                        status, &own);
   if (st != ATTN_OK) return st;
   const int blocks = (p.nb * p.g + kCombineRows - 1) / kCombineRows;
-  cfg.gridDim = dim3(static_cast<unsigned>(s.tiles * n_kv * blocks));
-  cfg.blockDim = dim3(32 * kCombineRows);
+  cfg.gridDim = dim3(static_cast<unsigned>(s.tiles * n_kv * blocks), kCombineY);
+  cfg.blockDim = dim3(32 * kCombineWarps);
   cfg.dynamicSmemBytes = 0;
   if (cudaLaunchKernelEx(&cfg, shared_combine_kernel, static_cast<uint16_t*>(o), lse, lens,
                          static_cast<int>(C), own, p) != cudaSuccess)
