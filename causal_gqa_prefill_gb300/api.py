@@ -162,7 +162,9 @@ class _Call:
         self.other = None                 # the torch stream, when it is not the current one
         if torch.cuda.current_device() != device.index:
             self.guard = torch.cuda.device(device)
-        self.handle = torch.cuda.current_stream(device).cuda_stream
+        # the handle that torch.cuda.current_stream(device).cuda_stream gives,
+        # without the two objects made on the way
+        self.handle = torch._C._cuda_getCurrentRawStream(device.index)
         if stream is not None:
             handle = stream if isinstance(stream, int) else stream.cuda_stream
             if handle != self.handle:
@@ -193,31 +195,53 @@ class _Call:
             if nbytes < 0:
                 raise AttnError(_abi.ATTN_ERR_UNSUPPORTED, size.__name__)
             return self.empty(nbytes, self.torch.uint8), nbytes
-        if not isinstance(given, self.torch.Tensor) or given.device != self.device:
+        if getattr(given, "device", None) != self.device:
             raise ValueError(f"workspace must be a tensor on {self.device}")
         if not given.is_contiguous():
             raise ValueError("workspace must be contiguous")
-        return given, given.numel() * given.element_size()
+        return given, given.nbytes
+
+
+def _wrong_tensor(name, t, shape, dtype, device=None):
+    """The error that says how ``t`` differs from a contiguous CUDA tensor of this
+    shape (None: any size) and dtype on ``device``; None if it does not."""
+    import torch
+
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dtype:
+        return TypeError(f"{name} must be a {str(dtype).replace('torch.', '')} CUDA tensor")
+    if device is not None and t.device != device:
+        return ValueError(f"{name} is on {t.device}, the other tensors are on {device}")
+    if t.dim() != len(shape) or any(a is not None and a != b for a, b in zip(shape, t.shape)):
+        want = ", ".join("*" if a is None else str(a) for a in shape)
+        return ValueError(f"{name} must be [{want}], not {list(t.shape)}")
+    if not t.is_contiguous():
+        return ValueError(f"{name} must be contiguous")
+    return None
 
 
 def _cuda_tensor(name, t, shape, dtype, device=None):
     """``t`` if it is a contiguous CUDA tensor of this shape (None: any size) and
-    dtype, on ``device``; else the error that says what it should be."""
+    dtype, on ``device``."""
+    # the usual case in as few steps as it takes (device is a CUDA device)
     if (getattr(t, "dtype", None) is dtype and t.device == device and t.shape == shape
             and t.is_contiguous()):
-        return t                          # the usual case, in as few steps as it takes
-    import torch
-
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dtype:
-        raise TypeError(f"{name} must be a {str(dtype).replace('torch.', '')} CUDA tensor")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the other tensors are on {device}")
-    if t.dim() != len(shape) or any(a is not None and a != b for a, b in zip(shape, t.shape)):
-        want = ", ".join("*" if a is None else str(a) for a in shape)
-        raise ValueError(f"{name} must be [{want}], not {list(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+        return t
+    wrong = _wrong_tensor(name, t, shape, dtype, device)
+    if wrong is not None:
+        raise wrong
     return t
+
+
+def _heads_of(name, t, first, length, dtype, device=None):
+    """The shape of the contiguous [first, length, heads, d] CUDA tensor ``t`` (None:
+    any size)."""
+    if (getattr(t, "dtype", None) is dtype and t.is_cuda and t.dim() == 4 and t.is_contiguous()
+            and (device is None or t.device == device)):
+        B, L, H, d = t.shape
+        if (first is None or first == B) and (length is None or length == L):
+            return B, L, H, d
+    wrong = _wrong_tensor(name, t, (first, length, None, None), dtype, device)
+    raise wrong
 
 
 def attn_key_weights_workspace_bytes(B, Lq, Lk, n_q, n_kv, d_h=128) -> int:
@@ -249,9 +273,11 @@ def attn_key_weights(q, k, lse, *, causal=True, scale=None, weights=None, accumu
     import torch
 
     bf16 = torch.bfloat16
-    B, Lq, n_q, d = _cuda_tensor("q", q, (None, None, None, None), bf16).shape
+    B, Lq, n_q, d = _heads_of("q", q, None, None, bf16)
     dev = q.device
-    Lk, n_kv = _cuda_tensor("k", k, (B, None, None, d), bf16, dev).shape[1:3]
+    _, Lk, n_kv, dk = _heads_of("k", k, B, None, bf16, dev)
+    if dk != d:
+        raise ValueError("q and k must have the same d_h")
     if Lk < Lq:
         raise ValueError("k must hold at least as many positions as q has rows")
     _cuda_tensor("lse", lse, (B, n_q, Lq), torch.float32, dev)
@@ -305,15 +331,17 @@ def attn_decode_ragged(q, k, v, lens, *, weights=None, scale=None, workspace=Non
     import torch
 
     bf16 = torch.bfloat16
-    B, _, n_q, d = _cuda_tensor("q", q, (None, 1, None, None), bf16).shape
+    B, _, n_q, d = _heads_of("q", q, None, 1, bf16)
     dev = q.device
-    C, n_kv = _cuda_tensor("k", k, (B, None, None, d), bf16, dev).shape[1:3]
-    _cuda_tensor("v", v, tuple(k.shape), bf16, dev)
+    _, C, n_kv, dk = _heads_of("k", k, B, None, bf16, dev)
+    if dk != d:
+        raise ValueError("q and k must have the same d_h")
+    _cuda_tensor("v", v, k.shape, bf16, dev)
     _cuda_tensor("lens", lens, (B,), torch.int32, dev)
     if weights is not None:
         _cuda_tensor("weights", weights, (B, n_kv, C), torch.float32, dev)
     if out is not None:
-        _cuda_tensor("out", out, tuple(q.shape), bf16, dev)
+        _cuda_tensor("out", out, q.shape, bf16, dev)
     if lse is not None:
         _cuda_tensor("lse", lse, (B, n_q, 1), torch.float32, dev)
     if scale is None:
@@ -363,15 +391,17 @@ def attn_decode_shared(q, prefix_k, prefix_v, k, v, lens, *, scale=None, workspa
     import torch
 
     bf16 = torch.bfloat16
-    B, _, n_q, d = _cuda_tensor("q", q, (None, 1, None, None), bf16).shape
+    B, _, n_q, d = _heads_of("q", q, None, 1, bf16)
     dev = q.device
-    P, n_kv = _cuda_tensor("prefix_k", prefix_k, (1, None, None, d), bf16, dev).shape[1:3]
-    _cuda_tensor("prefix_v", prefix_v, tuple(prefix_k.shape), bf16, dev)
-    C = _cuda_tensor("k", k, (B, None, n_kv, d), bf16, dev).shape[1]
-    _cuda_tensor("v", v, tuple(k.shape), bf16, dev)
+    _, P, n_kv, dp = _heads_of("prefix_k", prefix_k, 1, None, bf16, dev)
+    _cuda_tensor("prefix_v", prefix_v, prefix_k.shape, bf16, dev)
+    _, C, own_kv, dk = _heads_of("k", k, B, None, bf16, dev)
+    if dk != d or dp != d or own_kv != n_kv:
+        raise ValueError("q, prefix_k and k must agree on d_h, the caches on their heads")
+    _cuda_tensor("v", v, k.shape, bf16, dev)
     _cuda_tensor("lens", lens, (B,), torch.int32, dev)
     if out is not None:
-        _cuda_tensor("out", out, tuple(q.shape), bf16, dev)
+        _cuda_tensor("out", out, q.shape, bf16, dev)
     if lse is not None:
         _cuda_tensor("lse", lse, (B, n_q, 1), torch.float32, dev)
     if scale is None:
@@ -420,11 +450,12 @@ def attn_evict(k, v, weights, lens, budget, recent=0, *, capacity=None, k_out=No
     the room of the new caches. Outputs must not overlap the inputs."""
     import torch
 
-    if not isinstance(k, torch.Tensor) or k.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+    kind = getattr(k, "dtype", None)
+    if kind is not torch.bfloat16 and kind is not torch.float8_e4m3fn:
         raise TypeError("k must be a bfloat16 or float8_e4m3fn CUDA tensor")
-    B, C, n_kv, d = _cuda_tensor("k", k, (None, None, None, None), k.dtype).shape
+    B, C, n_kv, d = _heads_of("k", k, None, None, kind)
     dev = k.device
-    _cuda_tensor("v", v, tuple(k.shape), k.dtype, dev)
+    _cuda_tensor("v", v, k.shape, kind, dev)
     _cuda_tensor("weights", weights, (B, n_kv, C), torch.float32, dev)
     _cuda_tensor("lens", lens, (B,), torch.int32, dev)
     budget, recent = int(budget), int(recent)
@@ -434,8 +465,8 @@ def attn_evict(k, v, weights, lens, budget, recent=0, *, capacity=None, k_out=No
         capacity = budget if k_out is None or k_out.dim() != 4 else k_out.shape[1]
     if capacity < budget:
         raise ValueError("the new capacity must hold the budget")
-    wanted = {"k_out": (k_out, (B, capacity, n_kv, d), k.dtype),
-              "v_out": (v_out, (B, capacity, n_kv, d), k.dtype),
+    wanted = {"k_out": (k_out, (B, capacity, n_kv, d), kind),
+              "v_out": (v_out, (B, capacity, n_kv, d), kind),
               "weights_out": (weights_out, (B, n_kv, capacity), torch.float32),
               "lens_out": (lens_out, (B,), torch.int32),
               "index": (index, (B, n_kv, budget), torch.int32)}
