@@ -74,36 +74,13 @@ __device__ __forceinline__ float weight_of(uint32_t key, const float* at) {
 
 struct SelectSmem {
   unsigned int hist[kBins][32];            // [digit][lane]
-  unsigned int total[2][kBins];            // a pass's counts, read by the cluster
+  unsigned int total[2][kMaxCluster][kBins];   // a pass's counts of every CTA, written by it
   unsigned int warp_sum[32];
   unsigned long long wide_sum[kBins / 32];
   // the digit of the key sought: keys above it and at it in the row, and in
   // the parts of the CTAs before this one
   unsigned int digit, above, at, above_before, at_before;
 };
-
-// Inclusive sum of v over the CTA's kThreads threads; *total: the sum of all.
-template <int kThreads>
-__device__ __forceinline__ unsigned int block_scan(unsigned int v, SelectSmem& sm,
-                                                   unsigned int* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const unsigned int n = __shfl_up_sync(0xffffffffu, v, off);
-    if (lane >= off) v += n;
-  }
-  if (lane == 31) sm.warp_sum[warp] = v;
-  __syncthreads();
-  unsigned int s = lane < kThreads / 32 ? sm.warp_sum[lane] : 0u;   // every warp sums the warps
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const unsigned int n = __shfl_up_sync(0xffffffffu, s, off);
-    if (lane >= off) s += n;
-  }
-  *total = __shfl_sync(0xffffffffu, s, 31);
-  const unsigned int base = __shfl_sync(0xffffffffu, s, (warp + 31) & 31);
-  return (warp ? base : 0u) + v;
-}
 
 template <int kThreads>
 __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
@@ -118,6 +95,8 @@ evict_select_kernel(const EvictParams p) {
   const int b = row / p.n_kv;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // the cluster's CTAs write to one another's shared memory: all must have begun
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
   const int len = min(max(p.lens[b], 0), p.C);
@@ -135,9 +114,20 @@ evict_select_kernel(const EvictParams p) {
   // keys of positions from .. from + m - 1 to shared memory; up to the next
   // multiple of four, keys of nothing (0 is a NaN's: they are not counted)
   auto hold = [&](int from, int m) {
-#pragma unroll 4
-    for (int i = tid; i < (m + 3) / 4 * 4; i += kThreads)
-      held[i] = i < m ? order_key(w[from + i]) : 0u;
+    constexpr int kFlight = 16;                  // loads on their way at once
+    for (int i0 = tid; i0 < (m + 3) / 4 * 4; i0 += kFlight * kThreads) {
+      float x[kFlight];
+#pragma unroll
+      for (int e = 0; e < kFlight; ++e) {
+        const int i = i0 + e * kThreads;
+        x[e] = i < m ? w[from + i] : 0.0f;
+      }
+#pragma unroll
+      for (int e = 0; e < kFlight; ++e) {
+        const int i = i0 + e * kThreads;
+        if (i < (m + 3) / 4 * 4) held[i] = i < m ? order_key(x[e]) : 0u;
+      }
+    }
   };
   if (choose && in_smem) hold(lo, n);
   // what lies behind the kept positions, and the recent ones
@@ -149,6 +139,8 @@ evict_select_kernel(const EvictParams p) {
     index[i] = src;
   }
   if (rank == 0 && tid == 0 && row % p.n_kv == 0) p.lens_out[b] = kept;
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
   if (!choose) {
     if (need > 0)                                // all of them stay
       for (int i = lo + tid; i < hi; i += kThreads) {
@@ -188,11 +180,14 @@ evict_select_kernel(const EvictParams p) {
       for (int i = tid; i < n; i += kThreads) count(order_key(w[lo + i]));
     }
     __syncthreads();
+    if (tid < kBins) {
+      // (each thread starts at another lane's counter: all banks at once)
+      unsigned int sum = 0;
 #pragma unroll
-    for (int i = 0; i < kBins / kWarps; ++i) {
-      const int d = warp * (kBins / kWarps) + i;
-      const unsigned int sum = __reduce_add_sync(0xffffffffu, sm.hist[d][lane]);
-      if (lane == 0) sm.total[pass & 1][d] = sum;
+      for (int i = 0; i < 32; ++i) sum += sm.hist[tid][(tid + i) & 31];
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r)
+        if (r < ncta) *cluster.map_shared_rank(&sm.total[pass & 1][rank][tid], r) = sum;
     }
     cluster.sync();
     // digits in descending order, one per thread: counts of the row (low half)
@@ -202,8 +197,7 @@ evict_select_kernel(const EvictParams p) {
       unsigned int all = 0, before = 0;
 #pragma unroll
       for (int r = 0; r < kMaxCluster; ++r) {
-        unsigned int x = 0;
-        if (r < ncta) x = cluster.map_shared_rank(&sm.total[pass & 1][0], r)[kBins - 1 - tid];
+        const unsigned int x = r < ncta ? sm.total[pass & 1][r][kBins - 1 - tid] : 0u;
         all += x;
         before += r < rank ? x : 0u;
       }
@@ -240,8 +234,9 @@ evict_select_kernel(const EvictParams p) {
   // kept: keys above `prefix`, and the first `ties` of those equal to it
   const unsigned int ties = static_cast<unsigned int>(need) - above;
 
-  // in order, a piece of at most kPartSmem positions at a time; a thread takes
-  // a run of an odd number of fours (the lanes' reads then meet all banks)
+  // in order, a piece of at most kPartSmem positions at a time; a warp takes a
+  // run of whole rows of 32. First the warps' counts, then, with those before
+  // it known, each row's kept positions next to each other.
   for (int i0 = 0; i0 < n; i0 += kPartSmem) {
     const int m = min(n - i0, kPartSmem);
     if (!in_smem) {
@@ -249,41 +244,39 @@ evict_select_kernel(const EvictParams p) {
       hold(lo + i0, m);
       __syncthreads();
     }
-    const int run = 4 * (((m + 4 * kThreads - 1) / (4 * kThreads)) | 1);
-    const int r0 = min(tid * run, m), r1 = min(r0 + run, m);
-    unsigned int my_gt = 0, my_eq = 0;
-    for (int i = r0; i < r1; i += 4) {
-      const uint4 key = *reinterpret_cast<const uint4*>(held + i);
-      const uint32_t k[4] = {key.x >> shift, key.y >> shift, key.z >> shift, key.w >> shift};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (i + e >= r1) break;
-        my_gt += k[e] > prefix;
-        my_eq += k[e] == prefix;
-      }
+    const int run = ((m + 31) / 32 + kWarps - 1) / kWarps * 32;
+    const int r0 = min(warp * run, m), r1 = min(r0 + run, m);
+    unsigned int my = 0;                                     // larger | equal << 16
+    for (int i = r0 + lane; i < r1; i += 32) {
+      const uint32_t lead = held[i] >> shift;
+      my += lead > prefix ? 1u : 0u;
+      my += lead == prefix ? 1u << 16 : 0u;
     }
-    unsigned int t;
-    const unsigned int both = my_gt | my_eq << 16;           // a piece has fewer than 2^16
-    const unsigned int s = block_scan<kThreads>(both, sm, &t) - both;    // before this thread
-    unsigned int at_gt = gt + (s & 0xFFFFu), at_eq = eq + (s >> 16);
-    for (int i = r0; i < r1; i += 4) {
-      const uint4 key = *reinterpret_cast<const uint4*>(held + i);
-      const uint32_t k[4] = {key.x, key.y, key.z, key.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (i + e >= r1) break;
-        const uint32_t lead = k[e] >> shift;
-        if (lead > prefix || (lead == prefix && at_eq < ties)) {
-          const unsigned int to = at_gt + min(at_eq, ties);
-          w_out[to] = weight_of(k[e], w + lo + i0 + i + e);
-          index[to] = lo + i0 + i + e;
-        }
-        at_gt += lead > prefix;
-        at_eq += lead == prefix;
+    my = __reduce_add_sync(0xffffffffu, my);                 // a piece has fewer than 2^16
+    if (lane == 0) sm.warp_sum[warp] = my;
+    __syncthreads();
+    const unsigned int ws = lane < kWarps ? sm.warp_sum[lane] : 0u;
+    const unsigned int before = __reduce_add_sync(0xffffffffu, lane < warp ? ws : 0u);
+    const unsigned int all = __reduce_add_sync(0xffffffffu, ws);
+    unsigned int at_gt = gt + (before & 0xFFFFu), at_eq = eq + (before >> 16);
+    const unsigned int lower = (1u << lane) - 1u;
+    for (int i = r0; i < r1; i += 32) {
+      const uint32_t key = i + lane < r1 ? held[i + lane] : 0u;
+      const uint32_t lead = key >> shift;
+      const bool is_gt = i + lane < r1 && lead > prefix, is_eq = i + lane < r1 && lead == prefix;
+      const unsigned int mg = __ballot_sync(0xffffffffu, is_gt), me = __ballot_sync(0xffffffffu, is_eq);
+      const unsigned int my_eq = at_eq + __popc(me & lower);
+      if (is_gt || (is_eq && my_eq < ties)) {
+        const unsigned int to = at_gt + __popc(mg & lower) + min(my_eq, ties);
+        w_out[to] = weight_of(key, w + lo + i0 + i + lane);
+        index[to] = lo + i0 + i + lane;
       }
+      at_gt += __popc(mg);
+      at_eq += __popc(me);
     }
-    gt += t & 0xFFFFu;
-    eq += t >> 16;
+    gt += all & 0xFFFFu;
+    eq += all >> 16;
+    if (!in_smem) __syncthreads();
   }
   cluster.sync();                                // no CTA ends while its counts are read
 }
