@@ -87,6 +87,8 @@ constexpr int kStatusTimeout = 1;
 struct DecodeParams {
   float* part_o;         // fp32 [G * P_max * g, 128] normalised partial outputs
   float* part_lse;       // fp32 [G * P_max * g] partial log-sum-exp (natural log)
+  float2* part_ml;       // ragged step instead: running maximum (log2 units) and sum,
+                         // part_o not normalised
   int* status;           // per-device status word (timeouts)
   int Lk, n_q, n_kv, g;
   int T;                 // key tiles per K/V head
@@ -110,8 +112,8 @@ struct DecodeCtl {
   uint64_t o_done[2], o_free[2], drain;
   uint32_t tmem_base;
   int abort;
-  float red_m[4][kHeadsPad];
-  float red_l[4][kHeadsPad];
+  float4 red_m[kHeadsPad];      // per head, one value per softmax warp
+  float4 red_l[kHeadsPad];
   int start_b, start_u, start_t;    // ragged step: where this CTA's range starts
   long long tiles;                  // and how many tiles it has
 };
@@ -557,21 +559,37 @@ attn_decode_split_kernel(const __grid_constant__ CUtensorMap tmQ,
       tc_fence_before_sync();
       mbar_arrive(smem_addr(&ctl.o_free[num & 1]));
       const float part = reduce_heads<GP>(l_old, [](float a, float b) { return a + b; });
-      if (lane % (32 / GP) == 0) ctl.red_l[warp][lane / (32 / GP)] = part;
+      if (lane % (32 / GP) == 0)
+        reinterpret_cast<float*>(&ctl.red_l[lane / (32 / GP)])[warp] = part;
       bar_softmax();
       const size_t row0 = static_cast<size_t>(old.id) * p.g;
       if (kRagged && r == 0) {
         if (old.t0 == 0) p.ends[2 * old.hd] = cta;
         if (old.t0 + old.n == old.tiles) p.ends[2 * old.hd + 1] = cta;
       }
+      if (kRagged) {
+        // maximum, sum and output as they are: a division and a logarithm per
+        // head would be most of a short segment's time
 #pragma unroll
-      for (int h = 0; h < GP; ++h) {
-        if (h >= p.g) break;
-        const float l = ctl.red_l[0][h] + ctl.red_l[1][h] + ctl.red_l[2][h] + ctl.red_l[3][h];
-        p.part_o[(row0 + h) * kDim + r] = __uint_as_float(ov[h]) / l;
-        if (r == h)
-          p.part_lse[row0 + h] =
-              (m_old[h] + log2f(l)) * (kRagged ? 1.0f : 0.69314718055994530942f);
+        for (int h = 0; h < GP; ++h)
+          if (h < p.g) p.part_o[(row0 + h) * kDim + r] = __uint_as_float(ov[h]);
+        if (warp == 0) {
+#pragma unroll
+          for (int h = 0; h < GP; ++h)
+            if (lane == h && h < p.g) {
+              const float4 w = ctl.red_l[h];
+              p.part_ml[row0 + h] = make_float2(m_old[h], w.x + w.y + w.z + w.w);
+            }
+        }
+      } else {
+#pragma unroll
+        for (int h = 0; h < GP; ++h) {
+          if (h >= p.g) break;
+          const float4 w = ctl.red_l[h];
+          const float l = w.x + w.y + w.z + w.w;
+          p.part_o[(row0 + h) * kDim + r] = __uint_as_float(ov[h]) / l;
+          if (r == h) p.part_lse[row0 + h] = (m_old[h] + log2f(l)) * 0.69314718055994530942f;
+        }
       }
       return true;
     };
@@ -607,22 +625,21 @@ attn_decode_split_kernel(const __grid_constant__ CUtensorMap tmQ,
         if (bar_softmax_any(need)) {
           // exact maximum of this tile per head, then move the running maxima
           const float top = reduce_heads<GP>(x, [](float a, float b) { return fmaxf(a, b); });
-          if (lane % (32 / GP) == 0) ctl.red_m[warp][lane / (32 / GP)] = top;
+          if (lane % (32 / GP) == 0)
+            reinterpret_cast<float*>(&ctl.red_m[lane / (32 / GP)])[warp] = top;
           bar_softmax();
+          // (heads past the group's are computed along: no branch keeps one
+          // head's chain from running beside the others')
           float alpha[GP];
           bool scaled = false;
 #pragma unroll
           for (int h = 0; h < GP; ++h) {
-            alpha[h] = 1.0f;
-            if (h >= p.g) continue;
-            const float tm = fmaxf(fmaxf(ctl.red_m[0][h], ctl.red_m[1][h]),
-                                   fmaxf(ctl.red_m[2][h], ctl.red_m[3][h]));
-            const float mn = fmaxf(m_run[h], tm);
-            if (mn != m_run[h]) {
-              alpha[h] = (m_run[h] == -INFINITY) ? 0.0f : ex2_approx(m_run[h] - mn);
-              m_run[h] = mn;
-              scaled = true;
-            }
+            const float4 w = ctl.red_m[h];
+            const float mn = fmaxf(m_run[h], fmaxf(fmaxf(w.x, w.y), fmaxf(w.z, w.w)));
+            const bool moved = mn != m_run[h];
+            alpha[h] = !moved ? 1.0f : (m_run[h] == -INFINITY) ? 0.0f : ex2_approx(m_run[h] - mn);
+            scaled |= moved;
+            m_run[h] = mn;
             l_thr[h] *= alpha[h];
           }
           if (t > 0 && scaled) {
@@ -649,11 +666,11 @@ attn_decode_split_kernel(const __grid_constant__ CUtensorMap tmQ,
         uint8_t* pb = pgen + (gt & 1) * kPBytes + p_chunk + p_byte;
 #pragma unroll
         for (int h = 0; h < GP; ++h) {
-          if (h >= p.g) break;
           const float e = valid ? ex2_approx(x[h] - m_run[h]) : 0.0f;
           l_thr[h] += e;
-          *reinterpret_cast<uint16_t*>(pb + h * 128 + ((p_unit ^ (h & 7)) << 4)) =
-              static_cast<uint16_t>(pack_bf16x2(e, 0.0f) & 0xFFFFu);
+          if (h < p.g)
+            *reinterpret_cast<uint16_t*>(pb + h * 128 + ((p_unit ^ (h & 7)) << 4)) =
+                static_cast<uint16_t>(pack_bf16x2(e, 0.0f) & 0xFFFFu);
         }
         if (kRagged && (sg.t0 + t + 1) * kKeys > sg.len) {
           // a tile that ends past the sequence: zeros over what V holds there
@@ -778,8 +795,8 @@ attn_decode_combine_kernel(uint16_t* o, float* lse, const DecodeParams p) {
 }
 
 // The ragged step's combine. The first `merges` CTAs merge the segments of
-// eight / kPerRow heads' rows each, segments hd + first .. hd + last CTA, as above
-// (their log-sum-exps are in log2 units): one warp per row where a head has few
+// eight / kPerRow heads' rows each, segments hd + first .. hd + last CTA, through
+// their maxima m and sums l: O = sum_s 2^(m_s - m) O_s / sum_s 2^(m_s - m) l_s: one warp per row where a head has few
 // segments (16384 rows of one or two: 12 us, with eight warps per row 145), eight
 // where it has many. A sequence without a key gets O = 0 and LSE = -inf. With
 // weights, `chunks` CTAs per (b, K/V head) follow, one per kWeightKeys positions:
@@ -824,12 +841,13 @@ attn_decode_ragged_combine_kernel(uint16_t* o, float* lse, float* weights, int m
         x[h][e] = h < p.g && e * 32 * kCombineWarps < n ? sc[h * p.ld + e * 32 * kCombineWarps]
                                                          : -INFINITY;
     for (int h = warp; h < p.g; h += kCombineWarps) {
+      const float2* ml = p.part_ml + (hd + c0) * p.g + h;
       float m = -INFINITY;
-      for (int s = lane; s < ns; s += 32) m = fmaxf(m, p.part_lse[(hd + c0 + s) * p.g + h]);
+      for (int s = lane; s < ns; s += 32) m = fmaxf(m, ml[s * p.g].x);
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
       float w = 0.0f;
-      for (int s = lane; s < ns; s += 32) w += exp2f(p.part_lse[(hd + c0 + s) * p.g + h] - m);
+      for (int s = lane; s < ns; s += 32) w += exp2f(ml[s * p.g].x - m) * ml[s * p.g].y;
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) w += __shfl_xor_sync(0xffffffffu, w, off);
       if (lane == 0) lse2[h] = m + log2f(w);
@@ -863,13 +881,13 @@ attn_decode_ragged_combine_kernel(uint16_t* o, float* lse, float* weights, int m
 #pragma unroll 4
     for (int s = sub; s < ns; s += kPerRow) {
       const size_t sr = static_cast<size_t>((hd + c0 + s) * p.g + r);
-      const float ls = p.part_lse[sr];
+      const float2 ml = p.part_ml[sr];
       const float4 v = *reinterpret_cast<const float4*>(p.part_o + sr * kDim + 4 * lane);
-      const float mn = fmaxf(m, ls);
+      const float mn = fmaxf(m, ml.x);
       const float a = (m == -INFINITY) ? 0.0f : exp2f(m - mn);
-      const float w = exp2f(ls - mn);
+      const float w = exp2f(ml.x - mn);
       m = mn;
-      wsum = fmaf(wsum, a, w);
+      wsum = fmaf(w, ml.y, wsum * a);
       acc.x = fmaf(w, v.x, acc.x * a);
       acc.y = fmaf(w, v.y, acc.y * a);
       acc.z = fmaf(w, v.z, acc.z * a);
@@ -1016,10 +1034,10 @@ DecodeShape decode_shape(int64_t B, int64_t Lk, int32_t n_kv) {
   return s;
 }
 
-// The ragged step's workspace: partial outputs and log-sum-exps of at most
+// The ragged step's workspace: partial outputs, maxima and sums of at most
 // B * n_kv + G segments, the heads' first and last CTAs, and the scores.
 struct RaggedShape {
-  int64_t G, ld, lse_at, ends_at, scores_at, bytes;
+  int64_t G, ld, ml_at, ends_at, scores_at, bytes;
 };
 RaggedShape ragged_shape(int64_t B, int64_t C, int32_t n_q, int32_t n_kv, bool weighted) {
   RaggedShape s;
@@ -1028,8 +1046,8 @@ RaggedShape ragged_shape(int64_t B, int64_t C, int32_t n_q, int32_t n_kv, bool w
   s.ld = T * kKeys;
   const int64_t rows = (B * n_kv + s.G) * (n_q / n_kv);
   auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
-  s.lse_at = up(rows * kDim * 4);
-  s.ends_at = s.lse_at + up(rows * 4);
+  s.ml_at = up(rows * kDim * 4);
+  s.ends_at = s.ml_at + up(rows * 8);
   s.scores_at = s.ends_at + up(B * n_kv * 8);
   s.bytes = s.scores_at + (weighted ? B * n_q * s.ld * 4 : 0);
   return s;
@@ -1055,7 +1073,7 @@ attn_status_t launch_ragged_split(const void* q, const void* k, const void* v, c
   char* ws = static_cast<char*>(workspace);
   DecodeParams p{};
   p.part_o = reinterpret_cast<float*>(ws);
-  p.part_lse = reinterpret_cast<float*>(ws + s.lse_at);
+  p.part_ml = reinterpret_cast<float2*>(ws + s.ml_at);
   p.ends = reinterpret_cast<int*>(ws + s.ends_at);
   p.scores = weighted ? reinterpret_cast<float*>(ws + s.scores_at) : nullptr;
   p.ld = s.ld;
@@ -1106,7 +1124,7 @@ attn_status_t ragged_split_beside(const void* q, const void* k, const void* v, c
   DecodeParams p;
   const attn_status_t st = launch_ragged_split(q, k, v, lens, workspace, B, C, n_q, n_kv, scale,
                                                false, true, stream, status, &p);
-  *parts = {p.part_o, p.part_lse, p.ends};
+  *parts = {p.part_o, p.part_ml, p.ends};
   return st;
 }
 

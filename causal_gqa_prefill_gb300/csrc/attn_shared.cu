@@ -7,7 +7,7 @@
 // rows for every 512 bytes of K and V. (Each sequence reading its own copy would
 // be bound by memory at B times the bytes.) The own positions have g rows per
 // sequence and stay bound by memory; the decode step's ragged split kernel
-// takes them. The two softmaxes are joined through their log-sum-exps.
+// takes them. The two softmaxes are joined through their maxima and sums.
 //
 //   prefix kernel  persistent, one CTA per SM. 128 rows of one K/V head are one
 //                  tile (128 / g sequences, all heads of the group: one TMA box);
@@ -19,9 +19,9 @@
 //                  the two row tiles take turns on the tensor cores. Where a unit
 //                  has one row tile, its two softmax warpgroups take its even and
 //                  its odd key tiles instead, so the turns stay.
-//                  Every segment leaves a normalised fp32 partial output, four
-//                  dimensions of 128 rows at a time (whole 512-byte stores from
-//                  one-row threads), and log-sum-exps.
+//                  Every segment leaves an fp32 partial output, four dimensions of
+//                  128 rows at a time (whole 512-byte stores from one-row
+//                  threads), and its rows' running maxima and sums.
 //   ragged split   (attn_decode.cu) starts on the SMs that the prefix kernel
 //                  leaves free, without waiting for it.
 //   combine        one thread per row and eight dimensions: merges the row's
@@ -61,7 +61,7 @@ constexpr int kPartFloats = kDim * kRows;     // one row tile's partial output
 
 struct Params {
   float* part_o;         // [2 * (units + G)][32][128][4]
-  float* part_lse2;      // [2 * (units + G)][128]
+  float2* part_ml;       // [2 * (units + G)][128] running maximum (log2 units) and sum
   int* status;
   int P, T;              // prefix positions and key tiles
   int B, n_q, n_kv, g;
@@ -326,7 +326,7 @@ __device__ void softmax_role(int slot, Ctl& ctl, const Params& p, uint32_t tmem)
     const int n = sg.count(slot);
     const size_t part = 2 * (static_cast<size_t>(sg.unit) + blockIdx.x) + slot;
     if (n == 0) {
-      p.part_lse2[part * kRows + r] = -INFINITY;
+      p.part_ml[part * kRows + r] = make_float2(-INFINITY, 0.0f);
       continue;
     }
     float m_run = -INFINITY, l_run = 0.0f;
@@ -402,7 +402,6 @@ __device__ void softmax_role(int slot, Ctl& ctl, const Params& p, uint32_t tmem)
     if (!wait_warp(smem_addr(&ctl.o_done[slot]), ph_o, ctl, p)) return;
     ph_o ^= 1;
     tc_fence_after_sync();
-    const float inv = 1.0f / l_run;
     float4* out = reinterpret_cast<float4*>(p.part_o + part * kPartFloats) + r;
 #pragma unroll 1
     for (int q = 0; q < kDim; q += 32) {
@@ -412,11 +411,11 @@ __device__ void softmax_role(int slot, Ctl& ctl, const Params& p, uint32_t tmem)
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         out[(q / 4 + i) * kRows] =
-            make_float4(__uint_as_float(ov[4 * i]) * inv, __uint_as_float(ov[4 * i + 1]) * inv,
-                        __uint_as_float(ov[4 * i + 2]) * inv, __uint_as_float(ov[4 * i + 3]) * inv);
+            make_float4(__uint_as_float(ov[4 * i]), __uint_as_float(ov[4 * i + 1]),
+                        __uint_as_float(ov[4 * i + 2]), __uint_as_float(ov[4 * i + 3]));
     }
     tc_fence_before_sync();
-    p.part_lse2[part * kRows + r] = m_run + log2f(l_run);
+    p.part_ml[part * kRows + r] = make_float2(m_run, l_run);
   }
 }
 
@@ -510,13 +509,13 @@ shared_combine_kernel(uint16_t* o, float* lse, const int* lens, int C,
   float m = -INFINITY, wsum = 0.0f;
   float4 acc[2];
   acc[0] = acc[1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  auto add = [&](float ls, const float4& u, const float4& v) {
-    if (ls == -INFINITY) return;                          // an empty part: u, v are not written
-    const float mn = fmaxf(m, ls);
+  auto add = [&](const float2& ml, const float4& u, const float4& v) {
+    if (ml.x == -INFINITY) return;                        // an empty part: u, v are not written
+    const float mn = fmaxf(m, ml.x);
     const float a = (m == -INFINITY) ? 0.0f : exp2f(m - mn);
-    const float w = exp2f(ls - mn);
+    const float w = exp2f(ml.x - mn);
     m = mn;
-    wsum = fmaf(wsum, a, w);
+    wsum = fmaf(w, ml.y, wsum * a);
     acc[0].x = fmaf(w, u.x, acc[0].x * a);
     acc[0].y = fmaf(w, u.y, acc[0].y * a);
     acc[0].z = fmaf(w, u.z, acc[0].z * a);
@@ -539,20 +538,20 @@ shared_combine_kernel(uint16_t* o, float* lse, const int* lens, int C,
   const int count = (c1 - c0 + 1) * slots;
   constexpr int kBatch = 4;              // partials on their way at once
   for (int e0 = 0; e0 < count; e0 += kBatch) {
-    float ls[kBatch];
+    float2 ml[kBatch];
     float4 u[kBatch], v[kBatch];
 #pragma unroll
     for (int e = 0; e < kBatch; ++e) {
-      ls[e] = -INFINITY;
+      ml[e] = make_float2(-INFINITY, 0.0f);
       if (e0 + e < count) {
         const size_t at = first + static_cast<size_t>(e0 + e) * step;
-        ls[e] = p.part_lse2[at * kRows + r];
+        ml[e] = p.part_ml[at * kRows + r];
         u[e] = part[at * (kPartFloats / 4)];
         v[e] = part[at * (kPartFloats / 4) + kRows];
       }
     }
 #pragma unroll
-    for (int e = 0; e < kBatch; ++e) add(ls[e], u[e], v[e]);
+    for (int e = 0; e < kBatch; ++e) add(ml[e], u[e], v[e]);
   }
   if (min(lens[b], C) > 0) {
     const size_t hd = static_cast<size_t>(b) * p.n_kv + kvh;
@@ -560,7 +559,7 @@ shared_combine_kernel(uint16_t* o, float* lse, const int* lens, int C,
     for (int c = e0; c <= e1; ++c) {
       const size_t row = (hd + c) * p.g + h;
       const float4* src = reinterpret_cast<const float4*>(own.o) + row * 32 + d4;
-      add(own.lse2[row], src[0], src[1]);
+      add(own.ml[row], src[0], src[1]);
     }
   }
   const float inv = 1.0f / wsum;
@@ -633,7 +632,7 @@ bool encode(CUtensorMap* map, const void* ptr, int H, int64_t L, int heads, int 
 }
 
 struct Shape {
-  int64_t nb, tiles, pairs, units, T, W, G, lse_at, own_at, own, bytes;
+  int64_t nb, tiles, pairs, units, T, W, G, ml_at, own_at, own, bytes;
 };
 
 // False where a size is beyond the kernels' limits.
@@ -649,8 +648,8 @@ bool shape_of(int64_t B, int64_t P, int64_t C, int32_t n_q, int32_t n_kv, int32_
   s->G = s->W < kCtas ? s->W : kCtas;
   const int64_t parts = 2 * (s->units + s->G);
   auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
-  s->lse_at = up(parts * kPartFloats * 4);
-  s->own_at = s->lse_at + up(parts * kRows * 4);
+  s->ml_at = up(parts * kPartFloats * 4);
+  s->own_at = s->ml_at + up(parts * kRows * 8);
   s->bytes = s->own_at + s->own;
   return s->units <= (int64_t{1} << 30) && s->W <= (int64_t{1} << 40) &&
          s->tiles * n_kv * (kRows / kCombineRows) <= INT32_MAX;
@@ -697,7 +696,7 @@ attn_status_t attn_decode_shared_fwd(const void* q, const void* prefix_k, const 
   Params p{};
   char* ws = static_cast<char*>(workspace);
   p.part_o = reinterpret_cast<float*>(ws);
-  p.part_lse2 = reinterpret_cast<float*>(ws + s.lse_at);
+  p.part_ml = reinterpret_cast<float2*>(ws + s.ml_at);
   p.status = status;
   p.P = static_cast<int>(P);
   p.T = static_cast<int>(s.T);

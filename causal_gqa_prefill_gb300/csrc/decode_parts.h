@@ -12,11 +12,12 @@ namespace gb300_host {
 
 // Partial results of the ragged split kernel: for K/V head hd (= b * n_kv + u)
 // of a sequence with lens[b] > 0 keys, segments hd + c for the CTAs
-// c = ends[2 hd] .. ends[2 hd + 1], each with g rows: normalised outputs
-// [row][128] and log-sum-exps in log2 units.
+// c = ends[2 hd] .. ends[2 hd + 1], each with g rows: the running maximum m
+// (log2 units), the sum l of 2^(score - m) and the output [row][128] not yet
+// divided by it.
 struct RaggedParts {
   const float* o;
-  const float* lse2;
+  const float2* ml;
   const int* ends;
 };
 
