@@ -13,7 +13,7 @@
 // the 64 sums of a warp's 32 rows folded (62 shuffles) and the four warps' added.
 // (With the keys on the lanes a column sum needs no folding at all, but then
 // every score takes its row's lse2 from shared memory, whose reads queue behind
-// the exponentials: 2130 clocks a step against MEASURED_STEP.)
+// the exponentials: 2130 clocks a step against 1750 here.)
 //
 //   rows     packed: a step holds nr = 128 / g consecutive query rows of all g
 //            heads of the group (lane = row * g + head, which is what one TMA box
@@ -32,9 +32,15 @@
 //
 // S is double-buffered (all 512 TMEM columns), so the product of a step runs
 // under the exponentials of the one before; both take 1024 clocks a step, the
-// exponentials at 32 a clock and SM. K is fetched a unit ahead, and where a
-// head's steps fit the Q ring they stay there from unit to unit (a prompt's last
-// rows against a long cache: K is then all that is read).
+// exponentials at 32 a clock and SM. Measured, 8192-token 32-head layer: 200 us;
+// 147 without any sums (both operands come from shared memory, and the next Q
+// tile arrives in it), 167 with everything but the exponentials: what is left is
+// the latency of load, exponential and addition, which four warps a scheduler
+// and 32 scores at a time cover only in part (16 at a time: 214).
+//
+// K is fetched a unit ahead, and where a head's steps fit the Q ring they stay
+// there from unit to unit (a prompt's last rows against a long cache: K is then
+// all that is read).
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -62,8 +68,8 @@ constexpr int kSumWarps = 4 * kGroups;
 constexpr int kThreads = 32 * kSumWarps + 128;
 constexpr int kLoadWarp = kSumWarps, kMmaWarp = kSumWarps + 1, kStatWarp = kSumWarps + 2;
 constexpr int kFold = kCols / 32;     // keys per lane once the rows are folded
-// registers per thread: the sums of 64 keys, and their scores 16 at a time
-constexpr int kSumRegs = 104, kOtherRegs = 64;
+// registers per thread: the sums of 64 keys, and their scores 32 at a time
+constexpr int kSumRegs = 112, kOtherRegs = 32;
 constexpr int kLaunchRegs = 96;
 constexpr int kRegBudget = 32 * kSumWarps * kSumRegs + 128 * kOtherRegs;
 static_assert(kRegBudget <= kThreads * kLaunchRegs, "setmaxnreg split exceeds the launch allocation");
@@ -211,11 +217,11 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, const 
     if (static_cast<long long>(clock64_now() - t0) > p.spin_limit) return;
 }
 
-// acc += 2^(c s + nl) for the 16 keys whose scores are in s, two at a time.
-__device__ __forceinline__ void add_weights(uint64_t* acc, const uint32_t (&s)[16], uint64_t c2,
+// acc += 2^(c s + nl) for the 32 keys whose scores are in s, two at a time.
+__device__ __forceinline__ void add_weights(uint64_t* acc, const uint32_t (&s)[32], uint64_t c2,
                                             uint64_t nl2) {
 #pragma unroll
-  for (int i = 0; i < 16; i += 2) {
+  for (int i = 0; i < 32; i += 2) {
     float x0, x1;
     f32x2_unpack(ffma2(f32x2_pack(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), c2, nl2), x0, x1);
     const uint64_t e = f32x2_pack(ex2_approx(x0), ex2_approx(x1));
@@ -273,25 +279,25 @@ __device__ void sum_role(Ctl& ctl, const Params& p, const Starts& starts, uint32
         const float nl = ctl.nl[buf][r];
         const uint64_t nl2 = f32x2_pack(nl, nl);
         const uint32_t taddr = lanes + kUnitKeys * buf;
-        uint32_t s[16];
+        uint32_t s[32];
         if (st >= until) {
 #pragma unroll
-          for (int q = 0; q < kCols / 16; ++q) {
-            tmem_ld16(taddr + 16 * q, s);
-            tmem_wait_ld16(s);
-            add_weights(acc + 8 * q, s, c2, nl2);
+          for (int q = 0; q < kCols / 32; ++q) {
+            tmem_ld32(taddr + 32 * q, s);
+            tmem_wait_ld(s);
+            add_weights(acc + 16 * q, s, c2, nl2);
           }
         } else {
           // this row's position sees key0 + i for i <= keep
           const int keep = p.off + st * p.nr + row - key0;
 #pragma unroll
-          for (int q = 0; q < kCols / 16; ++q) {
-            tmem_ld16(taddr + 16 * q, s);
-            tmem_wait_ld16(s);
+          for (int q = 0; q < kCols / 32; ++q) {
+            tmem_ld32(taddr + 32 * q, s);
+            tmem_wait_ld(s);
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (16 * q + i > keep) s[i] = hidden;
-            add_weights(acc + 8 * q, s, c2, nl2);
+            for (int i = 0; i < 32; ++i)
+              if (32 * q + i > keep) s[i] = hidden;
+            add_weights(acc + 16 * q, s, c2, nl2);
           }
         }
         tc_fence_before_sync();
