@@ -824,22 +824,27 @@ attn_decode_ragged_combine_kernel(uint16_t* o, float* lse, float* weights, int m
   const long long row = static_cast<long long>(blockIdx.x) * kRows + warp / kPerRow;   // b * n_q + h
   const bool live = !merge || row < static_cast<long long>(p.B) * p.n_q;
   const long long hd = merge ? (live ? row / p.g : 0) : rest / chunks;
+  // (both loads at once: a head without keys has no ends, what is there is not used)
+  const int2 ends = reinterpret_cast<const int2*>(p.ends)[hd];
   const int len = clamp_len(p.lens[hd / p.n_kv], p.Lk);
-  const long long c0 = len > 0 ? p.ends[2 * hd] : 0;
-  const int ns = len > 0 ? static_cast<int>(p.ends[2 * hd + 1] - c0 + 1) : 0;
+  const long long c0 = len > 0 ? ends.x : 0;
+  const int ns = len > 0 ? ends.y - ends.x + 1 : 0;
 
   if (!merge) {
-    const int j0 = static_cast<int>(rest - hd * chunks) * kWeightKeys;
-    if (j0 >= len) return;
-    const float* sc = p.scores + hd * p.g * p.ld + j0 + threadIdx.x;
-    const int n = len - j0 - static_cast<int>(threadIdx.x);   // position e is live while e * 256 < n
-    float x[kWeightAhead][kWeightPer];
+    const int first = static_cast<int>(rest - hd * chunks) * kWeightKeys, j0 = first + threadIdx.x;
+    if (first >= len) return;
+    const float* sc = p.scores + hd * p.g * p.ld + j0;
+    float* out = weights + hd * p.Lk + j0;
+    const int n = len - j0;                       // position e is live while e * 256 < n
+    float x[kWeightAhead][kWeightPer], old[kWeightPer];
 #pragma unroll
-    for (int h = 0; h < kWeightAhead; ++h)
+    for (int e = 0; e < kWeightPer; ++e) {
+      const int at = e * 32 * kCombineWarps;
 #pragma unroll
-      for (int e = 0; e < kWeightPer; ++e)
-        x[h][e] = h < p.g && e * 32 * kCombineWarps < n ? sc[h * p.ld + e * 32 * kCombineWarps]
-                                                         : -INFINITY;
+      for (int h = 0; h < kWeightAhead; ++h)
+        x[h][e] = h < p.g && at < n ? sc[h * p.ld + at] : -INFINITY;
+      old[e] = at < n ? out[at] : 0.0f;
+    }
     for (int h = warp; h < p.g; h += kCombineWarps) {
       const float2* ml = p.part_ml + (hd + c0) * p.g + h;
       float m = -INFINITY;
@@ -867,10 +872,9 @@ attn_decode_ragged_combine_kernel(uint16_t* o, float* lse, float* weights, int m
         if (e * 32 * kCombineWarps < n)
           sum[e] += ex2_approx(sc[h * p.ld + e * 32 * kCombineWarps] - lse2[h]);
     }
-    float* out = weights + hd * p.Lk + j0 + threadIdx.x;
 #pragma unroll
     for (int e = 0; e < kWeightPer; ++e)
-      if (e * 32 * kCombineWarps < n) out[e * 32 * kCombineWarps] += sum[e];
+      if (e * 32 * kCombineWarps < n) out[e * 32 * kCombineWarps] = old[e] + sum[e];
     return;
   }
 

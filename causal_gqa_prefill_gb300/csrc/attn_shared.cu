@@ -506,6 +506,11 @@ shared_combine_kernel(uint16_t* o, float* lse, const int* lens, int C,
   if (r >= p.nb * p.g || b >= p.B) return;
   const int d4 = 2 * (blockIdx.y * kCombineWarps + (threadIdx.x >> 5));   // first of two
 
+  // where the own positions' partials are, on its way from the start
+  const size_t hd = static_cast<size_t>(b) * p.n_kv + kvh;
+  const int2 ends = reinterpret_cast<const int2*>(own.ends)[hd];
+  const int own_len = min(lens[b], C);
+
   float m = -INFINITY, wsum = 0.0f;
   float4 acc[2];
   acc[0] = acc[1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -553,10 +558,8 @@ shared_combine_kernel(uint16_t* o, float* lse, const int* lens, int C,
 #pragma unroll
     for (int e = 0; e < kBatch; ++e) add(ml[e], u[e], v[e]);
   }
-  if (min(lens[b], C) > 0) {
-    const size_t hd = static_cast<size_t>(b) * p.n_kv + kvh;
-    const int e0 = own.ends[2 * hd], e1 = own.ends[2 * hd + 1];
-    for (int c = e0; c <= e1; ++c) {
+  if (own_len > 0) {
+    for (int c = ends.x; c <= ends.y; ++c) {
       const size_t row = (hd + c) * p.g + h;
       const float4* src = reinterpret_cast<const float4*>(own.o) + row * 32 + d4;
       add(own.ml[row], src[0], src[1]);
