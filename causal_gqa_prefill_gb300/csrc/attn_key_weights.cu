@@ -185,8 +185,9 @@ __device__ __forceinline__ bool seen(const Params& p, int key, int step) {
   return !p.causal || key <= last + p.off;
 }
 
-__device__ __forceinline__ bool spin_wait(uint32_t bar, uint32_t parity, Ctl& ctl,
-                                          const Params& p) {
+// (for both kernels' control blocks and parameters)
+template <typename C, typename P>
+__device__ __forceinline__ bool spin_wait(uint32_t bar, uint32_t parity, C& ctl, const P& p) {
   if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = clock64_now();
   while (true) {
@@ -200,18 +201,20 @@ __device__ __forceinline__ bool spin_wait(uint32_t bar, uint32_t parity, Ctl& ct
   }
 }
 
-__device__ __forceinline__ bool wait_slowly(uint32_t bar, uint32_t parity, Ctl& ctl, const Params& p) {
+template <typename C, typename P>
+__device__ __forceinline__ bool wait_slowly(uint32_t bar, uint32_t parity, C& ctl, const P& p) {
   return __all_sync(0xffffffffu, spin_wait(bar, parity, ctl, p));
 }
 
-__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, Ctl& ctl,
-                                          const Params& p) {
+template <typename C, typename P>
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, C& ctl, const P& p) {
   if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
   return wait_slowly(bar, parity, ctl, p);
 }
 
 // Wait used while draining after an abort: ignores the abort flag.
-__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, const Params& p) {
+template <typename P>
+__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, const P& p) {
   const uint64_t t0 = clock64_now();
   while (!mbar_try_wait(bar, parity))
     if (static_cast<long long>(clock64_now() - t0) > p.spin_limit) return;
@@ -617,6 +620,342 @@ key_weights_reduce_kernel(const __grid_constant__ Params p, const __grid_constan
   *out = p.accumulate ? *out + sum : sum;
 }
 
+// ------------------------------------------------------------- few rows
+//
+// Where all rows of a head's group fit one tile of at most 256 columns
+// (Lq * g <= 256: a prompt's last rows against a long cache), the step is a
+// stream of K, and the tiles turn round: S^T = K Q^T with 128 keys on the TMEM
+// lanes and every row of the group as a column. A thread owns a key, its sum is
+// complete after one tile, and nothing has to be folded or cut; the rows and
+// their -lse2 stay in shared memory for as long as the head stays the same.
+// (The kernel above spends about as long folding 128 rows into one as on a
+// unit's two steps: 32 rows of 6 heads against 131072 keys of 6 K/V heads, 70 us
+// there and 42 here; K alone is 30 us at the measured copy rate.)
+//
+// The key tiles of all heads are cut into equal ranges, one per CTA. Two S^T
+// buffers of 256 columns; of the four warpgroups two take each buffer's tiles,
+// half of the columns each, and the second hands its sums to the first.
+
+constexpr int kWinKeys = 128, kWinCols = 256;
+
+template <int D>
+struct WinGeometry {
+  static constexpr int kChunks = D * 2 / 128;
+  static constexpr int kTileBytes = kWinKeys * D * 2;
+  static constexpr int kChunkBytes = kWinKeys * 128;
+  static constexpr int kQBytes = kWinCols * D * 2;          // one buffer of 256 rows, or two of 128
+  static constexpr int kRing = D == 128 ? 5 : 10;
+  static constexpr int kTilesBytes = kQBytes + kRing * kTileBytes;
+};
+
+struct __align__(16) WinCtl {
+  uint64_t k_full[10], k_empty[10];
+  uint64_t q_full[2], q_empty[2], n_full[2], n_empty[2];
+  uint64_t s_full[2], s_free[2], half_full[2], half_free[2];
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort;
+  __align__(16) float nl[kWinCols];      // -lse2 of the Q buffers' columns
+  float half_sum[2][kWinKeys];
+};
+constexpr int kWinCtlBytes = (sizeof(WinCtl) + 1023) / 1024 * 1024;    // then the tiles
+template <int D>
+__host__ __device__ constexpr int win_smem_bytes() {
+  return kWinCtlBytes + WinGeometry<D>::kTilesBytes;
+}
+static_assert(win_smem_bytes<128>() <= 232448 && win_smem_bytes<64>() <= 232448, "shared memory");
+
+struct WinParams {
+  const float* lse;
+  float* weights;
+  int* status;
+  int Lq, Lk, off, n_q, n_kv, g;
+  int cols, chunks;      // Lq * g, and 32-column pieces
+  int bufs;              // Q buffers: 2 where cols <= 128
+  int T;                 // key tiles per (b, K/V head)
+  long long W;           // B * n_kv * T
+  int causal, accumulate;
+  float c;
+  long long spin_limit;
+};
+
+// Key tiles [t0, t0 + n) of head = b * n_kv + kvh.
+struct WinSegment {
+  int head, t0, n;
+};
+
+struct WinWalk {
+  const WinParams& p;
+  long long x, end;
+  __device__ explicit WinWalk(const WinParams& params) : p(params) {
+    x = blockIdx.x * params.W / gridDim.x;
+    end = (blockIdx.x + 1ll) * params.W / gridDim.x;
+  }
+  __device__ bool next(WinSegment& s) {
+    if (x >= end) return false;
+    s.head = static_cast<int>(x / p.T);
+    const long long first = static_cast<long long>(s.head) * p.T;
+    s.t0 = static_cast<int>(x - first);
+    s.n = static_cast<int>((end - first < p.T ? end - first : p.T) - s.t0);
+    x += s.n;
+    return true;
+  }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+key_weights_few_rows_kernel(const __grid_constant__ CUtensorMap tmQ,
+                            const __grid_constant__ CUtensorMap tmK,
+                            const __grid_constant__ WinParams p) {
+  using G = WinGeometry<D>;
+  extern __shared__ __align__(1024) uint8_t dyn_smem[];
+  WinCtl& ctl = *reinterpret_cast<WinCtl*>(dyn_smem);
+  const uint32_t start = smem_addr(dyn_smem);
+  const uint32_t base = (start + static_cast<uint32_t>(sizeof(WinCtl)) + 1023u) & ~1023u;
+  if (base + G::kTilesBytes > start + win_smem_bytes<D>()) {     // as in the kernel above
+    if (threadIdx.x == 0) atomicOr(p.status, kStatusCheck);
+    return;
+  }
+  const uint32_t sQ = base, sK = base + G::kQBytes;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rows_per_buf = kWinCols / p.bufs;
+  const uint32_t q_chunk = rows_per_buf * 128, q_buf = G::kChunks * q_chunk;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < G::kRing; ++s) {
+      mbar_init(smem_addr(&ctl.k_full[s]), 1);
+      mbar_init(smem_addr(&ctl.k_empty[s]), 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(smem_addr(&ctl.q_full[s]), 1);
+      mbar_init(smem_addr(&ctl.q_empty[s]), 1);
+      mbar_init(smem_addr(&ctl.n_full[s]), 1);
+      mbar_init(smem_addr(&ctl.n_empty[s]), kSumWarps);
+      mbar_init(smem_addr(&ctl.s_full[s]), 1);
+      mbar_init(smem_addr(&ctl.s_free[s]), 8);
+      mbar_init(smem_addr(&ctl.half_full[s]), 4);
+      mbar_init(smem_addr(&ctl.half_free[s]), 4);
+    }
+    mbar_init(smem_addr(&ctl.drain), 1);
+    ctl.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == kLoadWarp && lane == 0) {
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmK);
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_addr(&ctl.tmem_base), kTmemCols);
+    tmem_relinquish();
+  }
+  if (warp < kSumWarps) {
+    // columns past Lq * g are never loaded: zeros, so that their scores are 0
+    uint4* z = reinterpret_cast<uint4*>(dyn_smem + (sQ - start));
+    for (int i = threadIdx.x; i < G::kQBytes / 16; i += 32 * kSumWarps)
+      z[i] = make_uint4(0u, 0u, 0u, 0u);
+    fence_proxy_async_smem();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = ctl.tmem_base;
+  // programmatic dependent of the kernel before it: set-up overlaps that
+  // kernel, global memory is touched only after it has completed
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+
+  WinWalk walk(p);
+  WinSegment sg;
+  uint32_t seg = 0, it = 0;          // segments and key tiles so far
+  if (warp == kLoadWarp) {
+    if (lane == 0) {
+      bool ok = true;
+      const uint32_t q_bytes = static_cast<uint32_t>(G::kChunks * 128 * p.cols);
+      while (ok && walk.next(sg)) {
+        const int b = sg.head / p.n_kv, kvh = sg.head - b * p.n_kv;
+        const uint32_t qb = seg % p.bufs, use = seg / p.bufs;
+        if (use > 0 && !spin_wait(smem_addr(&ctl.q_empty[qb]), (use - 1) & 1, ctl, p)) {
+          ok = false;
+          break;
+        }
+        const uint32_t qbar = smem_addr(&ctl.q_full[qb]);
+        mbar_arrive_expect_tx(qbar, q_bytes);
+        for (int ch = 0; ch < G::kChunks; ++ch)
+          tma_load_4d(sQ + qb * q_buf + ch * q_chunk, &tmQ, qbar, ch * 64, kvh * p.g, 0, b);
+        ++seg;
+        for (int t = 0; t < sg.n; ++t, ++it) {
+          const uint32_t slot = it % G::kRing, u = it / G::kRing;
+          if (u > 0 && !spin_wait(smem_addr(&ctl.k_empty[slot]), (u - 1) & 1, ctl, p)) {
+            ok = false;
+            break;
+          }
+          const uint32_t bar = smem_addr(&ctl.k_full[slot]);
+          mbar_arrive_expect_tx(bar, G::kTileBytes);
+          for (int ch = 0; ch < G::kChunks; ++ch)
+            tma_load_4d(sK + slot * G::kTileBytes + ch * G::kChunkBytes, &tmK, bar, ch * 64, kvh,
+                        (sg.t0 + t) * kWinKeys, b);
+        }
+      }
+      if (!ok) {
+        // let every copy this thread started land before the CTA can exit
+        for (uint32_t q = 0; q < static_cast<uint32_t>(p.bufs) && q < seg; ++q)
+          drain_wait(smem_addr(&ctl.q_full[q]), ((seg - 1 - q) / p.bufs) & 1, p);
+        for (uint32_t s = 0; s < G::kRing && s < it; ++s)
+          drain_wait(smem_addr(&ctl.k_full[s]), ((it - 1 - s) / G::kRing) & 1, p);
+      }
+    }
+  } else if (warp == kMmaWarp) {
+    const bool leader = elect_one();
+    const uint32_t idesc = idesc_bf16_f32(kWinKeys, 32 * p.chunks, false);
+    bool ok = true;
+    while (ok && walk.next(sg)) {
+      const uint32_t qb = seg % p.bufs;
+      if (!wait_warp(smem_addr(&ctl.q_full[qb]), (seg / p.bufs) & 1, ctl, p)) break;
+      ++seg;
+      const uint64_t q0 = sdesc_sw128(sQ + qb * q_buf, 16, 1024);
+      for (int t = 0; t < sg.n; ++t, ++it) {
+        const uint32_t slot = it % G::kRing, buf = it & 1;
+        if (!wait_warp(smem_addr(&ctl.k_full[slot]), (it / G::kRing) & 1, ctl, p) ||
+            (it >= 2 && !wait_warp(smem_addr(&ctl.s_free[buf]), ((it >> 1) - 1) & 1, ctl, p))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after_sync();
+        const uint64_t k0 = sdesc_sw128(sK + slot * G::kTileBytes, 16, 1024);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t ko = ((kk >> 2) * G::kChunkBytes + (kk & 3) * 32) >> 4;
+          const uint32_t qo = ((kk >> 2) * q_chunk + (kk & 3) * 32) >> 4;
+          if (leader) mma_ss(tmem + kWinCols * buf, k0 + ko, q0 + qo, idesc, kk > 0 ? 1u : 0u);
+        }
+        if (leader) mma_commit(smem_addr(&ctl.s_full[buf]));
+        if (leader) mma_commit(smem_addr(&ctl.k_empty[slot]));
+      }
+      if (leader && ok) mma_commit(smem_addr(&ctl.q_empty[qb]));
+    }
+    // no MMA may still be running when TMEM is released
+    if (leader) mma_commit(smem_addr(&ctl.drain));
+    drain_wait(smem_addr(&ctl.drain), 0, p);
+    __syncwarp();
+  } else if (warp == kStatWarp) {
+    while (walk.next(sg)) {
+      const int b = sg.head / p.n_kv, kvh = sg.head - b * p.n_kv;
+      const uint32_t qb = seg % p.bufs, use = seg / p.bufs;
+      const float* lse = p.lse + (static_cast<size_t>(b) * p.n_q + kvh * p.g) * p.Lq;
+      float l[kWinCols / 32];
+#pragma unroll
+      for (int m = 0; m < kWinCols / 32; ++m) {
+        const int col = lane + 32 * m, i = col / p.g;
+        l[m] = col < p.cols ? lse[static_cast<size_t>(col - i * p.g) * p.Lq + i] : -INFINITY;
+      }
+      if (use > 0 && !wait_warp(smem_addr(&ctl.n_empty[qb]), (use - 1) & 1, ctl, p)) break;
+      // a row without keys, like a column without a row, has no weight
+#pragma unroll
+      for (int m = 0; m < kWinCols / 32; ++m)
+        if (lane + 32 * m < rows_per_buf)
+          ctl.nl[qb * rows_per_buf + lane + 32 * m] =
+              l[m] == -INFINITY ? -INFINITY : -l[m] * kLog2e;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&ctl.n_full[qb]));
+      ++seg;
+    }
+  } else if (warp < kSumWarps) {
+    const int buf = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3;
+    const int r = quarter * 32 + lane;                     // key of the tile = TMEM lane
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + kWinCols * buf;
+    const uint64_t c2 = f32x2_pack(p.c, p.c);
+    const int split = (p.chunks + 1) / 2;                  // 32-column pieces of the first half
+    const int c_from = half ? split : 0, c_to = half ? p.chunks : split;
+    bool ok = true;
+    while (ok && walk.next(sg)) {
+      const uint32_t qb = seg % p.bufs;
+      if (!wait_warp(smem_addr(&ctl.n_full[qb]), (seg / p.bufs) & 1, ctl, p)) break;
+      ++seg;
+      const float* nl_buf = ctl.nl + qb * rows_per_buf;
+      for (int t = 0; t < sg.n; ++t, ++it) {
+        if ((it & 1) != static_cast<uint32_t>(buf)) continue;
+        const uint32_t turn = it >> 1;                     // of this buffer
+        if (!wait_warp(smem_addr(&ctl.s_full[buf]), turn & 1, ctl, p)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after_sync();
+        const int key0 = (sg.t0 + t) * kWinKeys, key = key0 + r;
+        const bool mask = p.causal && key0 + kWinKeys - 1 > p.off;
+        const int from = (key - p.off) * p.g;              // columns before it do not see the key
+        uint64_t a0 = f32x2_pack(0.0f, 0.0f), a1 = a0;
+        for (int ch = c_from; ch < c_to; ++ch) {
+          uint32_t s[32];
+          tmem_ld32(lanes + 32 * ch, s);
+          tmem_wait_ld(s);
+          if (ch == c_to - 1) {
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&ctl.s_free[buf]));
+          }
+          const float* nl = nl_buf + 32 * ch;
+#pragma unroll
+          for (int i = 0; i < 32; i += 4) {
+            const float4 l = *reinterpret_cast<const float4*>(nl + i);
+            float x0, x1, x2, x3;
+            f32x2_unpack(ffma2(f32x2_pack(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), c2,
+                               f32x2_pack(l.x, l.y)), x0, x1);
+            f32x2_unpack(ffma2(f32x2_pack(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3])), c2,
+                               f32x2_pack(l.z, l.w)), x2, x3);
+            float e0 = ex2_approx(x0), e1 = ex2_approx(x1), e2 = ex2_approx(x2), e3 = ex2_approx(x3);
+            if (mask) {
+              const int col = 32 * ch + i;
+              if (col < from) e0 = 0.0f;
+              if (col + 1 < from) e1 = 0.0f;
+              if (col + 2 < from) e2 = 0.0f;
+              if (col + 3 < from) e3 = 0.0f;
+            }
+            a0 = fadd2(a0, f32x2_pack(e0, e1));
+            a1 = fadd2(a1, f32x2_pack(e2, e3));
+          }
+        }
+        if (c_from == c_to) {                              // a single piece: nothing for this half
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_addr(&ctl.s_free[buf]));
+        }
+        float lo, hi;
+        f32x2_unpack(fadd2(a0, a1), lo, hi);
+        float sum = lo + hi;
+        if (half == 1) {
+          if (turn > 0 && !wait_warp(smem_addr(&ctl.half_free[buf]), (turn - 1) & 1, ctl, p)) {
+            ok = false;
+            break;
+          }
+          ctl.half_sum[buf][r] = sum;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_addr(&ctl.half_full[buf]));
+        } else {
+          float* out = p.weights + static_cast<size_t>(sg.head) * p.Lk + key;
+          const float old = p.accumulate && key < p.Lk ? *out : 0.0f;
+          if (!wait_warp(smem_addr(&ctl.half_full[buf]), turn & 1, ctl, p)) {
+            ok = false;
+            break;
+          }
+          sum += ctl.half_sum[buf][r];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_addr(&ctl.half_free[buf]));
+          if (key < p.Lk) *out = p.accumulate ? old + sum : sum;
+        }
+      }
+      if (!ok) break;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&ctl.n_empty[qb]));
+    }
+  }
+
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                                    const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
                                    const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
@@ -635,7 +974,10 @@ bool configure() {
       fa.numRegs * kThreads < kRegBudget)
     return false;
   return cudaFuncSetAttribute(key_weights_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              smem_bytes<D>()) == cudaSuccess;
+                              smem_bytes<D>()) == cudaSuccess &&
+         cudaFuncSetAttribute(key_weights_few_rows_kernel<D>,
+                              cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              win_smem_bytes<D>()) == cudaSuccess;
 }
 
 attn_status_t weights_device_ready(cudaStream_t stream, int** status) {
@@ -721,6 +1063,53 @@ bool supported(int64_t B, int64_t Lq, int64_t Lk, int32_t n_q, int32_t n_kv, int
          units * steps / kCtas < INT32_MAX / 2 && Lk * (n_q / n_kv) <= INT32_MAX;
 }
 
+attn_status_t launch_few_rows(const void* q, const void* k, const float* lse, float* weights,
+                              int* status, int64_t B, int64_t Lq, int64_t Lk, int32_t n_q,
+                              int32_t n_kv, int32_t d_h, int32_t causal, int32_t accumulate,
+                              float scale, cudaStream_t stream) {
+  WinParams p{};
+  p.lse = lse;
+  p.weights = weights;
+  p.status = status;
+  p.Lq = static_cast<int>(Lq);
+  p.Lk = static_cast<int>(Lk);
+  p.off = static_cast<int>(Lk - Lq);
+  p.n_q = n_q;
+  p.n_kv = n_kv;
+  p.g = n_q / n_kv;
+  p.cols = p.Lq * p.g;
+  p.chunks = (p.cols + 31) / 32;
+  p.bufs = p.cols <= kWinCols / 2 ? 2 : 1;
+  p.T = static_cast<int>((Lk + kWinKeys - 1) / kWinKeys);
+  p.W = B * n_kv * p.T;
+  p.causal = causal;
+  p.accumulate = accumulate;
+  p.c = scale * kLog2e;
+  p.spin_limit = 1ll << 31;   // about a second at 2 GHz
+  CUtensorMap mq, mk;
+  if (!encode(&mq, q, d_h, n_q, Lq, B, p.g, p.Lq) || !encode(&mk, k, d_h, n_kv, Lk, B, 1, kWinKeys))
+    return ATTN_ERR_CUDA;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.W < kCtas ? p.W : kCtas));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e;
+  if (d_h == 128) {
+    cfg.dynamicSmemBytes = win_smem_bytes<128>();
+    e = cudaLaunchKernelEx(&cfg, key_weights_few_rows_kernel<128>, mq, mk, p);
+  } else {
+    cfg.dynamicSmemBytes = win_smem_bytes<64>();
+    e = cudaLaunchKernelEx(&cfg, key_weights_few_rows_kernel<64>, mq, mk, p);
+  }
+  if (e != cudaSuccess) return ATTN_ERR_CUDA;
+  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
 bool sizes_ok(int64_t B, int64_t Lq, int64_t Lk, int32_t n_q, int32_t n_kv, int32_t d_h) {
   return B >= 1 && Lq >= 1 && Lk >= Lq && n_q >= 1 && n_kv >= 1 && n_q % n_kv == 0 && d_h >= 1;
 }
@@ -758,6 +1147,9 @@ attn_status_t attn_key_weights_fwd(const void* q, const void* k, const float* ls
   const attn_status_t ds = weights_device_ready(stream, &status);
   if (ds != ATTN_OK) return ds;
 
+  if (Lq * (n_q / n_kv) <= kWinCols)
+    return launch_few_rows(q, k, lse, weights, status, B, Lq, Lk, n_q, n_kv, d_h, causal, accumulate,
+                           scale, stream);
   Params p{};
   p.lse = lse;
   p.weights = weights;

@@ -75,6 +75,15 @@ CASES = [
     (2, 128, 640, 12, 4, 128),
     (4, 33, 65, 2, 1, 128),
     (40, 20, 200, 2, 2, 64),           # more units than CTAs
+    # up to 256 columns (rows x heads of a group): one tile for all of them
+    (1, 64, 900, 8, 2, 128),           # 256
+    (2, 32, 1300, 8, 2, 64),           # 128: two Q buffers
+    (1, 43, 700, 6, 1, 128),           # 258: one too many
+    (3, 33, 40, 4, 1, 128),            # 132, most keys hidden from most rows
+    (1, 2, 130, 128, 1, 64),           # 256 of two rows
+    (7, 5, 1000, 35, 5, 128),          # 35, heads change inside CTAs' ranges
+    (1, 256, 256, 1, 1, 128),
+    (30, 3, 64, 8, 8, 64),             # a tile a head, 240 heads
     (1, 1500, 1501, 2, 1, 128),
 ]
 
@@ -136,6 +145,22 @@ def test_hidden_values_do_not_leak():
     w = attn_key_weights(bad, k, lse)
     assert torch.isnan(w[0, 1, :101]).all() and not torch.isnan(w[0, 1, 101:]).any()
     assert torch.equal(w[0, 0], good[0, 0])
+
+
+def test_hidden_values_do_not_leak_from_few_rows():
+    q, k, lse = inputs(1, 30, 400, 4, 2, 128, True, seed=7)
+    good = attn_key_weights(q, k, lse)
+    bad = k.clone()
+    bad[0, 385, 0] = float("nan")
+    w = attn_key_weights(q, bad, lse)
+    assert torch.isnan(w).nonzero().tolist() == [[0, 0, 385]]
+    bad = q.clone()
+    bad[0, 10, 3] = float("inf")                    # a row at position 380
+    w = attn_key_weights(bad, k, lse)
+    assert not torch.isfinite(w[0, 1, :381]).any() and torch.equal(w[0, 1, 381:], good[0, 1, 381:])
+    assert torch.equal(w[0, 0], good[0, 0])
+    lse[0, 1, 7] = lse[0, 2, 20:] = -float("inf")   # rows without keys
+    check(q, k, lse, attn_key_weights(q, k, lse))
 
 
 def test_long_prompt_against_the_row_sums():
