@@ -846,13 +846,15 @@ attn_decode_ragged_combine_kernel(uint16_t* o, float* lse, float* weights, int m
       old[e] = at < n ? out[at] : 0.0f;
     }
     for (int h = warp; h < p.g; h += kCombineWarps) {
+      // (a lane's first segment stays in registers: there is rarely a second)
       const float2* ml = p.part_ml + (hd + c0) * p.g + h;
-      float m = -INFINITY;
-      for (int s = lane; s < ns; s += 32) m = fmaxf(m, ml[s * p.g].x);
+      const float2 own = lane < ns ? ml[lane * p.g] : make_float2(-INFINITY, 0.0f);
+      float m = own.x;
+      for (int s = lane + 32; s < ns; s += 32) m = fmaxf(m, ml[s * p.g].x);
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-      float w = 0.0f;
-      for (int s = lane; s < ns; s += 32) w += exp2f(ml[s * p.g].x - m) * ml[s * p.g].y;
+      float w = exp2f(own.x - m) * own.y;
+      for (int s = lane + 32; s < ns; s += 32) w += exp2f(ml[s * p.g].x - m) * ml[s * p.g].y;
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) w += __shfl_xor_sync(0xffffffffu, w, off);
       if (lane == 0) lse2[h] = m + log2f(w);
