@@ -399,6 +399,7 @@ __device__ void load_role(const CUtensorMap* tmQ, const CUtensorMap* tmK, Ctl& c
                           const Starts& starts, uint32_t sK, uint32_t sQ, bool stay) {
   using G = Geometry<D>;
   uint32_t qn = 0, kn = 0, gn = 0;         // Q steps, K buffers and heads issued
+  int begun = 0;                           // steps issued of a head that a wait cut short
   const uint32_t q_bytes = static_cast<uint32_t>(G::kChunks * 128 * p.g * p.nr);
   auto load_k = [&](const Segment& s) {
     const uint32_t kb = kn & 1;
@@ -435,8 +436,11 @@ __device__ void load_role(const CUtensorMap* tmQ, const CUtensorMap* tmK, Ctl& c
     if (stay) {
       if (sg.head == head) continue;
       head = sg.head;
-      for (int i = 0; i < p.steps && ok; ++i) ok = load_q(sg, i, i, gn);
-      if (ok) ++gn;
+      for (begun = 0; begun < p.steps && (ok = load_q(sg, begun, begun, gn)); ++begun) {
+      }
+      if (!ok) break;
+      begun = 0;
+      ++gn;
     } else {
       for (int i = 0; i < sg.n && ok; ++i) {
         ok = load_q(sg, sg.s0 + i, qn % G::kQStages, qn / G::kQStages);
@@ -445,17 +449,14 @@ __device__ void load_role(const CUtensorMap* tmQ, const CUtensorMap* tmK, Ctl& c
     }
   }
   if (!ok) {
-    // let every copy this thread started land before the CTA can exit: each
-    // barrier is waited for in its last phase, and in the one before, which
-    // covers a round of loads that was cut short
+    // let every copy this thread started land before the CTA can exit: the last
+    // use of each buffer
     for (uint32_t s = 0; s < 2 && s < kn; ++s)
       drain_wait(smem_addr(&ctl.k_full[s]), ((kn - 1 - s) >> 1) & 1, p);
     for (int s = 0; s < G::kQStages; ++s) {
-      if (stay) {
-        if (s < p.steps && gn > 0) drain_wait(smem_addr(&ctl.q_full[s]), (gn - 1) & 1, p);
-      } else if (static_cast<uint32_t>(s) < qn) {
-        drain_wait(smem_addr(&ctl.q_full[s]), ((qn - 1 - s) / G::kQStages) & 1, p);
-      }
+      const uint32_t uses = stay ? (s < p.steps ? gn + (s < begun ? 1u : 0u) : 0u)
+                                 : (qn + G::kQStages - 1 - s) / G::kQStages;
+      if (uses > 0) drain_wait(smem_addr(&ctl.q_full[s]), (uses - 1) & 1, p);
     }
   }
 }
