@@ -135,6 +135,13 @@ __host__ __device__ __forceinline__ int first_step(int t, int off, int nr, int c
                             : 0;
 }
 
+// First row of a step. The last one ends with the last row, so that every row of
+// the tile is one (a zero row's product with an infinite key is NaN); the rows
+// that the step before has too count there. (Lq > nr: else few rows, below.)
+__device__ __forceinline__ int first_row(int step, const Params& p) {
+  return min(step * p.nr, p.Lq - p.nr);
+}
+
 struct Segment {
   int head, b, kvh, key0, s0, n;   // head = b * n_kv + kvh
   bool first, whole;               // the range's first segment; a unit that nothing cuts
@@ -266,10 +273,12 @@ __device__ void sum_role(Ctl& ctl, const Params& p, const Starts& starts, uint32
     const int past = p.causal ? key0 - p.off : 0;
     int from = past > 0 ? static_cast<int>(static_cast<unsigned>(past) / static_cast<unsigned>(p.nr)) : 0;
     if (key0 >= p.Lk) from = p.steps;
-    const int until =
+    int until =
         p.causal && past + kCols - 1 > 0
             ? static_cast<int>(static_cast<unsigned>(past + kCols - 2 + p.nr) / static_cast<unsigned>(p.nr))
             : 0;
+    // (nor do the rows that the last step has a second time)
+    if (until == p.steps - 1 && past + kCols - 1 > p.Lq - p.nr) until = p.steps;
     uint64_t acc[kCols / 2];
 #pragma unroll
     for (int i = 0; i < kCols / 2; ++i) acc[i] = f32x2_pack(0.0f, 0.0f);
@@ -292,7 +301,7 @@ __device__ void sum_role(Ctl& ctl, const Params& p, const Starts& starts, uint32
           }
         } else {
           // this row's position sees key0 + i for i <= keep
-          const int keep = p.off + st * p.nr + row - key0;
+          const int keep = p.off + first_row(st, p) + row - key0;
 #pragma unroll
           for (int q = 0; q < kCols / 32; ++q) {
             tmem_ld32(taddr + 32 * q, s);
@@ -312,7 +321,10 @@ __device__ void sum_role(Ctl& ctl, const Params& p, const Starts& starts, uint32
     // to warp 0
     float v[kCols];
 #pragma unroll
-    for (int i = 0; i < kCols / 2; ++i) f32x2_unpack(acc[i], v[2 * i], v[2 * i + 1]);
+    for (int i = 0; i < kCols / 2; ++i) {
+      if (row >= p.nr) acc[i] = f32x2_pack(0.0f, 0.0f);   // a lane without rows
+      f32x2_unpack(acc[i], v[2 * i], v[2 * i + 1]);
+    }
     fold_lanes(v);
     if (quarter == 3) {
       if (seg > 0 && !wait_warp(smem_addr(&ctl.fold_free[group]), (seg - 1) & 1, ctl, p)) return;
@@ -352,24 +364,26 @@ __device__ void stat_role(Ctl& ctl, const Params& p, const Starts& starts) {
 #pragma unroll
   for (int m = 0; m < 4; ++m) {
     const int r = lane + 32 * m;
-    row[m] = r < p.nr * p.g ? r / p.g : p.Lq;            // past the last row: none
+    row[m] = r / p.g;                                    // (nr and more: none)
     at[m] = (r % p.g) * p.Lq + row[m];
   }
   Walk walk(p, starts, blockIdx.x);
   Segment sg;
-  int left = 0, i0 = 0;
+  int left = 0, step = 0;
   const float* lse = nullptr;
   auto fetch = [&](float (&v)[4]) {
     if (left == 0) {
       if (!walk.next(sg)) return false;
       left = sg.n;
-      i0 = sg.s0 * p.nr;
+      step = sg.s0;
       lse = p.lse + (static_cast<size_t>(sg.b) * p.n_q + sg.kvh * p.g) * p.Lq;
     }
+    const int from = first_row(step, p), again = step * p.nr - from;   // rows of the step before
 #pragma unroll
-    for (int m = 0; m < 4; ++m) v[m] = row[m] < p.Lq - i0 ? lse[at[m] + i0] : -INFINITY;
+    for (int m = 0; m < 4; ++m)
+      v[m] = row[m] < p.nr && row[m] >= again ? lse[at[m] + from] : -INFINITY;
     --left;
-    i0 += p.nr;
+    ++step;
     return true;
   };
   float l[kAhead][4];
@@ -418,7 +432,7 @@ __device__ void load_role(const CUtensorMap* tmQ, const CUtensorMap* tmK, Ctl& c
     mbar_arrive_expect_tx(bar, q_bytes);
     for (int ch = 0; ch < G::kChunks; ++ch)
       tma_load_4d(sQ + slot * G::kQBytes + ch * G::kQChunk, tmQ, bar, ch * 64, s.kvh * p.g,
-                  step * p.nr, s.b);
+                  first_row(step, p), s.b);
     return true;
   };
   Walk walk(p, starts, blockIdx.x);
@@ -882,8 +896,11 @@ key_weights_few_rows_kernel(const __grid_constant__ CUtensorMap tmQ,
         }
         tc_fence_after_sync();
         const int key0 = (sg.t0 + t) * kWinKeys, key = key0 + r;
-        const bool mask = p.causal && key0 + kWinKeys - 1 > p.off;
-        const int from = (key - p.off) * p.g;              // columns before it do not see the key
+        // columns before `from` do not see the key; those past Lq * g are zeros,
+        // and their scores NaN where the key is infinite
+        const bool mask = (p.causal && key0 + kWinKeys - 1 > p.off) || p.cols % 32 != 0;
+        const int from = p.causal ? max((key - p.off) * p.g, 0) : 0;
+        const unsigned int seen = max(p.cols - from, 0);
         uint64_t a0 = f32x2_pack(0.0f, 0.0f), a1 = a0;
         for (int ch = c_from; ch < c_to; ++ch) {
           uint32_t s[32];
@@ -905,11 +922,11 @@ key_weights_few_rows_kernel(const __grid_constant__ CUtensorMap tmQ,
                                f32x2_pack(l.z, l.w)), x2, x3);
             float e0 = ex2_approx(x0), e1 = ex2_approx(x1), e2 = ex2_approx(x2), e3 = ex2_approx(x3);
             if (mask) {
-              const int col = 32 * ch + i;
-              if (col < from) e0 = 0.0f;
-              if (col + 1 < from) e1 = 0.0f;
-              if (col + 2 < from) e2 = 0.0f;
-              if (col + 3 < from) e3 = 0.0f;
+              const int col = 32 * ch + i - from;
+              if (static_cast<unsigned int>(col) >= seen) e0 = 0.0f;
+              if (static_cast<unsigned int>(col + 1) >= seen) e1 = 0.0f;
+              if (static_cast<unsigned int>(col + 2) >= seen) e2 = 0.0f;
+              if (static_cast<unsigned int>(col + 3) >= seen) e3 = 0.0f;
             }
             a0 = fadd2(a0, f32x2_pack(e0, e1));
             a1 = fadd2(a1, f32x2_pack(e2, e3));

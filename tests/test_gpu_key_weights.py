@@ -163,6 +163,22 @@ def test_hidden_values_do_not_leak_from_few_rows():
     check(q, k, lse, attn_key_weights(q, k, lse))
 
 
+@pytest.mark.parametrize("Lq,n_q,d", [(300, 4, 128), (301, 6, 64), (300, 10, 128), (30, 4, 128), (7, 6, 64)])
+def test_a_key_of_weight_zero(Lq, n_q, d):
+    """A key whose every score is -inf has weight 0 and changes no other, also where
+    a tile has rows that are none (0 * inf)."""
+    q, k, lse = inputs(1, Lq, 400, n_q, 2, d, True, seed=Lq)
+    q[..., 0] = q[..., 0].abs() + 0.125
+    good = attn_key_weights(q, k, lse)
+    for j in (37, 390, 399):
+        bad = k.clone()
+        bad[0, j, :, 0] = -float("inf")
+        w = attn_key_weights(q, bad, lse)
+        assert (w[..., j] == 0).all(), j
+        w[..., j] = good[..., j]
+        assert torch.equal(w, good), j
+
+
 def test_long_prompt_against_the_row_sums():
     """L = 8192 of the 32-head layer: sampled keys in 64 bits, and the total."""
     w = W.WORKLOADS[3]
