@@ -169,7 +169,8 @@ class _Call:
             handle = stream if isinstance(stream, int) else stream.cuda_stream
             if handle != self.handle:
                 self.handle = handle
-                self.other = torch.cuda.ExternalStream(handle, device=device)
+                self.other = (torch.cuda.ExternalStream(handle, device=device) if handle
+                              else torch.cuda.default_stream(device))
 
     def __enter__(self):
         if self.guard is not None:
@@ -181,11 +182,16 @@ class _Call:
             self.guard.__exit__(*exc)
 
     def empty(self, shape, dtype):
-        """Memory for the call; on another stream than the current one it is not
-        handed out again before that stream is done with it."""
-        t = self.torch.empty(shape, dtype=dtype, device=self.device)
-        if self.other is not None:
-            t.record_stream(self.other)
+        """Memory for the call. On another stream than the current one it is that
+        stream's (the current one may still be at work on memory of its own that
+        was freed), and is not handed out again before the current stream is done
+        with it either."""
+        if self.other is None:
+            return self.torch.empty(shape, dtype=dtype, device=self.device)
+        current = self.torch.cuda.current_stream(self.device)
+        with self.torch.cuda.stream(self.other):
+            t = self.torch.empty(shape, dtype=dtype, device=self.device)
+        t.record_stream(current)
         return t
 
     def workspace(self, given, size, *sizes):
@@ -462,7 +468,7 @@ def attn_evict(k, v, weights, lens, budget, recent=0, *, capacity=None, k_out=No
     if budget < 1 or not 0 <= recent <= budget:
         raise ValueError("budget must be at least 1 and recent between 0 and budget")
     if capacity is None:
-        capacity = budget if k_out is None or k_out.dim() != 4 else k_out.shape[1]
+        capacity = budget if getattr(k_out, "ndim", 0) != 4 else k_out.shape[1]
     if capacity < budget:
         raise ValueError("the new capacity must hold the budget")
     wanted = {"k_out": (k_out, (B, capacity, n_kv, d), kind),

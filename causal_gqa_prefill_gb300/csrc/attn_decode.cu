@@ -547,7 +547,7 @@ attn_decode_split_kernel(const __grid_constant__ CUtensorMap tmQ,
     // The segment before, finished but for its output: its product is still
     // running when its last P is written, so its output waits until this
     // segment's first P is under way.
-    Segment old;
+    Segment old{};
     float m_old[GP], l_old[GP];
     bool pending = false;
     // O^T / l and the log-sum-exp of segment number `num`
@@ -666,7 +666,9 @@ attn_decode_split_kernel(const __grid_constant__ CUtensorMap tmQ,
         uint8_t* pb = pgen + (gt & 1) * kPBytes + p_chunk + p_byte;
 #pragma unroll
         for (int h = 0; h < GP; ++h) {
-          const float e = valid ? ex2_approx(x[h] - m_run[h]) : 0.0f;
+          // (infinite keys can leave a ragged head's tiles without a finite score)
+          const float m_use = kRagged && m_run[h] == -INFINITY ? 0.0f : m_run[h];
+          const float e = valid ? ex2_approx(x[h] - m_use) : 0.0f;
           l_thr[h] += e;
           if (h < p.g)
             *reinterpret_cast<uint16_t*>(pb + h * 128 + ((p_unit ^ (h & 7)) << 4)) =
@@ -891,7 +893,7 @@ attn_decode_ragged_combine_kernel(uint16_t* o, float* lse, float* weights, int m
       const float4 v = *reinterpret_cast<const float4*>(p.part_o + sr * kDim + 4 * lane);
       const float mn = fmaxf(m, ml.x);
       const float a = (m == -INFINITY) ? 0.0f : exp2f(m - mn);
-      const float w = exp2f(ml.x - mn);
+      const float w = (ml.x == -INFINITY) ? 0.0f : exp2f(ml.x - mn);
       m = mn;
       wsum = fmaf(w, ml.y, wsum * a);
       acc.x = fmaf(w, v.x, acc.x * a);

@@ -165,6 +165,46 @@ def test_cache_past_2_to_the_31_elements():
     torch.cuda.empty_cache()
 
 
+@pytest.mark.parametrize("n_q", [2, 8, 24])
+def test_a_tile_without_a_finite_score(n_q):
+    """Keys whose scores are all -inf have weight 0, also where they are all that a
+    tile or a range holds: as if the sequence ended before them."""
+    q, k, v, lens, acc = make(2, 700, n_q, 2, [600, 129], seed=11, junk=False)
+    q[..., 0] = q[..., 0].abs() + 0.125
+    k[0, 256:, :, 0] = k[1, 128:, :, 0] = -float("inf")
+    before = acc.clone()
+    o, lse = attn_decode_ragged(q, k, v, lens, weights=acc)
+    short = torch.tensor([256, 128], dtype=torch.int32, device="cuda")
+    check(q, k, v, short, before, o, lse, acc)
+    assert attn_device_check() == ATTN_OK
+
+
+def test_memory_of_another_stream():
+    """What a call on another stream allocates is not memory that the current
+    stream was given and may still be at work on."""
+    q, k, v, lens, acc = make(4, 3000, 8, 2, [3000, 17, 0, 2222], seed=7)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    nbytes = attn_decode_ragged_workspace_bytes(4, 3000, 8, 2)
+    mine = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in (nbytes, q.nbytes, 512)]
+    spans = [(x.untyped_storage().data_ptr(), x.nbytes) for x in mine]
+    del mine
+    side = torch.cuda.Stream()
+    want = attn_decode_ragged(q, k, v, lens)
+    torch.cuda.synchronize()
+    for stream in (side, side.cuda_stream):
+        got = attn_decode_ragged(q, k, v, lens, stream=stream)
+        torch.cuda.synchronize()
+        for x, y in zip(got, want):
+            assert torch.equal(x.view(torch.int16), y.view(torch.int16))
+            assert all(not at <= x.data_ptr() < at + n for at, n in spans)
+    with torch.cuda.stream(side):                  # the default stream by its handle
+        got = attn_decode_ragged(q, k, v, lens, stream=0)
+    torch.cuda.synchronize()
+    for x, y in zip(got, want):
+        assert torch.equal(x.view(torch.int16), y.view(torch.int16))
+
+
 def test_refusals():
     q, k, v, lens, acc = make(2, 64, 8, 2, [3, 4], seed=1)
     with pytest.raises(ValueError):
