@@ -24,7 +24,8 @@
 //                 thread per key; the running maximum moves lazily, so the
 //                 cross-thread maximum is only taken when a score exceeds it
 //                 by the threshold). It writes the segment's normalised partial
-//                 output and log-sum-exp to the workspace. Both the scores
+//                 output and log-sum-exp to the workspace (the ragged step: its
+//                 maximum, sum and undivided output). Both the scores
 //                 of the next tile and the output of the segment before run
 //                 across segment borders (two O^T accumulators), so many short
 //                 segments go at the pace of one long one.
@@ -43,7 +44,10 @@
 // With weights, the split kernel also writes the scores (4 g bytes per
 // position and K/V head beside the 512 of K and V), and CTAs of the combine
 // turn them into softmax weights once the row's log-sum-exp is known, summed
-// over the group's heads.
+// over the group's heads. Measured: 16 sequences of 1024 to 8192 positions, 32
+// heads on 8, with weights 60 us (302 MB of K and V; split 56, combine 8 when
+// timed one by one), one of 131072, 36 heads on 6, 67 us (403 MB, 6.0 TB/s): the
+// stream of K and V bounds both, and the combine's latency is what is left.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -797,10 +801,10 @@ attn_decode_combine_kernel(uint16_t* o, float* lse, const DecodeParams p) {
 }
 
 // The ragged step's combine. The first `merges` CTAs merge the segments of
-// eight / kPerRow heads' rows each, segments hd + first .. hd + last CTA, through
-// their maxima m and sums l: O = sum_s 2^(m_s - m) O_s / sum_s 2^(m_s - m) l_s: one warp per row where a head has few
-// segments (16384 rows of one or two: 12 us, with eight warps per row 145), eight
-// where it has many. A sequence without a key gets O = 0 and LSE = -inf. With
+// eight / kPerRow rows (of one head each), segments hd + first .. hd + last CTA,
+// through their maxima m and sums l:
+//   O = sum_s 2^(m_s - m) O_s / sum_s 2^(m_s - m) l_s.
+// A sequence without a key gets O = 0 and LSE = -inf. With
 // weights, `chunks` CTAs per (b, K/V head) follow, one per kWeightKeys positions:
 // each rebuilds the log-sum-exps of the group's heads and adds
 //   sum_h 2^(score_hj - lse2_h)
@@ -1252,7 +1256,10 @@ attn_status_t attn_decode_ragged_fwd(const void* q, const void* k, const void* v
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  // segments per head: one, and one more for every range border inside it
+  // segments per head: one, and one more for every range border inside it. Eight
+  // warps per row where a head has more than nine on average (a whole step with 8
+  // heads of 152: 17 us, 41 with one warp; 32 of 20: 48, 51; 64 of 10: 86, 87), one
+  // where it has fewer (the combine of 16384 rows of one or two: 12, 145 with eight)
   const bool many = p.G > 8 * B * n_kv;
   const int64_t merges = many ? B * n_q : (B * n_q + kCombineWarps - 1) / kCombineWarps;
   cfg.gridDim = dim3(static_cast<unsigned>(merges + B * n_kv * chunks));

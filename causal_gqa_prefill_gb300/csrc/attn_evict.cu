@@ -18,11 +18,15 @@
 //           CTA counts into 32 histograms, one per lane, whose counters lie in
 //           the lane's own bank: weights crowd into a few exponents, and with one
 //           histogram the atomics on its few busy counters took most of the time
-//           (39 us of a call for 6 rows of 131072; 19 now). The cluster's
-//           counts are summed through distributed shared memory. A last pass
-//           compacts the kept positions in order and writes index and weight.
+//           (39 us of a call for 6 rows of 131072). The cluster's counts are
+//           summed through distributed shared memory. A last pass compacts the
+//           kept positions in order and writes index and weight. Bound by the
+//           latency of its steps: of 16 us for 128 rows of up to 8192, some
+//           1.5 to 2.5 us a pass go to the counters' sums, the cluster's barrier
+//           and the scan, 0.4 to the counting.
 //   gather  copies the kept K and V rows, in the order of the destination, 16
-//           bytes a lane; it is what the call's bytes are.
+//           bytes a lane; it is what the call's bytes are: 259 MB in 41 us (6.3
+//           TB/s, 93 % of a copy's) for 16 sequences of 8 heads brought to 2048.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -416,6 +420,9 @@ extern "C" attn_status_t attn_cache_evict(const void* k, const void* v, const fl
   if (ds != ATTN_OK) return ds;
 
   const int64_t rows = B * n_kv;
+  // CTAs per row while two fit an SM and each has 4096 positions: few long rows
+  // need them (the selection among 6 rows of 131072: 96, 55, 29 and 22 us with 1, 2,
+  // 4 and 8, no less with 16), for 128 rows of 8192 one or two are the same (21)
   int cluster = 1;
   while (cluster < kMaxCluster && rows * cluster * 2 <= 2 * kSms && C >= 4096 * 2 * cluster)
     cluster *= 2;
@@ -440,8 +447,11 @@ extern "C" attn_status_t attn_cache_evict(const void* k, const void* v, const fl
   attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(rows * cluster));
-  // more CTAs than SMs: two of 512 threads to an SM
-  const bool wide = rows * cluster <= kSms;
+  // 1024 threads to a CTA, or two CTAs of 512 to an SM where there are more CTAs
+  // than SMs (512 rows of 2048: 31 us, 40 with 1024) or so many large clusters that
+  // some would wait for eight free SMs side by side (16 rows of 131072: 33, 40);
+  // else 1024 are as fast or faster (64 rows of 8192: 16, 18)
+  const bool wide = rows * cluster <= (cluster < 4 ? kSms : kSms / 2);
   cfg.blockDim = dim3(wide ? 1024 : 512);
   cfg.dynamicSmemBytes = static_cast<size_t>(p.part <= kPartSmem ? (p.part + 3) / 4 * 4 : kPartSmem) * 4;
   cfg.stream = stream;

@@ -32,8 +32,8 @@
 //
 // S is double-buffered (all 512 TMEM columns), so the product of a step runs
 // under the exponentials of the one before; both take 1024 clocks a step, the
-// exponentials at 32 a clock and SM. Measured, 8192-token 32-head layer: 200 us;
-// 147 without any sums (both operands come from shared memory, and the next Q
+// exponentials at 32 a clock and SM. Measured, 8192-token 32-head layer: 202 us,
+// both pipes busy 60 % of it; 147 without any sums (both operands come from shared memory, and the next Q
 // tile arrives in it), 167 with everything but the exponentials: what is left is
 // the latency of load, exponential and addition, which four warps a scheduler
 // and 32 scores at a time cover only in part (16 at a time: 214).
@@ -645,7 +645,7 @@ key_weights_reduce_kernel(const __grid_constant__ Params p, const __grid_constan
 // their -lse2 stay in shared memory for as long as the head stays the same.
 // (The kernel above spends about as long folding 128 rows into one as on a
 // unit's two steps: 32 rows of 6 heads against 131072 keys of 6 K/V heads, 70 us
-// there and 42 here; K alone is 30 us at the measured copy rate.)
+// there and 43 here; K alone is 30 us at the measured copy rate.)
 //
 // The key tiles of all heads are cut into equal ranges, one per CTA. Two S^T
 // buffers of 256 columns; of the four warpgroups two take each buffer's tiles,
