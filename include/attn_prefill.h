@@ -1,7 +1,8 @@
 /*
  * attn_prefill.h — C ABI of the GB300 (sm_103a) causal GQA prefill attention:
  * the forward pass (square and chunked, bf16 and fp8), decode, the backward
- * pass and two diagnostics.
+ * pass, the cache operators (key weights, ragged decode, decode behind a shared
+ * prefix, eviction) and diagnostics.
  *
  * Operation (one call computes, for every batch b, query head h and row i):
  *
@@ -70,9 +71,11 @@ typedef enum {
   ATTN_ERR_TIMEOUT = 4,      /* a kernel wait ran past its limit (reported by
                                 attn_device_check); outputs of that launch are
                                 undefined */
-  ATTN_ERR_CHECK = 5         /* a device-side consistency check failed (only the
-                                library built with ATTN_DEBUG runs them; reported
-                                by attn_device_check); outputs undefined */
+  ATTN_ERR_CHECK = 5         /* a device-side consistency check failed (run by the
+                                library built with ATTN_DEBUG, and by the key
+                                weights' kernels, whether their shared memory
+                                fits; reported by attn_device_check); outputs
+                                undefined */
 } attn_status_t;
 
 /*
