@@ -13,7 +13,7 @@
 // the 64 sums of a warp's 32 rows folded (62 shuffles) and the four warps' added.
 // (With the keys on the lanes a column sum needs no folding at all, but then
 // every score takes its row's lse2 from shared memory, whose reads queue behind
-// the exponentials: 2130 clocks a step against 1750 here.)
+// the exponentials: 2130 clocks a step against 1600 here.)
 //
 //   rows     packed: a step holds nr = 128 / g consecutive query rows of all g
 //            heads of the group (lane = row * g + head, which is what one TMA box
@@ -32,11 +32,12 @@
 //
 // S is double-buffered (all 512 TMEM columns), so the product of a step runs
 // under the exponentials of the one before; both take 1024 clocks a step, the
-// exponentials at 32 a clock and SM. Measured, 8192-token 32-head layer: 202 us,
-// both pipes busy 60 % of it; 147 without any sums (both operands come from shared memory, and the next Q
-// tile arrives in it), 167 with everything but the exponentials: what is left is
-// the latency of load, exponential and addition, which four warps a scheduler
-// and 32 scores at a time cover only in part (16 at a time: 214).
+// exponentials at 32 a clock and SM. Measured, 8192-token 32-head layer: 186 us,
+// both pipes busy 65 % of it. Without any sums it is 147: both operands come from
+// shared memory and the next Q tile arrives in it, which fills its bandwidth (two
+// products of 128 keys, which read the rows twice: 198). The rest is the latency of
+// load, exponential and addition, which four warps a scheduler and 32 scores at a
+// time cover in part (16 at a time: 196).
 //
 // K is fetched a unit ahead, and where a head's steps fit the Q ring they stay
 // there from unit to unit (a prompt's last rows against a long cache: K is then
@@ -263,6 +264,14 @@ __device__ void sum_role(Ctl& ctl, const Params& p, const Starts& starts, uint32
   const uint64_t c2 = f32x2_pack(p.c, p.c);
   const uint32_t hidden = p.c > 0.0f ? 0xff800000u : 0x7f800000u;   // c * hidden = -inf
   const int row = r / p.g;
+  // a buffer is free once its last scores are in registers, before they are
+  // summed: the next product starts half a step earlier, and a warp that is ahead
+  // finds its scores (released after the sums: 203 us)
+  auto release = [&](uint32_t buf) {
+    tc_fence_before_sync();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_addr(&ctl.s_free[buf]));
+  };
   Walk walk(p, starts, blockIdx.x);
   Segment sg;
   uint32_t n = 0, seg = 0;
@@ -297,6 +306,7 @@ __device__ void sum_role(Ctl& ctl, const Params& p, const Starts& starts, uint32
           for (int q = 0; q < kCols / 32; ++q) {
             tmem_ld32(taddr + 32 * q, s);
             tmem_wait_ld(s);
+            if (q == kCols / 32 - 1) release(buf);
             add_weights(acc + 16 * q, s, c2, nl2);
           }
         } else {
@@ -306,16 +316,16 @@ __device__ void sum_role(Ctl& ctl, const Params& p, const Starts& starts, uint32
           for (int q = 0; q < kCols / 32; ++q) {
             tmem_ld32(taddr + 32 * q, s);
             tmem_wait_ld(s);
+            if (q == kCols / 32 - 1) release(buf);
 #pragma unroll
             for (int i = 0; i < 32; ++i)
               if (32 * q + i > keep) s[i] = hidden;
             add_weights(acc + 16 * q, s, c2, nl2);
           }
         }
-        tc_fence_before_sync();
-        __syncwarp();
+      } else {
+        release(buf);
       }
-      if (lane == 0) mbar_arrive(smem_addr(&ctl.s_free[buf]));
     }
     // fold the rows: over the warp's lanes, then from warp 3 of the warpgroup
     // to warp 0
@@ -496,6 +506,9 @@ __device__ void mma_role(Ctl& ctl, const Params& p, const Starts& starts, uint32
       const uint32_t slot = stay ? sg.s0 + i : qn % G::kQStages;
       const uint32_t use = stay ? gn : qn / G::kQStages;
       const uint32_t buf = qn & 1;
+      // keys that no row of the step sees are not computed, 128 at a time
+      const uint32_t idesc =
+          seen(p, sg.key0 + kUnitKeys / 2, sg.s0 + i) ? kIdWide : kIdHalf;
       if (!wait_warp(smem_addr(&ctl.q_full[slot]), use & 1, ctl, p) ||
           (qn >= 2 && !wait_warp(smem_addr(&ctl.s_free[buf]), ((qn >> 1) - 1) & 1, ctl, p))) {
         ok = false;
@@ -503,9 +516,6 @@ __device__ void mma_role(Ctl& ctl, const Params& p, const Starts& starts, uint32
       }
       tc_fence_after_sync();
       const uint64_t q0 = sdesc_sw128(sQ + slot * G::kQBytes, 16, 1024);
-      // keys that no row of the step sees are not computed, 128 at a time
-      const uint32_t idesc =
-          seen(p, sg.key0 + kUnitKeys / 2, sg.s0 + i) ? kIdWide : kIdHalf;
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         const uint32_t qo = ((kk >> 2) * G::kQChunk + (kk & 3) * 32) >> 4;
