@@ -14,7 +14,8 @@
 //   select  one cluster of 1 to 8 CTAs per (b, u), each with its part of the row
 //           in shared memory. A radix select over the weights' order-preserving
 //           integer keys, 8 bits a pass, finds the (N - R)-th largest key; it
-//           ends early when a pass leaves exactly the keys that are needed. A
+//           ends early when a pass leaves exactly the keys that are needed, or
+//           few enough to compare with one another. A
 //           CTA counts into 32 histograms, one per lane, whose counters lie in
 //           the lane's own bank: weights crowd into a few exponents, and with one
 //           histogram the atomics on its few busy counters took most of the time
@@ -23,10 +24,10 @@
 //           kept positions in order and writes index and weight. Bound by the
 //           latency of its steps: of 16 us for 128 rows of up to 8192, some
 //           1.5 to 2.5 us a pass go to the counters' sums, the cluster's barrier
-//           and the scan, 0.4 to the counting.
+//           and the scan, 0.4 to the counting; 22 us for 6 rows of 131072.
 //   gather  copies the kept K and V rows, in the order of the destination, 16
-//           bytes a lane; it is what the call's bytes are: 259 MB in 41 us (6.3
-//           TB/s, 93 % of a copy's) for 16 sequences of 8 heads brought to 2048.
+//           bytes a lane; it is what the call's bytes are: 259 MB in 39 us (6.6
+//           TB/s, 98 % of a copy's) for 16 sequences of 8 heads brought to 2048.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -84,7 +85,15 @@ struct SelectSmem {
   // the digit of the key sought: keys above it and at it in the row, and in
   // the parts of the CTAs before this one
   unsigned int digit, above, at, above_before, at_before;
+  unsigned int listed;                     // candidates of this CTA in the list so far
 };
+
+// With at most this many keys left to choose from, they are listed (over the
+// histograms) and compared with one another instead of counted digit by digit, which
+// spares a pass or two (128 rows of 8192: 21 us without, 18 with 128, 20 with 256,
+// whose comparisons are four times as many).
+constexpr int kList = 128;
+static_assert(kList <= 512, "a thread per candidate");
 
 template <int kThreads>
 __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
@@ -233,7 +242,48 @@ evict_select_kernel(const EvictParams p) {
     above = sm.above;
     gt += sm.above_before;
     eq = sm.at_before;
-    if (above + sm.at == static_cast<unsigned int>(need)) break;   // all of these stay
+    const unsigned int left = sm.at;                  // keys that share the digits so far
+    if (above + left == static_cast<unsigned int>(need)) break;    // all of these stay
+    if (left <= kList && pass < 3) {
+      // every CTA's candidates to every CTA's list, those of the CTAs before first
+      const unsigned int first = eq;
+      unsigned int* const list = &sm.hist[0][0];
+      if (tid == 0) sm.listed = first;
+      __syncthreads();
+      auto put = [&](uint32_t key) {
+        if ((key >> shift) != prefix) return;
+        const unsigned int slot = atomicAdd(&sm.listed, 1u);
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r)
+          if (r < ncta) *cluster.map_shared_rank(list + slot, r) = key;
+      };
+      if (in_smem) {
+        for (int i = tid; i < n; i += kThreads) put(held[i]);
+      } else {
+        for (int i = tid; i < n; i += kThreads) put(order_key(w[lo + i]));
+      }
+      cluster.sync();
+      const uint32_t key = tid < left ? list[tid] : 0u;
+      if (tid < left) {
+        unsigned int larger = 0, same = 0;
+        for (unsigned int j = 0; j < left; ++j) {
+          larger += list[j] > key ? 1u : 0u;
+          same += list[j] == key ? 1u : 0u;
+        }
+        const unsigned int k = static_cast<unsigned int>(need) - above;
+        if (larger < k && larger + same >= k) {       // (equal keys write the same)
+          sm.digit = key;
+          sm.above = above + larger;
+        }
+      }
+      __syncthreads();
+      prefix = sm.digit;
+      above = sm.above;
+      shift = 0;
+      gt += __syncthreads_count(tid < left && tid < first && key > prefix);
+      eq = __syncthreads_count(tid < left && tid < first && key == prefix);
+      break;
+    }
   }
   // kept: keys above `prefix`, and the first `ties` of those equal to it
   const unsigned int ties = static_cast<unsigned int>(need) - above;
@@ -421,7 +471,7 @@ extern "C" attn_status_t attn_cache_evict(const void* k, const void* v, const fl
 
   const int64_t rows = B * n_kv;
   // CTAs per row while two fit an SM and each has 4096 positions: few long rows
-  // need them (the selection among 6 rows of 131072: 96, 55, 29 and 22 us with 1, 2,
+  // need them (a call for 6 rows of 131072 and few kept: 96, 55, 29 and 22 us with 1, 2,
   // 4 and 8, no less with 16), for 128 rows of 8192 one or two are the same (21)
   int cluster = 1;
   while (cluster < kMaxCluster && rows * cluster * 2 <= 2 * kSms && C >= 4096 * 2 * cluster)

@@ -106,6 +106,24 @@ def test_parts_too_long_for_shared_memory(B, C, n_kv):
     check(k, v, w, [C - 3 * i for i in range(B)], 500, 20)
 
 
+@pytest.mark.parametrize("C,near", [(20000, 3), (70001, 40), (70001, 127), (330000, 100), (500, 128)])
+def test_the_last_few_are_near_or_equal(C, near):
+    """Most weights far apart, and as many as are listed and compared one by one (or
+    one more) that differ in their last bits or not at all, spread over all CTAs."""
+    k, v, w = make(1, C, 2, 64, torch.float8_e4m3fn, "plain", seed=C + near)
+    g = torch.Generator().manual_seed(near)
+    for extra in (0, 2):
+        at = torch.randperm(C - 20, generator=g)[:near + extra].cuda()
+        bits = torch.full((near + extra,), 0x3F812300, dtype=torch.int32, device="cuda")
+        w.copy_(torch.rand(w.shape, device="cuda") * 0.9 + 4.0 * (torch.rand(w.shape, device="cuda") < 0.01))
+        bits += torch.randint(0, 4, bits.shape, generator=g, dtype=torch.int32).cuda()
+        w[0, 0, at] = bits.view(torch.float32)
+        w[0, 1, at] = 1.0087890625
+        larger = int((w[0, :, :C - 20] >= 2).sum(1).max())
+        for n in (1, near // 2 + 1, near):
+            check(k, v, w, [C], 20 + larger + n, 20)
+
+
 def test_lengths_out_of_range_are_clamped():
     k, v, w = make(2, 100, 2, 64, torch.bfloat16, "plain", seed=4)
     check(k, v, w, [1000, -5], 30, 5)
