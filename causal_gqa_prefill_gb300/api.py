@@ -160,7 +160,8 @@ class _Call:
         self.device = device
         self.guard = None
         self.other = None                 # the torch stream, when it is not the current one
-        if torch.cuda.current_device() != device.index:
+        # (a tensor is on the device, so CUDA is up: no need to ask whether it is)
+        if torch._C._cuda_getDevice() != device.index:
             self.guard = torch.cuda.device(device)
         # the handle that torch.cuda.current_stream(device).cuda_stream gives,
         # without the two objects made on the way
@@ -208,6 +209,18 @@ class _Call:
         return given, given.nbytes
 
 
+def _laid_out(index, dtype, *tensors):
+    """Are all of these (None: not given) contiguous, of this dtype and on CUDA device
+    ``index``? With the shapes, what a call takes: where the answer is no, the
+    checks below say what is wrong. (Run for every call they are 1 of a small
+    call's 25 microseconds.)"""
+    for t in tensors:
+        if t is not None and (t.dtype is not dtype or t.get_device() != index
+                              or not t.is_contiguous()):
+            return False
+    return index >= 0
+
+
 def _wrong_tensor(name, t, shape, dtype, device=None):
     """The error that says how ``t`` differs from a contiguous CUDA tensor of this
     shape (None: any size) and dtype on ``device``; None if it does not."""
@@ -228,10 +241,6 @@ def _wrong_tensor(name, t, shape, dtype, device=None):
 def _cuda_tensor(name, t, shape, dtype, device=None):
     """``t`` if it is a contiguous CUDA tensor of this shape (None: any size) and
     dtype, on ``device``."""
-    # the usual case in as few steps as it takes (device is a CUDA device)
-    if (getattr(t, "dtype", None) is dtype and t.device == device and t.shape == shape
-            and t.is_contiguous()):
-        return t
     wrong = _wrong_tensor(name, t, shape, dtype, device)
     if wrong is not None:
         raise wrong
@@ -241,13 +250,7 @@ def _cuda_tensor(name, t, shape, dtype, device=None):
 def _heads_of(name, t, first, length, dtype, device=None):
     """The shape of the contiguous [first, length, heads, d] CUDA tensor ``t`` (None:
     any size)."""
-    if (getattr(t, "dtype", None) is dtype and t.is_cuda and t.dim() == 4 and t.is_contiguous()
-            and (device is None or t.device == device)):
-        B, L, H, d = t.shape
-        if (first is None or first == B) and (length is None or length == L):
-            return B, L, H, d
-    wrong = _wrong_tensor(name, t, (first, length, None, None), dtype, device)
-    raise wrong
+    return _cuda_tensor(name, t, (first, length, None, None), dtype, device).shape
 
 
 def attn_key_weights_workspace_bytes(B, Lq, Lk, n_q, n_kv, d_h=128) -> int:
@@ -278,26 +281,35 @@ def attn_key_weights(q, k, lse, *, causal=True, scale=None, weights=None, accumu
     of the tensor's positions that exist as its own contiguous tensor)."""
     import torch
 
-    bf16 = torch.bfloat16
-    B, Lq, n_q, d = _heads_of("q", q, None, None, bf16)
-    dev = q.device
-    _, Lk, n_kv, dk = _heads_of("k", k, B, None, bf16, dev)
-    if dk != d:
-        raise ValueError("q and k must have the same d_h")
-    if Lk < Lq:
-        raise ValueError("k must hold at least as many positions as q has rows")
-    _cuda_tensor("lse", lse, (B, n_q, Lq), torch.float32, dev)
-    if weights is not None:
-        _cuda_tensor("weights", weights, (B, n_kv, Lk), torch.float32, dev)
-    elif accumulate:
-        raise ValueError("accumulate needs the weights to add to")
+    bf16, f32 = torch.bfloat16, torch.float32
+    try:
+        B, Lq, n_q, d = q.shape
+        _, Lk, n_kv, _ = k.shape
+        index = q.get_device()
+        usual = (k.shape == (B, Lk, n_kv, d) and Lk >= Lq and lse.shape == (B, n_q, Lq)
+                 and (not accumulate if weights is None else weights.shape == (B, n_kv, Lk))
+                 and _laid_out(index, bf16, q, k) and _laid_out(index, f32, lse, weights))
+    except (AttributeError, ValueError):
+        usual = False
+    if not usual:
+        B, Lq, n_q, d = _heads_of("q", q, None, None, bf16)
+        _, Lk, n_kv, dk = _heads_of("k", k, B, None, bf16, q.device)
+        if dk != d:
+            raise ValueError("q and k must have the same d_h")
+        if Lk < Lq:
+            raise ValueError("k must hold at least as many positions as q has rows")
+        _cuda_tensor("lse", lse, (B, n_q, Lq), f32, q.device)
+        if weights is not None:
+            _cuda_tensor("weights", weights, (B, n_kv, Lk), f32, q.device)
+        elif accumulate:
+            raise ValueError("accumulate needs the weights to add to")
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    with _Call(torch, dev, stream) as call:
+    with _Call(torch, q.device, stream) as call:
         workspace, nbytes = call.workspace(workspace, attn_key_weights_workspace_bytes, B, Lq, Lk,
                                            n_q, n_kv, d)
         if weights is None:
-            weights = call.empty((B, n_kv, Lk), torch.float32)
+            weights = call.empty((B, n_kv, Lk), f32)
         st = _abi.load().attn_key_weights_fwd(
             q.data_ptr(), k.data_ptr(), lse.data_ptr(), weights.data_ptr(), workspace.data_ptr(),
             nbytes, B, Lq, Lk, n_q, n_kv, d, bool(causal), bool(accumulate), scale, call.handle)
@@ -336,29 +348,42 @@ def attn_decode_ragged(q, k, v, lens, *, weights=None, scale=None, workspace=Non
     given."""
     import torch
 
-    bf16 = torch.bfloat16
-    B, _, n_q, d = _heads_of("q", q, None, 1, bf16)
-    dev = q.device
-    _, C, n_kv, dk = _heads_of("k", k, B, None, bf16, dev)
-    if dk != d:
-        raise ValueError("q and k must have the same d_h")
-    _cuda_tensor("v", v, k.shape, bf16, dev)
-    _cuda_tensor("lens", lens, (B,), torch.int32, dev)
-    if weights is not None:
-        _cuda_tensor("weights", weights, (B, n_kv, C), torch.float32, dev)
-    if out is not None:
-        _cuda_tensor("out", out, q.shape, bf16, dev)
-    if lse is not None:
-        _cuda_tensor("lse", lse, (B, n_q, 1), torch.float32, dev)
+    bf16, f32 = torch.bfloat16, torch.float32
+    try:
+        B, one, n_q, d = q.shape
+        _, C, n_kv, _ = k.shape
+        index = q.get_device()
+        usual = (one == 1 and v.shape == k.shape == (B, C, n_kv, d) and lens.shape == (B,)
+                 and (weights is None or weights.shape == (B, n_kv, C))
+                 and (out is None or out.shape == q.shape)
+                 and (lse is None or lse.shape == (B, n_q, 1))
+                 and _laid_out(index, bf16, q, k, v, out) and _laid_out(index, f32, weights, lse)
+                 and _laid_out(index, torch.int32, lens))
+    except (AttributeError, ValueError):
+        usual = False
+    if not usual:
+        B, _, n_q, d = _heads_of("q", q, None, 1, bf16)
+        dev = q.device
+        _, C, n_kv, dk = _heads_of("k", k, B, None, bf16, dev)
+        if dk != d:
+            raise ValueError("q and k must have the same d_h")
+        _cuda_tensor("v", v, k.shape, bf16, dev)
+        _cuda_tensor("lens", lens, (B,), torch.int32, dev)
+        if weights is not None:
+            _cuda_tensor("weights", weights, (B, n_kv, C), f32, dev)
+        if out is not None:
+            _cuda_tensor("out", out, q.shape, bf16, dev)
+        if lse is not None:
+            _cuda_tensor("lse", lse, (B, n_q, 1), f32, dev)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    with _Call(torch, dev, stream) as call:
+    with _Call(torch, q.device, stream) as call:
         workspace, nbytes = call.workspace(workspace, attn_decode_ragged_workspace_bytes, B, C, n_q,
                                            n_kv, d, weights is not None)
         if out is None:
             out = call.empty(q.shape, bf16)
         if lse is None:
-            lse = call.empty((B, n_q, 1), torch.float32)
+            lse = call.empty((B, n_q, 1), f32)
         st = _abi.load().attn_decode_ragged_fwd(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), lens.data_ptr(), _ptr(weights),
             out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), nbytes, B, C, n_q, n_kv, d, scale,
@@ -396,29 +421,43 @@ def attn_decode_shared(q, prefix_k, prefix_v, k, v, lens, *, scale=None, workspa
     not given."""
     import torch
 
-    bf16 = torch.bfloat16
-    B, _, n_q, d = _heads_of("q", q, None, 1, bf16)
-    dev = q.device
-    _, P, n_kv, dp = _heads_of("prefix_k", prefix_k, 1, None, bf16, dev)
-    _cuda_tensor("prefix_v", prefix_v, prefix_k.shape, bf16, dev)
-    _, C, own_kv, dk = _heads_of("k", k, B, None, bf16, dev)
-    if dk != d or dp != d or own_kv != n_kv:
-        raise ValueError("q, prefix_k and k must agree on d_h, the caches on their heads")
-    _cuda_tensor("v", v, k.shape, bf16, dev)
-    _cuda_tensor("lens", lens, (B,), torch.int32, dev)
-    if out is not None:
-        _cuda_tensor("out", out, q.shape, bf16, dev)
-    if lse is not None:
-        _cuda_tensor("lse", lse, (B, n_q, 1), torch.float32, dev)
+    bf16, f32 = torch.bfloat16, torch.float32
+    try:
+        B, one, n_q, d = q.shape
+        _, C, n_kv, _ = k.shape
+        P = prefix_k.shape[1]
+        index = q.get_device()
+        usual = (one == 1 and prefix_v.shape == prefix_k.shape == (1, P, n_kv, d)
+                 and v.shape == k.shape == (B, C, n_kv, d) and lens.shape == (B,)
+                 and (out is None or out.shape == q.shape)
+                 and (lse is None or lse.shape == (B, n_q, 1))
+                 and _laid_out(index, bf16, q, prefix_k, prefix_v, k, v, out)
+                 and _laid_out(index, f32, lse) and _laid_out(index, torch.int32, lens))
+    except (AttributeError, ValueError, IndexError):
+        usual = False
+    if not usual:
+        B, _, n_q, d = _heads_of("q", q, None, 1, bf16)
+        dev = q.device
+        _, P, n_kv, dp = _heads_of("prefix_k", prefix_k, 1, None, bf16, dev)
+        _cuda_tensor("prefix_v", prefix_v, prefix_k.shape, bf16, dev)
+        _, C, own_kv, dk = _heads_of("k", k, B, None, bf16, dev)
+        if dk != d or dp != d or own_kv != n_kv:
+            raise ValueError("q, prefix_k and k must agree on d_h, the caches on their heads")
+        _cuda_tensor("v", v, k.shape, bf16, dev)
+        _cuda_tensor("lens", lens, (B,), torch.int32, dev)
+        if out is not None:
+            _cuda_tensor("out", out, q.shape, bf16, dev)
+        if lse is not None:
+            _cuda_tensor("lse", lse, (B, n_q, 1), f32, dev)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    with _Call(torch, dev, stream) as call:
+    with _Call(torch, q.device, stream) as call:
         workspace, nbytes = call.workspace(workspace, attn_decode_shared_workspace_bytes, B, P, C,
                                            n_q, n_kv, d)
         if out is None:
             out = call.empty(q.shape, bf16)
         if lse is None:
-            lse = call.empty((B, n_q, 1), torch.float32)
+            lse = call.empty((B, n_q, 1), f32)
         st = _abi.load().attn_decode_shared_fwd(
             q.data_ptr(), prefix_k.data_ptr(), prefix_v.data_ptr(), k.data_ptr(), v.data_ptr(),
             lens.data_ptr(), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), nbytes, B, P, C,
@@ -459,11 +498,7 @@ def attn_evict(k, v, weights, lens, budget, recent=0, *, capacity=None, k_out=No
     kind = getattr(k, "dtype", None)
     if kind is not torch.bfloat16 and kind is not torch.float8_e4m3fn:
         raise TypeError("k must be a bfloat16 or float8_e4m3fn CUDA tensor")
-    B, C, n_kv, d = _heads_of("k", k, None, None, kind)
-    dev = k.device
-    _cuda_tensor("v", v, k.shape, kind, dev)
-    _cuda_tensor("weights", weights, (B, n_kv, C), torch.float32, dev)
-    _cuda_tensor("lens", lens, (B,), torch.int32, dev)
+    f32, i32 = torch.float32, torch.int32
     budget, recent = int(budget), int(recent)
     if budget < 1 or not 0 <= recent <= budget:
         raise ValueError("budget must be at least 1 and recent between 0 and budget")
@@ -471,21 +506,51 @@ def attn_evict(k, v, weights, lens, budget, recent=0, *, capacity=None, k_out=No
         capacity = budget if getattr(k_out, "ndim", 0) != 4 else k_out.shape[1]
     if capacity < budget:
         raise ValueError("the new capacity must hold the budget")
-    wanted = {"k_out": (k_out, (B, capacity, n_kv, d), kind),
-              "v_out": (v_out, (B, capacity, n_kv, d), kind),
-              "weights_out": (weights_out, (B, n_kv, capacity), torch.float32),
-              "lens_out": (lens_out, (B,), torch.int32),
-              "index": (index, (B, n_kv, budget), torch.int32)}
-    with _Call(torch, dev, stream) as call:
-        outs = [call.empty(shape, dtype) if t is None else _cuda_tensor(name, t, shape, dtype, dev)
-                for name, (t, shape, dtype) in wanted.items()]
+    try:
+        B, C, n_kv, d = k.shape
+        dev, device = k.get_device(), k.device
+        usual = (v.shape == k.shape and weights.shape == (B, n_kv, C) and lens.shape == (B,)
+                 and (k_out is None or k_out.shape == (B, capacity, n_kv, d))
+                 and (v_out is None or v_out.shape == (B, capacity, n_kv, d))
+                 and (weights_out is None or weights_out.shape == (B, n_kv, capacity))
+                 and (lens_out is None or lens_out.shape == (B,))
+                 and (index is None or index.shape == (B, n_kv, budget))
+                 and _laid_out(dev, kind, k, v, k_out, v_out)
+                 and _laid_out(dev, f32, weights, weights_out)
+                 and _laid_out(dev, i32, lens, lens_out, index))
+    except (AttributeError, ValueError):
+        usual = False
+    if not usual:
+        B, C, n_kv, d = _heads_of("k", k, None, None, kind)
+        device = k.device
+        _cuda_tensor("v", v, k.shape, kind, device)
+        _cuda_tensor("weights", weights, (B, n_kv, C), f32, device)
+        _cuda_tensor("lens", lens, (B,), i32, device)
+        for name, t, shape, dtype in (("k_out", k_out, (B, capacity, n_kv, d), kind),
+                                      ("v_out", v_out, (B, capacity, n_kv, d), kind),
+                                      ("weights_out", weights_out, (B, n_kv, capacity), f32),
+                                      ("lens_out", lens_out, (B,), i32),
+                                      ("index", index, (B, n_kv, budget), i32)):
+            if t is not None:
+                _cuda_tensor(name, t, shape, dtype, device)
+    with _Call(torch, device, stream) as call:
+        if k_out is None:
+            k_out = call.empty((B, capacity, n_kv, d), kind)
+        if v_out is None:
+            v_out = call.empty((B, capacity, n_kv, d), kind)
+        if weights_out is None:
+            weights_out = call.empty((B, n_kv, capacity), f32)
+        if lens_out is None:
+            lens_out = call.empty((B,), i32)
+        if index is None:
+            index = call.empty((B, n_kv, budget), i32)
         st = _abi.load().attn_cache_evict(
-            k.data_ptr(), v.data_ptr(), weights.data_ptr(), lens.data_ptr(),
-            *(t.data_ptr() for t in outs), B, C, capacity, budget, recent, n_kv, d,
-            k.element_size(), call.handle)
+            k.data_ptr(), v.data_ptr(), weights.data_ptr(), lens.data_ptr(), k_out.data_ptr(),
+            v_out.data_ptr(), weights_out.data_ptr(), lens_out.data_ptr(), index.data_ptr(),
+            B, C, capacity, budget, recent, n_kv, d, k.element_size(), call.handle)
     if st != _abi.ATTN_OK:
         raise AttnError(st, "attn_cache_evict")
-    return tuple(outs)
+    return k_out, v_out, weights_out, lens_out, index
 
 
 def attn_prefill_bwd_workspace_bytes(B, L, n_q, n_kv, d_h=128) -> int:
