@@ -525,7 +525,9 @@ shared_combine_kernel(uint16_t* o, float* lse, const int* lens, int C,
   float4 acc[2];
   acc[0] = acc[1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   auto add = [&](const float2& ml, const float4& u, const float4& v) {
-    if (ml.x == -INFINITY) return;                        // an empty part: u, v are not written
+    // an empty part: u, v are not written (with NaN for a sum it has keys, none of
+    // whose scores is a number)
+    if (ml.x == -INFINITY && ml.y == 0.0f) return;
     const float mn = fmaxf(m, ml.x);
     const float a = (m == -INFINITY) ? 0.0f : exp2f(m - mn);
     const float w = exp2f(ml.x - mn);

@@ -205,6 +205,34 @@ def test_memory_of_another_stream():
         assert torch.equal(x.view(torch.int16), y.view(torch.int16))
 
 
+def test_nan_in_visible_places():
+    """A NaN query makes its own row NaN and no other; a NaN key those of
+    its sequence and K/V head, also where it is all that the sequence has."""
+    q, k, v, lens, acc = make(4, 300, 8, 2, [300, 1, 0, 133], seed=3, junk=False)
+    good, good_lse = attn_decode_ragged(q, k, v, lens, weights=acc.clone())
+
+    def bad_rows(want, q, k):
+        mine = acc.clone()
+        o, lse = attn_decode_ragged(q, k, v, lens, weights=mine)
+        got = torch.isnan(o[:, 0]).all(2)
+        assert got.nonzero().tolist() == want and torch.isnan(o).sum() == 128 * len(want)
+        assert torch.equal(torch.isnan(lse[..., 0]), got)
+        assert torch.equal(o[:, 0][~got], good[:, 0][~got])
+        assert torch.equal(lse[..., 0][~got], good_lse[..., 0][~got])
+        heads = got.reshape(4, 2, 4).any(2)
+        for b in range(4):
+            for u in range(2):
+                assert torch.isnan(mine[b, u, :lens[b]]).all() == heads[b, u] or lens[b] == 0
+                assert not torch.isnan(mine[b, u, lens[b]:]).any()
+
+    q2, k2 = q.clone(), k.clone()
+    q2[0, 0, 3, 7] = q2[1, 0, 5, 0] = float("nan")
+    q2[2, 0, 1, 0] = float("nan")                  # a sequence without keys stays 0
+    bad_rows([[0, 3], [1, 5]], q2, k)
+    k2[1, 0, 1, 9] = k2[3, 130, 0, 9] = float("nan")
+    bad_rows([[1, 4], [1, 5], [1, 6], [1, 7], [3, 0], [3, 1], [3, 2], [3, 3]], q, k2)
+
+
 def test_refusals():
     q, k, v, lens, acc = make(2, 64, 8, 2, [3, 4], seed=1)
     with pytest.raises(ValueError):

@@ -173,6 +173,30 @@ def test_large_batch_on_sampled_rows():
         assert abs(torch.logsumexp(s, 0) - lse[b, h, 0].double()) <= 1e-4
 
 
+def test_nan_in_visible_places():
+    """A NaN query makes its own row NaN and no other; a NaN key those of
+    its sequence and K/V head, also where it is all that the sequence has."""
+    q, prefix, k, v, lens = inputs(4, 300, 40, 8, 2, [40, 1, 0, 33], seed=3, junk=False)
+    good, good_lse = attn_decode_shared(q, *prefix, k, v, lens)
+
+    def bad_rows(want, *args):
+        o, lse = attn_decode_shared(*args, lens)
+        got = torch.isnan(o[:, 0]).all(2)
+        assert got.nonzero().tolist() == want and torch.isnan(o).sum() == 128 * len(want)
+        assert torch.equal(torch.isnan(lse[..., 0]), got)
+        assert torch.equal(o[:, 0][~got], good[:, 0][~got])
+        assert torch.equal(lse[..., 0][~got], good_lse[..., 0][~got])
+
+    q2, k2, p2 = q.clone(), k.clone(), prefix[0].clone()
+    q2[0, 0, 3, 7] = q2[2, 0, 5, 0] = float("nan")
+    bad_rows([[0, 3], [2, 5]], q2, *prefix, k, v)
+    k2[1, 0, 1, 9] = float("nan")                  # the only own position of sequence 1
+    k2[3, 20, 0, 9] = float("nan")
+    bad_rows([[1, 4], [1, 5], [1, 6], [1, 7], [3, 0], [3, 1], [3, 2], [3, 3]], q, *prefix, k2, v)
+    p2[0, 299, 1, 0] = float("nan")
+    bad_rows([[b, h] for b in range(4) for h in range(4, 8)], q, p2, prefix[1], k, v)
+
+
 def test_refusals():
     q, prefix, k, v, lens = inputs(2, 64, 32, 8, 2, [3, 4], seed=1)
     with pytest.raises(ValueError):
