@@ -228,14 +228,22 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, const 
     if (static_cast<long long>(clock64_now() - t0) > p.spin_limit) return;
 }
 
-// acc += 2^(c s + nl) for the 32 keys whose scores are in s, two at a time.
+// acc += 2^(c s + nl) for the 32 keys whose scores are in s, two at a time; with
+// kMask those past key `keep` are hidden (after the product with the row's lse: one
+// that is NaN reaches the keys that the row sees and no others).
+template <bool kMask>
 __device__ __forceinline__ void add_weights(uint64_t* acc, const uint32_t (&s)[32], uint64_t c2,
-                                            uint64_t nl2) {
+                                            uint64_t nl2, int keep) {
 #pragma unroll
   for (int i = 0; i < 32; i += 2) {
     float x0, x1;
     f32x2_unpack(ffma2(f32x2_pack(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), c2, nl2), x0, x1);
-    const uint64_t e = f32x2_pack(ex2_approx(x0), ex2_approx(x1));
+    if (kMask) {
+      if (i > keep) x0 = -INFINITY;
+      if (i + 1 > keep) x1 = -INFINITY;
+    }
+    const float e0 = ex2_approx(x0), e1 = ex2_approx(x1);
+    const uint64_t e = f32x2_pack(e0, e1);
     asm("add.f32x2 %0, %0, %1;" : "+l"(acc[i / 2]) : "l"(e));
   }
 }
@@ -262,7 +270,6 @@ __device__ void sum_role(Ctl& ctl, const Params& p, const Starts& starts, uint32
   const int r = quarter * 32 + lane;                   // row of the step = TMEM lane
   const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + kCols * group;
   const uint64_t c2 = f32x2_pack(p.c, p.c);
-  const uint32_t hidden = p.c > 0.0f ? 0xff800000u : 0x7f800000u;   // c * hidden = -inf
   const int row = r / p.g;
   // a buffer is free once its last scores are in registers, before they are
   // summed: the next product starts half a step earlier, and a warp that is ahead
@@ -307,7 +314,7 @@ __device__ void sum_role(Ctl& ctl, const Params& p, const Starts& starts, uint32
             tmem_ld32(taddr + 32 * q, s);
             tmem_wait_ld(s);
             if (q == kCols / 32 - 1) release(buf);
-            add_weights(acc + 16 * q, s, c2, nl2);
+            add_weights<false>(acc + 16 * q, s, c2, nl2, 0);
           }
         } else {
           // this row's position sees key0 + i for i <= keep
@@ -317,10 +324,7 @@ __device__ void sum_role(Ctl& ctl, const Params& p, const Starts& starts, uint32
             tmem_ld32(taddr + 32 * q, s);
             tmem_wait_ld(s);
             if (q == kCols / 32 - 1) release(buf);
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (32 * q + i > keep) s[i] = hidden;
-            add_weights(acc + 16 * q, s, c2, nl2);
+            add_weights<true>(acc + 16 * q, s, c2, nl2, keep - 32 * q);
           }
         }
       } else {
@@ -1194,9 +1198,7 @@ attn_status_t attn_key_weights_fwd(const void* q, const void* k, const float* ls
   p.T = static_cast<int>((Lk + kUnitKeys - 1) / kUnitKeys);
   p.causal = causal;
   p.accumulate = accumulate;
-  // (a scale of 0 as one that no score notices: a hidden score still has to
-  // come out as -inf)
-  p.c = scale != 0.0f ? scale * kLog2e : 1e-30f;
+  p.c = scale * kLog2e;
   p.spin_limit = 1ll << 31;   // about a second at 2 GHz
 
   // equal ranges of the steps of all units

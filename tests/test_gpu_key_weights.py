@@ -163,6 +163,21 @@ def test_hidden_values_do_not_leak_from_few_rows():
     check(q, k, lse, attn_key_weights(q, k, lse))
 
 
+@pytest.mark.parametrize("Lq", [400, 30])
+def test_a_row_of_nan(Lq):
+    """A row whose query and lse are NaN makes the keys that it sees NaN and no others."""
+    q, k, lse = inputs(1, Lq, 400, 4, 2, 128, True, seed=12)
+    good = attn_key_weights(q, k, lse)
+    for row in (0, 13, Lq - 2):
+        bad, bad_lse = q.clone(), lse.clone()
+        bad[0, row, 2], bad_lse[0, 2, row] = float("nan"), float("nan")
+        w = attn_key_weights(bad, k, bad_lse)
+        at = 400 - Lq + row
+        assert torch.isnan(w[0, 1, :at + 1]).all(), row
+        assert torch.equal(w[0, 1, at + 1:], good[0, 1, at + 1:]), row
+        assert torch.equal(w[0, 0], good[0, 0]), row
+
+
 @pytest.mark.parametrize("Lq,n_q,d", [(300, 4, 128), (301, 6, 64), (300, 10, 128), (30, 4, 128), (7, 6, 64)])
 def test_a_key_of_weight_zero(Lq, n_q, d):
     """A key whose every score is -inf has weight 0 and changes no other, also where
