@@ -533,8 +533,14 @@ __device__ void mma_role(Ctl& ctl, const Params& p, const Starts& starts, uint32
     if (leader) mma_commit(smem_addr(&ctl.k_empty[seg & 1]));
     ++seg;
     if (stay && last_of_head) {
-      for (int i = 0; i < p.steps; ++i)
-        if (leader) mma_commit(smem_addr(&ctl.q_empty[i]));
+      // Steps that the range leaves out (it begins or ends inside a unit) were copied
+      // to the ring all the same. Their copies have landed too before a slot is given
+      // back, and before the CTA ends: the loader must not arm a barrier whose phase
+      // is still open, nor a copy write to shared memory that is another CTA's by then.
+      for (int i = 0; i < p.steps && ok; ++i) {
+        ok = wait_warp(smem_addr(&ctl.q_full[i]), gn & 1, ctl, p);
+        if (ok && leader) mma_commit(smem_addr(&ctl.q_empty[i]));
+      }
       ++gn;
     }
   }
