@@ -276,7 +276,8 @@ def attn_key_weights(q, k, lse, *, causal=True, scale=None, weights=None, accumu
 
     q bf16 [B, Lq, n_q, d], k bf16 [B, Lk, n_kv, d] (d 64 or 128, rows the last
     Lq of the Lk positions), lse fp32 [B, n_q, Lq] as attn_prefill returned it
-    for the same causal and scale. ``weights`` receives the result, or with
+    for the same causal and scale; a row whose lse is -inf (a padded one, say)
+    adds nothing, whatever its q holds. ``weights`` receives the result, or with
     ``accumulate`` is added to (chunk after chunk of one prompt: pass the part
     of the tensor's positions that exist as its own contiguous tensor)."""
     import torch

@@ -45,6 +45,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 #include <mutex>
@@ -78,6 +79,14 @@ constexpr uint32_t kTmemCols = 512;   // S at columns 0 and 256
 constexpr int kStatusTimeout = 1, kStatusCheck = 2;
 constexpr uint32_t kSuspendNs = 2000;
 constexpr float kLog2e = 1.4426950408889634f;
+
+// What stands for a row in the exponents: -lse2, or kNoWeight where there is no row or
+// its lse is -inf (a row without keys). No other row has that value.
+constexpr float kNoWeight = INFINITY;
+__device__ __forceinline__ float exponent_of(float lse) {
+  const float x = -lse * kLog2e;
+  return lse == -INFINITY ? kNoWeight : x > FLT_MAX ? FLT_MAX : x;   // (a NaN stays one)
+}
 
 template <int D>
 struct Geometry {
@@ -308,7 +317,12 @@ __device__ void sum_role(Ctl& ctl, const Params& p, const Starts& starts, uint32
         const uint64_t nl2 = f32x2_pack(nl, nl);
         const uint32_t taddr = lanes + kUnitKeys * buf;
         uint32_t s[32];
-        if (st >= until) {
+        // a row without weight (lanes without rows are dropped when the rows are folded)
+        // takes its warp to the sum with a mask, where it sees no key: its query may be
+        // anything, and a NaN score plus -inf is NaN (a vote of the warp: 0.3 % of the
+        // 8192-token layer, 1 % with a flag from the statistics' warp)
+        const bool none = nl == kNoWeight;
+        if (st >= until && !__any_sync(0xffffffffu, none && row < p.nr)) {
 #pragma unroll
           for (int q = 0; q < kCols / 32; ++q) {
             tmem_ld32(taddr + 32 * q, s);
@@ -318,7 +332,7 @@ __device__ void sum_role(Ctl& ctl, const Params& p, const Starts& starts, uint32
           }
         } else {
           // this row's position sees key0 + i for i <= keep
-          const int keep = p.off + first_row(st, p) + row - key0;
+          const int keep = none ? -1 : p.causal ? p.off + first_row(st, p) + row - key0 : kCols;
 #pragma unroll
           for (int q = 0; q < kCols / 32; ++q) {
             tmem_ld32(taddr + 32 * q, s);
@@ -413,8 +427,7 @@ __device__ void stat_role(Ctl& ctl, const Params& p, const Starts& starts) {
       if (n >= 2 && !wait_warp(smem_addr(&ctl.s_free[buf]), ((n >> 1) - 1) & 1, ctl, p)) return;
       // a row without keys, like a lane without a row, has no weight
 #pragma unroll
-      for (int m = 0; m < 4; ++m)
-        ctl.nl[buf][lane + 32 * m] = l[u][m] == -INFINITY ? -INFINITY : -l[u][m] * kLog2e;
+      for (int m = 0; m < 4; ++m) ctl.nl[buf][lane + 32 * m] = exponent_of(l[u][m]);
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_addr(&ctl.s_full[buf]));
       have[u] = fetch(l[u]);
@@ -595,8 +608,8 @@ key_weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     tmem_relinquish();
   }
   if (p.nr * p.g < kRows && warp < kSumWarps) {
-    // rows past nr * g are never loaded: zeros, so that their scores are 0 and
-    // their weights 2^(0 - inf) too
+    // rows past nr * g are never loaded: zeros (the sums of their lanes are dropped
+    // when the rows are folded)
     uint4* z = reinterpret_cast<uint4*>(dyn_smem + (sQ - start));
     for (int i = threadIdx.x; i < G::kQStages * G::kQBytes / 16; i += 32 * kSumWarps)
       z[i] = make_uint4(0u, 0u, 0u, 0u);
@@ -692,6 +705,7 @@ struct __align__(16) WinCtl {
   int abort;
   __align__(16) float nl[kWinCols];      // -lse2 of the Q buffers' columns
   float half_sum[2][kWinKeys];
+  int without[2];                        // has a row of a Q buffer no weight?
 };
 constexpr int kWinCtlBytes = (sizeof(WinCtl) + 1023) / 1024 * 1024;    // then the tiles
 template <int D>
@@ -885,11 +899,15 @@ key_weights_few_rows_kernel(const __grid_constant__ CUtensorMap tmQ,
       }
       if (use > 0 && !wait_warp(smem_addr(&ctl.n_empty[qb]), (use - 1) & 1, ctl, p)) break;
       // a row without keys, like a column without a row, has no weight
+      bool without = false;
 #pragma unroll
-      for (int m = 0; m < kWinCols / 32; ++m)
+      for (int m = 0; m < kWinCols / 32; ++m) {
         if (lane + 32 * m < rows_per_buf)
-          ctl.nl[qb * rows_per_buf + lane + 32 * m] =
-              l[m] == -INFINITY ? -INFINITY : -l[m] * kLog2e;
+          ctl.nl[qb * rows_per_buf + lane + 32 * m] = exponent_of(l[m]);
+        without |= lane + 32 * m < p.cols && l[m] == -INFINITY;
+      }
+      without = __any_sync(0xffffffffu, without);
+      if (lane == 0) ctl.without[qb] = without;
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_addr(&ctl.n_full[qb]));
       ++seg;
@@ -907,6 +925,7 @@ key_weights_few_rows_kernel(const __grid_constant__ CUtensorMap tmQ,
       if (!wait_warp(smem_addr(&ctl.n_full[qb]), (seg / p.bufs) & 1, ctl, p)) break;
       ++seg;
       const float* nl_buf = ctl.nl + qb * rows_per_buf;
+      const bool without = ctl.without[qb] != 0;
       for (int t = 0; t < sg.n; ++t, ++it) {
         if ((it & 1) != static_cast<uint32_t>(buf)) continue;
         const uint32_t turn = it >> 1;                     // of this buffer
@@ -947,6 +966,12 @@ key_weights_few_rows_kernel(const __grid_constant__ CUtensorMap tmQ,
               if (static_cast<unsigned int>(col + 1) >= seen) e1 = 0.0f;
               if (static_cast<unsigned int>(col + 2) >= seen) e2 = 0.0f;
               if (static_cast<unsigned int>(col + 3) >= seen) e3 = 0.0f;
+            }
+            if (without) {      // (their queries may be anything, and their scores NaN)
+              if (l.x == kNoWeight) e0 = 0.0f;
+              if (l.y == kNoWeight) e1 = 0.0f;
+              if (l.z == kNoWeight) e2 = 0.0f;
+              if (l.w == kNoWeight) e3 = 0.0f;
             }
             a0 = fadd2(a0, f32x2_pack(e0, e1));
             a1 = fadd2(a1, f32x2_pack(e2, e3));

@@ -189,7 +189,8 @@ attn_status_t attn_decode_fwd(const void* q, const void* k, const void* v, void*
  *
  *   q        bf16 [B, Lq, n_q, d_h]        k    bf16 [B, Lk, n_kv, d_h]
  *   lse      fp32 [B, n_q, Lq], of the same q, k, causal and scale; a row whose
- *            lse is -inf (one without keys) adds nothing
+ *            lse is -inf (one without keys, a padded one) adds nothing, whatever
+ *            its q and the keys hold
  *   weights  fp32 [B, n_kv, Lk], 4-byte aligned; accumulate = 0: written,
  *            1: added to
  *   workspace  at least attn_key_weights_workspace_bytes bytes, 16-byte aligned,

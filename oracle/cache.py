@@ -33,7 +33,7 @@ def key_weights(q, k, lse, *, causal=True, scale=None):
     """W [B, n_kv, Lk] from q [B, Lq, n_q, d], k [B, Lk, n_kv, d], lse [B, n_q, Lq].
 
     Row i sits at position i + Lk - Lq. A row whose lse is -inf has no keys and
-    adds nothing."""
+    adds nothing, whatever its q holds."""
     B, Lq, n_q, d = q.shape
     Lk, n_kv = k.shape[1], k.shape[2]
     g = n_q // n_kv
@@ -43,7 +43,8 @@ def key_weights(q, k, lse, *, causal=True, scale=None):
         for h in range(n_q):
             s = scale * (q[b, :, h] @ k[b, :, h // g].T)
             live = lse[b, h] != -np.inf
-            p = np.exp(s - np.where(live, lse[b, h], 0.0)[:, None]) * live[:, None]
+            # (a choice, not a product with 0: its scores may be NaN or infinite)
+            p = np.where(live[:, None], np.exp(s - np.where(live, lse[b, h], 0.0)[:, None]), 0.0)
             if causal:
                 p = np.where(np.arange(Lk)[None] <= np.arange(Lq)[:, None] + Lk - Lq, p, 0.0)
             w[b, h // g] += p.sum(0)

@@ -209,6 +209,19 @@ def test_oracle_key_weights():
     assert np.allclose(less[0, 0].sum(), 9.0) and np.allclose(less[0, 1], w[0, 1])
 
 
+def test_oracle_key_weights_of_padded_rows():
+    """A row whose lse is -inf adds nothing, whatever its q and the keys hold."""
+    rng = np.random.default_rng(5)
+    q, k = rng.normal(size=(1, 6, 4, 8)), rng.normal(size=(1, 6, 2, 8))
+    _, lse = oracle.attention(q, k, k, causal=True)
+    lse[0, 1, 2:4] = lse[0, 2, 5] = -np.inf
+    want = oracle.cache.key_weights(q, k, lse)
+    for bad in (np.nan, np.inf, -np.inf):
+        padded = q.copy()
+        padded[0, 2:4, 1] = padded[0, 5, 2] = bad
+        assert np.array_equal(oracle.cache.key_weights(padded, k, lse), want), bad
+
+
 def test_oracle_eviction_by_hand():
     w = np.array([[[3.0, 1.0, np.nan, 1.0, 5.0, 0.0, -0.0, 2.0]]])
     index, lens = oracle.cache.evicted_index(w, [8], 4, 1)
