@@ -27,6 +27,7 @@ DEBUG_LIBNAME = "libattn_prefill_debug.so"
 SOURCES = ["attn_prefill.cu", "attn_decode.cu", "attn_backward.cu", "attn_host.cu",
            "attn_key_weights.cu", "attn_evict.cu", "attn_shared.cu"]
 HEADERS = [os.path.join(CSRC, "sm103_ptx.cuh"), os.path.join(CSRC, "decode_parts.h"),
+           os.path.join(CSRC, "key_weights_ranges.h"),
            os.path.join(INCLUDE, "attn_prefill.h")]
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 

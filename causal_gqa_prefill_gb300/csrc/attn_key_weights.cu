@@ -51,6 +51,7 @@
 #include <mutex>
 
 #include "attn_prefill.h"
+#include "key_weights_ranges.h"
 #include "sm103_ptx.cuh"
 
 namespace gb300_host {
@@ -60,10 +61,8 @@ attn_status_t device_status_word(cudaStream_t stream, int** status);
 namespace {
 
 using namespace gb300;
+using namespace gb300_key_weights;    // kUnitKeys (N), kRows (TMEM lanes), kCtas
 
-constexpr int kUnitKeys = 256;        // keys per unit (N)
-constexpr int kRows = 128;            // rows (query positions x heads) per step (TMEM lanes)
-constexpr int kCtas = 152;            // one CTA per SM on a 152-SM GB300
 constexpr int kGroups = 4;            // warpgroups of the sums
 constexpr int kCols = kUnitKeys / kGroups;    // keys per thread
 constexpr int kSumWarps = 4 * kGroups;
@@ -113,11 +112,6 @@ struct Params {
   long long spin_limit;
 };
 
-// Where each CTA's range starts: unit, step, and the number of steps.
-struct Starts {
-  int unit[kCtas], step[kCtas], count[kCtas];
-};
-
 struct __align__(16) Ctl {
   uint64_t k_full[2], k_empty[2];
   uint64_t q_full[6], q_empty[6];
@@ -138,12 +132,6 @@ __host__ __device__ constexpr int smem_bytes() {
   return kCtlBytes + Geometry<D>::kTileBytes;
 }
 static_assert(smem_bytes<128>() <= 232448 && smem_bytes<64>() <= 232448, "shared memory");
-
-__host__ __device__ __forceinline__ int first_step(int t, int off, int nr, int causal) {
-  const int past = t * kUnitKeys - off;
-  return causal && past > 0 ? static_cast<int>(static_cast<unsigned>(past) / static_cast<unsigned>(nr))
-                            : 0;
-}
 
 // First row of a step. The last one ends with the last row, so that every row of
 // the tile is one (a zero row's product with an infinite key is NaN); the rows
@@ -1086,35 +1074,6 @@ bool encode(CUtensorMap* map, const void* ptr, int D, int H, int64_t L, int64_t 
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// sum_{i=0}^{n-1} floor((a i + b) / m) for n >= 0, m >= 1, a, b >= 0, by
-// splitting off whole multiples and exchanging the axes of the lattice points
-// below the line (the Euclidean algorithm on a and m).
-int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
-  int64_t total = 0;
-  while (n > 0) {
-    total += n * (n - 1) / 2 * (a / m) + n * (b / m);
-    a %= m;
-    b %= m;
-    const int64_t top = a * n + b;
-    if (top < m) break;
-    n = top / m;
-    b = top % m;
-    const int64_t old = m;
-    m = a;
-    a = old;
-  }
-  return total;
-}
-
-// Steps of units 0 .. t-1 of one (b, K/V head).
-int64_t steps_before(const Params& p, int64_t t) {
-  int64_t n = t * p.steps;
-  const int64_t s0 = p.off / kUnitKeys + 1;        // first unit that starts past row 0's position
-  if (p.causal && t > s0)
-    n -= floor_sum(t - s0, p.nr, kUnitKeys, s0 * kUnitKeys - p.off);
-  return n;
-}
-
 bool supported(int64_t B, int64_t Lq, int64_t Lk, int32_t n_q, int32_t n_kv, int32_t d_h) {
   if ((d_h != 64 && d_h != 128) || n_q / n_kv > kRows) return false;
   constexpr int64_t kMost = int64_t{1} << 30;
@@ -1232,25 +1191,9 @@ attn_status_t attn_key_weights_fwd(const void* q, const void* k, const float* ls
   p.c = scale * kLog2e;
   p.spin_limit = 1ll << 31;   // about a second at 2 GHz
 
-  // equal ranges of the steps of all units
-  const int64_t per_group = steps_before(p, p.T), W = per_group * B * n_kv;
-  p.G = static_cast<int>(W < kCtas ? W : kCtas);
   Starts st;
-  bool cut = false;
-  for (int c = 0; c < p.G; ++c) {
-    const int64_t x = c * W / p.G;
-    st.count[c] = static_cast<int>((c + 1) * W / p.G - x);
-    const int64_t grp = x / per_group, rest = x - grp * per_group;
-    int64_t lo = 0, hi = p.T;                     // the unit that holds step `rest`
-    while (hi - lo > 1) {
-      const int64_t mid = (lo + hi) / 2;
-      (steps_before(p, mid) <= rest ? lo : hi) = mid;
-    }
-    const int first = first_step(static_cast<int>(lo), p.off, p.nr, causal);
-    st.unit[c] = static_cast<int>(grp * p.T + lo);
-    st.step[c] = first + static_cast<int>(rest - steps_before(p, lo));
-    cut |= st.step[c] != first;
-  }
+  bool cut;
+  p.G = cut_ranges({p.off, p.nr, p.steps, p.T, causal}, B * n_kv, &st, &cut);
 
   CUtensorMap mq, mk;
   if (!encode(&mq, q, d_h, n_q, Lq, B, p.g, p.nr) || !encode(&mk, k, d_h, n_kv, Lk, B, 1, kUnitKeys))
