@@ -121,3 +121,57 @@ def test_query_rows_that_stay(case, causal):
     got = before.clone()
     attn_key_weights(q, k, lse, causal=causal, weights=got, accumulate=True)
     check(q, k, lse, got, causal, cuts, before=before)
+
+
+# whole units of several steps, and several units a CTA, beside units that are cut
+WHOLE = [
+    # B, Lq, Lk, n_q, n_kv, d
+    (40, 513, 513, 16, 4, 128),     # 17 steps a unit, g = 4
+    (40, 300, 900, 16, 4, 64),      # a chunk
+    (120, 257, 400, 12, 2, 64),     # g = 6
+    (60, 200, 300, 40, 5, 128),     # g = 8
+]
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("case", WHOLE, ids=lambda c: "B%d_%dx%d_q%d_kv%d_d%d" % c)
+def test_whole_units_of_several_steps(case, causal):
+    """Units that one CTA sums alone, step after step, written and added to."""
+    B, Lq, Lk, n_q, n_kv, d = case
+    cuts, units = ranges(B, Lq, Lk, n_q, n_kv, causal)
+    assert units[0].stop > RING[d]                  # the rows pass through the ring
+    alone = sum(len(u) > 1 and [s for h2, t2, s in r if (h2, t2) == (h, t)] == list(u)
+                for r in cuts for h, t in dict.fromkeys((h, t) for h, t, _ in r)
+                for u in [units[t]])
+    assert alone > CTAS and len(units) * B * n_kv > alone
+    q, k, lse = inputs(*case, causal, seed=sum(case))
+    first = attn_key_weights(q, k, lse, causal=causal)
+    assert attn_device_check() == ATTN_OK
+    check(q, k, lse, first, causal, cuts)
+    before = torch.rand(first.shape, device="cuda", generator=torch.Generator("cuda").manual_seed(2))
+    got = before.clone()
+    attn_key_weights(q, k, lse, causal=causal, weights=got, accumulate=True)
+    check(q, k, lse, got, causal, cuts, before=before)
+
+
+@pytest.mark.parametrize("n_q", [8, 32])
+def test_many_steps_in_one_sum(n_q):
+    """Few keys and many rows: hundreds of steps of one unit in one CTA."""
+    case = (1, 16384, 16384, n_q, 2, 64)
+    cuts, _ = ranges(*case[:5], True)
+    assert max(len(r) for r in cuts) > 200
+    q, k, lse = inputs(*case, True, seed=n_q)
+    got = attn_key_weights(q, k, lse).double()
+    assert attn_device_check() == ATTN_OK
+    keys = torch.tensor([0, 1, 255, 256, 5000, 8191, 16000, 16383], device="cuda")
+    size = 64 ** -0.5 * (q.float().norm(dim=3).max() * k.float().norm(dim=3).max()).item()
+    rel = (66 * 2.0 ** -24 * size + 2.0 ** -22 * (size + lse.abs().max().item()) + 2.0 ** -22
+           + additions(cuts) * 2.0 ** -24)
+    g, rows = n_q // 2, torch.arange(16384, device="cuda")
+    for u in range(2):
+        ref = torch.zeros(len(keys), dtype=torch.float64, device="cuda")
+        for h in range(g * u, g * u + g):
+            s = q[0, :, h].double() @ k[0, keys, u].double().T * 64 ** -0.5
+            p = torch.exp(s - lse[0, h].double()[:, None])
+            ref += torch.where(keys[None] <= rows[:, None], p, 0.0).sum(0)
+        assert ((got[0, u, keys] - ref).abs() <= rel * ref).all()
