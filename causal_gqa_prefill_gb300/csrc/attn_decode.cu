@@ -433,14 +433,13 @@ attn_decode_split_kernel(const __grid_constant__ CUtensorMap tmQ,
           }
         }
       }
-      if (!ok) {
-        // Let every copy this thread started land before the CTA can exit.
-        for (uint32_t s = 0; s < kQBufs && s < qn; ++s)
-          drain_wait(smem_addr(&ctl.q_full[s]), ((qn - 1 - s) / kQBufs) & 1, p);
-        for (uint32_t s = 0; s < kRing && s < it; ++s) {
-          const uint32_t last = s + ((it - 1 - s) / kRing) * kRing;
-          drain_wait(smem_addr(&ctl.full[s]), (last / kRing) & 1, p);
-        }
+      // Let every copy this thread started land before the CTA can exit, also
+      // where another role has given up.
+      for (uint32_t s = 0; s < kQBufs && s < qn; ++s)
+        drain_wait(smem_addr(&ctl.q_full[s]), ((qn - 1 - s) / kQBufs) & 1, p);
+      for (uint32_t s = 0; s < kRing && s < it; ++s) {
+        const uint32_t last = s + ((it - 1 - s) / kRing) * kRing;
+        drain_wait(smem_addr(&ctl.full[s]), (last / kRing) & 1, p);
       }
     }
   } else if (warp == kMmaWarp) {

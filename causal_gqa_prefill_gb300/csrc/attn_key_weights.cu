@@ -477,16 +477,14 @@ __device__ void load_role(const CUtensorMap* tmQ, const CUtensorMap* tmK, Ctl& c
       }
     }
   }
-  if (!ok) {
-    // let every copy this thread started land before the CTA can exit: the last
-    // use of each buffer
-    for (uint32_t s = 0; s < 2 && s < kn; ++s)
-      drain_wait(smem_addr(&ctl.k_full[s]), ((kn - 1 - s) >> 1) & 1, p);
-    for (int s = 0; s < G::kQStages; ++s) {
-      const uint32_t uses = stay ? (s < p.steps ? gn + (s < begun ? 1u : 0u) : 0u)
-                                 : (qn + G::kQStages - 1 - s) / G::kQStages;
-      if (uses > 0) drain_wait(smem_addr(&ctl.q_full[s]), (uses - 1) & 1, p);
-    }
+  // let every copy this thread started land before the CTA can exit, also where
+  // another role has given up: the last use of each buffer
+  for (uint32_t s = 0; s < 2 && s < kn; ++s)
+    drain_wait(smem_addr(&ctl.k_full[s]), ((kn - 1 - s) >> 1) & 1, p);
+  for (int s = 0; s < G::kQStages; ++s) {
+    const uint32_t uses = stay ? (s < p.steps ? gn + (s < begun ? 1u : 0u) : 0u)
+                               : (qn + G::kQStages - 1 - s) / G::kQStages;
+    if (uses > 0) drain_wait(smem_addr(&ctl.q_full[s]), (uses - 1) & 1, p);
   }
 }
 
@@ -833,13 +831,12 @@ key_weights_few_rows_kernel(const __grid_constant__ CUtensorMap tmQ,
                         (sg.t0 + t) * kWinKeys, b);
         }
       }
-      if (!ok) {
-        // let every copy this thread started land before the CTA can exit
-        for (uint32_t q = 0; q < static_cast<uint32_t>(p.bufs) && q < seg; ++q)
-          drain_wait(smem_addr(&ctl.q_full[q]), ((seg - 1 - q) / p.bufs) & 1, p);
-        for (uint32_t s = 0; s < G::kRing && s < it; ++s)
-          drain_wait(smem_addr(&ctl.k_full[s]), ((it - 1 - s) / G::kRing) & 1, p);
-      }
+      // let every copy this thread started land before the CTA can exit, also where
+      // another role has given up
+      for (uint32_t q = 0; q < static_cast<uint32_t>(p.bufs) && q < seg; ++q)
+        drain_wait(smem_addr(&ctl.q_full[q]), ((seg - 1 - q) / p.bufs) & 1, p);
+      for (uint32_t s = 0; s < G::kRing && s < it; ++s)
+        drain_wait(smem_addr(&ctl.k_full[s]), ((it - 1 - s) / G::kRing) & 1, p);
     }
   } else if (warp == kMmaWarp) {
     const bool leader = elect_one();

@@ -215,12 +215,11 @@ __device__ void load_role(const CUtensorMap* tmQ, const CUtensorMap* tmK, const 
       }
     }
   }
-  if (!ok) {
-    // let every copy this thread started land before the CTA can exit
-    if (qn) drain_wait(qbar, (qn - 1) & 1, p);
-    for (uint32_t s = 0; s < kRing && s < it; ++s)
-      drain_wait(smem_addr(&ctl.full[s]), ((it - 1 - s) / kRing) & 1, p);
-  }
+  // let every copy this thread started land before the CTA can exit, also where
+  // another role has given up
+  if (qn) drain_wait(qbar, (qn - 1) & 1, p);
+  for (uint32_t s = 0; s < kRing && s < it; ++s)
+    drain_wait(smem_addr(&ctl.full[s]), ((it - 1 - s) / kRing) & 1, p);
 }
 
 __device__ void mma_role(Ctl& ctl, const Params& p, uint32_t tmem, uint32_t sQ, uint32_t sKV) {
