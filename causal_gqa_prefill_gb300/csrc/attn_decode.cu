@@ -666,6 +666,11 @@ attn_decode_split_kernel(const __grid_constant__ CUtensorMap tmQ,
           ok = false;
           break;
         }
+        // P is rounded to bf16, as in the prefill: V is bf16 and both operands of a
+        // product have one type. Two halves of 8 bits (P and what its rounding
+        // leaves) would double the second product and P's stores to take the error
+        // of O from 2.4e-3 to the 1.7e-3 of O's own rounding. The row sum keeps the
+        // unrounded e, and so do the weights of the ragged step (from the scores).
         uint8_t* pb = pgen + (gt & 1) * kPBytes + p_chunk + p_byte;
 #pragma unroll
         for (int h = 0; h < GP; ++h) {

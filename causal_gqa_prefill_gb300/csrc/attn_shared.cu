@@ -369,7 +369,11 @@ __device__ void softmax_role(int slot, Ctl& ctl, const Params& p, uint32_t tmem)
         m_run = m_new;
       }
       // P = 2^(c s - m), bf16 pairs over the scores' first columns (every score
-      // of the row is in registers); the row sum keeps the unrounded values
+      // of the row is in registers); the row sum keeps the unrounded values. bf16
+      // because V is (both operands of a product have one type): a second product
+      // with what the rounding leaves would make a kernel that the tensor cores
+      // bound half as long again, to take the error of O from 2.4e-3 to the 1.7e-3
+      // of O's own rounding.
       const float m_use = (m_run == -INFINITY) ? 0.0f : m_run;
       const uint64_t negm2 = f32x2_pack(-m_use, -m_use);
       uint64_t sum2 = f32x2_pack(0.0f, 0.0f);
