@@ -737,6 +737,42 @@ struct WinWalk {
   }
 };
 
+// a0, a1 += 2^(c s + nl) for the 32 columns whose scores are in s. Column i of them is
+// column col0 + i of those that may see the key; with kSeen or kWeighted only the first
+// `seen` (from 0 on) count, with kWeighted only rows that have a weight: an infinite key
+// or a query that may be anything makes the others' scores NaN. (The loop is chosen for
+// 32 columns at once: branches inside it, also uniform ones that are not taken, cost the
+// kernel 42 us instead of 38.)
+enum Columns { kAll, kSeen, kWeighted };
+template <Columns kWhich>
+__device__ __forceinline__ void add_columns(uint64_t& a0, uint64_t& a1, const uint32_t (&s)[32],
+                                            const float* nl, uint64_t c2, int col0,
+                                            unsigned int seen) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 4) {
+    const float4 l = *reinterpret_cast<const float4*>(nl + i);
+    float x0, x1, x2, x3;
+    f32x2_unpack(ffma2(f32x2_pack(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), c2,
+                       f32x2_pack(l.x, l.y)), x0, x1);
+    f32x2_unpack(ffma2(f32x2_pack(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3])), c2,
+                       f32x2_pack(l.z, l.w)), x2, x3);
+    float e0 = ex2_approx(x0), e1 = ex2_approx(x1), e2 = ex2_approx(x2), e3 = ex2_approx(x3);
+    if (kWhich != kAll) {
+      const int col = col0 + i;
+      if (static_cast<unsigned int>(col) >= seen || (kWhich == kWeighted && l.x == kNoWeight))
+        e0 = 0.0f;
+      if (static_cast<unsigned int>(col + 1) >= seen || (kWhich == kWeighted && l.y == kNoWeight))
+        e1 = 0.0f;
+      if (static_cast<unsigned int>(col + 2) >= seen || (kWhich == kWeighted && l.z == kNoWeight))
+        e2 = 0.0f;
+      if (static_cast<unsigned int>(col + 3) >= seen || (kWhich == kWeighted && l.w == kNoWeight))
+        e3 = 0.0f;
+    }
+    a0 = fadd2(a0, f32x2_pack(e0, e1));
+    a1 = fadd2(a1, f32x2_pack(e2, e3));
+  }
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 key_weights_few_rows_kernel(const __grid_constant__ CUtensorMap tmQ,
@@ -936,31 +972,13 @@ key_weights_few_rows_kernel(const __grid_constant__ CUtensorMap tmQ,
             if (lane == 0) mbar_arrive(smem_addr(&ctl.s_free[buf]));
           }
           const float* nl = nl_buf + 32 * ch;
-#pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            const float4 l = *reinterpret_cast<const float4*>(nl + i);
-            float x0, x1, x2, x3;
-            f32x2_unpack(ffma2(f32x2_pack(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), c2,
-                               f32x2_pack(l.x, l.y)), x0, x1);
-            f32x2_unpack(ffma2(f32x2_pack(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3])), c2,
-                               f32x2_pack(l.z, l.w)), x2, x3);
-            float e0 = ex2_approx(x0), e1 = ex2_approx(x1), e2 = ex2_approx(x2), e3 = ex2_approx(x3);
-            if (mask) {
-              const int col = 32 * ch + i - from;
-              if (static_cast<unsigned int>(col) >= seen) e0 = 0.0f;
-              if (static_cast<unsigned int>(col + 1) >= seen) e1 = 0.0f;
-              if (static_cast<unsigned int>(col + 2) >= seen) e2 = 0.0f;
-              if (static_cast<unsigned int>(col + 3) >= seen) e3 = 0.0f;
-            }
-            if (without) {      // (their queries may be anything, and their scores NaN)
-              if (l.x == kNoWeight) e0 = 0.0f;
-              if (l.y == kNoWeight) e1 = 0.0f;
-              if (l.z == kNoWeight) e2 = 0.0f;
-              if (l.w == kNoWeight) e3 = 0.0f;
-            }
-            a0 = fadd2(a0, f32x2_pack(e0, e1));
-            a1 = fadd2(a1, f32x2_pack(e2, e3));
-          }
+          const int col0 = 32 * ch - from;
+          if (without)
+            add_columns<kWeighted>(a0, a1, s, nl, c2, col0, seen);
+          else if (mask)
+            add_columns<kSeen>(a0, a1, s, nl, c2, col0, seen);
+          else
+            add_columns<kAll>(a0, a1, s, nl, c2, col0, seen);
         }
         if (c_from == c_to) {                              // a single piece: nothing for this half
           __syncwarp();
