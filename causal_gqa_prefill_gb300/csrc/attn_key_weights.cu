@@ -32,8 +32,9 @@
 //
 // S is double-buffered (all 512 TMEM columns), so the product of a step runs
 // under the exponentials of the one before; both take 1024 clocks a step, the
-// exponentials at 32 a clock and SM. Measured, 8192-token 32-head layer: 186 us,
-// both pipes busy 65 % of it. Without any sums it is 147: both operands come from
+// exponentials at 32 a clock and SM. Measured, 8192-token 32-head layer, calls back to
+// back on one set of inputs (as all times in these comments): 186 us, both pipes busy
+// 66 % of it; 200 with inputs from memory. Without any sums it is 147: both operands come from
 // shared memory and the next Q tile arrives in it, which fills its bandwidth (two
 // products of 128 keys, which read the rows twice: 198). The rest is the latency of
 // load, exponential and addition, which four warps a scheduler and 32 scores at a
@@ -664,7 +665,9 @@ key_weights_reduce_kernel(const __grid_constant__ Params p, const __grid_constan
 // their -lse2 stay in shared memory for as long as the head stays the same.
 // (The kernel above spends about as long folding 128 rows into one as on a
 // unit's two steps: 32 rows of 6 heads against 131072 keys of 6 K/V heads, 70 us
-// there and 43 here; K alone is 30 us at the measured copy rate.)
+// there and 38 here; K alone is 30 us at the measured copy rate. Nothing is full: 61 %
+// of the memory's rate, 45 % of the tensor cores', 46 % of the exponential unit's; the
+// warps wait for a tile's scores, its exponentials and one another.)
 //
 // The key tiles of all heads are cut into equal ranges, one per CTA. Two S^T
 // buffers of 256 columns; of the four warpgroups two take each buffer's tiles,
