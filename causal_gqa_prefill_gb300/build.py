@@ -16,6 +16,7 @@ import os
 import shutil
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -65,6 +66,12 @@ def _stale(out: str) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _run(cmd) -> tuple:
+    """(did it succeed, the command and what it printed)"""
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    return res.returncode == 0, " ".join(cmd) + "\n" + res.stdout + res.stderr
+
+
 def build(force: bool = False, verbose: bool = False, debug: bool = False) -> str:
     """Compile the library (the ATTN_DEBUG one with ``debug``) if it is missing
     or older than its sources; return its path."""
@@ -73,29 +80,36 @@ def build(force: bool = False, verbose: bool = False, debug: bool = False) -> st
         return out
     os.makedirs(LIBDIR, exist_ok=True)
     tmp = out + ".tmp%d" % os.getpid()
-    cmd = [_nvcc(), "-shared", "-Xcompiler", "-fPIC", "-O3", "-std=c++17", "-lineinfo", ARCH,
-           "-Xptxas", "-v", "-I" + INCLUDE, "-I" + CSRC]
+    common = [_nvcc(), "-Xcompiler", "-fPIC", "-O3", "-std=c++17", "-lineinfo", ARCH, "-Xptxas", "-v",
+              "-I" + INCLUDE, "-I" + CSRC]
     if debug:
-        cmd.append("-DATTN_DEBUG")
-    cmd += [os.path.join(CSRC, s) for s in SOURCES]
-    cmd += ["-o", tmp]
-    res = subprocess.run(cmd, capture_output=True, text=True)
+        common.append("-DATTN_DEBUG")
+    # one object per source, compiled side by side, then linked
+    objects = [tmp + "." + os.path.splitext(src)[0] + ".o" for src in SOURCES]
+    steps = [common + ["-c", os.path.join(CSRC, src), "-o", obj]
+             for src, obj in zip(SOURCES, objects)]
+    with ThreadPoolExecutor(max_workers=len(steps)) as ex:
+        done = list(ex.map(_run, steps))
+    if all(ok for ok, _ in done):
+        done.append(_run([_nvcc(), "-shared", ARCH, "-o", tmp] + objects))
     with open(os.path.join(LIBDIR, "ptxas_debug.log" if debug else "ptxas.log"), "w") as f:
-        f.write(" ".join(cmd) + "\n" + res.stdout + res.stderr)
-    if res.returncode != 0:
+        f.write("".join(text for _, text in done))
+    for path in objects:
+        if os.path.exists(path):
+            os.remove(path)
+    failed = [text for ok, text in done if not ok]
+    if failed:
         if os.path.exists(tmp):
             os.remove(tmp)
-        raise RuntimeError("nvcc failed:\n" + res.stderr[-4000:])
+        raise RuntimeError("nvcc failed:\n" + failed[0][-4000:])
     os.replace(tmp, out)
     if verbose:
-        print(res.stderr)
+        print("".join(text for _, text in done))
     return out
 
 
 def build_all(force: bool = False) -> tuple:
     """Both libraries, compiled in parallel; returns (release path, debug path)."""
-    from concurrent.futures import ThreadPoolExecutor
-
     with ThreadPoolExecutor(max_workers=2) as ex:
         rel = ex.submit(build, force, False, False)
         dbg = ex.submit(build, force, False, True)
