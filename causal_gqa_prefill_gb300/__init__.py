@@ -17,6 +17,9 @@ from .api import (AttnError, attn_cache_evict, attn_decode, attn_decode_fwd, att
                   attn_prefill, attn_prefill_fp8, attn_prefill_fwd, attn_prefill_fwd_chunk,
                   attn_prefill_fwd_fp8, attn_device_check, attn_prefill_grid_size,
                   attn_prefill_backward, attn_prefill_bwd, attn_prefill_bwd_workspace_bytes,
+                  attn_prefill_window, attn_prefill_window_fwd, attn_prefill_window_backward,
+                  attn_prefill_window_bwd, attn_prefill_window_bwd_workspace_bytes,
+                  attn_decode_window, attn_decode_window_fwd, attn_decode_window_workspace_bytes,
                   attn_selftest_wait_timeout, attn_selftest_wait_timeout_noalloc,
                   attn_prefill_fwd_host,
                   attn_prefill_host_staging_bytes)
@@ -31,5 +34,8 @@ __all__ = [
     "attn_key_weights_fwd", "attn_key_weights_workspace_bytes", "attn_device_check", "attn_prefill_backward",
     "attn_prefill_bwd", "attn_prefill_bwd_workspace_bytes", "attn_selftest_wait_timeout",
     "attn_selftest_wait_timeout_noalloc", "attn_prefill_fwd_host", "attn_prefill_host_staging_bytes",
+    "attn_prefill_window", "attn_prefill_window_fwd", "attn_prefill_window_backward",
+    "attn_prefill_window_bwd", "attn_prefill_window_bwd_workspace_bytes", "attn_decode_window",
+    "attn_decode_window_fwd", "attn_decode_window_workspace_bytes",
     "attn_prefill_grid_size", "load_library", "library_path", "status_string",
 ]

@@ -77,6 +77,19 @@ _SIGNATURES = {
                                         ctypes.c_int64, ctypes.c_int64, ctypes.c_int32,
                                         ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
                                         ctypes.c_float, ctypes.c_void_p]),
+    "attn_prefill_window_fwd": (ctypes.c_int, [ctypes.c_void_p] * 5 + [ctypes.c_int64] * 3
+                                + [ctypes.c_int32] * 3 + [ctypes.c_int64] * 2
+                                + [ctypes.c_float, ctypes.c_void_p]),
+    "attn_prefill_window_bwd_workspace_bytes": (ctypes.c_int64, [ctypes.c_int64] * 2
+                                                + [ctypes.c_int32] * 3 + [ctypes.c_int64] * 2),
+    "attn_prefill_window_bwd": (ctypes.c_int, [ctypes.c_void_p] * 10 + [ctypes.c_int64] * 3
+                                + [ctypes.c_int32] * 3 + [ctypes.c_int64] * 2
+                                + [ctypes.c_float, ctypes.c_void_p]),
+    "attn_decode_window_workspace_bytes": (ctypes.c_int64, [ctypes.c_int64] * 2
+                                           + [ctypes.c_int32] * 3 + [ctypes.c_int64] * 2),
+    "attn_decode_window_fwd": (ctypes.c_int, [ctypes.c_void_p] * 7 + [ctypes.c_int64] * 3
+                               + [ctypes.c_int32] * 3 + [ctypes.c_int64] * 2
+                               + [ctypes.c_float, ctypes.c_void_p]),
     "attn_selftest_wait_timeout": (ctypes.c_int, [ctypes.c_int64, ctypes.c_void_p]),
     "attn_selftest_wait_timeout_noalloc": (ctypes.c_int, [ctypes.c_int64, ctypes.c_void_p]),
     "attn_prefill_host_staging_bytes": (ctypes.c_int64, [ctypes.c_int64, ctypes.c_int64,

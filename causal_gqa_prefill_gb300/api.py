@@ -9,6 +9,7 @@ runs entirely in the CUDA library, and a status other than ATTN_OK raises.
 from __future__ import annotations
 
 import math
+import operator
 
 from . import _abi
 
@@ -609,6 +610,221 @@ def attn_prefill_backward(q, k, v, o, lse, dout, *, causal=True, scale=None, wor
     if st != _abi.ATTN_OK:
         raise AttnError(st, "attn_prefill_bwd")
     return dq, dk, dv
+
+
+_SIZE_LIMIT = 1 << 30      # positions that the library indexes; a larger window hides nothing either
+
+
+def _window(window, sinks):
+    """(window, sinks) as the library takes them."""
+    window, sinks = operator.index(window), operator.index(sinks)
+    if window < 1 or sinks < 0:
+        raise ValueError("window must be at least 1 and sinks at least 0")
+    return min(window, _SIZE_LIMIT), min(sinks, _SIZE_LIMIT)
+
+
+def attn_prefill_window_fwd(q, k, v, o, lse, B, Lq, Lk, n_q, n_kv, d_h, window, sinks, scale,
+                            stream=None) -> int:
+    """Direct call of the windowed forward C entry point; returns the raw status code."""
+    lib = _abi.load()
+    return int(lib.attn_prefill_window_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), int(B),
+                                           int(Lq), int(Lk), int(n_q), int(n_kv), int(d_h),
+                                           int(window), int(sinks), float(scale),
+                                           _stream_handle(stream)))
+
+
+def attn_prefill_window(q, k, v, window, sinks=0, *, scale=None, out=None, lse=None, stream=None):
+    """Causal attention behind a sliding window with sinks: the row at position p sees
+    the keys j <= p with j > p - window (the last ``window`` positions, its own
+    among them) or j < sinks (the first ones, which stay visible).
+
+    q bf16 [B, Lq, n_q, d], k/v bf16 [B, Lk, n_kv, d], d 64 or 128, rows the last
+    Lq of the Lk positions. Returns (o bf16 [B, Lq, n_q, d], lse fp32 [B, n_q, Lq]).
+    Positions that no row of the call sees may hold anything."""
+    import torch
+
+    bf16, f32 = torch.bfloat16, torch.float32
+    window, sinks = _window(window, sinks)
+    try:
+        B, Lq, n_q, d = q.shape
+        _, Lk, n_kv, _ = k.shape
+        index = q.get_device()
+        usual = (v.shape == k.shape == (B, Lk, n_kv, d) and Lk >= Lq
+                 and (out is None or out.shape == q.shape)
+                 and (lse is None or lse.shape == (B, n_q, Lq))
+                 and _laid_out(index, bf16, q, k, v, out) and _laid_out(index, f32, lse))
+    except (AttributeError, ValueError):
+        usual = False
+    if not usual:
+        B, Lq, n_q, d = _heads_of("q", q, None, None, bf16)
+        dev = q.device
+        _, Lk, n_kv, dk = _heads_of("k", k, B, None, bf16, dev)
+        if dk != d:
+            raise ValueError("q and k must have the same d_h")
+        if Lk < Lq:
+            raise ValueError("k must hold at least as many positions as q has rows")
+        _cuda_tensor("v", v, k.shape, bf16, dev)
+        if out is not None:
+            _cuda_tensor("out", out, q.shape, bf16, dev)
+        if lse is not None:
+            _cuda_tensor("lse", lse, (B, n_q, Lq), f32, dev)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    with _Call(torch, q.device, stream) as call:
+        if out is None:
+            out = call.empty(q.shape, bf16)
+        if lse is None:
+            lse = call.empty((B, n_q, Lq), f32)
+        st = _abi.load().attn_prefill_window_fwd(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), B, Lq, Lk,
+            n_q, n_kv, d, window, sinks, scale, call.handle)
+    if st != _abi.ATTN_OK:
+        raise AttnError(st, "attn_prefill_window_fwd")
+    return out, lse
+
+
+def attn_prefill_window_bwd_workspace_bytes(B, L, n_q, n_kv, d_h=128, window=1, sinks=0) -> int:
+    return int(_abi.load().attn_prefill_window_bwd_workspace_bytes(
+        int(B), int(L), int(n_q), int(n_kv), int(d_h), int(window), int(sinks)))
+
+
+def attn_prefill_window_bwd(q, k, v, o, lse, dout, dq, dk, dv, workspace, workspace_bytes, B, L,
+                            n_q, n_kv, d_h, window, sinks, scale, stream=None) -> int:
+    """Direct call of the windowed backward C entry point; returns the raw status code."""
+    lib = _abi.load()
+    return int(lib.attn_prefill_window_bwd(
+        _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dout), _ptr(dq), _ptr(dk), _ptr(dv),
+        _ptr(workspace), int(workspace_bytes), int(B), int(L), int(n_q), int(n_kv), int(d_h),
+        int(window), int(sinks), float(scale), _stream_handle(stream)))
+
+
+def attn_prefill_window_backward(q, k, v, o, lse, dout, window, sinks=0, *, scale=None,
+                                 workspace=None, dq=None, dk=None, dv=None, stream=None):
+    """Gradients (dq, dk, dv) of attn_prefill_window (Lq = Lk = L) for the upstream
+    gradient ``dout``.
+
+    q, o, dout: bf16 [B, L, n_q, d]; k, v: bf16 [B, L, n_kv, d], d 64 or 128; lse:
+    the forward's fp32 [B, n_q, L]; window, sinks and scale the forward's.
+    ``workspace`` (at least attn_prefill_window_bwd_workspace_bytes bytes) is
+    allocated with torch when not given."""
+    import torch
+
+    bf16, f32 = torch.bfloat16, torch.float32
+    window, sinks = _window(window, sinks)
+    try:
+        B, L, n_q, d = q.shape
+        n_kv = k.shape[2]
+        index = q.get_device()
+        usual = (v.shape == k.shape == (B, L, n_kv, d) and o.shape == dout.shape == q.shape
+                 and lse.shape == (B, n_q, L) and (dq is None or dq.shape == q.shape)
+                 and (dk is None or dk.shape == k.shape) and (dv is None or dv.shape == k.shape)
+                 and _laid_out(index, bf16, q, k, v, o, dout, dq, dk, dv)
+                 and _laid_out(index, f32, lse))
+    except (AttributeError, ValueError, IndexError):
+        usual = False
+    if not usual:
+        B, L, n_q, d = _heads_of("q", q, None, None, bf16)
+        dev = q.device
+        n_kv = _heads_of("k", k, B, L, bf16, dev)[2]
+        _cuda_tensor("k", k, (B, L, n_kv, d), bf16, dev)
+        _cuda_tensor("lse", lse, (B, n_q, L), f32, dev)
+        for name, t, like in (("v", v, k), ("o", o, q), ("dout", dout, q)):
+            _cuda_tensor(name, t, like.shape, bf16, dev)
+        for name, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, k)):
+            if t is not None:
+                _cuda_tensor(name, t, like.shape, bf16, dev)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    with _Call(torch, q.device, stream) as call:
+        workspace, nbytes = call.workspace(workspace, attn_prefill_window_bwd_workspace_bytes, B, L,
+                                           n_q, n_kv, d, window, sinks)
+        dq = call.empty(q.shape, bf16) if dq is None else dq
+        dk = call.empty(k.shape, bf16) if dk is None else dk
+        dv = call.empty(k.shape, bf16) if dv is None else dv
+        st = _abi.load().attn_prefill_window_bwd(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
+            dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), workspace.data_ptr(),
+            nbytes, B, L, n_q, n_kv, d, window, sinks, scale, call.handle)
+    if st != _abi.ATTN_OK:
+        raise AttnError(st, "attn_prefill_window_bwd")
+    return dq, dk, dv
+
+
+def attn_decode_window_workspace_bytes(B, C, n_q, n_kv, d_h=128, window=1, sinks=0) -> int:
+    return int(_abi.load().attn_decode_window_workspace_bytes(
+        int(B), int(C), int(n_q), int(n_kv), int(d_h), int(window), int(sinks)))
+
+
+def attn_decode_window_fwd(q, k, v, lens, o, lse, workspace, workspace_bytes, B, C, n_q, n_kv, d_h,
+                           window, sinks, scale, stream=None) -> int:
+    """Direct call of the windowed decode C entry point; returns the raw status code."""
+    lib = _abi.load()
+    return int(lib.attn_decode_window_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(lens), _ptr(o),
+                                          _ptr(lse), _ptr(workspace), int(workspace_bytes), int(B),
+                                          int(C), int(n_q), int(n_kv), int(d_h), int(window),
+                                          int(sinks), float(scale), _stream_handle(stream)))
+
+
+def attn_decode_window(q, k, v, lens, window, sinks=0, *, scale=None, workspace=None, out=None,
+                       lse=None, stream=None):
+    """One decode step behind a sliding window with sinks: q bf16 [B, 1, n_q, 128], the
+    new token of each sequence, against the positions j < lens[b] of k/v bf16
+    [B, C, n_kv, 128] with j >= lens[b] - window or j < sinks (lens: int32 CUDA
+    tensor [B], clamped to 0 .. C; it counts the new token's own row).
+
+    Returns (o bf16 [B, 1, n_q, 128], lse fp32 [B, n_q, 1]); a sequence of
+    length 0 gets o = 0 and lse = -inf. ``workspace`` (at least
+    attn_decode_window_workspace_bytes bytes) is allocated with torch when not
+    given."""
+    import torch
+
+    window, sinks = _window(window, sinks)
+    B, C, n_q, n_kv, d = _step_sizes(torch, q, k, v, lens, out, lse)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    with _Call(torch, q.device, stream) as call:
+        workspace, nbytes = call.workspace(workspace, attn_decode_window_workspace_bytes, B, C, n_q,
+                                           n_kv, d, window, sinks)
+        if out is None:
+            out = call.empty(q.shape, torch.bfloat16)
+        if lse is None:
+            lse = call.empty((B, n_q, 1), torch.float32)
+        st = _abi.load().attn_decode_window_fwd(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), lens.data_ptr(), out.data_ptr(),
+            lse.data_ptr(), workspace.data_ptr(), nbytes, B, C, n_q, n_kv, d, window, sinks, scale,
+            call.handle)
+    if st != _abi.ATTN_OK:
+        raise AttnError(st, "attn_decode_window_fwd")
+    return out, lse
+
+
+def _step_sizes(torch, q, k, v, lens, out, lse):
+    """(B, C, n_q, n_kv, d) of a decode step's checked tensors."""
+    bf16, f32 = torch.bfloat16, torch.float32
+    try:
+        B, one, n_q, d = q.shape
+        _, C, n_kv, _ = k.shape
+        index = q.get_device()
+        if (one == 1 and v.shape == k.shape == (B, C, n_kv, d) and lens.shape == (B,)
+                and (out is None or out.shape == q.shape)
+                and (lse is None or lse.shape == (B, n_q, 1))
+                and _laid_out(index, bf16, q, k, v, out) and _laid_out(index, f32, lse)
+                and _laid_out(index, torch.int32, lens)):
+            return B, C, n_q, n_kv, d
+    except (AttributeError, ValueError):
+        pass
+    B, _, n_q, d = _heads_of("q", q, None, 1, bf16)
+    dev = q.device
+    _, C, n_kv, dk = _heads_of("k", k, B, None, bf16, dev)
+    if dk != d:
+        raise ValueError("q and k must have the same d_h")
+    _cuda_tensor("v", v, k.shape, bf16, dev)
+    _cuda_tensor("lens", lens, (B,), torch.int32, dev)
+    if out is not None:
+        _cuda_tensor("out", out, q.shape, bf16, dev)
+    if lse is not None:
+        _cuda_tensor("lse", lse, (B, n_q, 1), f32, dev)
+    return B, C, n_q, n_kv, d
 
 
 def attn_device_check(stream=None) -> int:

@@ -29,6 +29,13 @@
 // N = 128 (or D) wide, and order their products so that the tensor cores run
 // the next tile's scores while the compute warps turn this tile's into P/dS.
 //
+// Sliding window with sinks (kWin instances; a row at position p sees keys j <= p
+// with j > p - W or j < S): a key tile meets only the query tiles whose windows
+// reach it and a query tile only the sinks' and its window's key tiles. Key tiles
+// that hold a sink are seen by every later row; they come first, each cut into
+// `pieces` CTAs of equal runs of (head, query tile) steps, which write fp32 parts
+// that a join kernel adds in order (no atomics).
+//
 // Each kernel has a TMA producer warp, an MMA warp (warp-wide loop, one elected
 // issuing lane) and kComputeWGs compute warpgroups that split the 128 columns
 // of a tile (thread = TMEM lane = tile row; warpgroup w owns columns
@@ -82,7 +89,69 @@ struct BwdParams {
   uint16_t* dv;
   int* status;
   int q_units;              // dQ work units: B * n_q * T query tiles
+  // kWin instances
+  int window, sinks;        // W and S, both at most L
+  int heavy, pieces;        // key tiles that hold a sink, and CTAs per such tile
+  float* parts;             // fp32 [groups * heavy][pieces][dV, dK][128][D] (pieces > 1)
 };
+
+// The key tiles that query tile i sees, in order: tiles [0, na), which hold sinks
+// before its window, then tiles lo .. i.
+struct SeenTiles {
+  int na, lo, n;
+};
+template <bool kWin>
+__device__ __forceinline__ SeenTiles seen_tiles(int i, const BwdParams& p) {
+  if (!kWin) return {0, 0, p.causal ? i + 1 : p.T};
+  SeenTiles x;
+  x.lo = max(0, i * kT - p.window + 1) / kT;
+  x.na = min(p.heavy, x.lo);
+  x.n = x.na + i - x.lo + 1;
+  return x;
+}
+template <bool kWin>
+__device__ __forceinline__ int seen_tile(const SeenTiles& x, int t) {
+  return !kWin || t < x.na ? t : t - x.na + x.lo;
+}
+
+// One CTA's work in the dK/dV kernel: steps first .. first + n - 1 of the
+// (head, query tile) pairs of key tile j, `per_head` query tiles from i0 on each.
+struct KeyWork {
+  int j, grp, i0, per_head, first, n, piece;
+};
+template <bool kWin>
+__device__ __forceinline__ KeyWork key_work(const BwdParams& p) {
+  KeyWork w;
+  if (!kWin) {
+    const int groups = static_cast<int>(gridDim.x) / p.T;
+    w.j = blockIdx.x / groups;                        // ascending = most work first
+    w.grp = blockIdx.x - w.j * groups;
+    w.i0 = p.causal ? w.j : 0;
+    w.per_head = p.T - w.i0;
+    w.first = 0;
+    w.n = p.g * w.per_head;
+    w.piece = 0;
+    return w;
+  }
+  const int rows = p.heavy * p.pieces + p.T - p.heavy;
+  const int groups = static_cast<int>(gridDim.x) / rows;
+  const int slot = blockIdx.x / groups;
+  w.grp = blockIdx.x - slot * groups;
+  const bool heavy = slot < p.heavy * p.pieces;
+  w.j = heavy ? slot / p.pieces : slot - p.heavy * p.pieces + p.heavy;
+  w.piece = heavy ? slot - w.j * p.pieces : 0;
+  w.i0 = w.j;
+  // the last row that sees the tile's last key
+  const int last = heavy ? p.T - 1
+                         : static_cast<int>(min(static_cast<long long>(p.T) - 1,
+                               (static_cast<long long>(w.j) * kT + kT - 1 + p.window - 1) / kT));
+  w.per_head = last - w.i0 + 1;
+  const long long total = static_cast<long long>(p.g) * w.per_head;
+  w.first = heavy ? static_cast<int>(total * w.piece / p.pieces) : 0;
+  w.n = (heavy ? static_cast<int>(total * (w.piece + 1) / p.pieces) : static_cast<int>(total)) -
+        w.first;
+  return w;
+}
 
 constexpr int kStages = 3;               // dQ: ring of streamed K/V tiles
 constexpr int kStagesKV = 2;             // dK/dV: ring of streamed Q/dO tiles (V_j is resident)
@@ -281,14 +350,27 @@ __device__ __forceinline__ void store_chunk(uint32_t taddr, uint16_t* dst, float
   }
 }
 
+// The same 32 columns times `mul`, kept in fp32.
+__device__ __forceinline__ void store_chunk_f32(uint32_t taddr, float* dst, float mul) {
+  uint32_t v[32];
+  tmem_ld32(taddr, v);
+  tmem_wait_ld(v);
+  float4* d4 = reinterpret_cast<float4*>(dst);
+#pragma unroll
+  for (int q = 0; q < 8; ++q)
+    d4[q] = make_float4(__uint_as_float(v[4 * q]) * mul, __uint_as_float(v[4 * q + 1]) * mul,
+                        __uint_as_float(v[4 * q + 2]) * mul, __uint_as_float(v[4 * q + 3]) * mul);
+}
+
 // dK/dV phase 1 for one warpgroup: P^T = 2^(c S^T + nl) for its kColsQ query
 // columns of this thread's key row (S^T read from TMEM at `taddr`, the row
 // statistics nl from shared memory), kept in `pr` and written back as bf16
 // over the first consumed columns. kMask: the diagonal tile, where query
-// column q0 + k is masked when q0 + k < r (q_minus_r = q0 - r).
-template <bool kMask>
+// column q0 + k is masked when q0 + k < r (q_minus_r = q0 - r). kWin: or when
+// it is past the last row that sees the key (q_to_end, from q0 on).
+template <bool kMask, bool kWin>
 __device__ __forceinline__ void pt_from_st(uint32_t taddr, const float4* nl4, uint64_t c2,
-                                           int q_minus_r, float (&pr)[kColsQ]) {
+                                           int q_minus_r, int q_to_end, float (&pr)[kColsQ]) {
 #pragma unroll
   for (int cc = 0; cc < kColsQ / 32; ++cc) {
     uint32_t sv[32];
@@ -307,8 +389,8 @@ __device__ __forceinline__ void pt_from_st(uint32_t taddr, const float4* nl4, ui
         f32x2_unpack(x, x0, x1);
         float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
         if (kMask) {
-          if (q_minus_r + 32 * cc + jj < 0) p0 = 0.0f;
-          if (q_minus_r + 32 * cc + jj + 1 < 0) p1 = 0.0f;
+          if (q_minus_r + 32 * cc + jj < 0 || (kWin && 32 * cc + jj > q_to_end)) p0 = 0.0f;
+          if (q_minus_r + 32 * cc + jj + 1 < 0 || (kWin && 32 * cc + jj + 1 > q_to_end)) p1 = 0.0f;
         }
         pr[32 * cc + jj] = p0;
         pr[32 * cc + jj + 1] = p1;
@@ -322,9 +404,10 @@ __device__ __forceinline__ void pt_from_st(uint32_t taddr, const float4* nl4, ui
 // dQ phase 1 for one warpgroup: P = 2^(c S + nl) for its kColsQ key columns
 // [k0, k0 + kColsQ) of this thread's query row, kept in `pr`. kMask: keys
 // after in-tile index `keep` are masked (the diagonal tile, or keys past L).
-template <bool kMask>
+// kWin: so are those up to `out` (before the window) from `sink` on.
+template <bool kMask, bool kWin>
 __device__ __forceinline__ void p_from_s(uint32_t taddr, uint64_t c2, uint64_t nl2, int k0,
-                                         int keep, float (&pr)[kColsQ]) {
+                                         int keep, int out, int sink, float (&pr)[kColsQ]) {
 #pragma unroll
   for (int c = 0; c < kColsQ / 32; ++c) {
     uint32_t sv[32];
@@ -338,8 +421,9 @@ __device__ __forceinline__ void p_from_s(uint32_t taddr, uint64_t c2, uint64_t n
       f32x2_unpack(x, x0, x1);
       float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
       if (kMask) {
-        if (k0 + 32 * c + 2 * e > keep) p0 = 0.0f;
-        if (k0 + 32 * c + 2 * e + 1 > keep) p1 = 0.0f;
+        const int at = k0 + 32 * c + 2 * e;
+        if (at > keep || (kWin && at <= out && at >= sink)) p0 = 0.0f;
+        if (at + 1 > keep || (kWin && at + 1 <= out && at + 1 >= sink)) p1 = 0.0f;
       }
       pr[32 * c + 2 * e] = p0;
       pr[32 * c + 2 * e + 1] = p1;
@@ -441,7 +525,7 @@ __device__ __forceinline__ void drain_ring(Sync& sy, int issued) {
   }
 }
 
-template <int D>
+template <int D, bool kWin>
 __global__ void __launch_bounds__(kThreads, 1)
 dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmdO,
             const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -454,12 +538,11 @@ dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
   const uint32_t sK = base, sV = base + kTileBytes, sRing = base + 2 * kTileBytes;
   constexpr uint32_t kStage = 2 * kTileBytes + 1024;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int groups = static_cast<int>(gridDim.x) / p.T;
-  const int j = blockIdx.x / groups;                  // key tile (ascending = most work first)
-  const int grp = blockIdx.x - j * groups;
+  const KeyWork work = key_work<kWin>(p);
+  const int j = work.j, grp = work.grp;                // key tile, (sequence, K/V head)
   const int b = grp / p.n_kv, kvh = grp - b * p.n_kv;
-  const int i0 = p.causal ? j : 0;
-  const int nsteps = p.g * (p.T - i0);                 // (head, query tile) pairs
+  const int i0 = work.i0;
+  const int nsteps = work.n;                           // (head, query tile) pairs
   setup(sy);
   // Launched as the row kernel's programmatic dependent: the set-up above
   // overlaps its end; the row statistics are read only after it completed.
@@ -487,8 +570,8 @@ dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
       for (; t < nsteps; ++t) {
         const int st = t % kStagesKV, use = t / kStagesKV;
         if (use > 0 && !wait_bounded(smem_addr(&sy.empty[st]), (use - 1) & 1, sy, p)) break;
-        const int h = kvh * p.g + t / (p.T - i0);
-        const int i = i0 + t % (p.T - i0);
+        const int h = kvh * p.g + (work.first + t) / work.per_head;
+        const int i = i0 + (work.first + t) % work.per_head;
         const uint32_t dst = sRing + st * kStage, bar = smem_addr(&sy.full[st]);
         mbar_arrive_expect_tx(bar, 2 * kTileBytes + 1024);
         for (int c = 0; c < D / 64; ++c) {
@@ -560,7 +643,7 @@ dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
     bool ok = true;
     for (int t = 0; t < nsteps; ++t) {
       const int st = t % kStagesKV;
-      const int i = i0 + t % (p.T - i0);
+      const int i = i0 + (work.first + t) % work.per_head;
       if (!__all_sync(0xffffffffu, wait_bounded(smem_addr(&sy.s_full[0]), t & 1, sy, p)) ||
           // the staged row statistics arrived with the stage's copies
           !__all_sync(0xffffffffu,
@@ -578,8 +661,15 @@ dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
       float pr[kColsQ];
       // the causal mask only touches the diagonal tile: a separate copy of the
       // loop keeps its compares and selects out of every other tile
-      if (diag) pt_from_st<true>(lane_base + cS + q0, nl4, c2, q0 - r, pr);
-      else pt_from_st<false>(lane_base + cS + q0, nl4, c2, q0 - r, pr);
+      if (kWin && (i - j) * kT + kT - 1 >= p.window) {
+        // rows that see key krow: all later ones of a sink, else those within W of it
+        const int q_to_end = krow < p.sinks ? kT : krow + p.window - 1 - i * kT - q0;
+        pt_from_st<true, true>(lane_base + cS + q0, nl4, c2, (i - j) * kT + q0 - r, q_to_end, pr);
+      } else if (diag) {
+        pt_from_st<true, false>(lane_base + cS + q0, nl4, c2, q0 - r, 0, pr);
+      } else {
+        pt_from_st<false, false>(lane_base + cS + q0, nl4, c2, q0 - r, 0, pr);
+      }
       tmem_wait_st();
       tc_fence_before_sync();
       mbar_arrive(smem_addr(&sy.p_full[0]));
@@ -623,6 +713,13 @@ dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
 #pragma unroll 1
       for (int q = cw * kPer; q < (cw + 1) * kPer; ++q) {
         const int col = (q % kHalfOut) * 32;
+        if (kWin && j < p.heavy && p.pieces > 1) {
+          // (rows past L are zeros: their keys are, and no row sees them)
+          const size_t part = (static_cast<size_t>(grp) * p.heavy + j) * p.pieces + work.piece;
+          float* dst = p.parts + ((2 * part + (q < kHalfOut ? 0 : 1)) * kT + r) * D + col;
+          store_chunk_f32(lane_base + (q < kHalfOut ? cDV : cDK) + col, dst, 1.0f);
+          continue;
+        }
         if (q < kHalfOut) store_chunk(lane_base + cDV + col, p.dv + koff + col, 1.0f, valid);
         else store_chunk(lane_base + cDK + col, p.dk + koff + col, p.scale, valid);
       }
@@ -631,13 +728,52 @@ dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
   teardown(sy, p, false);
 }
 
+// The parts of the key tiles that hold a sink, added in order of the pieces:
+// a thread per four columns of one row of dV or dK.
+template <int D>
+__global__ void __launch_bounds__(256)
+join_kernel(const BwdParams p, long long items) {
+  // (the grid before this one ends only once dK/dV has)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const long long item = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
+  if (item >= items) return;
+  constexpr int kQuads = D / 4;
+  const int col = static_cast<int>(item % kQuads) * 4;
+  const int r = static_cast<int>(item / kQuads) % kT;
+  const long long rest = item / (kQuads * kT);         // (tile, dV or dK)
+  const int which = static_cast<int>(rest & 1);
+  const long long tile = rest >> 1;
+  const int j = static_cast<int>(tile % p.heavy);
+  const long long grp = tile / p.heavy;
+  const int row = j * kT + r;
+  if (row >= p.L) return;
+  const float* src = p.parts + ((2 * tile * p.pieces + which) * kT + r) * D + col;
+  float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+  for (int k = 0; k < p.pieces; ++k) {
+    const float4 v = *reinterpret_cast<const float4*>(src + static_cast<size_t>(k) * 2 * kT * D);
+    sum.x += v.x;
+    sum.y += v.y;
+    sum.z += v.z;
+    sum.w += v.w;
+  }
+  const float mul = which ? p.scale : 1.0f;
+  const long long b = grp / p.n_kv, kvh = grp % p.n_kv;
+  uint16_t* out = (which ? p.dk : p.dv) + ((b * p.L + row) * p.n_kv + kvh) * D + col;
+  *reinterpret_cast<uint2*>(out) =
+      make_uint2(pack_bf16x2(sum.x * mul, sum.y * mul), pack_bf16x2(sum.z * mul, sum.w * mul));
+}
+
 // ------------------------------------------------------------------------ dQ
 
 // dQ unit u (longest first): query tile i = T - 1 - u / groups of head
 // (b, h) = u % groups, groups = B * n_q.
 struct DqUnit {
   int b, h, i, n;
+  SeenTiles seen;
 };
+template <bool kWin>
 __device__ __forceinline__ DqUnit dq_unit(int u, const BwdParams& p) {
   const int groups = p.q_units / p.T;
   DqUnit x;
@@ -645,7 +781,8 @@ __device__ __forceinline__ DqUnit dq_unit(int u, const BwdParams& p) {
   const int grp = u - (p.T - 1 - x.i) * groups;
   x.b = grp / p.n_q;
   x.h = grp - x.b * p.n_q;
-  x.n = p.causal ? x.i + 1 : p.T;
+  x.seen = seen_tiles<kWin>(x.i, p);
+  x.n = x.seen.n;
   return x;
 }
 
@@ -658,7 +795,7 @@ __device__ __forceinline__ int dq_snake(int r) {
   return r * G + ((r & 1) ? (G - 1 - c) : c);
 }
 
-template <int D>
+template <int D, bool kWin>
 __global__ void __launch_bounds__(kThreads, 1)
 dq_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
           const __grid_constant__ CUtensorMap tmdO, const uint16_t* __restrict__ q_rows,
@@ -691,7 +828,7 @@ dq_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
       for (int r = 0; r * G < units && ok; ++r) {
         const int u = dq_snake(r);
         if (u >= units) continue;
-        const DqUnit x = dq_unit(u, p);
+        const DqUnit x = dq_unit<kWin>(u, p);
         const int kvh = x.h / p.g;
         // The first ring's worth of this unit's K/V tiles goes out while the
         // previous unit still runs; dO_i's buffer is free only once every
@@ -715,9 +852,10 @@ dq_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
           }
           const uint32_t dst = sRing + st * kStage, bar = smem_addr(&sy.full[st]);
           mbar_arrive_expect_tx(bar, 2 * kTileBytes);
+          const int key0 = seen_tile<kWin>(x.seen, t) * kT;
           for (int c = 0; c < D / 64; ++c) {
-            tma_load_4d(dst + c * kT * 128, &tmK, bar, c * 64, kvh, t * kT, x.b);
-            tma_load_4d(dst + kTileBytes + c * kT * 128, &tmV, bar, c * 64, kvh, t * kT, x.b);
+            tma_load_4d(dst + c * kT * 128, &tmK, bar, c * 64, kvh, key0, x.b);
+            tma_load_4d(dst + kTileBytes + c * kT * 128, &tmV, bar, c * 64, kvh, key0, x.b);
           }
         }
         if (ok && pre == x.n) {
@@ -744,7 +882,7 @@ dq_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
     for (int r = 0; r * G < units && ok; ++r) {
       const int u = dq_snake(r);
       if (u >= units) continue;
-      const int n = dq_unit(u, p).n;
+      const int n = dq_unit<kWin>(u, p).n;
       auto stage_of = [&](int t) { return sRing + ((it + t) % kStages) * kStage; };
       auto wait_stage = [&](int t) -> bool {
         return wait_all(sy.full[(it + t) % kStages], (it + t) / kStages);
@@ -799,7 +937,7 @@ dq_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
     for (int rr = 0; rr * G < units && ok; ++rr) {
       const int u = dq_snake(rr);
       if (u >= units) continue;
-      const DqUnit x = dq_unit(u, p);
+      const DqUnit x = dq_unit<kWin>(u, p);
       const int i = x.i, n = x.n;
       const int row = i * kT + r;
       const size_t qoff = ((static_cast<size_t>(x.b) * p.L + row) * p.n_q + x.h) * D;
@@ -823,8 +961,14 @@ dq_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
         const bool masked = p.causal ? (t == i) : (p.L - t * kT < kT);
         const int keep = p.causal ? r : p.L - 1 - t * kT;
         float pr[kColsQ];
-        if (masked) p_from_s<true>(lane_base + cS + k0, c2, nl2, k0, keep, pr);
-        else p_from_s<false>(lane_base + cS + k0, c2, nl2, k0, keep, pr);
+        const int ahead = i - seen_tile<kWin>(x.seen, t);    // tiles from the key tile to the row's
+        if (kWin && ahead * kT + kT - 1 >= p.window)
+          p_from_s<true, true>(lane_base + cS + k0, c2, nl2, k0, ahead * kT + r,
+                               ahead * kT + r - p.window, p.sinks - (i - ahead) * kT, pr);
+        else if (kWin ? ahead == 0 : masked)
+          p_from_s<true, false>(lane_base + cS + k0, c2, nl2, k0, keep, 0, 0, pr);
+        else
+          p_from_s<false, false>(lane_base + cS + k0, c2, nl2, k0, keep, 0, 0, pr);
         tc_fence_before_sync();
         mbar_arrive(smem_addr(&sy.p_full[0]));
         // phase 2: dP read out (its columns are then free for the next tile),
@@ -896,6 +1040,14 @@ constexpr int dkdv_smem() { return 2 * tile_bytes<D>() + kStagesKV * (2 * tile_b
 template <int D>
 constexpr int dq_smem() { return tile_bytes<D>() + kStages * (2 * tile_bytes<D>()) + 1024; }
 
+template <int D, bool kWin>
+bool set_smem() {
+  return cudaFuncSetAttribute(dkdv_kernel<D, kWin>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              dkdv_smem<D>()) == cudaSuccess &&
+         cudaFuncSetAttribute(dq_kernel<D, kWin>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              dq_smem<D>()) == cudaSuccess;
+}
+
 attn_status_t bwd_device_ready(cudaStream_t stream, int** status) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return ATTN_ERR_CUDA;
@@ -920,14 +1072,8 @@ attn_status_t bwd_device_ready(cudaStream_t stream, int** status) {
         return ATTN_ERR_CUDA;
       g_bwd_encode = reinterpret_cast<EncodeTiledFn>(fn);
     }
-    if (cudaFuncSetAttribute(dkdv_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             dkdv_smem<128>()) != cudaSuccess ||
-        cudaFuncSetAttribute(dq_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             dq_smem<128>()) != cudaSuccess ||
-        cudaFuncSetAttribute(dkdv_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             dkdv_smem<64>()) != cudaSuccess ||
-        cudaFuncSetAttribute(dq_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             dq_smem<64>()) != cudaSuccess)
+    if (!set_smem<128, false>() || !set_smem<64, false>() || !set_smem<128, true>() ||
+        !set_smem<64, true>())
       return ATTN_ERR_CUDA;
     g_bwd_ready[dev] = true;
   }
@@ -936,7 +1082,7 @@ attn_status_t bwd_device_ready(cudaStream_t stream, int** status) {
 
 // dK/dV is launched as the row kernel's programmatic dependent: its CTAs set
 // up while the row kernel finishes and wait for it before reading anything.
-template <int D>
+template <int D, bool kWin>
 cudaError_t launch_dkdv(unsigned grid, cudaStream_t stream, const CUtensorMap& mq,
                         const CUtensorMap& mdo, const CUtensorMap& mk, const CUtensorMap& mv,
                         const BwdParams& p) {
@@ -950,14 +1096,14 @@ cudaError_t launch_dkdv(unsigned grid, cudaStream_t stream, const CUtensorMap& m
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, dkdv_kernel<D>, mq, mdo, mk, mv, p);
+  return cudaLaunchKernelEx(&cfg, dkdv_kernel<D, kWin>, mq, mdo, mk, mv, p);
 }
 
 // dQ is launched as the dK/dV kernel's programmatic dependent: it reads only
 // the inputs and the row statistics (complete once dK/dV's CTAs are past their
 // wait, which is when they let dQ launch), so it needs no grid-dependency wait
 // and its persistent CTAs take the SMs that dK/dV's last CTAs free.
-template <int D>
+template <int D, bool kWin>
 cudaError_t launch_dq(unsigned grid, cudaStream_t stream, const CUtensorMap& mk,
                       const CUtensorMap& mv, const CUtensorMap& mdo, const uint16_t* qh,
                       const BwdParams& p) {
@@ -971,7 +1117,23 @@ cudaError_t launch_dq(unsigned grid, cudaStream_t stream, const CUtensorMap& mk,
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, dq_kernel<D>, mk, mv, mdo, qh, p);
+  return cudaLaunchKernelEx(&cfg, dq_kernel<D, kWin>, mk, mv, mdo, qh, p);
+}
+
+// The join is dQ's programmatic dependent: it waits until that grid, and with it
+// dK/dV, has ended.
+template <int D>
+cudaError_t launch_join(cudaStream_t stream, const BwdParams& p, long long items) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((items + 255) / 256));
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, join_kernel<D>, p, items);
 }
 
 bool encode_tile_map(CUtensorMap* map, const void* ptr, int D, int H, int64_t L, int64_t B) {
@@ -988,22 +1150,73 @@ bool encode_tile_map(CUtensorMap* map, const void* ptr, int D, int H, int64_t L,
                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-}  // namespace
-
-extern "C" {
-
-int64_t attn_prefill_bwd_workspace_bytes(int64_t B, int64_t L, int32_t n_q, int32_t n_kv,
-                                         int32_t d_h) {
-  if (B < 1 || L < 1 || n_q < 1 || n_kv < 1 || n_q % n_kv != 0 || (d_h != 64 && d_h != 128)) return -1;
+// 32-bit tile indexing, and the row kernel's grid (128 rows x B*n_q*T / 32)
+bool sizes_fit(int64_t B, int64_t L, int32_t n_q, int32_t n_kv) {
   const int64_t T = (L + kT - 1) / kT;
-  return 2 * B * n_q * T * kT * 4;
+  return L <= (int64_t{1} << 30) && B <= INT32_MAX && B * n_q <= INT32_MAX &&
+         B * n_kv * T <= INT32_MAX && B * n_q * T <= INT32_MAX / 4;
 }
 
-attn_status_t attn_prefill_bwd(const void* q, const void* k, const void* v, const void* o,
-                               const float* lse, const void* dout, void* dq, void* dk, void* dv,
-                               void* workspace, int64_t workspace_bytes, int64_t B, int64_t L,
-                               int32_t n_q, int32_t n_kv, int32_t d_h, int32_t causal,
-                               float scale, void* stream_ptr) {
+// Row statistics of a call, in bytes: two fp32 per query row, rows padded to tiles.
+int64_t row_bytes(int64_t B, int64_t L, int32_t n_q) {
+  return 2 * B * n_q * ((L + kT - 1) / kT) * kT * 4;
+}
+
+// How the key tiles that hold a sink are cut. Such a tile meets every later query
+// tile, up to T * g steps where the others take about W / 128 * g: left whole, the
+// few of them would run on long after the rest. A piece is at least as long as
+// another tile's CTA, and all pieces together are about two per SM, which also
+// bounds the parts' memory (128 KiB each at d_h = 128). A rule on the shape alone,
+// not on the device, so that the workspace's size is.
+struct SinkSplit {
+  int64_t heavy, pieces, bytes;
+};
+SinkSplit sink_split(int64_t B, int64_t L, int32_t n_q, int32_t n_kv, int32_t d_h, int64_t window,
+                     int64_t sinks) {
+  const int64_t T = (L + kT - 1) / kT, g = n_q / n_kv;
+  window = window < L ? window : L;
+  sinks = sinks < L ? sinks : L;
+  SinkSplit s;
+  s.heavy = window < L ? (sinks + kT - 1) / kT : 0;
+  s.pieces = 1;
+  s.bytes = 0;
+  if (s.heavy == 0) return s;
+  const int64_t others = g * ((window + kT - 2) / kT + 1);
+  const int64_t most = g * T / (others > 8 ? others : 8);
+  const int64_t fill = 2 * 152 / (B * n_kv * s.heavy);
+  s.pieces = most < fill ? most : fill;
+  const int64_t least = g * (T - s.heavy + 1);          // steps of the shortest such tile
+  if (s.pieces > least) s.pieces = least;
+  if (s.pieces < 1) s.pieces = 1;
+  if (s.pieces > 1) s.bytes = B * n_kv * s.heavy * s.pieces * 2 * kT * d_h * 4;
+  return s;
+}
+
+template <int D, bool kWin>
+attn_status_t launch_all(cudaStream_t stream, unsigned row_blocks, unsigned kv_ctas,
+                         unsigned dq_grid, const uint16_t* o, const uint16_t* dout,
+                         const float* lse, const uint16_t* q, float* nlse2, float* nrowdot, int B,
+                         const CUtensorMap& mq, const CUtensorMap& mdo, const CUtensorMap& mk,
+                         const CUtensorMap& mv, const BwdParams& p) {
+  rowdot_kernel<D><<<row_blocks, 256, 0, stream>>>(o, dout, lse, nlse2, nrowdot, B, p.L, p.n_q,
+                                                   p.T * kT);
+  if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
+  if (launch_dkdv<D, kWin>(kv_ctas, stream, mq, mdo, mk, mv, p) != cudaSuccess)
+    return ATTN_ERR_CUDA;
+  if (launch_dq<D, kWin>(dq_grid, stream, mk, mv, mdo, q, p) != cudaSuccess) return ATTN_ERR_CUDA;
+  if (kWin && p.pieces > 1) {
+    const long long items = static_cast<long long>(B) * p.n_kv * p.heavy * 2 * kT * (D / 4);
+    if (launch_join<D>(stream, p, items) != cudaSuccess) return ATTN_ERR_CUDA;
+  }
+  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+// window > 0: the windowed instances (causal). Both entry points' checks and launches.
+attn_status_t backward(const void* q, const void* k, const void* v, const void* o,
+                       const float* lse, const void* dout, void* dq, void* dk, void* dv,
+                       void* workspace, int64_t workspace_bytes, int64_t B, int64_t L, int32_t n_q,
+                       int32_t n_kv, int32_t d_h, int32_t causal, int64_t window, int64_t sinks,
+                       float scale, void* stream_ptr) {
   if (!q || !k || !v || !o || !lse || !dout || !dq || !dk || !dv || !workspace)
     return ATTN_ERR_INVALID_ARG;
   if (B < 1 || L < 1 || n_q < 1 || n_kv < 1 || n_q % n_kv != 0) return ATTN_ERR_INVALID_ARG;
@@ -1017,11 +1230,10 @@ attn_status_t attn_prefill_bwd(const void* q, const void* k, const void* v, cons
     return ATTN_ERR_INVALID_ARG;
   if (d_h != 64 && d_h != 128) return ATTN_ERR_UNSUPPORTED;
   const int64_t T = (L + kT - 1) / kT;
-  // 32-bit tile indexing, and the row kernel's grid (128 rows x B*n_q*T / 32)
-  if (L > (int64_t{1} << 30) || B * n_kv * T > INT32_MAX || B * n_q * T > INT32_MAX / 4)
-    return ATTN_ERR_UNSUPPORTED;
-  if (workspace_bytes < attn_prefill_bwd_workspace_bytes(B, L, n_q, n_kv, d_h))
-    return ATTN_ERR_INVALID_ARG;
+  if (!sizes_fit(B, L, n_q, n_kv)) return ATTN_ERR_UNSUPPORTED;
+  const bool win = window > 0;
+  const SinkSplit split = win ? sink_split(B, L, n_q, n_kv, d_h, window, sinks) : SinkSplit{0, 1, 0};
+  if (workspace_bytes < row_bytes(B, L, n_q) + split.bytes) return ATTN_ERR_INVALID_ARG;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
   int* status = nullptr;
   const attn_status_t ds = bwd_device_ready(stream, &status);
@@ -1031,7 +1243,7 @@ attn_status_t attn_prefill_bwd(const void* q, const void* k, const void* v, cons
   if (!encode_tile_map(&mq, q, d_h, n_q, L, B) || !encode_tile_map(&mk, k, d_h, n_kv, L, B) ||
       !encode_tile_map(&mv, v, d_h, n_kv, L, B) || !encode_tile_map(&mdo, dout, d_h, n_q, L, B))
     return ATTN_ERR_CUDA;
-  BwdParams p;
+  BwdParams p{};
   p.L = static_cast<int>(L);
   p.n_q = n_q;
   p.n_kv = n_kv;
@@ -1049,6 +1261,11 @@ attn_status_t attn_prefill_bwd(const void* q, const void* k, const void* v, cons
   p.dv = static_cast<uint16_t*>(dv);
   p.status = status;
   p.q_units = static_cast<int>(B * n_q * T);
+  p.window = static_cast<int>(window < L ? window : L);
+  p.sinks = static_cast<int>(sinks < L ? sinks : L);
+  p.heavy = static_cast<int>(split.heavy);
+  p.pieces = static_cast<int>(split.pieces);
+  p.parts = nrowdot + B * n_q * T * kT;
 
   const int64_t rows = B * n_q * T * kT;
   constexpr int kRowdotRowsPerBlock = 8 * kRowdotRowsPerWarp;   // 256 threads
@@ -1061,23 +1278,57 @@ attn_status_t attn_prefill_bwd(const void* q, const void* k, const void* v, cons
   const uint16_t* oh = static_cast<const uint16_t*>(o);
   const uint16_t* qh = static_cast<const uint16_t*>(q);
   const uint16_t* doh = static_cast<const uint16_t*>(dout);
-  const int Lp = static_cast<int>(T * kT);
-  const unsigned kv_tiles = static_cast<unsigned>(B * n_kv * T);
+  const unsigned kv_ctas =
+      static_cast<unsigned>(B * n_kv * (T - split.heavy + split.heavy * split.pieces));
   const unsigned dq_grid = static_cast<unsigned>(B * n_q * T < sms ? B * n_q * T : sms);
-  if (d_h == 128) {
-    rowdot_kernel<128><<<row_blocks, 256, 0, stream>>>(oh, doh, lse, nlse2, nrowdot,
-                                                       static_cast<int>(B), p.L, n_q, Lp);
-    if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
-    if (launch_dkdv<128>(kv_tiles, stream, mq, mdo, mk, mv, p) != cudaSuccess) return ATTN_ERR_CUDA;
-    if (launch_dq<128>(dq_grid, stream, mk, mv, mdo, qh, p) != cudaSuccess) return ATTN_ERR_CUDA;
-  } else {
-    rowdot_kernel<64><<<row_blocks, 256, 0, stream>>>(oh, doh, lse, nlse2, nrowdot,
-                                                      static_cast<int>(B), p.L, n_q, Lp);
-    if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
-    if (launch_dkdv<64>(kv_tiles, stream, mq, mdo, mk, mv, p) != cudaSuccess) return ATTN_ERR_CUDA;
-    if (launch_dq<64>(dq_grid, stream, mk, mv, mdo, qh, p) != cudaSuccess) return ATTN_ERR_CUDA;
-  }
-  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  const int batch = static_cast<int>(B);
+  if (d_h == 128)
+    return win ? launch_all<128, true>(stream, row_blocks, kv_ctas, dq_grid, oh, doh, lse, qh,
+                                       nlse2, nrowdot, batch, mq, mdo, mk, mv, p)
+               : launch_all<128, false>(stream, row_blocks, kv_ctas, dq_grid, oh, doh, lse, qh,
+                                        nlse2, nrowdot, batch, mq, mdo, mk, mv, p);
+  return win ? launch_all<64, true>(stream, row_blocks, kv_ctas, dq_grid, oh, doh, lse, qh, nlse2,
+                                    nrowdot, batch, mq, mdo, mk, mv, p)
+             : launch_all<64, false>(stream, row_blocks, kv_ctas, dq_grid, oh, doh, lse, qh, nlse2,
+                                     nrowdot, batch, mq, mdo, mk, mv, p);
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t attn_prefill_bwd_workspace_bytes(int64_t B, int64_t L, int32_t n_q, int32_t n_kv,
+                                         int32_t d_h) {
+  if (B < 1 || L < 1 || n_q < 1 || n_kv < 1 || n_q % n_kv != 0 || (d_h != 64 && d_h != 128)) return -1;
+  return row_bytes(B, L, n_q);
+}
+
+attn_status_t attn_prefill_bwd(const void* q, const void* k, const void* v, const void* o,
+                               const float* lse, const void* dout, void* dq, void* dk, void* dv,
+                               void* workspace, int64_t workspace_bytes, int64_t B, int64_t L,
+                               int32_t n_q, int32_t n_kv, int32_t d_h, int32_t causal,
+                               float scale, void* stream_ptr) {
+  return backward(q, k, v, o, lse, dout, dq, dk, dv, workspace, workspace_bytes, B, L, n_q, n_kv,
+                  d_h, causal, 0, 0, scale, stream_ptr);
+}
+
+int64_t attn_prefill_window_bwd_workspace_bytes(int64_t B, int64_t L, int32_t n_q, int32_t n_kv,
+                                                int32_t d_h, int64_t window, int64_t sinks) {
+  if (B < 1 || L < 1 || n_q < 1 || n_kv < 1 || n_q % n_kv != 0 || (d_h != 64 && d_h != 128) ||
+      window < 1 || sinks < 0 || !sizes_fit(B, L, n_q, n_kv))
+    return -1;
+  return row_bytes(B, L, n_q) + sink_split(B, L, n_q, n_kv, d_h, window, sinks).bytes;
+}
+
+attn_status_t attn_prefill_window_bwd(const void* q, const void* k, const void* v, const void* o,
+                                      const float* lse, const void* dout, void* dq, void* dk,
+                                      void* dv, void* workspace, int64_t workspace_bytes, int64_t B,
+                                      int64_t L, int32_t n_q, int32_t n_kv, int32_t d_h,
+                                      int64_t window, int64_t sinks, float scale,
+                                      void* stream_ptr) {
+  if (window < 1 || sinks < 0) return ATTN_ERR_INVALID_ARG;
+  return backward(q, k, v, o, lse, dout, dq, dk, dv, workspace, workspace_bytes, B, L, n_q, n_kv,
+                  d_h, 1, window, sinks, scale, stream_ptr);
 }
 
 }  // extern "C"

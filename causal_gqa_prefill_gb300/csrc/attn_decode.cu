@@ -48,6 +48,13 @@
 // heads on 8, with weights 60 us (302 MB of K and V; split 56, combine 8 when
 // timed one by one), one of 131072, 36 heads on 6, 67 us (403 MB, 6.0 TB/s): the
 // stream of K and V bounds both, and the combine's latency is what is left.
+//
+// Behind a sliding window with sinks (kWindow: the new token sees the last W of
+// lens[b] positions and the first S) the ragged step's tiles are those of the
+// visible positions only: the sinks' from position 0 on, then the window's from its
+// own first position on (a TMA box may start at any row), so a window of W costs
+// ceil(W / 128) tiles wherever it lies. Hidden positions that share a tile with
+// visible ones are masked and zeroed like those past a length.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -106,6 +113,7 @@ struct DecodeParams {
   float* scores;         // with weights: fp32 [B * n_q, ld] scores * scale * log2(e)
   long long ld;
   int B;
+  int window, sinks;     // kWindow: W and S
   int beside;            // 1: wait for the kernel before only at the end (decode_parts.h)
 };
 
@@ -206,9 +214,12 @@ __device__ __forceinline__ float reduce_heads(const float (&in)[GP], Op op) {
 // One segment of a CTA's tile range: K/V head `hd` (= b * n_kv + kv head),
 // key tiles [t0, t0 + n) of its `len` keys (`tiles` in all), partial results in
 // row `id`.
+// kWindow: the first `na` of the tiles hold the positions below `sunk`, the rest
+// those from `low` on.
 struct Segment {
   int hd, t0, n, len, tiles;
   long long id;
+  int low, sunk, na;
 };
 
 // Walks CTA c's range segment by segment (every role takes the same walk).
@@ -237,15 +248,38 @@ struct SegmentWalk {
 __device__ __forceinline__ int clamp_len(int len, int C) { return min(max(len, 0), C); }
 __device__ __forceinline__ int key_tiles(int len) { return (len + kKeys - 1) / kKeys; }
 
+// The positions of a sequence of `len` that its new token sees: [0, sunk) and [low, len).
+template <bool kWindow>
+struct Seen {
+  int low, sunk, na, tiles;
+  __device__ Seen(const DecodeParams& p, int len) {
+    low = kWindow ? max(0, len - p.window) : 0;
+    sunk = kWindow ? min(p.sinks, low) : 0;
+    na = key_tiles(sunk);
+    tiles = na + key_tiles(len - low);
+  }
+};
+
+// First position of key tile x of a segment's list, and how many of its 128 count.
+template <bool kWindow>
+__device__ __forceinline__ int tile_pos(const Segment& s, int x) {
+  return !kWindow || x < s.na ? x * kKeys : s.low + (x - s.na) * kKeys;
+}
+template <bool kWindow>
+__device__ __forceinline__ int tile_end(const Segment& s, int x) {
+  return kWindow && x < s.na ? s.sunk : s.len;
+}
+
 // Where CTA c's range starts, by one warp: each lane sums the tiles of a run
 // of sequences, a warp scan places the runs, and the lane whose run holds the
 // first tile walks it.
+template <bool kWindow>
 __device__ __forceinline__ void ragged_start(const DecodeParams& p, DecodeCtl& ctl, int c) {
   const int lane = threadIdx.x & 31;
   const int run = (p.B + 31) / 32, b0 = min(lane * run, p.B), b1 = min(b0 + run, p.B);
   long long sum = 0;
 #pragma unroll 4
-  for (int b = b0; b < b1; ++b) sum += key_tiles(clamp_len(p.lens[b], p.Lk));
+  for (int b = b0; b < b1; ++b) sum += Seen<kWindow>(p, clamp_len(p.lens[b], p.Lk)).tiles;
   sum *= p.n_kv;
   long long incl = sum;
 #pragma unroll
@@ -263,7 +297,7 @@ __device__ __forceinline__ void ragged_start(const DecodeParams& p, DecodeCtl& c
   long long at = incl - sum;
   if (x0 < at || x0 >= incl) return;
   for (int b = b0; b < b1; ++b) {
-    const int T = key_tiles(clamp_len(p.lens[b], p.Lk));
+    const int T = Seen<kWindow>(p, clamp_len(p.lens[b], p.Lk)).tiles;
     const long long here = static_cast<long long>(T) * p.n_kv;
     if (x0 < at + here) {
       const int off = static_cast<int>(x0 - at);
@@ -279,17 +313,22 @@ __device__ __forceinline__ void ragged_start(const DecodeParams& p, DecodeCtl& c
 
 // The same walk over the ragged step's tiles, from the start that
 // ragged_start left in `ctl`.
+template <bool kWindow>
 struct RaggedWalk {
   const DecodeParams& p;
   long long left;
-  int cta, b, u, t, len, T;
+  int cta, b, u, t, len, T, low, sunk, na;
   __device__ RaggedWalk(const DecodeParams& params, const DecodeCtl& ctl, int c)
       : p(params), left(ctl.tiles), cta(c), b(ctl.start_b), u(ctl.start_u), t(ctl.start_t) {
     if (left > 0) sequence();
   }
   __device__ void sequence() {
     len = clamp_len(p.lens[b], p.Lk);
-    T = key_tiles(len);
+    const Seen<kWindow> seen(p, len);
+    T = seen.tiles;
+    low = seen.low;
+    sunk = seen.sunk;
+    na = seen.na;
   }
   __device__ bool next(Segment& s) {
     if (left <= 0) return false;
@@ -302,6 +341,9 @@ struct RaggedWalk {
     s.n = static_cast<int>(left < T - t ? left : T - t);
     s.len = len;
     s.tiles = T;
+    s.low = low;
+    s.sunk = sunk;
+    s.na = na;
     s.id = static_cast<long long>(s.hd) + cta;
     left -= s.n;
     t += s.n;
@@ -317,19 +359,19 @@ struct RaggedWalk {
   }
 };
 
-template <bool kRagged>
+template <bool kRagged, bool kWindow>
 struct WalkOf {
   using type = SegmentWalk;
 };
-template <>
-struct WalkOf<true> {
-  using type = RaggedWalk;
+template <bool kWindow>
+struct WalkOf<true, kWindow> {
+  using type = RaggedWalk<kWindow>;
 };
 
 // GP: the group's query heads padded to 4, 8 or 16 (g <= GP); the loops over
 // heads unroll to GP and skip h >= g. kRagged: the ragged step; kWeights: it
-// also writes the scores.
-template <int GP, bool kRagged, bool kWeights>
+// also writes the scores; kWindow: behind a window with sinks.
+template <int GP, bool kRagged, bool kWeights, bool kWindow = false>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_decode_split_kernel(const __grid_constant__ CUtensorMap tmQ,
                          const __grid_constant__ CUtensorMap tmK,
@@ -390,9 +432,9 @@ attn_decode_split_kernel(const __grid_constant__ CUtensorMap tmQ,
   // (the previous call's combine, or whatever wrote Q, K and V): the set-up
   // above overlaps it; global memory is touched only after it has completed.
   if (!kRagged || !p.beside) asm volatile("griddepcontrol.wait;" ::: "memory");
-  using Walk = typename WalkOf<kRagged>::type;
+  using Walk = typename WalkOf<kRagged, kWindow>::type;
   if (kRagged) {
-    if (warp == 0) ragged_start(p, ctl, cta);
+    if (warp == 0) ragged_start<kWindow>(p, ctl, cta);
     __syncthreads();
   }
 
@@ -428,7 +470,7 @@ attn_decode_split_kernel(const __grid_constant__ CUtensorMap tmQ,
             mbar_arrive_expect_tx(bar, kTileBytes);
             for (int ch = 0; ch < 2; ++ch)
               tma_load_4d(sRing + slot * kTileBytes + ch * kChunkBytes, kind ? &tmV : &tmK, bar,
-                          ch * 64, kvh, (sg.t0 + t) * kKeys, b);
+                          ch * 64, kvh, tile_pos<kWindow>(sg, sg.t0 + t), b);
             ++it;
           }
         }
@@ -610,8 +652,9 @@ attn_decode_split_kernel(const __grid_constant__ CUtensorMap tmQ,
         uint32_t sv[16];
         tmem_ld16(lane_base + kColS + 16 * (gt & 1), sv);
         tmem_wait_ld16(sv);
-        const int key = (sg.t0 + t) * kKeys + r;
-        const bool valid = key < sg.len;
+        const int key0 = tile_pos<kWindow>(sg, sg.t0 + t), end = tile_end<kWindow>(sg, sg.t0 + t);
+        const int key = key0 + r;
+        const bool valid = key < end;
         float x[GP];
         bool need = false;
 #pragma unroll
@@ -682,8 +725,8 @@ attn_decode_split_kernel(const __grid_constant__ CUtensorMap tmQ,
             *reinterpret_cast<uint16_t*>(pb + h * 128 + ((p_unit ^ (h & 7)) << 4)) =
                 static_cast<uint16_t>(pack_bf16x2(e, 0.0f) & 0xFFFFu);
         }
-        if (kRagged && (sg.t0 + t + 1) * kKeys > sg.len) {
-          // a tile that ends past the sequence: zeros over what V holds there
+        if (kRagged && key0 + kKeys > end) {
+          // a tile that ends past the sequence (or the sinks): zeros over what V holds there
           // (the tensor cores read V only after this tile's p_full)
           const uint32_t item = 2 * gt + 1, slot = item % kRing;
           if (!waited(smem_addr(&ctl.full[slot]), (item / kRing) & 1)) {
@@ -953,27 +996,30 @@ std::mutex g_decode_mutex;
 bool g_decode_ready[kMaxDevices] = {};
 EncodeTiledFn g_decode_encode = nullptr;
 
-template <int GP, bool kRagged, bool kWeights>
+template <int GP, bool kRagged, bool kWeights, bool kWindow = false>
 bool set_smem_of() {
-  return cudaFuncSetAttribute(attn_decode_split_kernel<GP, kRagged, kWeights>,
+  return cudaFuncSetAttribute(attn_decode_split_kernel<GP, kRagged, kWeights, kWindow>,
                               cudaFuncAttributeMaxDynamicSharedMemorySize,
                               kSmemBytes) == cudaSuccess;
 }
 template <int GP>
 bool set_smem() {
   return set_smem_of<GP, false, false>() && set_smem_of<GP, true, false>() &&
-         set_smem_of<GP, true, true>();
+         set_smem_of<GP, true, true>() && set_smem_of<GP, true, false, true>();
 }
 
 // The split kernel for groups of g query heads.
-template <bool kRagged, bool kWeights>
+template <bool kRagged, bool kWeights, bool kWindow = false>
 cudaError_t launch_split(const cudaLaunchConfig_t& cfg, const CUtensorMap& mq,
                          const CUtensorMap& mk, const CUtensorMap& mv, const DecodeParams& p) {
   if (p.g <= 4)
-    return cudaLaunchKernelEx(&cfg, attn_decode_split_kernel<4, kRagged, kWeights>, mq, mk, mv, p);
+    return cudaLaunchKernelEx(&cfg, attn_decode_split_kernel<4, kRagged, kWeights, kWindow>, mq,
+                              mk, mv, p);
   if (p.g <= 8)
-    return cudaLaunchKernelEx(&cfg, attn_decode_split_kernel<8, kRagged, kWeights>, mq, mk, mv, p);
-  return cudaLaunchKernelEx(&cfg, attn_decode_split_kernel<16, kRagged, kWeights>, mq, mk, mv, p);
+    return cudaLaunchKernelEx(&cfg, attn_decode_split_kernel<8, kRagged, kWeights, kWindow>, mq,
+                              mk, mv, p);
+  return cudaLaunchKernelEx(&cfg, attn_decode_split_kernel<16, kRagged, kWeights, kWindow>, mq, mk,
+                            mv, p);
 }
 
 attn_status_t decode_device_ready(cudaStream_t stream, int** status) {
@@ -1055,9 +1101,17 @@ DecodeShape decode_shape(int64_t B, int64_t Lk, int32_t n_kv) {
 struct RaggedShape {
   int64_t G, ld, ml_at, ends_at, scores_at, bytes;
 };
-RaggedShape ragged_shape(int64_t B, int64_t C, int32_t n_q, int32_t n_kv, bool weighted) {
+// (window > 0: a sequence has at most the tiles of its window and of its sinks)
+RaggedShape ragged_shape(int64_t B, int64_t C, int32_t n_q, int32_t n_kv, bool weighted,
+                         int64_t window = 0, int64_t sinks = 0) {
   RaggedShape s;
-  const int64_t T = (C + kKeys - 1) / kKeys, most = B * n_kv * T;
+  auto tiles = [](int64_t n) { return (n + kKeys - 1) / kKeys; };
+  int64_t T = tiles(C);
+  if (window > 0 && window < C) {
+    const int64_t seen = tiles(window) + tiles(sinks < C - window ? sinks : C - window);
+    if (seen < T) T = seen;
+  }
+  const int64_t most = B * n_kv * T;
   s.G = most < kDecodeCtas ? most : kDecodeCtas;
   s.ld = T * kKeys;
   const int64_t rows = (B * n_kv + s.G) * (n_q / n_kv);
@@ -1081,8 +1135,9 @@ bool ragged_supported(int64_t B, int64_t C, int32_t n_q, int32_t n_kv, int32_t d
 attn_status_t launch_ragged_split(const void* q, const void* k, const void* v, const int32_t* lens,
                                   void* workspace, int64_t B, int64_t C, int32_t n_q, int32_t n_kv,
                                   float scale, bool weighted, bool beside, cudaStream_t stream,
-                                  int* status, DecodeParams* out) {
-  const RaggedShape s = ragged_shape(B, C, n_q, n_kv, weighted);
+                                  int* status, DecodeParams* out, int64_t window = 0,
+                                  int64_t sinks = 0) {
+  const RaggedShape s = ragged_shape(B, C, n_q, n_kv, weighted, window, sinks);
   CUtensorMap mq, mk, mv;
   if (!encode_q(&mq, q, n_q, B) || !encode_kv(&mk, k, n_kv, C, B) || !encode_kv(&mv, v, n_kv, C, B))
     return ATTN_ERR_CUDA;
@@ -1094,6 +1149,8 @@ attn_status_t launch_ragged_split(const void* q, const void* k, const void* v, c
   p.scores = weighted ? reinterpret_cast<float*>(ws + s.scores_at) : nullptr;
   p.ld = s.ld;
   p.beside = beside ? 1 : 0;
+  p.window = static_cast<int>(window < C ? window : C);
+  p.sinks = static_cast<int>(sinks < C ? sinks : C);
   p.status = status;
   p.lens = lens;
   p.B = static_cast<int>(B);
@@ -1114,8 +1171,9 @@ attn_status_t launch_ragged_split(const void* q, const void* k, const void* v, c
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = weighted ? launch_split<true, true>(cfg, mq, mk, mv, p)
-                                 : launch_split<true, false>(cfg, mq, mk, mv, p);
+  const cudaError_t e = window > 0 ? launch_split<true, false, true>(cfg, mq, mk, mv, p)
+                        : weighted ? launch_split<true, true>(cfg, mq, mk, mv, p)
+                                   : launch_split<true, false>(cfg, mq, mk, mv, p);
   *out = p;
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
@@ -1230,11 +1288,13 @@ int64_t attn_decode_ragged_workspace_bytes(int64_t B, int64_t C, int32_t n_q, in
   return ragged_shape(B, C, n_q, n_kv, weighted != 0).bytes;
 }
 
-attn_status_t attn_decode_ragged_fwd(const void* q, const void* k, const void* v,
-                                     const int32_t* lens, float* weights, void* o, float* lse,
-                                     void* workspace, int64_t workspace_bytes, int64_t B, int64_t C,
-                                     int32_t n_q, int32_t n_kv, int32_t d_h, float scale,
-                                     void* stream_ptr) {
+// window > 0: behind a window with sinks, without weights. Both entry points'
+// checks and launches.
+static attn_status_t ragged_step(const void* q, const void* k, const void* v, const int32_t* lens,
+                                 float* weights, void* o, float* lse, void* workspace,
+                                 int64_t workspace_bytes, int64_t B, int64_t C, int32_t n_q,
+                                 int32_t n_kv, int32_t d_h, int64_t window, int64_t sinks,
+                                 float scale, void* stream_ptr) {
   if (!q || !k || !v || !lens || !o || !lse || !workspace) return ATTN_ERR_INVALID_ARG;
   if (!decode_sizes_ok(B, C, n_q, n_kv, d_h) || !std::isfinite(scale)) return ATTN_ERR_INVALID_ARG;
   auto misaligned = [](const void* ptr, uintptr_t a) {
@@ -1246,14 +1306,14 @@ attn_status_t attn_decode_ragged_fwd(const void* q, const void* k, const void* v
     return ATTN_ERR_INVALID_ARG;
   if (!ragged_supported(B, C, n_q, n_kv, d_h)) return ATTN_ERR_UNSUPPORTED;
   const bool weighted = weights != nullptr;
-  if (workspace_bytes < ragged_shape(B, C, n_q, n_kv, weighted).bytes) return ATTN_ERR_INVALID_ARG;
+  if (workspace_bytes < ragged_shape(B, C, n_q, n_kv, weighted, window, sinks).bytes) return ATTN_ERR_INVALID_ARG;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
   int* status = nullptr;
   attn_status_t st = decode_device_ready(stream, &status);
   if (st != ATTN_OK) return st;
   DecodeParams p;
   st = launch_ragged_split(q, k, v, lens, workspace, B, C, n_q, n_kv, scale, weighted, false,
-                           stream, status, &p);
+                           stream, status, &p, window, sinks);
   if (st != ATTN_OK) return st;
   const int chunks = weighted ? static_cast<int>((C + kWeightKeys - 1) / kWeightKeys) : 0;
   cudaLaunchAttribute attr[1];
@@ -1280,6 +1340,32 @@ attn_status_t attn_decode_ragged_fwd(const void* q, const void* k, const void* v
                                 chunks, p);
   if (e != cudaSuccess) return ATTN_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+attn_status_t attn_decode_ragged_fwd(const void* q, const void* k, const void* v,
+                                     const int32_t* lens, float* weights, void* o, float* lse,
+                                     void* workspace, int64_t workspace_bytes, int64_t B, int64_t C,
+                                     int32_t n_q, int32_t n_kv, int32_t d_h, float scale,
+                                     void* stream_ptr) {
+  return ragged_step(q, k, v, lens, weights, o, lse, workspace, workspace_bytes, B, C, n_q, n_kv,
+                     d_h, 0, 0, scale, stream_ptr);
+}
+
+int64_t attn_decode_window_workspace_bytes(int64_t B, int64_t C, int32_t n_q, int32_t n_kv,
+                                           int32_t d_h, int64_t window, int64_t sinks) {
+  if (!decode_sizes_ok(B, C, n_q, n_kv, d_h) || window < 1 || sinks < 0) return -1;
+  if (!ragged_supported(B, C, n_q, n_kv, d_h)) return -1;
+  return ragged_shape(B, C, n_q, n_kv, false, window, sinks).bytes;
+}
+
+attn_status_t attn_decode_window_fwd(const void* q, const void* k, const void* v,
+                                     const int32_t* lens, void* o, float* lse, void* workspace,
+                                     int64_t workspace_bytes, int64_t B, int64_t C, int32_t n_q,
+                                     int32_t n_kv, int32_t d_h, int64_t window, int64_t sinks,
+                                     float scale, void* stream_ptr) {
+  if (window < 1 || sinks < 0) return ATTN_ERR_INVALID_ARG;
+  return ragged_step(q, k, v, lens, nullptr, o, lse, workspace, workspace_bytes, B, C, n_q, n_kv,
+                     d_h, window, sinks, scale, stream_ptr);
 }
 
 }  // extern "C"

@@ -34,6 +34,15 @@
 // ring (32 KiB per tile) and 4 KiB per softmax warp through which the
 // epilogue turns each thread's O row into row-contiguous global stores.
 //
+// Sliding window with sinks (kWin instances): a row at position p sees the keys
+// j <= p with j > p - W or j < S. A unit's list of key tiles is then two runs, the
+// tiles of the sinks before its first window position and the tiles of its
+// window (list_tile); everything else is the same kernel, so what bounds it is
+// what bounds the whole causal forward. Positions that no row of the call sees are
+// never multiplied: the window's tiles come through tensor maps that begin at the
+// first one seen, the sinks' through maps that end at S, and a tile that reaches
+// over such an edge gets zeros there.
+//
 // MMA issue order per key tile j (ping-pong between the two query tiles, so
 // one tile's softmax overlaps the other tile's matrix products):
 //   S0_j = Q0 K_j^T ; O1 += P1_{j-1} V_{j-1} ; S1_j = Q1 K_j^T ; O0 += P0_j V_j
@@ -111,6 +120,8 @@ struct Params {
   int Tq, Tk;           // 128-row query tiles and 128-key tiles
   int causal;
   int scale_pos;        // 1 when c > 0
+  int window, sinks;    // kWin instances: W and S, both at most Lk
+  int first;            // kWin instances: position where the window's tensor maps begin
   float c;              // scale * log2(e) (times the Q and K descale factors for fp8)
   float o_scale;        // multiplies O / l in the epilogue (the V descale for fp8, else 1)
   int groups;           // B * n_kv
@@ -177,10 +188,20 @@ __device__ __forceinline__ bool dbg_ok(bool cond, Ctl& ctl, const Params& p) {
 #define DBG_RETURN_UNLESS(cond)
 #endif
 
+// kWin instances also: every row of the unit sees keys below `low` only as
+// sinks; the first `na` tiles of the list hold those, the rest begin with tile
+// `lo`, the one that holds position `low`.
 struct Unit {
   int b, kvh, nkv;
   int head[2], qtile[2], n[2];
+  int low, na, lo;
 };
+
+// Key tile number j of a unit's list.
+template <bool kWin>
+__device__ __forceinline__ int list_tile(const Unit& x, int j) {
+  return !kWin || j < x.na ? j : j - x.na + x.lo;
+}
 
 // Unit u -> (batch, K/V head, two query tiles). The (b, kv-head) groups are
 // taken in batches of p.batch consecutive groups (the last batch may be
@@ -196,6 +217,7 @@ struct Unit {
 // Within one (b, kv-head) group the g*T query tiles are listed longest first
 // and paired neighbour by neighbour: slot 1 holds the longer (or equal) tile,
 // slot 0 the next one, and their key-tile counts differ by at most one.
+template <bool kWin>
 __device__ __forceinline__ Unit decode_unit(int u, const Params& p) {
   Unit x;
   const int per_batch = p.batch * p.pairs;
@@ -223,6 +245,17 @@ __device__ __forceinline__ Unit decode_unit(int u, const Params& p) {
       x.qtile[s] = 0;
       x.n[s] = 0;
     }
+  }
+  if (kWin) {
+    // (slot 0 holds the earlier of two different query tiles: the list begins
+    // where its window does, and slot 1 may find one whole tile masked)
+    const int q0 = p.offset + (x.n[0] > 0 ? x.qtile[0] : x.qtile[1]) * kBM;
+    x.low = max(0, q0 - p.window + 1);
+    x.lo = x.low / kBN;
+    x.na = (min(p.sinks, x.low) + kBN - 1) / kBN;
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+      if (x.n[s] > 0) x.n[s] += x.na - x.lo;
   }
   x.nkv = x.n[1];
   return x;
@@ -289,9 +322,10 @@ __global__ void __launch_bounds__(64, 1) wait_selftest_kernel(const Params p) {
 
 // ------------------------------------------------------------------ producer
 
-template <int D, bool F8>
+template <int D, bool F8, bool kWin>
 __device__ void load_role(const CUtensorMap* tmQ, const CUtensorMap* tmK,
-                          const CUtensorMap* tmV, Ctl& ctl, const Params& p,
+                          const CUtensorMap* tmV, const CUtensorMap* tmKs,
+                          const CUtensorMap* tmVs, Ctl& ctl, const Params& p,
                           uint32_t sQ0, uint32_t sQ1, uint32_t sKV, uint32_t smem_end) {
   using TL = Tile<D, F8>;
   // Run by lane 0 alone: a whole warp polling the ring barriers would cost
@@ -314,7 +348,7 @@ __device__ void load_role(const CUtensorMap* tmQ, const CUtensorMap* tmK,
   for (int r = 0; r * static_cast<int>(gridDim.x) < p.units; ++r) {
     const int u = snake_unit(r);
     if (u >= p.units) continue;
-    const Unit x = decode_unit(u, p);
+    const Unit x = decode_unit<kWin>(u, p);
     if (uc > 0 && !wait_phase(smem_addr(&ctl.q_empty), (uc - 1) & 1, ctl, p)) { ok = false; break; }
     DBG_BREAK_UNLESS(uc == 0 || DBG_PHASE_OK(q_empty, static_cast<uint32_t>(uc - 1)))
     ++uc;
@@ -338,8 +372,13 @@ __device__ void load_role(const CUtensorMap* tmQ, const CUtensorMap* tmK,
 #endif
     DBG_ISSUE(q_full);
     for (int j = 0; j < x.nkv && ok; ++j) {
+      // (kWin: the sinks' maps begin at position 0; the window's begin at p.first, before
+      // which a tile that starts there reads zeros)
+      const bool sink = kWin && j < x.na;
+      const int key0 = list_tile<kWin>(x, j) * kBN - (kWin && !sink ? p.first : 0);
 #pragma unroll
       for (int kind = 0; kind < 2; ++kind) {
+        const CUtensorMap* tm = kind ? (sink ? tmVs : tmV) : (sink ? tmKs : tmK);
         const uint32_t slot = it % TL::kStages, use = it / TL::kStages;
         if (use > 0 && !wait_phase(smem_addr(&ctl.kv_empty[slot]), (use - 1) & 1, ctl, p)) {
           ok = false;
@@ -352,14 +391,13 @@ __device__ void load_role(const CUtensorMap* tmQ, const CUtensorMap* tmK,
         bool coords = true;
         for (int c = 0; c < TL::kChunks; ++c)
           coords = coords && tma_ok(dst + c * kBN * 128, c * TL::kChunkElems, x.kvh, p.n_kv,
-                                    j * kBN, p.Lk, x.b);
+                                    list_tile<kWin>(x, j) * kBN, p.Lk, x.b);
         DBG_BREAK_UNLESS(coords)
 #endif
         mbar_arrive_expect_tx(bar, TL::kKVBytes);
 #pragma unroll
         for (int c = 0; c < TL::kChunks; ++c)
-          tma_load_4d(dst + c * kBN * 128, kind ? tmV : tmK, bar, c * TL::kChunkElems, x.kvh, j * kBN,
-                      x.b);
+          tma_load_4d(dst + c * kBN * 128, tm, bar, c * TL::kChunkElems, x.kvh, key0, x.b);
         DBG_ISSUE(kv_full[slot]);
         ++it;
       }
@@ -415,7 +453,7 @@ __device__ __forceinline__ void issue_pv(bool leader, uint32_t d_tmem, uint32_t 
   }
 }
 
-template <int D, bool F8>
+template <int D, bool F8, bool kWin>
 __device__ void mma_role(Ctl& ctl, const Params& p, uint32_t tmem, uint32_t sQ0, uint32_t sQ1,
                          uint32_t sKV, uint32_t smem_end) {
   using TL = Tile<D, F8>;
@@ -438,7 +476,7 @@ __device__ void mma_role(Ctl& ctl, const Params& p, uint32_t tmem, uint32_t sQ0,
   for (int r = 0; r * static_cast<int>(gridDim.x) < p.units; ++r) {
     const int u = snake_unit(r);
     if (u >= p.units) continue;
-    const Unit x = decode_unit(u, p);
+    const Unit x = decode_unit<kWin>(u, p);
 #ifdef ATTN_DEBUG
     if (!tmem_ok) break;
 #endif
@@ -571,7 +609,7 @@ __device__ __forceinline__ float row_max128(const float* v) {
   return max3(max3(m[0], m[1], m[2]), max3(m[3], m[4], m[5]), fmaxf(m[6], m[7]));
 }
 
-template <int D, bool F8, bool kPos>
+template <int D, bool F8, bool kPos, bool kWin>
 __device__ void softmax_role(int slot, Ctl& ctl, const Params& p, uint32_t tmem,
                              uint32_t o_stage) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -595,7 +633,7 @@ __device__ void softmax_role(int slot, Ctl& ctl, const Params& p, uint32_t tmem,
   for (int rr = 0; rr * static_cast<int>(gridDim.x) < p.units; ++rr) {
     const int u = snake_unit(rr);
     if (u >= p.units) continue;
-    const Unit x = decode_unit(u, p);
+    const Unit x = decode_unit<kWin>(u, p);
     // this warpgroup's query tile (selected, not indexed: a runtime index
     // would put the unit in local memory)
     const int n = slot ? x.n[1] : x.n[0];
@@ -634,12 +672,40 @@ __device__ void softmax_role(int slot, Ctl& ctl, const Params& p, uint32_t tmem,
       // Keys after in-tile index `keep` are masked: past the row's absolute
       // position (causal; the diagonal tile, or the last two tiles when the
       // chunk offset is not a multiple of the tile), or past the last key.
-      const bool masked = p.causal ? (j * kBN + kBN - 1 > qrow0) : (p.Lk - j * kBN < kBN);
-      if (masked) {
-        const int keep = p.causal ? qrow0 + r - j * kBN : p.Lk - 1 - j * kBN;
+      if (kWin) {
+        // A sinks' tile holds the keys below min(S, low); a window's tile the keys
+        // from `low` on, of which a row sees those up to its position and either
+        // within W of it or below S. In-tile indices:
+        const int key0 = list_tile<true>(x, j) * kBN;
+        if (j < x.na) {
+          const int keep = min(p.sinks, x.low) - 1 - key0;
+          if (keep < kBN - 1) {
 #pragma unroll
-        for (int i = 0; i < 128; ++i)
-          if (i > keep) s[i] = -INFINITY;
+            for (int i = 0; i < 128; ++i)
+              if (i > keep) s[i] = -INFINITY;
+          }
+        } else if (key0 + kBN - 1 > qrow0 || key0 <= qrow0 + kBM - 1 - p.window) {
+          const int keep = qrow0 + r - key0;
+          const int out = keep - p.window;                    // up to here out of the window
+          const int sink0 = x.low - key0, sink1 = p.sinks - key0;
+          if (sink1 > max(sink0, 0)) {
+#pragma unroll
+            for (int i = 0; i < 128; ++i)
+              if (i > keep || (i <= out && (i < sink0 || i >= sink1))) s[i] = -INFINITY;
+          } else {
+#pragma unroll
+            for (int i = 0; i < 128; ++i)
+              if (i > keep || i <= out) s[i] = -INFINITY;
+          }
+        }
+      } else {
+        const bool masked = p.causal ? (j * kBN + kBN - 1 > qrow0) : (p.Lk - j * kBN < kBN);
+        if (masked) {
+          const int keep = p.causal ? qrow0 + r - j * kBN : p.Lk - 1 - j * kBN;
+#pragma unroll
+          for (int i = 0; i < 128; ++i)
+            if (i > keep) s[i] = -INFINITY;
+        }
       }
       const float m_tile = row_max128(s) * cc;
       const float m_new = fmaxf(m_run, m_tile);
@@ -774,11 +840,10 @@ __device__ void softmax_role(int slot, Ctl& ctl, const Params& p, uint32_t tmem,
 
 // -------------------------------------------------------------------- kernel
 
-template <int D, bool F8, bool kPos>
-__global__ void __launch_bounds__(kThreads, 1)
-attn_prefill_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
-                        const __grid_constant__ CUtensorMap tmK,
-                        const __grid_constant__ CUtensorMap tmV, const Params p) {
+template <int D, bool F8, bool kPos, bool kWin>
+__device__ __forceinline__ void forward_body(const CUtensorMap& tmQ, const CUtensorMap& tmK,
+                                             const CUtensorMap& tmV, const CUtensorMap& tmKs,
+                                             const CUtensorMap& tmVs, const Params& p) {
   using TL = Tile<D, F8>;
   extern __shared__ uint8_t dyn_smem[];
   __shared__ Ctl ctl;
@@ -822,13 +887,14 @@ attn_prefill_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
 
   if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-    softmax_role<D, F8, kPos>(warp >> 2, ctl, p, tmem, sKV + TL::kStages * TL::kKVBytes);
+    softmax_role<D, F8, kPos, kWin>(warp >> 2, ctl, p, tmem, sKV + TL::kStages * TL::kKVBytes);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == kLoadWarp) {
-      if (lane == 0) load_role<D, F8>(&tmQ, &tmK, &tmV, ctl, p, sQ0, sQ1, sKV, smem_end);
+      if (lane == 0)
+        load_role<D, F8, kWin>(&tmQ, &tmK, &tmV, &tmKs, &tmVs, ctl, p, sQ0, sQ1, sKV, smem_end);
     } else if (warp == kMmaWarp) {
-      mma_role<D, F8>(ctl, p, tmem, sQ0, sQ1, sKV, smem_end);
+      mma_role<D, F8, kWin>(ctl, p, tmem, sQ0, sQ1, sKV, smem_end);
     }
   }
 
@@ -841,6 +907,26 @@ attn_prefill_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
 #ifdef ATTN_DEBUG
   if (threadIdx.x == 0) atomicAdd(&g_dbg_checks, static_cast<unsigned long long>(ctl.dbg.checks));
 #endif
+}
+
+template <int D, bool F8, bool kPos>
+__global__ void __launch_bounds__(kThreads, 1)
+attn_prefill_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
+                        const __grid_constant__ CUtensorMap tmK,
+                        const __grid_constant__ CUtensorMap tmV, const Params p) {
+  forward_body<D, F8, kPos, false>(tmQ, tmK, tmV, tmK, tmV, p);
+}
+
+// The windowed instances: tmK and tmV begin at position p.first, tmKs and tmVs
+// hold the sinks.
+template <int D, bool F8, bool kPos>
+__global__ void __launch_bounds__(kThreads, 1)
+attn_prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
+                           const __grid_constant__ CUtensorMap tmK,
+                           const __grid_constant__ CUtensorMap tmV,
+                           const __grid_constant__ CUtensorMap tmKs,
+                           const __grid_constant__ CUtensorMap tmVs, const Params p) {
+  forward_body<D, F8, kPos, true>(tmQ, tmK, tmV, tmKs, tmVs, p);
 }
 
 // ---------------------------------------------------------------- host side
@@ -865,22 +951,32 @@ EncodeTiledFn g_encode = nullptr;
 // The softmax warpgroups raise their register limit with setmaxnreg; that
 // only succeeds if the CTA was launched with at least kRegBudget registers,
 // so refuse to launch a build whose register count does not cover the split.
+template <typename Kernel>
+bool configure(Kernel* kernel, int smem_bytes) {
+  cudaFuncAttributes fa;
+  if (cudaFuncGetAttributes(&fa, kernel) != cudaSuccess || fa.numRegs * kThreads < kRegBudget)
+    return false;
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes) ==
+         cudaSuccess;
+}
 template <int D, bool F8, bool kPos>
 bool configure_kernel() {
-  cudaFuncAttributes fa;
-  if (cudaFuncGetAttributes(&fa, attn_prefill_fwd_kernel<D, F8, kPos>) != cudaSuccess ||
-      fa.numRegs * kThreads < kRegBudget)
-    return false;
-  return cudaFuncSetAttribute(attn_prefill_fwd_kernel<D, F8, kPos>,
-                              cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              Tile<D, F8>::kSmemBytes) == cudaSuccess;
+  return configure(attn_prefill_fwd_kernel<D, F8, kPos>, Tile<D, F8>::kSmemBytes);
+}
+// (bf16 only: the fp8 forward has no windowed instance)
+bool configure_window_kernels() {
+  return configure(attn_prefill_window_kernel<64, false, true>, Tile<64, false>::kSmemBytes) &&
+         configure(attn_prefill_window_kernel<64, false, false>, Tile<64, false>::kSmemBytes) &&
+         configure(attn_prefill_window_kernel<128, false, true>, Tile<128, false>::kSmemBytes) &&
+         configure(attn_prefill_window_kernel<128, false, false>, Tile<128, false>::kSmemBytes);
 }
 
 // Register-split check and shared-memory limit for every kernel instance.
 bool configure_kernels() {
   return configure_kernel<64, false, true>() && configure_kernel<128, false, true>() &&
          configure_kernel<128, true, true>() && configure_kernel<64, false, false>() &&
-         configure_kernel<128, false, false>() && configure_kernel<128, true, false>();
+         configure_kernel<128, false, false>() && configure_kernel<128, true, false>() &&
+         configure_window_kernels();
 }
 
 attn_status_t device_state(cudaStream_t stream, DeviceState** out) {
@@ -932,12 +1028,14 @@ attn_status_t device_state(cudaStream_t stream, DeviceState** out) {
 
 // [B, L, H, D] (bf16, or e4m3 bytes when f8) as a 4-D tensor (D, H, L, B);
 // boxes of one 128-byte row chunk x 1 x 128 x 1 with 128-byte swizzle. Rows
-// past L read as zeros.
+// past L read as zeros; of a window's maps, all but rows [first, first + rows).
 bool encode_bhld(CUtensorMap* map, const void* ptr, int D, int H, int64_t L, int64_t B,
-                 bool f8 = false) {
+                 bool f8 = false, int64_t first = 0, int64_t rows = 0) {
   const cuuint64_t eb = f8 ? 1 : 2;
+  ptr = static_cast<const char*>(ptr) + first * H * D * static_cast<int64_t>(eb);
   const cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(H),
-                              static_cast<cuuint64_t>(L), static_cast<cuuint64_t>(B)};
+                              static_cast<cuuint64_t>(rows > 0 ? rows : L),
+                              static_cast<cuuint64_t>(B)};
   const cuuint64_t strides[3] = {static_cast<cuuint64_t>(D) * eb,
                                  static_cast<cuuint64_t>(H) * D * eb,
                                  static_cast<cuuint64_t>(L) * H * D * eb};
@@ -1002,22 +1100,43 @@ void launch_instance(int grid, cudaStream_t stream, const CUtensorMap& mq, const
         <<<grid, kThreads, Tile<64, false>::kSmemBytes, stream>>>(mq, mk, mv, p);
 }
 
+template <bool kPos>
+void launch_window(int grid, cudaStream_t stream, const CUtensorMap& mq, const CUtensorMap& mk,
+                   const CUtensorMap& mv, const CUtensorMap& mks, const CUtensorMap& mvs,
+                   const Params& p, int d_h) {
+  if (d_h == 128)
+    attn_prefill_window_kernel<128, false, kPos>
+        <<<grid, kThreads, Tile<128, false>::kSmemBytes, stream>>>(mq, mk, mv, mks, mvs, p);
+  else
+    attn_prefill_window_kernel<64, false, kPos>
+        <<<grid, kThreads, Tile<64, false>::kSmemBytes, stream>>>(mq, mk, mv, mks, mvs, p);
+}
+
 // Encodes the tensor maps, fills the parameters and launches (arguments
 // already validated). `status` is the device status word the kernel reports
 // wait timeouts into; `sms` the device's multiprocessor count.
 // f8: Q, K, V are e4m3 with the given descale factors (real value = stored
-// value * descale); otherwise bf16 and the descales are 1.
+// value * descale); otherwise bf16 and the descales are 1. window > 0: the
+// windowed instances (causal, bf16).
 attn_status_t launch_forward(const void* q, const void* k, const void* v, void* o, float* lse,
                              int64_t B, int64_t Lq, int64_t Lk, int32_t n_q, int32_t n_kv,
                              int32_t d_h, int32_t causal, float scale, cudaStream_t stream,
                              int* status, int sms, int l2, bool f8 = false,
                              float qk_descale = 1.0f,
-                             float v_descale = 1.0f) {
+                             float v_descale = 1.0f, int64_t window = 0, int64_t sinks = 0) {
   int Tq = 0, units = 0;
   count_units(B, Lq, Lk, n_q, n_kv, &Tq, &units);
-  CUtensorMap mq, mk, mv;
-  if (!encode_bhld(&mq, q, d_h, n_q, Lq, B, f8) || !encode_bhld(&mk, k, d_h, n_kv, Lk, B, f8) ||
-      !encode_bhld(&mv, v, d_h, n_kv, Lk, B, f8))
+  window = window < Lk ? window : Lk;
+  sinks = sinks < Lk ? sinks : Lk;
+  // the first position that some row sees in its window
+  const int64_t first = window > 0 && Lk - Lq - window + 1 > 0 ? Lk - Lq - window + 1 : 0;
+  CUtensorMap mq, mk, mv, mks, mvs;
+  if (!encode_bhld(&mq, q, d_h, n_q, Lq, B, f8) ||
+      !encode_bhld(&mk, k, d_h, n_kv, Lk, B, f8, first, Lk - first) ||
+      !encode_bhld(&mv, v, d_h, n_kv, Lk, B, f8, first, Lk - first))
+    return ATTN_ERR_CUDA;
+  if (window > 0 && (!encode_bhld(&mks, k, d_h, n_kv, Lk, B, f8, 0, sinks) ||
+                     !encode_bhld(&mvs, v, d_h, n_kv, Lk, B, f8, 0, sinks)))
     return ATTN_ERR_CUDA;
 
   Params p;
@@ -1036,6 +1155,9 @@ attn_status_t launch_forward(const void* q, const void* k, const void* v, void* 
   p.c = scale * qk_descale * 1.4426950408889634f;
   p.o_scale = v_descale;
   p.scale_pos = p.c > 0.0f ? 1 : 0;
+  p.window = static_cast<int>(window);
+  p.sinks = static_cast<int>(sinks);
+  p.first = static_cast<int>(first);
   p.groups = static_cast<int>(B * n_kv);
   p.units = units;
   p.pairs = units / p.groups;
@@ -1043,9 +1165,10 @@ attn_status_t launch_forward(const void* q, const void* k, const void* v, void* 
   {
     // Batches of groups only when the K/V of all groups is well beyond the
     // L2 (more than 1.5 times its size): then as many groups as fit half of
-    // it, but at least kBatchRounds rounds of the grid's units per batch.
+    // it, but at least kBatchRounds rounds of the grid's units per batch. (Behind
+    // a window the groups' units of one pair read only that window.)
     const int64_t kv_group = 2 * Lk * static_cast<int64_t>(d_h) * (f8 ? 1 : 2);
-    if (2 * kv_group * p.groups > 3 * static_cast<int64_t>(l2)) {
+    if (window == 0 && 2 * kv_group * p.groups > 3 * static_cast<int64_t>(l2)) {
       const int64_t grid_ctas = units < sms ? units : sms;
       const int64_t by_rounds = (kBatchRounds * grid_ctas + p.pairs - 1) / p.pairs;
       const int64_t by_l2 = (l2 / 2) / kv_group;
@@ -1057,7 +1180,11 @@ attn_status_t launch_forward(const void* q, const void* k, const void* v, void* 
   p.spin_limit = kSpinLimitCycles;
 
   const int grid = units < sms ? units : sms;
-  if (p.scale_pos)
+  if (window > 0 && p.scale_pos)
+    launch_window<true>(grid, stream, mq, mk, mv, mks, mvs, p, d_h);
+  else if (window > 0)
+    launch_window<false>(grid, stream, mq, mk, mv, mks, mvs, p, d_h);
+  else if (p.scale_pos)
     launch_instance<true>(grid, stream, mq, mk, mv, p, f8, d_h);
   else
     launch_instance<false>(grid, stream, mq, mk, mv, p, f8, d_h);
@@ -1222,6 +1349,21 @@ attn_status_t attn_prefill_fwd_fp8(const void* q, const void* k, const void* v, 
   return launch_forward(q, k, v, o, lse, B, Lq, Lk, n_q, n_kv, d_h, causal, scale, stream,
                         st->status, st->sms, st->l2, true, q_descale * k_descale,
                         v_descale);
+}
+
+attn_status_t attn_prefill_window_fwd(const void* q, const void* k, const void* v, void* o,
+                                      float* lse, int64_t B, int64_t Lq, int64_t Lk, int32_t n_q,
+                                      int32_t n_kv, int32_t d_h, int64_t window, int64_t sinks,
+                                      float scale, void* stream_ptr) {
+  if (window < 1 || sinks < 0) return ATTN_ERR_INVALID_ARG;
+  const attn_status_t bad = validate(q, k, v, o, lse, B, Lq, Lk, n_q, n_kv, d_h, 1, scale);
+  if (bad != ATTN_OK) return bad;
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
+  DeviceState* st = nullptr;
+  const attn_status_t ds = device_state(stream, &st);
+  if (ds != ATTN_OK) return ds;
+  return launch_forward(q, k, v, o, lse, B, Lq, Lk, n_q, n_kv, d_h, 1, scale, stream, st->status,
+                        st->sms, st->l2, false, 1.0f, 1.0f, window, sinks);
 }
 
 const char* attn_status_string(attn_status_t status) {

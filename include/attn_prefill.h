@@ -1,8 +1,9 @@
 /*
  * attn_prefill.h — C ABI of the GB300 (sm_103a) causal GQA prefill attention:
  * the forward pass (square and chunked, bf16 and fp8), decode, the backward
- * pass, the cache operators (key weights, ragged decode, decode behind a shared
- * prefix, eviction) and diagnostics.
+ * pass, the same three behind a sliding window with sinks, the cache operators
+ * (key weights, ragged decode, decode behind a shared prefix, eviction) and
+ * diagnostics.
  *
  * Operation (one call computes, for every batch b, query head h and row i):
  *
@@ -133,6 +134,26 @@ attn_status_t attn_prefill_fwd_chunk(const void* q, const void* k, const void* v
                                      void* stream);
 
 /*
+ * Sliding window with sinks: attn_prefill_fwd_chunk (causal) where a row sees the
+ * last `window` positions, its own among them, and the first `sinks`, which stay
+ * visible to every row:
+ *
+ *     p = i + Lk - Lq,   J(i) = { j <= p : j > p - window or j < sinks }
+ *
+ *   window   >= 1 (ATTN_ERR_INVALID_ARG otherwise); a window of Lk or more hides
+ *            nothing
+ *   sinks    >= 0 (ATTN_ERR_INVALID_ARG otherwise); 0: a plain window
+ *   Positions of k and v that no row of the call sees (of a chunk: those from
+ *   `sinks` up to Lk - Lq - window) may hold anything, NaN included. A position
+ *   that some rows see must be finite for the results of the other rows in its
+ *   256 neighbours to be. Everything else as attn_prefill_fwd_chunk.
+ */
+attn_status_t attn_prefill_window_fwd(const void* q, const void* k, const void* v,
+                                      void* o, float* lse, int64_t B, int64_t Lq, int64_t Lk,
+                                      int32_t n_q, int32_t n_kv, int32_t d_h, int64_t window,
+                                      int64_t sinks, float scale, void* stream);
+
+/*
  * FP8 variant: Q, K and V in e4m3 (OCP FP8 E4M3, 1 byte per element, same
  * [B, L, H, d_h] layouts) with per-tensor descale factors, so the real inputs
  * are q*q_descale, k*k_descale, v*v_descale ("prefill-attention" flop record
@@ -250,6 +271,25 @@ attn_status_t attn_decode_ragged_fwd(const void* q, const void* k, const void* v
                                      void* stream);
 
 /*
+ * Ragged decode behind a sliding window with sinks: the new token, which sits at
+ * position lens[b] - 1 (its own K and V are in the cache), sees
+ *
+ *     j < lens[b]  with  j >= lens[b] - window  or  j < sinks
+ *
+ *   window >= 1, sinks >= 0 (ATTN_ERR_INVALID_ARG otherwise). Only the visible
+ *   positions are read; the others of k and v may hold anything (NaN included).
+ *   Everything else as attn_decode_ragged_fwd without weights.
+ */
+int64_t attn_decode_window_workspace_bytes(int64_t B, int64_t C, int32_t n_q, int32_t n_kv,
+                                           int32_t d_h, int64_t window,
+                                           int64_t sinks);   /* -1 as above */
+attn_status_t attn_decode_window_fwd(const void* q, const void* k, const void* v,
+                                     const int32_t* lens, void* o, float* lse, void* workspace,
+                                     int64_t workspace_bytes, int64_t B, int64_t C, int32_t n_q,
+                                     int32_t n_kv, int32_t d_h, int64_t window, int64_t sinks,
+                                     float scale, void* stream);
+
+/*
  * Decode behind a shared prefix: one new token per sequence attends to P
  * positions that the whole batch shares (a system prompt, a document; stored
  * once) and to the first lens[b] positions of its own cache, in one softmax:
@@ -358,6 +398,24 @@ attn_status_t attn_prefill_bwd(const void* q, const void* k, const void* v, cons
                                void* workspace, int64_t workspace_bytes,
                                int64_t B, int64_t L, int32_t n_q, int32_t n_kv, int32_t d_h,
                                int32_t causal, float scale, void* stream);
+
+/*
+ * Backward of attn_prefill_window_fwd with Lq = Lk = L: attn_prefill_bwd with the
+ * sums over J(i) of that call. Key tiles that hold sinks, which every later row
+ * sees, are cut into parts that a fourth kernel adds, in a fixed order: results
+ * are deterministic. Its workspace depends on window and sinks too; window >= 1
+ * and sinks >= 0 (ATTN_ERR_INVALID_ARG otherwise). Everything else as
+ * attn_prefill_bwd.
+ */
+int64_t attn_prefill_window_bwd_workspace_bytes(int64_t B, int64_t L, int32_t n_q, int32_t n_kv,
+                                                int32_t d_h, int64_t window,
+                                                int64_t sinks);   /* -1 as above */
+attn_status_t attn_prefill_window_bwd(const void* q, const void* k, const void* v, const void* o,
+                                      const float* lse, const void* dout,
+                                      void* dq, void* dk, void* dv,
+                                      void* workspace, int64_t workspace_bytes,
+                                      int64_t B, int64_t L, int32_t n_q, int32_t n_kv, int32_t d_h,
+                                      int64_t window, int64_t sinks, float scale, void* stream);
 
 /*
  * Forward pass over host buffers (no counterpart on the pages: a deployment

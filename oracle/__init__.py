@@ -17,6 +17,8 @@ backward
 cache
     The cache operators: key weights, ragged decode, eviction and decode
     behind a shared prefix, one row or one head at a time.
+window
+    Attention behind a sliding window with sinks: forward, backward, decode.
 flops
     The cost model the pages use: the causal prefill FLOP count
     2*n_q*d_h*L^2, the dense count 4*L^2*d_h*n_q, the K/V byte count and the
@@ -24,14 +26,15 @@ flops
     prefill FLOPs.
 
 Parity status: every function here is pinned (``tests/test_oracle_pins.py``,
-``tests/test_oracle_backward_pins.py``, ``tests/test_cache_ops.py``)
+``tests/test_oracle_backward_pins.py``, ``tests/test_cache_ops.py``,
+``tests/test_window_ops.py``)
 to values the pages print, closed forms, invariants, brute force and a
 library routine; none is "parity unpinned".
 """
 
 from .attention import attention, attention_rows, kv_head_of
 from .backward import attention_backward, softmax_rowdot
-from . import cache, flops
+from . import cache, flops, window
 
 __all__ = ["attention", "attention_rows", "attention_backward", "softmax_rowdot", "kv_head_of",
-           "cache", "flops"]
+           "cache", "flops", "window"]
