@@ -20,6 +20,8 @@ from .api import (AttnError, attn_cache_evict, attn_decode, attn_decode_fwd, att
                   attn_prefill_window, attn_prefill_window_fwd, attn_prefill_window_backward,
                   attn_prefill_window_bwd, attn_prefill_window_bwd_workspace_bytes,
                   attn_decode_window, attn_decode_window_fwd, attn_decode_window_workspace_bytes,
+                  ROW4_BYTES, attn_cache_pack4, attn_cache_unpack4, attn_pack4, attn_unpack4,
+                  attn_decode4, attn_decode4_fwd, attn_decode4_workspace_bytes,
                   attn_selftest_wait_timeout, attn_selftest_wait_timeout_noalloc,
                   attn_prefill_fwd_host,
                   attn_prefill_host_staging_bytes)
@@ -36,6 +38,8 @@ __all__ = [
     "attn_selftest_wait_timeout_noalloc", "attn_prefill_fwd_host", "attn_prefill_host_staging_bytes",
     "attn_prefill_window", "attn_prefill_window_fwd", "attn_prefill_window_backward",
     "attn_prefill_window_bwd", "attn_prefill_window_bwd_workspace_bytes", "attn_decode_window",
-    "attn_decode_window_fwd", "attn_decode_window_workspace_bytes",
+    "attn_decode_window_fwd", "attn_decode_window_workspace_bytes", "ROW4_BYTES", "attn_pack4",
+    "attn_unpack4", "attn_cache_pack4", "attn_cache_unpack4", "attn_decode4", "attn_decode4_fwd",
+    "attn_decode4_workspace_bytes",
     "attn_prefill_grid_size", "load_library", "library_path", "status_string",
 ]

@@ -90,6 +90,15 @@ _SIGNATURES = {
     "attn_decode_window_fwd": (ctypes.c_int, [ctypes.c_void_p] * 7 + [ctypes.c_int64] * 3
                                + [ctypes.c_int32] * 3 + [ctypes.c_int64] * 2
                                + [ctypes.c_float, ctypes.c_void_p]),
+    "attn_cache_pack4": (ctypes.c_int, [ctypes.c_void_p] * 6 + [ctypes.c_int64] * 3
+                         + [ctypes.c_int32] * 2 + [ctypes.c_void_p]),
+    "attn_cache_unpack4": (ctypes.c_int, [ctypes.c_void_p] * 5 + [ctypes.c_int64] * 3
+                           + [ctypes.c_int32] * 2 + [ctypes.c_void_p]),
+    "attn_decode4_workspace_bytes": (ctypes.c_int64, [ctypes.c_int64] * 2 + [ctypes.c_int32] * 3
+                                     + [ctypes.c_int64] * 2),
+    "attn_decode4_fwd": (ctypes.c_int, [ctypes.c_void_p] * 7 + [ctypes.c_int64] * 3
+                         + [ctypes.c_int32] * 3 + [ctypes.c_int64] * 2
+                         + [ctypes.c_float, ctypes.c_void_p]),
     "attn_selftest_wait_timeout": (ctypes.c_int, [ctypes.c_int64, ctypes.c_void_p]),
     "attn_selftest_wait_timeout_noalloc": (ctypes.c_int, [ctypes.c_int64, ctypes.c_void_p]),
     "attn_prefill_host_staging_bytes": (ctypes.c_int64, [ctypes.c_int64, ctypes.c_int64,

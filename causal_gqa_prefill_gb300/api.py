@@ -827,6 +827,178 @@ def _step_sizes(torch, q, k, v, lens, out, lse):
     return B, C, n_q, n_kv, d
 
 
+ROW4_BYTES = 80      # a row of 128 channels in 4 bits: 64 bytes of codes, four scales and lowest values
+
+
+def attn_cache_pack4(k, v, k4, v4, at, counts, B, L, C, n_kv, d_h=128, stream=None) -> int:
+    """Direct call of the packing C entry point; returns the raw status code."""
+    lib = _abi.load()
+    return int(lib.attn_cache_pack4(_ptr(k), _ptr(v), _ptr(k4), _ptr(v4), _ptr(at), _ptr(counts),
+                                    int(B), int(L), int(C), int(n_kv), int(d_h),
+                                    _stream_handle(stream)))
+
+
+def attn_cache_unpack4(k4, v4, k, v, at, B, L, C, n_kv, d_h=128, stream=None) -> int:
+    """Direct call of the unpacking C entry point; returns the raw status code."""
+    lib = _abi.load()
+    return int(lib.attn_cache_unpack4(_ptr(k4), _ptr(v4), _ptr(k), _ptr(v), _ptr(at), int(B),
+                                      int(L), int(C), int(n_kv), int(d_h), _stream_handle(stream)))
+
+
+def attn_pack4(k, v, k4, v4, at=None, *, counts=None, stream=None):
+    """Stores rows in caches held in 4 bits: row i of k/v bf16 [B, L, n_kv, 128] of
+    sequence b as position at[b] + i of k4/v4 uint8 [B, n_kv, C, 80], a prompt's
+    rows or a decode step's (L = 1).
+
+    ``at`` (int32 CUDA tensor [B]) defaults to 0; with ``counts`` (int32 CUDA tensor
+    [B]) only the first counts[b] rows of sequence b are stored. Rows that would
+    lie outside the cache are left out, all other rows of the caches stay as they
+    are. Returns (k4, v4)."""
+    import torch
+
+    bf16, u8, i32 = torch.bfloat16, torch.uint8, torch.int32
+    try:
+        B, L, n_kv, d = k.shape
+        C = k4.shape[2]
+        index = k.get_device()
+        usual = (d == 128 and v.shape == k.shape
+                 and k4.shape == v4.shape == (B, n_kv, C, ROW4_BYTES)
+                 and (at is None or at.shape == (B,)) and (counts is None or counts.shape == (B,))
+                 and _laid_out(index, bf16, k, v) and _laid_out(index, u8, k4, v4)
+                 and _laid_out(index, i32, at, counts))
+    except (AttributeError, ValueError, IndexError):
+        usual = False
+    if not usual:
+        B, L, n_kv, d = _cuda_tensor("k", k, (None, None, None, 128), bf16).shape
+        dev = k.device
+        _cuda_tensor("v", v, k.shape, bf16, dev)
+        C = _cuda_tensor("k4", k4, (B, n_kv, None, ROW4_BYTES), u8, dev).shape[2]
+        _cuda_tensor("v4", v4, k4.shape, u8, dev)
+        for name, t in (("at", at), ("counts", counts)):
+            if t is not None:
+                _cuda_tensor(name, t, (B,), i32, dev)
+    with _Call(torch, k.device, stream) as call:
+        st = _abi.load().attn_cache_pack4(k.data_ptr(), v.data_ptr(), k4.data_ptr(), v4.data_ptr(),
+                                          _ptr(at), _ptr(counts), B, L, C, n_kv, 128, call.handle)
+    if st != _abi.ATTN_OK:
+        raise AttnError(st, "attn_cache_pack4")
+    return k4, v4
+
+
+def attn_unpack4(k4, v4, length, at=None, *, k=None, v=None, stream=None):
+    """Rows of caches held in 4 bits as bf16 (k, v) [B, length, n_kv, 128]: positions
+    at[b] .. at[b] + length - 1 of sequence b (``at``: int32 CUDA tensor [B], default
+    0), zeros for those outside the cache. What the earlier part of a prompt is
+    read back with before its next chunk's attn_prefill."""
+    import torch
+
+    bf16, u8, i32 = torch.bfloat16, torch.uint8, torch.int32
+    L = operator.index(length)
+    if L < 1:
+        raise ValueError("length must be at least 1")
+    try:
+        B, n_kv, C, row = k4.shape
+        index = k4.get_device()
+        shape = (B, L, n_kv, 128)
+        usual = (row == ROW4_BYTES and v4.shape == k4.shape and (at is None or at.shape == (B,))
+                 and (k is None or k.shape == shape) and (v is None or v.shape == shape)
+                 and _laid_out(index, u8, k4, v4) and _laid_out(index, bf16, k, v)
+                 and _laid_out(index, i32, at))
+    except (AttributeError, ValueError):
+        usual = False
+    if not usual:
+        B, n_kv, C, _ = _cuda_tensor("k4", k4, (None, None, None, ROW4_BYTES), u8).shape
+        dev = k4.device
+        _cuda_tensor("v4", v4, k4.shape, u8, dev)
+        shape = (B, L, n_kv, 128)
+        if at is not None:
+            _cuda_tensor("at", at, (B,), i32, dev)
+        for name, t in (("k", k), ("v", v)):
+            if t is not None:
+                _cuda_tensor(name, t, shape, bf16, dev)
+    with _Call(torch, k4.device, stream) as call:
+        k = call.empty(shape, bf16) if k is None else k
+        v = call.empty(shape, bf16) if v is None else v
+        st = _abi.load().attn_cache_unpack4(k4.data_ptr(), v4.data_ptr(), k.data_ptr(),
+                                            v.data_ptr(), _ptr(at), B, L, C, n_kv, 128, call.handle)
+    if st != _abi.ATTN_OK:
+        raise AttnError(st, "attn_cache_unpack4")
+    return k, v
+
+
+def attn_decode4_workspace_bytes(B, C, n_q, n_kv, d_h=128, window=0, sinks=0) -> int:
+    return int(_abi.load().attn_decode4_workspace_bytes(int(B), int(C), int(n_q), int(n_kv),
+                                                        int(d_h), int(window), int(sinks)))
+
+
+def attn_decode4_fwd(q, k4, v4, lens, o, lse, workspace, workspace_bytes, B, C, n_q, n_kv, d_h,
+                     window, sinks, scale, stream=None) -> int:
+    """Direct call of the C entry point of decode over 4-bit caches; returns the raw status code."""
+    lib = _abi.load()
+    return int(lib.attn_decode4_fwd(_ptr(q), _ptr(k4), _ptr(v4), _ptr(lens), _ptr(o), _ptr(lse),
+                                    _ptr(workspace), int(workspace_bytes), int(B), int(C), int(n_q),
+                                    int(n_kv), int(d_h), int(window), int(sinks), float(scale),
+                                    _stream_handle(stream)))
+
+
+def attn_decode4(q, k4, v4, lens, *, window=None, sinks=0, scale=None, workspace=None, out=None,
+                 lse=None, stream=None):
+    """One decode step against caches held in 4 bits: q bf16 [B, 1, n_q, 128], k4/v4
+    uint8 [B, n_kv, C, 80] (attn_pack4's) of which sequence b holds the first
+    lens[b] positions (int32 CUDA tensor [B], clamped to 0 .. C).
+
+    With ``window`` (and ``sinks``) the token sees what attn_decode_window's does.
+    Returns (o bf16 [B, 1, n_q, 128], lse fp32 [B, n_q, 1]); a sequence of length
+    0 gets o = 0 and lse = -inf. ``workspace`` (at least
+    attn_decode4_workspace_bytes bytes) is allocated with torch when not given."""
+    import torch
+
+    bf16, f32, u8, i32 = torch.bfloat16, torch.float32, torch.uint8, torch.int32
+    if window is None:
+        if operator.index(sinks) != 0:
+            raise ValueError("sinks need a window")
+        window = sinks = 0
+    else:
+        window, sinks = _window(window, sinks)
+    try:
+        B, one, n_q, d = q.shape
+        _, n_kv, C, row = k4.shape
+        index = q.get_device()
+        usual = (one == 1 and v4.shape == k4.shape == (B, n_kv, C, ROW4_BYTES) and d == 128
+                 and lens.shape == (B,) and (out is None or out.shape == q.shape)
+                 and (lse is None or lse.shape == (B, n_q, 1))
+                 and _laid_out(index, bf16, q, out) and _laid_out(index, u8, k4, v4)
+                 and _laid_out(index, f32, lse) and _laid_out(index, i32, lens))
+    except (AttributeError, ValueError):
+        usual = False
+    if not usual:
+        B, _, n_q, d = _cuda_tensor("q", q, (None, 1, None, 128), bf16).shape
+        dev = q.device
+        _, n_kv, C, _ = _cuda_tensor("k4", k4, (B, None, None, ROW4_BYTES), u8, dev).shape
+        _cuda_tensor("v4", v4, k4.shape, u8, dev)
+        _cuda_tensor("lens", lens, (B,), i32, dev)
+        if out is not None:
+            _cuda_tensor("out", out, q.shape, bf16, dev)
+        if lse is not None:
+            _cuda_tensor("lse", lse, (B, n_q, 1), f32, dev)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    with _Call(torch, q.device, stream) as call:
+        workspace, nbytes = call.workspace(workspace, attn_decode4_workspace_bytes, B, C, n_q, n_kv,
+                                           d, window, sinks)
+        if out is None:
+            out = call.empty(q.shape, bf16)
+        if lse is None:
+            lse = call.empty((B, n_q, 1), f32)
+        st = _abi.load().attn_decode4_fwd(
+            q.data_ptr(), k4.data_ptr(), v4.data_ptr(), lens.data_ptr(), out.data_ptr(),
+            lse.data_ptr(), workspace.data_ptr(), nbytes, B, C, n_q, n_kv, d, window, sinks, scale,
+            call.handle)
+    if st != _abi.ATTN_OK:
+        raise AttnError(st, "attn_decode4_fwd")
+    return out, lse
+
+
 def attn_device_check(stream=None) -> int:
     """Synchronise the stream and report device-side timeouts (raw status)."""
     return int(_abi.load().attn_device_check(_stream_handle(stream)))

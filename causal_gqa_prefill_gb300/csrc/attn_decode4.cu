@@ -1,0 +1,803 @@
+// attn_decode4.cu — decode attention (one new token per sequence) over caches
+// held in 4 bits (cache4.cuh), whole or behind a sliding window with sinks.
+//
+// A position costs 160 bytes per K/V head where bf16 takes 512, so at the copy
+// rate every element leaves a scheduler about three instruction slots per lane:
+// what bounds the step is the stream of rows and, close behind it, turning
+// codes into matrix operands. So the codes never leave registers between the
+// load and the product, and nothing but the products' results is kept in fp32:
+//
+//   * every warp streams its own run of positions of one head through a ring of
+//     kStages bulk copies (the rows of a head are contiguous) and works alone:
+//     no barrier but its own copies' until the end;
+//   * S^T = K Q^T with m16n8k16 products, 16 positions x 8 heads. A code is put
+//     into the upper mantissa bits of a bf16 16 (bits 3..6: 16 + code, exact),
+//     one shift and one logic instruction for two codes; the group's scale and
+//     offset are applied to the fp32 sums of its 32 channels:
+//       s = sum_g scale_g (sum (16 + code) q) + (lo_g - 16 scale_g) sum q,
+//     so no value of K is rounded;
+//   * O^T += V^T P^T likewise, 16 channels x 8 heads, with scale_g P (rounded to
+//     bf16) as the other operand and sum_j P_j lo_gj kept in fp32 beside it.
+//     P^T is turned by movmatrix; the two rows that a lane's operand pairs up
+//     are brought together by one byte permutation per four codes.
+// (mma.sync and not tcgen05: those operands come from shared memory or tensor
+// memory, and writing the bf16 values there would cost more than the product.)
+//
+// The list of 16-position chunks over all sequences and heads is cut into equal
+// runs, one per warp. At the end the warps of a CTA that stand in the same head
+// merge their results in shared memory, and a combine kernel merges what the
+// CTAs left. Lengths are read on the device.
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <mutex>
+
+#include "attn_prefill.h"
+#include "cache4.cuh"
+#include "sm103_ptx.cuh"
+
+namespace gb300_host {
+attn_status_t device_status_word(cudaStream_t stream, int** status);
+}
+
+namespace {
+
+using namespace gb300;
+
+constexpr int kChunk = 16;                         // positions per step of a warp
+constexpr int kChunkBytes = kChunk * kRow4Bytes;   // of K, and of V
+constexpr int kStages = 4;                         // chunks of K and V under way per warp
+constexpr int kWarpBytes = kStages * 2 * kChunkBytes;
+constexpr int kCtas = 152;                         // one per SM
+constexpr int kMaxG = 16;
+constexpr float kRescale = 8.0f;                   // lazy running maximum (log2 units)
+constexpr int kStatusTimeout = 1;
+constexpr long long kSpinLimit = 1ll << 31;        // about a second at 2 GHz
+
+// NT: the group's query heads in tiles of 8. 16 warps fit the registers with one
+// tile, 8 with two.
+template <int NT>
+constexpr int kWarpsOf = NT == 1 ? 16 : 8;
+template <int NT>
+constexpr int kSmemOf = kWarpsOf<NT> * kWarpBytes;
+static_assert(kMaxG * kRow4Dim * 4 <= kWarpBytes, "a warp's result fits its ring");
+
+struct Params4 {
+  const uint16_t* q;       // bf16 [B, n_q, 128]
+  const uint8_t *k4, *v4;
+  const int* lens;
+  float* part_o;           // fp32 [2 (B * n_kv + CTAs)][g][128]
+  float2* part_ml;         // running maximum (log2 units; -inf: nothing here) and sum
+  int* ends;               // [B * n_kv][2] CTAs that hold a head's first and last chunk
+  int* status;
+  int B, C, n_q, n_kv, g;
+  int window, sinks;       // window 0: everything before lens[b]
+  int walkers;             // warps that may have a run
+  float c;                 // scale * log2(e)
+};
+
+// A sequence's visible positions, [0, sunk) and [low, len), in chunks.
+struct Seen4 {
+  int len, low, sunk, na, chunks;
+  __device__ Seen4(const Params4& p, int b) {
+    len = min(max(p.lens[b], 0), p.C);
+    low = p.window > 0 ? max(0, len - p.window) : 0;
+    sunk = p.window > 0 ? min(p.sinks, low) : 0;
+    na = (sunk + kChunk - 1) / kChunk;
+    chunks = na + (len - low + kChunk - 1) / kChunk;
+  }
+};
+
+// A warp's place in the list: sequence, head, chunk; `left` chunks of its run to go.
+struct Walk4 {
+  int b, u, t, left;
+  int len, low, sunk, na, chunks;
+  __device__ void enter(const Params4& p) {
+    const Seen4 s(p, b);
+    len = s.len;
+    low = s.low;
+    sunk = s.sunk;
+    na = s.na;
+    chunks = s.chunks;
+  }
+  __device__ int pos() const { return t < na ? t * kChunk : low + (t - na) * kChunk; }
+  __device__ int count() const { return min(kChunk, (t < na ? sunk : len) - pos()); }
+  __device__ void advance(const Params4& p) {
+    ++t;
+    if (--left == 0 || t < chunks) return;
+    t = 0;
+    if (++u < p.n_kv) return;
+    u = 0;
+    do {
+      if (++b >= p.B) {     // (cannot be with chunks left)
+        left = 0;
+        return;
+      }
+      enter(p);
+    } while (chunks == 0);
+  }
+};
+
+// Where walker w's run starts: each lane sums a run of sequences, a scan places
+// them, and the lane that holds the first chunk finds it.
+__device__ __forceinline__ Walk4 walk_start(const Params4& p, int w) {
+  const int lane = threadIdx.x & 31;
+  const int run = (p.B + 31) / 32, b0 = min(lane * run, p.B), b1 = min(b0 + run, p.B);
+  long long sum = 0;
+#pragma unroll 4
+  for (int b = b0; b < b1; ++b) sum += Seen4(p, b).chunks;
+  sum *= p.n_kv;
+  long long incl = sum;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const long long n = __shfl_up_sync(0xffffffffu, incl, off);
+    if (lane >= off) incl += n;
+  }
+  const long long W = __shfl_sync(0xffffffffu, incl, 31);
+  const long long G = min(static_cast<long long>(p.walkers), W);   // every run has a chunk
+  Walk4 x{};
+  if (w >= G) return x;
+  const long long x0 = w * W / G;
+  const long long at0 = incl - sum;
+  const bool mine = x0 >= at0 && x0 < incl;
+  int b = 0, u = 0, t = 0;
+  if (mine) {
+    long long at = at0;
+    for (int i = b0; i < b1; ++i) {
+      const int T = Seen4(p, i).chunks;
+      const long long here = static_cast<long long>(T) * p.n_kv;
+      if (x0 < at + here) {
+        b = i;
+        u = static_cast<int>((x0 - at) / T);
+        t = static_cast<int>((x0 - at) % T);
+        break;
+      }
+      at += here;
+    }
+  }
+  const int src = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
+  x.b = __shfl_sync(0xffffffffu, b, src);
+  x.u = __shfl_sync(0xffffffffu, u, src);
+  x.t = __shfl_sync(0xffffffffu, t, src);
+  x.left = static_cast<int>((w + 1) * W / G - x0);
+  x.enter(p);
+  return x;
+}
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+
+// D += A B, 16 x 8 x 16, bf16 operands.
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
+// Codes n and n + 4 of a word (or the n-th of its two halves) as bf16 16 + code.
+template <int n>
+__device__ __forceinline__ uint32_t codes16(uint32_t w) {
+  const uint32_t at = n == 0 ? w << 3 : w >> (4 * n - 3);
+  return (at & 0x00780078u) | 0x41804180u;
+}
+// The same less 16: the codes themselves, exactly.
+template <int n>
+__device__ __forceinline__ uint32_t codes0(uint32_t w) {
+  uint32_t r;
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(codes16<n>(w)), "r"(0x41804180u));
+  return r;
+}
+
+// What a warp holds of one head: lane (r = lane / 4, t = lane % 4) has, for heads
+// 8 n + 2 t and + 1, channels 32 g + 4 r + 2 j (o[.][0..1]) and + 1 (o[.][2..3]),
+// its own share of sum_j P_j lo_gj and of the row sum, and the running maximum.
+template <int NT>
+struct Acc {
+  float o[NT][4][2][4];
+  float lows[NT][4][2];
+  float m[NT][2], l[NT][2];
+  __device__ void clear() {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[n][g][j][e] = 0.0f;
+        lows[n][g][0] = lows[n][g][1] = 0.0f;
+      }
+      m[n][0] = m[n][1] = -INFINITY;
+      l[n][0] = l[n][1] = 0.0f;
+    }
+  }
+  // Sums over the lanes; then lane (r, t) has head 8 n + 2 t + e whole.
+  __device__ void finish() {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) {
+          l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], off);
+#pragma unroll
+          for (int g = 0; g < 4; ++g)
+            lows[n][g][e] += __shfl_xor_sync(0xffffffffu, lows[n][g][e], off);
+        }
+      }
+  }
+  // Channels 32 g + 4 r .. + 3 of head 8 n + 2 t + e.
+  __device__ float4 channels(int n, int g, int e) const {
+    const float low = lows[n][g][e];
+    return make_float4(o[n][g][0][e] + low, o[n][g][0][2 + e] + low, o[n][g][1][e] + low,
+                       o[n][g][1][2 + e] + low);
+  }
+};
+
+template <int NT>
+__global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
+decode4_split_kernel(const Params4 p) {
+  constexpr int kWarps = kWarpsOf<NT>;
+  extern __shared__ __align__(128) uint8_t dyn_smem[];
+  __shared__ __align__(8) uint64_t full[kWarps][kStages];
+  __shared__ int head_of[kWarps];             // head that the warp ended in, -1: had no run
+  __shared__ float2 ml_of[kWarps][8 * NT];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r = lane >> 2, t = lane & 3;
+  const int cta = static_cast<int>(blockIdx.x), w = cta * kWarps + warp;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (lane < kStages) mbar_init(smem_addr(&full[warp][lane]), 1);
+  fence_mbar_init();
+  __syncwarp();
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+
+  const uint32_t ring = smem_addr(dyn_smem) + warp * kWarpBytes;
+  Walk4 cur = walk_start(p, w);
+  Walk4 ahead = cur;
+  uint32_t sent = 0, taken = 0;               // chunks under way or done, and done
+  auto send = [&]() {                         // the next chunk's rows of K and V
+    const int slot = sent % kStages;
+    if (lane == 0) {
+      const uint32_t bar = smem_addr(&full[warp][slot]);
+      const uint32_t dst = ring + slot * 2 * kChunkBytes;
+      const int n = ahead.count() * kRow4Bytes;
+      const int64_t at =
+          ((static_cast<int64_t>(ahead.b) * p.n_kv + ahead.u) * p.C + ahead.pos()) * kRow4Bytes;
+      mbar_arrive_expect_tx(bar, 2 * n);
+      bulk_load(dst, p.k4 + at, n, bar);
+      bulk_load(dst + kChunkBytes, p.v4 + at, n, bar);
+    }
+    ++sent;
+    ahead.advance(p);
+  };
+  for (int s = 0; s < kStages; ++s)
+    if (ahead.left > 0) send();
+
+  // position of row i of a chunk's products (i < 8; the others are 8 further on): rows
+  // 2 a and 2 a + 1 are positions a and a + 4, so that eight lanes' 16-byte loads of a
+  // chunk's 80-byte rows, of K (two rows) and of V (four), fall into different banks
+  const int kpos = (r >> 1) + 4 * (r & 1);
+  const uint32_t half = (r & 1) ? 0x7632u : 0x5410u;
+  Acc<NT> acc;
+  uint32_t qf[NT][4][4];                      // Q as the products' second operand
+  float qs[NT][4][2];                         // sums of a head's channels of a group
+  bool ok = true;
+  int hd = -1, t0 = 0, t_end = 0, T = 0;      // the segment: head, chunks [t0, t_end) of T
+
+  while (ok && cur.left > 0) {
+    hd = cur.b * p.n_kv + cur.u;
+    t0 = cur.t;
+    T = cur.chunks;
+    const int n_chunks = min(cur.left, T - t0);
+    t_end = t0 + n_chunks;
+    acc.clear();
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int h = 8 * n + r;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (h < p.g)
+          v = *reinterpret_cast<const uint4*>(
+              p.q + (static_cast<int64_t>(hd) * p.g + h) * kRow4Dim + 32 * g + 8 * t);
+        // channels e and e + 4 of the lane's eight, as the codes come
+        qf[n][g][0] = __byte_perm(v.x, v.z, 0x5410);
+        qf[n][g][1] = __byte_perm(v.x, v.z, 0x7632);
+        qf[n][g][2] = __byte_perm(v.y, v.w, 0x5410);
+        qf[n][g][3] = __byte_perm(v.y, v.w, 0x7632);
+        float sum = 0.0f;
+        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          sum += __uint_as_float(u[e] << 16) + __uint_as_float(u[e] & 0xFFFF0000u);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        qs[n][g][0] = __shfl_sync(0xffffffffu, sum, 8 * t);
+        qs[n][g][1] = __shfl_sync(0xffffffffu, sum, 8 * t + 4);
+      }
+    }
+
+    for (int i = 0; i < n_chunks; ++i) {
+      const int slot = taken % kStages;
+      const uint32_t bar = smem_addr(&full[warp][slot]), parity = (taken / kStages) & 1;
+      bool there = mbar_try_wait(bar, parity);
+      if (!there) {
+        const uint64_t since = clock64_now();
+        while (!(there = mbar_try_wait(bar, parity)))
+          if (static_cast<long long>(clock64_now() - since) > kSpinLimit) break;
+      }
+      if (!__all_sync(0xffffffffu, there)) {
+        if (lane == 0) atomicOr(p.status, kStatusTimeout);
+        ok = false;
+        break;
+      }
+      const int valid = cur.count();
+      const bool seen[2] = {kpos < valid, kpos + 8 < valid};
+      const uint32_t sk = ring + slot * 2 * kChunkBytes, sv = sk + kChunkBytes;
+      const uint32_t row0 = kpos * kRow4Bytes, row1 = row0 + 8 * kRow4Bytes;
+
+      // S^T: rows r and r + 8 of the chunk, heads 2 t and 2 t + 1 of each tile
+      float s[NT][4];
+      {
+        const uint4 k0 = lds128(sk + row0 + 16 * t), k1 = lds128(sk + row1 + 16 * t);
+        const uint4 p0 = lds128(sk + row0 + kRow4Codes), p1 = lds128(sk + row1 + kRow4Codes);
+        const uint32_t c0[4] = {k0.x, k0.y, k0.z, k0.w}, c1[4] = {k1.x, k1.y, k1.z, k1.w};
+        const uint32_t m0[4] = {p0.x, p0.y, p0.z, p0.w}, m1[4] = {p1.x, p1.y, p1.z, p1.w};
+#pragma unroll
+        for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.0f;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const uint32_t a00 = codes16<0>(c0[g]), a01 = codes16<0>(c1[g]);
+          const uint32_t a02 = codes16<1>(c0[g]), a03 = codes16<1>(c1[g]);
+          const uint32_t a10 = codes16<2>(c0[g]), a11 = codes16<2>(c1[g]);
+          const uint32_t a12 = codes16<3>(c0[g]), a13 = codes16<3>(c1[g]);
+          const float s0 = row4_scale(m0[g]), s1 = row4_scale(m1[g]);
+          const float l0 = fmaf(-16.0f, s0, row4_low(m0[g])), l1 = fmaf(-16.0f, s1, row4_low(m1[g]));
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            mma16816(d, a00, a01, a02, a03, qf[n][g][0], qf[n][g][1]);
+            mma16816(d, a10, a11, a12, a13, qf[n][g][2], qf[n][g][3]);
+            s[n][0] = fmaf(s0, d[0], fmaf(l0, qs[n][g][0], s[n][0]));
+            s[n][1] = fmaf(s0, d[1], fmaf(l0, qs[n][g][1], s[n][1]));
+            s[n][2] = fmaf(s1, d[2], fmaf(l1, qs[n][g][0], s[n][2]));
+            s[n][3] = fmaf(s1, d[3], fmaf(l1, qs[n][g][1], s[n][3]));
+          }
+        }
+      }
+      bool need = false;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          s[n][e] = seen[e >> 1] ? s[n][e] * p.c : -INFINITY;
+          need |= s[n][e] > acc.m[n][e & 1] + kRescale;
+        }
+      if (__any_sync(0xffffffffu, need)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float top = fmaxf(s[n][e], s[n][2 + e]);
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1)
+              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+            const float m = fmaxf(acc.m[n][e], top);
+            const float alpha = m == acc.m[n][e] ? 1.0f
+                                : acc.m[n][e] == -INFINITY ? 0.0f : ex2_approx(acc.m[n][e] - m);
+            acc.m[n][e] = m;
+            acc.l[n][e] *= alpha;
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              acc.lows[n][g][e] *= alpha;
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                acc.o[n][g][j][e] *= alpha;
+                acc.o[n][g][j][2 + e] *= alpha;
+              }
+            }
+          }
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float m = acc.m[n][e & 1];
+          s[n][e] = ex2_approx(s[n][e] - (m == -INFINITY ? 0.0f : m));
+          acc.l[n][e & 1] += s[n][e];
+        }
+
+      // O^T: P times the scale of its position's group, turned, against V's codes
+      {
+        const uint4 p0 = lds128(sv + row0 + kRow4Codes), p1 = lds128(sv + row1 + kRow4Codes);
+        // (rows that do not count may hold anything)
+        const uint32_t m0[4] = {seen[0] ? p0.x : 0u, seen[0] ? p0.y : 0u, seen[0] ? p0.z : 0u,
+                                seen[0] ? p0.w : 0u};
+        const uint32_t m1[4] = {seen[1] ? p1.x : 0u, seen[1] ? p1.y : 0u, seen[1] ? p1.z : 0u,
+                                seen[1] ? p1.w : 0u};
+        // rows 2 t, 2 t + 1 (positions t, t + 4) and 8 further on; codes of block r / 2
+        const uint32_t base = sv + t * kRow4Bytes + 16 * (r >> 1);
+        const uint4 va = lds128(base), vb = lds128(base + 4 * kRow4Bytes);
+        const uint4 vc = lds128(base + 8 * kRow4Bytes), vd = lds128(base + 12 * kRow4Bytes);
+        const uint32_t ca[4] = {va.x, va.y, va.z, va.w}, cb[4] = {vb.x, vb.y, vb.z, vb.w};
+        const uint32_t cc[4] = {vc.x, vc.y, vc.z, vc.w}, cd[4] = {vd.x, vd.y, vd.z, vd.w};
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const uint32_t ab = __byte_perm(ca[g], cb[g], half), gh = __byte_perm(cc[g], cd[g], half);
+          const uint32_t a0 = codes0<0>(ab), a1 = codes0<1>(ab), a2 = codes0<0>(gh),
+                         a3 = codes0<1>(gh);
+          const uint32_t b0 = codes0<2>(ab), b1 = codes0<3>(ab), b2 = codes0<2>(gh),
+                         b3 = codes0<3>(gh);
+          const float s0 = row4_scale(m0[g]), s1 = row4_scale(m1[g]);
+          const float l0 = row4_low(m0[g]), l1 = row4_low(m1[g]);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            const uint32_t x0 = transpose8x8(pack_bf16x2(s[n][0] * s0, s[n][1] * s0));
+            const uint32_t x1 = transpose8x8(pack_bf16x2(s[n][2] * s1, s[n][3] * s1));
+            acc.lows[n][g][0] = fmaf(s[n][0], l0, fmaf(s[n][2], l1, acc.lows[n][g][0]));
+            acc.lows[n][g][1] = fmaf(s[n][1], l0, fmaf(s[n][3], l1, acc.lows[n][g][1]));
+            mma16816(acc.o[n][g][0], a0, a1, a2, a3, x0, x1);
+            mma16816(acc.o[n][g][1], b0, b1, b2, b3, x0, x1);
+          }
+        }
+      }
+      ++taken;
+      cur.advance(p);
+      __syncwarp();
+      if (ahead.left > 0) send();
+    }
+    if (!ok || cur.left == 0) break;
+
+    // the head goes on in no other warp's run but earlier ones: its end goes out as it is
+    acc.finish();
+    if (lane == 0) {
+      if (t0 == 0) p.ends[2 * hd] = cta;
+      p.ends[2 * hd + 1] = cta;
+    }
+    const int64_t slot = 2 * (static_cast<int64_t>(hd) + cta) + 1;
+    // without a run of this CTA before it, the run's place stays empty
+    const bool alone = t0 == 0 || warp == 0;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int h = 8 * n + 2 * t + e;
+        if (h >= p.g) continue;
+        float* out = p.part_o + (slot * p.g + h) * kRow4Dim + 4 * r;
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          *reinterpret_cast<float4*>(out + 32 * g) = acc.channels(n, g, e);
+        if (r == 0) {
+          p.part_ml[slot * p.g + h] = make_float2(acc.m[n][e], acc.l[n][e]);
+          if (alone) p.part_ml[(slot - 1) * p.g + h] = make_float2(-INFINITY, 0.0f);
+        }
+      }
+  }
+
+  // Every copy this warp started has landed before the CTA can end.
+  for (uint32_t c = taken; c < sent; ++c) {
+    const uint32_t bar = smem_addr(&full[warp][c % kStages]);
+    const uint64_t since = clock64_now();
+    while (!mbar_try_wait(bar, (c / kStages) & 1))
+      if (static_cast<long long>(clock64_now() - since) > kSpinLimit) break;
+  }
+  __syncwarp();
+
+  // The warps that ended in one head are neighbours: their results meet in shared memory.
+  if (hd >= 0) {
+    acc.finish();
+    float* own = reinterpret_cast<float*>(dyn_smem + warp * kWarpBytes);
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int h = 8 * n + 2 * t + e;
+        if (h >= p.g) continue;
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          *reinterpret_cast<float4*>(own + h * kRow4Dim + 32 * g + 4 * r) = acc.channels(n, g, e);
+        if (r == 0) ml_of[warp][h] = make_float2(acc.m[n][e], acc.l[n][e]);
+      }
+    if (lane == 0) {
+      if (t0 == 0) p.ends[2 * hd] = cta;
+      if (t_end == T) p.ends[2 * hd + 1] = cta;
+    }
+  }
+  if (lane == 0) head_of[warp] = hd;
+  __syncthreads();
+  if (hd < 0) return;
+  int first = warp, last = warp + 1;
+  while (first > 0 && head_of[first - 1] == hd) --first;
+  while (last < kWarps && head_of[last] == hd) ++last;
+  const int64_t slot = 2 * (static_cast<int64_t>(hd) + cta);
+  // the head's end is in this CTA, in the next warp's first segment, or not here
+  const bool tail = last < kWarps && head_of[last] >= 0 && t_end < T;
+  for (int item = (warp - first) * 32 + lane; item < p.g * 32; item += (last - first) * 32) {
+    const int h = item >> 5, quad = item & 31;
+    float m = -INFINITY;
+    for (int i = first; i < last; ++i) m = fmaxf(m, ml_of[i][h].x);
+    float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float l = 0.0f;
+    for (int i = first; i < last; ++i) {
+      const float2 ml = ml_of[i][h];
+      const float f = ml.x == -INFINITY ? 0.0f : ex2_approx(ml.x - m);
+      const float4 v =
+          *reinterpret_cast<const float4*>(dyn_smem + i * kWarpBytes + (h * kRow4Dim + 4 * quad) * 4);
+      sum.x = fmaf(f, v.x, sum.x);
+      sum.y = fmaf(f, v.y, sum.y);
+      sum.z = fmaf(f, v.z, sum.z);
+      sum.w = fmaf(f, v.w, sum.w);
+      l = fmaf(f, ml.y, l);
+    }
+    *reinterpret_cast<float4*>(p.part_o + (slot * p.g + h) * kRow4Dim + 4 * quad) = sum;
+    if (quad == 0) p.part_ml[slot * p.g + h] = make_float2(m, l);
+  }
+  if (warp == last - 1 && !tail && lane < p.g)
+    p.part_ml[(slot + 1) * p.g + lane] = make_float2(-INFINITY, 0.0f);
+}
+
+// O = sum_s 2^(m_s - m) O_s / sum_s 2^(m_s - m) l_s over a row's places (two per
+// CTA of the head, some empty): kPerRow warps per (b, query head). A warp reads
+// the maxima and sums of 32 places at once, a lane each, and then only the outputs
+// of those that hold something, four under way. A sequence without a key gets
+// O = 0 and LSE = -inf.
+constexpr int kCombineWarps = 8;
+
+template <int kPerRow>
+__global__ void __launch_bounds__(32 * kCombineWarps)
+decode4_combine_kernel(uint16_t* o, float* lse, const Params4 p) {
+  constexpr int kRows = kCombineWarps / kPerRow;
+  __shared__ float red_m[kCombineWarps], red_w[kCombineWarps];
+  __shared__ float4 red_o[kCombineWarps][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp % kPerRow;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + warp / kPerRow;   // b * n_q + h
+  const bool live = row < static_cast<int64_t>(p.B) * p.n_q;
+  float m = -INFINITY, l = 0.0f;
+  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  bool keys = false;
+  if (live) {
+    const int64_t hd = row / p.g;
+    const int h = static_cast<int>(row - hd * p.g);
+    keys = p.lens[hd / p.n_kv] > 0;
+    const int2 ends = reinterpret_cast<const int2*>(p.ends)[hd];
+    const int64_t first = 2 * (hd + ends.x);
+    const int n = keys ? 2 * (ends.y - ends.x + 1) : 0;
+    for (int at = 32 * sub; at < n; at += 32 * kPerRow) {
+      const float2 ml = at + lane < n ? p.part_ml[(first + at + lane) * p.g + h]
+                                      : make_float2(-INFINITY, 0.0f);
+      float top = ml.x;
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1)
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+      const float mn = fmaxf(m, top);
+      const float a = m == -INFINITY ? 0.0f : ex2_approx(m - mn);
+      const float f = ml.x == -INFINITY ? 0.0f : ex2_approx(ml.x - mn);
+      float part = f * ml.y;
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) part += __shfl_xor_sync(0xffffffffu, part, off);
+      l = fmaf(l, a, part);
+      m = mn;
+      acc.x *= a;
+      acc.y *= a;
+      acc.z *= a;
+      acc.w *= a;
+      // (a place whose scores are all NaN has no maximum but a sum)
+      unsigned some = __ballot_sync(0xffffffffu, !(ml.x == -INFINITY && ml.y == 0.0f));
+      while (some) {
+        float4 v[4];
+        float fs[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int src = some ? __ffs(some) - 1 : -1;
+          some &= some - 1;
+          fs[k] = __shfl_sync(0xffffffffu, ml.x == -INFINITY ? ml.y : f, src < 0 ? 0 : src);
+          v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          if (src >= 0)
+            v[k] = *reinterpret_cast<const float4*>(
+                p.part_o + ((first + at + src) * p.g + h) * kRow4Dim + 4 * lane);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          acc.x = fmaf(fs[k], v[k].x, acc.x);
+          acc.y = fmaf(fs[k], v[k].y, acc.y);
+          acc.z = fmaf(fs[k], v[k].z, acc.z);
+          acc.w = fmaf(fs[k], v[k].w, acc.w);
+        }
+      }
+    }
+  }
+  if (kPerRow > 1) {
+    red_o[warp][lane] = acc;
+    if (lane == 0) {
+      red_m[warp] = m;
+      red_w[warp] = l;
+    }
+    __syncthreads();
+    if (sub != 0) return;
+    m = red_m[warp];
+#pragma unroll
+    for (int k = 1; k < kPerRow; ++k) m = fmaxf(m, red_m[warp + k]);
+    acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    l = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kPerRow; ++k) {
+      const float f = red_m[warp + k] == -INFINITY ? 1.0f : ex2_approx(red_m[warp + k] - m);
+      const float4 v = red_o[warp + k][lane];
+      acc.x = fmaf(f, v.x, acc.x);
+      acc.y = fmaf(f, v.y, acc.y);
+      acc.z = fmaf(f, v.z, acc.z);
+      acc.w = fmaf(f, v.w, acc.w);
+      l = fmaf(f, red_w[warp + k], l);
+    }
+  }
+  if (!live) return;
+  const float inv = keys ? 1.0f / l : 0.0f;
+  *reinterpret_cast<uint2*>(o + row * kRow4Dim + 4 * lane) =
+      make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+  if (lane == 0) lse[row] = keys ? (m + log2f(l)) * 0.69314718055994530942f : -INFINITY;
+}
+
+// --------------------------------------------------------------------- host
+
+constexpr int kMaxDevices = 64;
+std::mutex g_mutex;
+bool g_ready[kMaxDevices];
+
+attn_status_t device_ready(cudaStream_t stream, int** status) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return ATTN_ERR_CUDA;
+  if (dev < 0 || dev >= kMaxDevices) return ATTN_ERR_UNSUPPORTED;
+  // device check (sm_103) and the status word come from the forward's set-up
+  const attn_status_t ds = gb300_host::device_status_word(stream, status);
+  if (ds != ATTN_OK) return ds;
+  std::lock_guard<std::mutex> lock(g_mutex);
+  if (g_ready[dev]) return ATTN_OK;
+  // one-time set-up: not inside a stream capture
+  cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(stream, &cs) != cudaSuccess || cs != cudaStreamCaptureStatusNone) {
+    cudaGetLastError();
+    return ATTN_ERR_UNSUPPORTED;
+  }
+  if (cudaFuncSetAttribute(decode4_split_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           kSmemOf<1>) != cudaSuccess ||
+      cudaFuncSetAttribute(decode4_split_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           kSmemOf<2>) != cudaSuccess)
+    return ATTN_ERR_CUDA;
+  g_ready[dev] = true;
+  return ATTN_OK;
+}
+
+bool sizes_ok(int64_t B, int64_t C, int32_t n_q, int32_t n_kv, int32_t d_h, int64_t window,
+              int64_t sinks) {
+  return B >= 1 && C >= 1 && n_q >= 1 && n_kv >= 1 && n_q % n_kv == 0 && d_h >= 1 && window >= 0 &&
+         sinks >= 0 && (window > 0 || sinks == 0);
+}
+bool supported(int64_t B, int64_t C, int32_t n_q, int32_t n_kv, int32_t d_h) {
+  return d_h == kRow4Dim && n_q / n_kv <= kMaxG && C <= (int64_t{1} << 30) &&
+         B <= (int64_t{1} << 24) && B * n_kv <= (int64_t{1} << 24) &&
+         B * n_kv * (C / kChunk + 1) <= (int64_t{1} << 40);
+}
+
+// Grid and workspace: two places for each head and each CTA that may stand in it.
+struct Shape4 {
+  int64_t ctas, ml_at, ends_at, bytes;
+};
+Shape4 shape4(int64_t B, int64_t C, int32_t n_q, int32_t n_kv, int64_t window, int64_t sinks) {
+  auto chunks = [](int64_t n) { return (n + kChunk - 1) / kChunk; };
+  int64_t T = chunks(C);
+  if (window > 0 && window < C) {
+    const int64_t seen = chunks(window) + chunks(sinks < C - window ? sinks : C - window);
+    if (seen < T) T = seen;
+  }
+  const int64_t g = n_q / n_kv, warps = g <= 8 ? kWarpsOf<1> : kWarpsOf<2>;
+  const int64_t most = (B * n_kv * T + warps - 1) / warps;
+  Shape4 s;
+  s.ctas = most < kCtas ? most : kCtas;
+  const int64_t rows = 2 * (B * n_kv + s.ctas) * g;
+  auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
+  s.ml_at = up(rows * kRow4Dim * 4);
+  s.ends_at = s.ml_at + up(rows * 8);
+  s.bytes = s.ends_at + up(B * n_kv * 8);
+  return s;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t attn_decode4_workspace_bytes(int64_t B, int64_t C, int32_t n_q, int32_t n_kv, int32_t d_h,
+                                     int64_t window, int64_t sinks) {
+  if (!sizes_ok(B, C, n_q, n_kv, d_h, window, sinks) || !supported(B, C, n_q, n_kv, d_h)) return -1;
+  return shape4(B, C, n_q, n_kv, window, sinks).bytes;
+}
+
+attn_status_t attn_decode4_fwd(const void* q, const void* k4, const void* v4, const int32_t* lens,
+                               void* o, float* lse, void* workspace, int64_t workspace_bytes,
+                               int64_t B, int64_t C, int32_t n_q, int32_t n_kv, int32_t d_h,
+                               int64_t window, int64_t sinks, float scale, void* stream_ptr) {
+  if (!q || !k4 || !v4 || !lens || !o || !lse || !workspace) return ATTN_ERR_INVALID_ARG;
+  if (!sizes_ok(B, C, n_q, n_kv, d_h, window, sinks) || !std::isfinite(scale))
+    return ATTN_ERR_INVALID_ARG;
+  auto misaligned = [](const void* ptr, uintptr_t a) {
+    return (reinterpret_cast<uintptr_t>(ptr) & (a - 1)) != 0;
+  };
+  if (misaligned(q, 16) || misaligned(k4, 16) || misaligned(v4, 16) || misaligned(o, 16) ||
+      misaligned(lse, 4) || misaligned(lens, 4) || misaligned(workspace, 16))
+    return ATTN_ERR_INVALID_ARG;
+  if (!supported(B, C, n_q, n_kv, d_h)) return ATTN_ERR_UNSUPPORTED;
+  const Shape4 s = shape4(B, C, n_q, n_kv, window, sinks);
+  if (workspace_bytes < s.bytes) return ATTN_ERR_INVALID_ARG;
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
+  int* status = nullptr;
+  const attn_status_t ds = device_ready(stream, &status);
+  if (ds != ATTN_OK) return ds;
+  char* ws = static_cast<char*>(workspace);
+  Params4 p{};
+  p.q = static_cast<const uint16_t*>(q);
+  p.k4 = static_cast<const uint8_t*>(k4);
+  p.v4 = static_cast<const uint8_t*>(v4);
+  p.lens = lens;
+  p.part_o = reinterpret_cast<float*>(ws);
+  p.part_ml = reinterpret_cast<float2*>(ws + s.ml_at);
+  p.ends = reinterpret_cast<int*>(ws + s.ends_at);
+  p.status = status;
+  p.B = static_cast<int>(B);
+  p.C = static_cast<int>(C);
+  p.n_q = n_q;
+  p.n_kv = n_kv;
+  p.g = n_q / n_kv;
+  p.window = static_cast<int>(window < C ? window : C);
+  p.sinks = static_cast<int>(sinks < C ? sinks : C);
+  const bool two = p.g > 8;
+  p.walkers = static_cast<int>(s.ctas) * (two ? kWarpsOf<2> : kWarpsOf<1>);
+  p.c = scale * 1.4426950408889634f;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(s.ctas));
+  cfg.blockDim = dim3(32 * (two ? kWarpsOf<2> : kWarpsOf<1>));
+  cfg.dynamicSmemBytes = two ? kSmemOf<2> : kSmemOf<1>;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = two ? cudaLaunchKernelEx(&cfg, decode4_split_kernel<2>, p)
+                      : cudaLaunchKernelEx(&cfg, decode4_split_kernel<1>, p);
+  if (e != cudaSuccess) return ATTN_ERR_CUDA;
+  // eight warps per row where a head may have more places than a warp reads at once
+  const bool many = s.ctas > 16 * B * n_kv;
+  cfg.gridDim = dim3(static_cast<unsigned>(many ? B * n_q : (B * n_q + kCombineWarps - 1) / kCombineWarps));
+  cfg.blockDim = dim3(32 * kCombineWarps);
+  cfg.dynamicSmemBytes = 0;
+  uint16_t* o16 = static_cast<uint16_t*>(o);
+  e = many ? cudaLaunchKernelEx(&cfg, decode4_combine_kernel<kCombineWarps>, o16, lse, p)
+           : cudaLaunchKernelEx(&cfg, decode4_combine_kernel<1>, o16, lse, p);
+  if (e != cudaSuccess) return ATTN_ERR_CUDA;
+  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+}  // extern "C"

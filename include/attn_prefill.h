@@ -2,8 +2,8 @@
  * attn_prefill.h — C ABI of the GB300 (sm_103a) causal GQA prefill attention:
  * the forward pass (square and chunked, bf16 and fp8), decode, the backward
  * pass, the same three behind a sliding window with sinks, the cache operators
- * (key weights, ragged decode, decode behind a shared prefix, eviction) and
- * diagnostics.
+ * (key weights, ragged decode, decode behind a shared prefix, eviction), caches
+ * held in 4 bits and diagnostics.
  *
  * Operation (one call computes, for every batch b, query head h and row i):
  *
@@ -320,6 +320,69 @@ attn_status_t attn_decode_shared_fwd(const void* q, const void* prefix_k, const 
                                      float* lse, void* workspace, int64_t workspace_bytes, int64_t B,
                                      int64_t P, int64_t C, int32_t n_q, int32_t n_kv, int32_t d_h,
                                      float scale, void* stream);
+
+/*
+ * Caches held in 4 bits: a cache of K or V is uint8 [B, n_kv, C, 80], one row of 80
+ * bytes per sequence, K/V head and position, 0.31 of what bf16 takes. Each of the
+ * four groups of 32 channels of a row has a lowest value lo and a scale, both
+ * bf16, and 32 codes of 0 .. 15:
+ *
+ *     lo = min x    scale = (max x - lo) / 15, rounded to fp32 and then to bf16
+ *     code = (x - lo) / scale to the nearest integer, ties to even, at most 15;
+ *            0 where the scale is 0
+ *     a code stands for lo + scale * code; a group that holds something not
+ *     finite has lo and scale NaN and stands for NaN
+ *
+ *   bytes  0 .. 63   16 little-endian 32-bit words; word 4 t + g holds the codes of
+ *                    channels 32 g + 8 t .. + 7, the first in the lowest four bits
+ *   bytes 64 .. 79   four words; word g holds scale (low half) and lo of group g
+ *
+ * attn_cache_pack4 writes rows into caches, attn_cache_unpack4 reads them back as
+ * bf16 (lo + scale * code rounded once), attn_decode4_fwd attends to them.
+ *
+ *   k, v     bf16 [B, L, n_kv, 128]      k4, v4  uint8 [B, n_kv, C, 80]
+ *            row i of sequence b is position at[b] + i of the caches
+ *   at       int32 [B], device memory, read when the kernel runs; NULL: 0
+ *   counts   (packing) int32 [B], device memory: of sequence b the first counts[b]
+ *            of the L rows are stored; NULL: all L
+ *   Rows whose position is not in 0 .. C - 1 are not stored, and read as zeros;
+ *   all other rows of the caches stay as they are.
+ *   B, L, C, n_kv >= 1; d_h = 128 (ATTN_ERR_UNSUPPORTED otherwise); k, v, k4 and v4
+ *   16-byte aligned, at and counts 4. An output that overlaps an input or the
+ *   other output is ATTN_ERR_INVALID_ARG. One kernel each, a programmatic
+ *   dependent as in attn_decode_fwd; no workspace; deterministic.
+ */
+attn_status_t attn_cache_pack4(const void* k, const void* v, void* k4, void* v4,
+                               const int32_t* at, const int32_t* counts, int64_t B, int64_t L,
+                               int64_t C, int32_t n_kv, int32_t d_h, void* stream);
+attn_status_t attn_cache_unpack4(const void* k4, const void* v4, void* k, void* v,
+                                 const int32_t* at, int64_t B, int64_t L, int64_t C, int32_t n_kv,
+                                 int32_t d_h, void* stream);
+
+/*
+ * Ragged decode over caches held in 4 bits, whole or behind a sliding window with
+ * sinks: attn_decode_ragged_fwd (without weights) and attn_decode_window_fwd on
+ * the values that the codes of k4 and v4 stand for.
+ *
+ *   k4, v4   uint8 [B, n_kv, C, 80] as above; rows that no token sees may hold
+ *            anything
+ *   window   0: the whole of lens[b] (sinks must be 0); else window and sinks of
+ *            attn_decode_window_fwd
+ *   Rounding: the values of K and V are not rounded; scores, statistics, LSE and
+ *   sum_j p_j lo_j are fp32; a softmax weight times the scale of a group of V is
+ *   rounded to bf16 (the matrix instructions' operand), and O once, so with
+ *   A = sum_j p_j (V_j - lo_j) and the scores off by at most E in fp32
+ *       |O - O_exact| <= 2^-8 ((1 + 2^-6) A + |O_exact|)
+ *                        + (2 E + 2^-20) (sum_j p_j (|lo_j| + |V_j|) + |O_exact|)
+ *   Everything else as attn_decode_ragged_fwd. Two kernels, programmatic
+ *   dependents; no atomics: results are deterministic.
+ */
+int64_t attn_decode4_workspace_bytes(int64_t B, int64_t C, int32_t n_q, int32_t n_kv, int32_t d_h,
+                                     int64_t window, int64_t sinks);   /* -1 as above */
+attn_status_t attn_decode4_fwd(const void* q, const void* k4, const void* v4, const int32_t* lens,
+                               void* o, float* lse, void* workspace, int64_t workspace_bytes,
+                               int64_t B, int64_t C, int32_t n_q, int32_t n_kv, int32_t d_h,
+                               int64_t window, int64_t sinks, float scale, void* stream);
 
 /*
  * Eviction: brings caches down to a budget, keeping the positions whose

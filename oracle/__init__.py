@@ -19,6 +19,8 @@ cache
     behind a shared prefix, one row or one head at a time.
 window
     Attention behind a sliding window with sinks: forward, backward, decode.
+cache4
+    Rows of caches held in 4 bits: into codes and back.
 flops
     The cost model the pages use: the causal prefill FLOP count
     2*n_q*d_h*L^2, the dense count 4*L^2*d_h*n_q, the K/V byte count and the
@@ -27,14 +29,14 @@ flops
 
 Parity status: every function here is pinned (``tests/test_oracle_pins.py``,
 ``tests/test_oracle_backward_pins.py``, ``tests/test_cache_ops.py``,
-``tests/test_window_ops.py``)
+``tests/test_window_ops.py``, ``tests/test_cache4_ops.py``)
 to values the pages print, closed forms, invariants, brute force and a
 library routine; none is "parity unpinned".
 """
 
 from .attention import attention, attention_rows, kv_head_of
 from .backward import attention_backward, softmax_rowdot
-from . import cache, flops, window
+from . import cache, cache4, flops, window
 
 __all__ = ["attention", "attention_rows", "attention_backward", "softmax_rowdot", "kv_head_of",
-           "cache", "flops", "window"]
+           "cache", "cache4", "flops", "window"]
