@@ -32,6 +32,7 @@
 #include <cmath>
 #include <cstdint>
 #include <mutex>
+#include <type_traits>
 
 #include "attn_prefill.h"
 #include "cache4.cuh"
@@ -45,20 +46,24 @@ namespace {
 
 using namespace gb300;
 
-constexpr int kChunk = 16;                         // positions per step of a warp
-constexpr int kChunkBytes = kChunk * kRow4Bytes;   // of K, and of V
-constexpr int kStages = 4;                         // chunks of K and V under way per warp
-constexpr int kWarpBytes = kStages * 2 * kChunkBytes;
+constexpr int kChunk = 16;                         // positions per product, unit of the runs
+constexpr int kStep = 2 * kChunk;                  // positions per step of a warp
+constexpr int kStepBytes = kStep * kRow4Bytes;     // of K, and of V
+constexpr int kStages = 3;                         // steps under way per warp
+constexpr int kWarpBytes = kStages * 2 * kStepBytes;
 constexpr int kCtas = 152;                         // one per SM
 constexpr int kMaxG = 16;
 constexpr float kRescale = 8.0f;                   // lazy running maximum (log2 units)
+// A running maximum before the first score: below every one that counts, and finite,
+// so that nothing has to be told apart from a maximum of -inf.
+constexpr float kNoMax = -3.4028234663852886e38f;
 constexpr int kStatusTimeout = 1;
 constexpr long long kSpinLimit = 1ll << 31;        // about a second at 2 GHz
 
-// NT: the group's query heads in tiles of 8. 16 warps fit the registers with one
+// NT: the group's query heads in tiles of 8. 12 warps fit the registers with one
 // tile, 8 with two.
 template <int NT>
-constexpr int kWarpsOf = NT == 1 ? 16 : 8;
+constexpr int kWarpsOf = NT == 1 ? 12 : 8;
 template <int NT>
 constexpr int kSmemOf = kWarpsOf<NT> * kWarpBytes;
 static_assert(kMaxG * kRow4Dim * 4 <= kWarpBytes, "a warp's result fits its ring");
@@ -68,7 +73,7 @@ struct Params4 {
   const uint8_t *k4, *v4;
   const int* lens;
   float* part_o;           // fp32 [2 (B * n_kv + CTAs)][g][128]
-  float2* part_ml;         // running maximum (log2 units; -inf: nothing here) and sum
+  float2* part_ml;         // running maximum (log2 units) and sum (0: nothing here)
   int* ends;               // [B * n_kv][2] CTAs that hold a head's first and last chunk
   int* status;
   int B, C, n_q, n_kv, g;
@@ -101,11 +106,11 @@ struct Walk4 {
     na = s.na;
     chunks = s.chunks;
   }
-  __device__ int pos() const { return t < na ? t * kChunk : low + (t - na) * kChunk; }
-  __device__ int count() const { return min(kChunk, (t < na ? sunk : len) - pos()); }
-  __device__ void advance(const Params4& p) {
-    ++t;
-    if (--left == 0 || t < chunks) return;
+  // Past n chunks of this head.
+  __device__ void move(const Params4& p, int n) {
+    t += n;
+    left -= n;
+    if (left == 0 || t < chunks) return;
     t = 0;
     if (++u < p.n_kv) return;
     u = 0;
@@ -116,6 +121,34 @@ struct Walk4 {
       }
       enter(p);
     } while (chunks == 0);
+  }
+};
+
+// A run of neighbouring positions of one head: the next part of a walk.
+struct Part4 {
+  int units, pos, rows;    // chunks, first position, rows that count
+  __device__ Part4(const Walk4& w) {
+    const bool sink = w.t < w.na;
+    const int until = sink ? w.na : w.chunks, end = sink ? w.sunk : w.len;
+    pos = sink ? w.t * kChunk : w.low + (w.t - w.na) * kChunk;
+    units = min(w.left, until - w.t);
+    rows = w.t + units == until ? end - pos : units * kChunk;
+  }
+};
+
+// The warp's copies: the same walk, ahead of the products.
+struct Sender {
+  Walk4 w;
+  int rows;                // rows to go in this part
+  int64_t at;              // byte offset of the next of them
+  __device__ bool more(const Params4& p) {
+    if (rows > 0) return true;
+    if (w.left == 0) return false;
+    const Part4 part(w);
+    rows = part.rows;
+    at = ((static_cast<int64_t>(w.b) * p.n_kv + w.u) * p.C + part.pos) * kRow4Bytes;
+    w.move(p, part.units);
+    return true;
   }
 };
 
@@ -180,19 +213,19 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   return v;
 }
 
-// D += A B, 16 x 8 x 16, bf16 operands.
+// D = A B + C, 16 x 8 x 16, bf16 operands.
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+                                         uint32_t a3, uint32_t b0, uint32_t b1, float c0, float c1,
+                                         float c2, float c3) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%10, %11, %12, %13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   uint32_t r;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
 }
 
@@ -229,7 +262,7 @@ struct Acc {
           for (int e = 0; e < 4; ++e) o[n][g][j][e] = 0.0f;
         lows[n][g][0] = lows[n][g][1] = 0.0f;
       }
-      m[n][0] = m[n][1] = -INFINITY;
+      m[n][0] = m[n][1] = kNoMax;
       l[n][0] = l[n][1] = 0.0f;
     }
   }
@@ -275,25 +308,26 @@ decode4_split_kernel(const Params4 p) {
 
   const uint32_t ring = smem_addr(dyn_smem) + warp * kWarpBytes;
   Walk4 cur = walk_start(p, w);
-  Walk4 ahead = cur;
-  uint32_t sent = 0, taken = 0;               // chunks under way or done, and done
-  auto send = [&]() {                         // the next chunk's rows of K and V
-    const int slot = sent % kStages;
+  Sender ahead;
+  ahead.w = cur;
+  ahead.rows = 0;
+  uint32_t sent = 0, taken = 0;               // steps under way or done, and done
+  auto send = [&]() {                         // the next step's rows of K and V
+    if (!ahead.more(p)) return;
     if (lane == 0) {
+      const int slot = sent % kStages;
       const uint32_t bar = smem_addr(&full[warp][slot]);
-      const uint32_t dst = ring + slot * 2 * kChunkBytes;
-      const int n = ahead.count() * kRow4Bytes;
-      const int64_t at =
-          ((static_cast<int64_t>(ahead.b) * p.n_kv + ahead.u) * p.C + ahead.pos()) * kRow4Bytes;
+      const uint32_t dst = ring + slot * 2 * kStepBytes;
+      const int n = min(ahead.rows, kStep) * kRow4Bytes;
       mbar_arrive_expect_tx(bar, 2 * n);
-      bulk_load(dst, p.k4 + at, n, bar);
-      bulk_load(dst + kChunkBytes, p.v4 + at, n, bar);
+      bulk_load(dst, p.k4 + ahead.at, n, bar);
+      bulk_load(dst + kStepBytes, p.v4 + ahead.at, n, bar);
     }
     ++sent;
-    ahead.advance(p);
+    ahead.rows -= kStep;
+    ahead.at += kStepBytes;
   };
-  for (int s = 0; s < kStages; ++s)
-    if (ahead.left > 0) send();
+  for (int i = 0; i < kStages; ++i) send();
 
   // position of row i of a chunk's products (i < 8; the others are 8 further on): rows
   // 2 a and 2 a + 1 are positions a and a + 4, so that eight lanes' 16-byte loads of a
@@ -302,7 +336,7 @@ decode4_split_kernel(const Params4 p) {
   const uint32_t half = (r & 1) ? 0x7632u : 0x5410u;
   Acc<NT> acc;
   uint32_t qf[NT][4][4];                      // Q as the products' second operand
-  float qs[NT][4][2];                         // sums of a head's channels of a group
+  float qs[NT][4][2], qb[NT][4][2];           // sums of a head's channels of a group; -16 of them
   bool ok = true;
   int hd = -1, t0 = 0, t_end = 0, T = 0;      // the segment: head, chunks [t0, t_end) of T
 
@@ -310,8 +344,7 @@ decode4_split_kernel(const Params4 p) {
     hd = cur.b * p.n_kv + cur.u;
     t0 = cur.t;
     T = cur.chunks;
-    const int n_chunks = min(cur.left, T - t0);
-    t_end = t0 + n_chunks;
+    t_end = min(t0 + cur.left, T);
     acc.clear();
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -336,37 +369,28 @@ decode4_split_kernel(const Params4 p) {
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
         qs[n][g][0] = __shfl_sync(0xffffffffu, sum, 8 * t);
         qs[n][g][1] = __shfl_sync(0xffffffffu, sum, 8 * t + 4);
+        qb[n][g][0] = -16.0f * qs[n][g][0];
+        qb[n][g][1] = -16.0f * qs[n][g][1];
       }
     }
 
-    for (int i = 0; i < n_chunks; ++i) {
-      const int slot = taken % kStages;
-      const uint32_t bar = smem_addr(&full[warp][slot]), parity = (taken / kStages) & 1;
-      bool there = mbar_try_wait(bar, parity);
-      if (!there) {
-        const uint64_t since = clock64_now();
-        while (!(there = mbar_try_wait(bar, parity)))
-          if (static_cast<long long>(clock64_now() - since) > kSpinLimit) break;
-      }
-      if (!__all_sync(0xffffffffu, there)) {
-        if (lane == 0) atomicOr(p.status, kStatusTimeout);
-        ok = false;
-        break;
-      }
-      const int valid = cur.count();
-      const bool seen[2] = {kpos < valid, kpos + 8 < valid};
-      const uint32_t sk = ring + slot * 2 * kChunkBytes, sv = sk + kChunkBytes;
+    // One step's products; kFull: all of its rows count.
+    auto step = [&](auto full_step, int slot, int valid) {
+      constexpr bool kFull = decltype(full_step)::value;
+      const uint32_t sk = ring + slot * 2 * kStepBytes, sv = sk + kStepBytes;
       const uint32_t row0 = kpos * kRow4Bytes, row1 = row0 + 8 * kRow4Bytes;
 
-      // S^T: rows r and r + 8 of the chunk, heads 2 t and 2 t + 1 of each tile
-      float s[NT][4];
-      {
-        const uint4 k0 = lds128(sk + row0 + 16 * t), k1 = lds128(sk + row1 + 16 * t);
-        const uint4 p0 = lds128(sk + row0 + kRow4Codes), p1 = lds128(sk + row1 + kRow4Codes);
+      // S^T: rows r and r + 8 of each chunk, heads 2 t and 2 t + 1 of each tile
+      float s[2][NT][4];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const uint32_t at = sk + c * kChunk * kRow4Bytes;
+        const uint4 k0 = lds128(at + row0 + 16 * t), k1 = lds128(at + row1 + 16 * t);
+        const uint4 p0 = lds128(at + row0 + kRow4Codes), p1 = lds128(at + row1 + kRow4Codes);
         const uint32_t c0[4] = {k0.x, k0.y, k0.z, k0.w}, c1[4] = {k1.x, k1.y, k1.z, k1.w};
         const uint32_t m0[4] = {p0.x, p0.y, p0.z, p0.w}, m1[4] = {p1.x, p1.y, p1.z, p1.w};
 #pragma unroll
-        for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.0f;
+        for (int n = 0; n < NT; ++n) s[c][n][0] = s[c][n][1] = s[c][n][2] = s[c][n][3] = 0.0f;
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
           const uint32_t a00 = codes16<0>(c0[g]), a01 = codes16<0>(c1[g]);
@@ -374,39 +398,43 @@ decode4_split_kernel(const Params4 p) {
           const uint32_t a10 = codes16<2>(c0[g]), a11 = codes16<2>(c1[g]);
           const uint32_t a12 = codes16<3>(c0[g]), a13 = codes16<3>(c1[g]);
           const float s0 = row4_scale(m0[g]), s1 = row4_scale(m1[g]);
-          const float l0 = fmaf(-16.0f, s0, row4_low(m0[g])), l1 = fmaf(-16.0f, s1, row4_low(m1[g]));
+          const float l0 = row4_low(m0[g]), l1 = row4_low(m1[g]);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            mma16816(d, a00, a01, a02, a03, qf[n][g][0], qf[n][g][1]);
-            mma16816(d, a10, a11, a12, a13, qf[n][g][2], qf[n][g][3]);
-            s[n][0] = fmaf(s0, d[0], fmaf(l0, qs[n][g][0], s[n][0]));
-            s[n][1] = fmaf(s0, d[1], fmaf(l0, qs[n][g][1], s[n][1]));
-            s[n][2] = fmaf(s1, d[2], fmaf(l1, qs[n][g][0], s[n][2]));
-            s[n][3] = fmaf(s1, d[3], fmaf(l1, qs[n][g][1], s[n][3]));
+            // (from -16 sum q: the products are with 16 + code)
+            float d[4];
+            mma16816(d, a00, a01, a02, a03, qf[n][g][0], qf[n][g][1], qb[n][g][0], qb[n][g][1],
+                     qb[n][g][0], qb[n][g][1]);
+            mma16816(d, a10, a11, a12, a13, qf[n][g][2], qf[n][g][3], d[0], d[1], d[2], d[3]);
+            s[c][n][0] = fmaf(s0, d[0], fmaf(l0, qs[n][g][0], s[c][n][0]));
+            s[c][n][1] = fmaf(s0, d[1], fmaf(l0, qs[n][g][1], s[c][n][1]));
+            s[c][n][2] = fmaf(s1, d[2], fmaf(l1, qs[n][g][0], s[c][n][2]));
+            s[c][n][3] = fmaf(s1, d[3], fmaf(l1, qs[n][g][1], s[c][n][3]));
           }
         }
       }
       bool need = false;
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int c = 0; c < 2; ++c)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          s[n][e] = seen[e >> 1] ? s[n][e] * p.c : -INFINITY;
-          need |= s[n][e] > acc.m[n][e & 1] + kRescale;
-        }
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            s[c][n][e] = kFull || c * kChunk + kpos + 4 * (e & 2) < valid ? s[c][n][e] * p.c
+                                                                          : -INFINITY;
+            need |= s[c][n][e] > acc.m[n][e & 1] + kRescale;
+          }
       if (__any_sync(0xffffffffu, need)) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float top = fmaxf(s[n][e], s[n][2 + e]);
+            float top = fmaxf(fmaxf(s[0][n][e], s[0][n][2 + e]), fmaxf(s[1][n][e], s[1][n][2 + e]));
 #pragma unroll
             for (int off = 4; off < 32; off <<= 1)
               top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
             const float m = fmaxf(acc.m[n][e], top);
-            const float alpha = m == acc.m[n][e] ? 1.0f
-                                : acc.m[n][e] == -INFINITY ? 0.0f : ex2_approx(acc.m[n][e] - m);
+            const float alpha = ex2_approx(acc.m[n][e] - m);
             acc.m[n][e] = m;
             acc.l[n][e] *= alpha;
 #pragma unroll
@@ -421,24 +449,27 @@ decode4_split_kernel(const Params4 p) {
           }
       }
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int c = 0; c < 2; ++c)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float m = acc.m[n][e & 1];
-          s[n][e] = ex2_approx(s[n][e] - (m == -INFINITY ? 0.0f : m));
-          acc.l[n][e & 1] += s[n][e];
-        }
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            s[c][n][e] = ex2_approx(s[c][n][e] - acc.m[n][e & 1]);
+            acc.l[n][e & 1] += s[c][n][e];
+          }
 
       // O^T: P times the scale of its position's group, turned, against V's codes
-      {
-        const uint4 p0 = lds128(sv + row0 + kRow4Codes), p1 = lds128(sv + row1 + kRow4Codes);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const uint32_t at = sv + c * kChunk * kRow4Bytes;
+        const uint4 p0 = lds128(at + row0 + kRow4Codes), p1 = lds128(at + row1 + kRow4Codes);
         // (rows that do not count may hold anything)
-        const uint32_t m0[4] = {seen[0] ? p0.x : 0u, seen[0] ? p0.y : 0u, seen[0] ? p0.z : 0u,
-                                seen[0] ? p0.w : 0u};
-        const uint32_t m1[4] = {seen[1] ? p1.x : 0u, seen[1] ? p1.y : 0u, seen[1] ? p1.z : 0u,
-                                seen[1] ? p1.w : 0u};
+        const uint32_t keep0 = kFull || c * kChunk + kpos < valid ? ~0u : 0u;
+        const uint32_t keep1 = kFull || c * kChunk + kpos + 8 < valid ? ~0u : 0u;
+        const uint32_t m0[4] = {p0.x & keep0, p0.y & keep0, p0.z & keep0, p0.w & keep0};
+        const uint32_t m1[4] = {p1.x & keep1, p1.y & keep1, p1.z & keep1, p1.w & keep1};
         // rows 2 t, 2 t + 1 (positions t, t + 4) and 8 further on; codes of block r / 2
-        const uint32_t base = sv + t * kRow4Bytes + 16 * (r >> 1);
+        const uint32_t base = at + t * kRow4Bytes + 16 * (r >> 1);
         const uint4 va = lds128(base), vb = lds128(base + 4 * kRow4Bytes);
         const uint4 vc = lds128(base + 8 * kRow4Bytes), vd = lds128(base + 12 * kRow4Bytes);
         const uint32_t ca[4] = {va.x, va.y, va.z, va.w}, cb[4] = {vb.x, vb.y, vb.z, vb.w};
@@ -454,19 +485,42 @@ decode4_split_kernel(const Params4 p) {
           const float l0 = row4_low(m0[g]), l1 = row4_low(m1[g]);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            const uint32_t x0 = transpose8x8(pack_bf16x2(s[n][0] * s0, s[n][1] * s0));
-            const uint32_t x1 = transpose8x8(pack_bf16x2(s[n][2] * s1, s[n][3] * s1));
-            acc.lows[n][g][0] = fmaf(s[n][0], l0, fmaf(s[n][2], l1, acc.lows[n][g][0]));
-            acc.lows[n][g][1] = fmaf(s[n][1], l0, fmaf(s[n][3], l1, acc.lows[n][g][1]));
-            mma16816(acc.o[n][g][0], a0, a1, a2, a3, x0, x1);
-            mma16816(acc.o[n][g][1], b0, b1, b2, b3, x0, x1);
+            const float* x = s[c][n];
+            const uint32_t x0 = transpose8x8(pack_bf16x2(x[0] * s0, x[1] * s0));
+            const uint32_t x1 = transpose8x8(pack_bf16x2(x[2] * s1, x[3] * s1));
+            acc.lows[n][g][0] = fmaf(x[0], l0, fmaf(x[2], l1, acc.lows[n][g][0]));
+            acc.lows[n][g][1] = fmaf(x[1], l0, fmaf(x[3], l1, acc.lows[n][g][1]));
+            float(&d0)[4] = acc.o[n][g][0];
+            float(&d1)[4] = acc.o[n][g][1];
+            mma16816(d0, a0, a1, a2, a3, x0, x1, d0[0], d0[1], d0[2], d0[3]);
+            mma16816(d1, b0, b1, b2, b3, x0, x1, d1[0], d1[1], d1[2], d1[3]);
           }
         }
       }
-      ++taken;
-      cur.advance(p);
-      __syncwarp();
-      if (ahead.left > 0) send();
+    };
+    while (ok && cur.left > 0 && cur.b * p.n_kv + cur.u == hd) {
+      const Part4 part(cur);
+      for (int rows = part.rows; rows > 0; rows -= kStep) {
+        const int slot = taken % kStages;
+        const uint32_t bar = smem_addr(&full[warp][slot]), parity = (taken / kStages) & 1;
+        bool there = mbar_try_wait(bar, parity);
+        if (!there) {
+          const uint64_t since = clock64_now();
+          while (!(there = mbar_try_wait(bar, parity)))
+            if (static_cast<long long>(clock64_now() - since) > kSpinLimit) break;
+        }
+        if (!__all_sync(0xffffffffu, there)) {
+          if (lane == 0) atomicOr(p.status, kStatusTimeout);
+          ok = false;
+          break;
+        }
+        if (rows >= kStep) step(std::true_type{}, slot, kStep);
+        else step(std::false_type{}, slot, rows);
+        ++taken;
+        __syncwarp();
+        send();
+      }
+      cur.move(p, part.units);
     }
     if (!ok || cur.left == 0) break;
 
@@ -491,7 +545,7 @@ decode4_split_kernel(const Params4 p) {
           *reinterpret_cast<float4*>(out + 32 * g) = acc.channels(n, g, e);
         if (r == 0) {
           p.part_ml[slot * p.g + h] = make_float2(acc.m[n][e], acc.l[n][e]);
-          if (alone) p.part_ml[(slot - 1) * p.g + h] = make_float2(-INFINITY, 0.0f);
+          if (alone) p.part_ml[(slot - 1) * p.g + h] = make_float2(kNoMax, 0.0f);
         }
       }
   }
@@ -536,13 +590,13 @@ decode4_split_kernel(const Params4 p) {
   const bool tail = last < kWarps && head_of[last] >= 0 && t_end < T;
   for (int item = (warp - first) * 32 + lane; item < p.g * 32; item += (last - first) * 32) {
     const int h = item >> 5, quad = item & 31;
-    float m = -INFINITY;
+    float m = kNoMax;
     for (int i = first; i < last; ++i) m = fmaxf(m, ml_of[i][h].x);
     float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     float l = 0.0f;
     for (int i = first; i < last; ++i) {
       const float2 ml = ml_of[i][h];
-      const float f = ml.x == -INFINITY ? 0.0f : ex2_approx(ml.x - m);
+      const float f = ex2_approx(ml.x - m);
       const float4 v =
           *reinterpret_cast<const float4*>(dyn_smem + i * kWarpBytes + (h * kRow4Dim + 4 * quad) * 4);
       sum.x = fmaf(f, v.x, sum.x);
@@ -555,13 +609,13 @@ decode4_split_kernel(const Params4 p) {
     if (quad == 0) p.part_ml[slot * p.g + h] = make_float2(m, l);
   }
   if (warp == last - 1 && !tail && lane < p.g)
-    p.part_ml[(slot + 1) * p.g + lane] = make_float2(-INFINITY, 0.0f);
+    p.part_ml[(slot + 1) * p.g + lane] = make_float2(kNoMax, 0.0f);
 }
 
 // O = sum_s 2^(m_s - m) O_s / sum_s 2^(m_s - m) l_s over a row's places (two per
 // CTA of the head, some empty): kPerRow warps per (b, query head). A warp reads
-// the maxima and sums of 32 places at once, a lane each, and then only the outputs
-// of those that hold something, four under way. A sequence without a key gets
+// the maxima and sums of its share of the places at once, a lane each, and then
+// only the outputs of those that hold something, four under way. A sequence without a key gets
 // O = 0 and LSE = -inf.
 constexpr int kCombineWarps = 8;
 
@@ -576,7 +630,7 @@ decode4_combine_kernel(uint16_t* o, float* lse, const Params4 p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + warp / kPerRow;   // b * n_q + h
   const bool live = row < static_cast<int64_t>(p.B) * p.n_q;
-  float m = -INFINITY, l = 0.0f;
+  float m = kNoMax, l = 0.0f;
   float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   bool keys = false;
   if (live) {
@@ -586,16 +640,16 @@ decode4_combine_kernel(uint16_t* o, float* lse, const Params4 p) {
     const int2 ends = reinterpret_cast<const int2*>(p.ends)[hd];
     const int64_t first = 2 * (hd + ends.x);
     const int n = keys ? 2 * (ends.y - ends.x + 1) : 0;
-    for (int at = 32 * sub; at < n; at += 32 * kPerRow) {
-      const float2 ml = at + lane < n ? p.part_ml[(first + at + lane) * p.g + h]
-                                      : make_float2(-INFINITY, 0.0f);
+    const int share = min(32, (n + kPerRow - 1) / kPerRow);
+    for (int at = share * sub; at < n; at += share * kPerRow) {
+      const float2 ml = lane < share && at + lane < n ? p.part_ml[(first + at + lane) * p.g + h]
+                                                      : make_float2(kNoMax, 0.0f);
       float top = ml.x;
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1)
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
       const float mn = fmaxf(m, top);
-      const float a = m == -INFINITY ? 0.0f : ex2_approx(m - mn);
-      const float f = ml.x == -INFINITY ? 0.0f : ex2_approx(ml.x - mn);
+      const float a = ex2_approx(m - mn), f = ex2_approx(ml.x - mn);
       float part = f * ml.y;
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) part += __shfl_xor_sync(0xffffffffu, part, off);
@@ -605,8 +659,8 @@ decode4_combine_kernel(uint16_t* o, float* lse, const Params4 p) {
       acc.y *= a;
       acc.z *= a;
       acc.w *= a;
-      // (a place whose scores are all NaN has no maximum but a sum)
-      unsigned some = __ballot_sync(0xffffffffu, !(ml.x == -INFINITY && ml.y == 0.0f));
+      // (a place whose scores are all NaN has no maximum, but NaN for a sum)
+      unsigned some = __ballot_sync(0xffffffffu, ml.y != 0.0f);
       while (some) {
         float4 v[4];
         float fs[4];
@@ -614,7 +668,7 @@ decode4_combine_kernel(uint16_t* o, float* lse, const Params4 p) {
         for (int k = 0; k < 4; ++k) {
           const int src = some ? __ffs(some) - 1 : -1;
           some &= some - 1;
-          fs[k] = __shfl_sync(0xffffffffu, ml.x == -INFINITY ? ml.y : f, src < 0 ? 0 : src);
+          fs[k] = __shfl_sync(0xffffffffu, f, src < 0 ? 0 : src);
           v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
           if (src >= 0)
             v[k] = *reinterpret_cast<const float4*>(
@@ -645,7 +699,7 @@ decode4_combine_kernel(uint16_t* o, float* lse, const Params4 p) {
     l = 0.0f;
 #pragma unroll
     for (int k = 0; k < kPerRow; ++k) {
-      const float f = red_m[warp + k] == -INFINITY ? 1.0f : ex2_approx(red_m[warp + k] - m);
+      const float f = ex2_approx(red_m[warp + k] - m);
       const float4 v = red_o[warp + k][lane];
       acc.x = fmaf(f, v.x, acc.x);
       acc.y = fmaf(f, v.y, acc.y);

@@ -23,7 +23,8 @@ def bf16_bits(x):
 
 
 def bf16_value(bits):
-    return (np.asarray(bits, dtype=np.uint32) << 16).view(np.float32).astype(np.float64)
+    with np.errstate(invalid="ignore"):                   # (signalling NaNs)
+        return (np.asarray(bits, dtype=np.uint32) << 16).view(np.float32).astype(np.float64)
 
 
 def pack(x):
@@ -50,15 +51,43 @@ def pack(x):
     return out
 
 
-def unpack(rows):
-    """(values [..., 128], lo of each value's group [..., 128]) that rows stand for."""
-    val, low = np.zeros(rows.shape[:-1] + (128,)), np.zeros(rows.shape[:-1] + (128,))
+def parts(rows):
+    """(lo, scale * code) [..., 128] of rows of 80 bytes, both exact."""
+    low, product = np.zeros(rows.shape[:-1] + (128,)), np.zeros(rows.shape[:-1] + (128,))
     word = lambda at: rows[..., at].astype(np.uint32) | (rows[..., at + 1].astype(np.uint32) << 8)  # noqa: E731
     for g in range(4):
         s, lo = bf16_value(word(64 + 4 * g)), bf16_value(word(66 + 4 * g))
         for t in range(4):
             for i in range(8):
                 code = (rows[..., 4 * (4 * t + g) + i // 2] >> (4 * (i % 2))) & 15
-                val[..., 32 * g + 8 * t + i] = lo + s * code
+                with np.errstate(invalid="ignore"):       # (an infinite scale times 0)
+                    product[..., 32 * g + 8 * t + i] = s * code
                 low[..., 32 * g + 8 * t + i] = lo
-    return val, low
+    return low, product
+
+
+def unpack(rows):
+    """(values [..., 128], lo of each value's group [..., 128]) that rows stand for."""
+    low, product = parts(rows)
+    with np.errstate(invalid="ignore"):
+        return low + product, low
+
+
+def rounded(rows):
+    """The values rounded once to bf16 (ties to even, infinite beyond its range).
+
+    lo and scale * code may be so far apart that their fp64 sum drops bits; those
+    only matter where the sum is half-way between two bf16."""
+    low, product = parts(rows)
+    with np.errstate(invalid="ignore"):
+        x = low + product
+        back = x - low
+        left = (low - (x - back)) + (product - back)      # x + left is the exact sum
+    sane = np.isfinite(x)
+    y = np.where(sane, x, 0.0)
+    ulp = np.ldexp(1.0, np.maximum(np.frexp(y)[1], -125) - 8)   # 8 bits; 2^-133 at least
+    q = y / ulp
+    down = np.floor(q)
+    up = np.where(q - down == 0.5, np.where(left == 0, down % 2 == 1, left > 0), q - down > 0.5)
+    y = (down + up) * ulp
+    return np.where(sane, np.where(np.abs(y) >= 2.0 ** 128, np.copysign(np.inf, y), y), x)

@@ -19,7 +19,8 @@ def _bf16(x):
 def test_bf16_against_torch():
     torch = pytest.importorskip("torch")
     x = np.random.default_rng(0).standard_normal(4000).astype(np.float32)
-    x = np.concatenate([x, x * 1e-39, x * 1e38, [0.0, -0.0, np.inf, -np.inf]]).astype(np.float32)
+    x = np.concatenate([x, x * np.float32(1e-39), x * np.float32(1e37), [0.0, -0.0, np.inf, -np.inf]])
+    x = x.astype(np.float32)
     t = torch.from_numpy(x).to(torch.bfloat16).view(torch.int16).numpy().view(np.uint16)
     assert np.array_equal(cache4.bf16_bits(x), t)
 
@@ -54,6 +55,29 @@ def test_constant_groups_and_what_is_not_finite():
     assert np.array_equal(val[0], x[0])
     assert np.isnan(val[1, 32:64]).all() and not val[1, 64:].any() and not val[1, :32].any()
     assert np.isnan(val[2, 96:]).all() and np.array_equal(val[2, 64:96], x[2, 64:96])
+
+
+def test_rounded_once():
+    """Random bytes: exact fractions decide which bf16 a value goes to."""
+    from fractions import Fraction
+
+    rows = np.random.default_rng(5).integers(0, 256, (40, 80)).astype(np.uint8)
+    low, product = cache4.parts(rows)
+    got = cache4.rounded(rows)
+    checked = 0
+    for lo, p, y in zip(low.ravel(), product.ravel(), got.ravel()):
+        if not np.isfinite(lo + p) or not np.isfinite(y):
+            continue
+        exact = Fraction(lo) + Fraction(p)
+        bits = int(cache4.bf16_bits(np.float32(y)))
+        assert float(cache4.bf16_value(np.uint16(bits))) == y
+        for n in (bits - 1, bits + 1):                 # the neighbours are no nearer
+            if bits & 0x7FFF and (n & 0x7FFF) < 0x7F80:
+                other = abs(Fraction(float(cache4.bf16_value(np.uint16(n)))) - exact)
+                own = abs(Fraction(y) - exact)
+                assert own < other or (own == other and bits % 2 == 0)
+        checked += 1
+    assert checked > 4000
 
 
 def test_ties_go_to_the_even_code():
