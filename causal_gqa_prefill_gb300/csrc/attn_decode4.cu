@@ -7,19 +7,23 @@
 // codes into matrix operands. So the codes never leave registers between the
 // load and the product, and nothing but the products' results is kept in fp32:
 //
-//   * every warp streams its own run of positions of one head through a ring of
-//     kStages bulk copies (the rows of a head are contiguous) and works alone:
-//     no barrier but its own copies' until the end;
+//   * every warp streams its own run of positions of one head (the rows of a head
+//     are contiguous) through a ring of kStages steps and works alone: it waits for
+//     nothing but its own copies until the end. They are 16-byte asynchronous copies,
+//     ten a lane and step, and not bulk ones: those cost a warp of this size some
+//     sixty instructions a step in moves to uniform registers and barriers (419 a
+//     chunk in all, where it is now 350);
 //   * S^T = K Q^T with m16n8k16 products, 16 positions x 8 heads. A code is put
 //     into the upper mantissa bits of a bf16 16 (bits 3..6: 16 + code, exact),
-//     one shift and one logic instruction for two codes; the group's scale and
-//     offset are applied to the fp32 sums of its 32 channels:
-//       s = sum_g scale_g (sum (16 + code) q) + (lo_g - 16 scale_g) sum q,
-//     so no value of K is rounded;
-//   * O^T += V^T P^T likewise, 16 channels x 8 heads, with scale_g P (rounded to
-//     bf16) as the other operand and sum_j P_j lo_gj kept in fp32 beside it.
-//     P^T is turned by movmatrix; the two rows that a lane's operand pairs up
-//     are brought together by one byte permutation per four codes.
+//     one shift and one logic instruction for two codes; a group's scale is
+//     applied to the fp32 sum of its 32 channels, and the rest is a product of its
+//     own, in which a position's words of (scale, lo) are the operand as they are:
+//       s = sum_g scale_g (sum (16 + code) q) + (scale_g, lo_g) . (-16 sum q, sum q)
+//     (the sums of q in three bf16 parts), so no value of K is rounded;
+//   * O^T += V^T P^T likewise, 16 channels x 8 heads, with codes (the 16 taken off
+//     again, exactly) and scale_g P (rounded to bf16); sum_j P_j lo_gj is kept in
+//     fp32 beside it. P^T is turned by movmatrix; the two rows that a lane's operand
+//     pairs up are brought together by one byte permutation per four codes.
 // (mma.sync and not tcgen05: those operands come from shared memory or tensor
 // memory, and writing the bf16 values there would cost more than the product.)
 //
@@ -49,7 +53,7 @@ using namespace gb300;
 constexpr int kChunk = 16;                         // positions per product, unit of the runs
 constexpr int kStep = 2 * kChunk;                  // positions per step of a warp
 constexpr int kStepBytes = kStep * kRow4Bytes;     // of K, and of V
-constexpr int kStages = 3;                         // steps under way per warp
+constexpr int kStages = 2;                           // steps under way per warp
 constexpr int kWarpBytes = kStages * 2 * kStepBytes;
 constexpr int kCtas = 152;                         // one per SM
 constexpr int kMaxG = 16;
@@ -57,8 +61,6 @@ constexpr float kRescale = 8.0f;                   // lazy running maximum (log2
 // A running maximum before the first score: below every one that counts, and finite,
 // so that nothing has to be told apart from a maximum of -inf.
 constexpr float kNoMax = -3.4028234663852886e38f;
-constexpr int kStatusTimeout = 1;
-constexpr long long kSpinLimit = 1ll << 31;        // about a second at 2 GHz
 
 // NT: the group's query heads in tiles of 8. 12 warps fit the registers with one
 // tile, 8 with two.
@@ -75,11 +77,11 @@ struct Params4 {
   float* part_o;           // fp32 [2 (B * n_kv + CTAs)][g][128]
   float2* part_ml;         // running maximum (log2 units) and sum (0: nothing here)
   int* ends;               // [B * n_kv][2] CTAs that hold a head's first and last chunk
-  int* status;
   int B, C, n_q, n_kv, g;
   int window, sinks;       // window 0: everything before lens[b]
   int walkers;             // warps that may have a run
   float c;                 // scale * log2(e)
+  uint32_t sixteens;       // bf16 16 twice (codes16)
 };
 
 // A sequence's visible positions, [0, sunk) and [low, len), in chunks.
@@ -136,54 +138,81 @@ struct Part4 {
   }
 };
 
-// The warp's copies: the same walk, ahead of the products.
+// What a part is to its segment, which is what one run has of one head.
+constexpr int kFirst = 1, kLast = 2;            // it is its first, last part
+constexpr int kHeadStart = 4, kHeadEnd = 8;     // it holds the head's first, last chunk
+constexpr int kRunEnd = 16;
+constexpr int kNotes = kStages + 1;             // parts that copies may be ahead by, and one
+
+// The warp's copies: walks the run and leaves a note of each part for the products, so
+// that only one place of the walk is kept.
 struct Sender {
   Walk4 w;
-  int rows;                // rows to go in this part
-  int64_t at;              // byte offset of the next of them
-  __device__ bool more(const Params4& p) {
-    if (rows > 0) return true;
-    if (w.left == 0) return false;
+  int rows;                    // of this part, to go
+  uint32_t parts;              // begun so far
+  int64_t at;                  // byte offset of the next row
+  bool fresh;                  // the next part begins a segment
+  __device__ void begin(const Walk4& walk) {
+    w = walk;
+    rows = 0;
+    parts = 0;
+    fresh = true;
+  }
+  // The next part; its note is (rows, head, flags).
+  __device__ int4 next(const Params4& p) {
     const Part4 part(w);
     rows = part.rows;
-    at = ((static_cast<int64_t>(w.b) * p.n_kv + w.u) * p.C + part.pos) * kRow4Bytes;
+    const int hd = w.b * p.n_kv + w.u;
+    at = (static_cast<int64_t>(hd) * p.C + part.pos) * kRow4Bytes;
+    const bool head_end = w.t + part.units == w.chunks, run_end = part.units == w.left;
+    const int start = (fresh ? kFirst : 0) | (w.t == 0 ? kHeadStart : 0);
+    fresh = head_end || run_end;
     w.move(p, part.units);
-    return true;
+    ++parts;
+    return make_int4(rows, hd,
+                     start | (fresh ? kLast : 0) | (head_end ? kHeadEnd : 0) | (run_end ? kRunEnd : 0),
+                     0);
   }
 };
+
+// w W / G, by a 32-bit division where that holds it (a 64-bit one is a hundred
+// instructions of a short step).
+__device__ __forceinline__ int part_of(int w, int W, int G) {
+  const uint64_t x = static_cast<uint64_t>(w) * static_cast<uint32_t>(W);
+  return (x >> 32) == 0 ? static_cast<int>(static_cast<uint32_t>(x) / static_cast<uint32_t>(G))
+                        : static_cast<int>(x / static_cast<uint32_t>(G));
+}
 
 // Where walker w's run starts: each lane sums a run of sequences, a scan places
 // them, and the lane that holds the first chunk finds it.
 __device__ __forceinline__ Walk4 walk_start(const Params4& p, int w) {
   const int lane = threadIdx.x & 31;
   const int run = (p.B + 31) / 32, b0 = min(lane * run, p.B), b1 = min(b0 + run, p.B);
-  long long sum = 0;
+  int sum = 0;                                 // (all chunks together are below 2^31)
 #pragma unroll 4
   for (int b = b0; b < b1; ++b) sum += Seen4(p, b).chunks;
   sum *= p.n_kv;
-  long long incl = sum;
+  int incl = sum;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
-    const long long n = __shfl_up_sync(0xffffffffu, incl, off);
+    const int n = __shfl_up_sync(0xffffffffu, incl, off);
     if (lane >= off) incl += n;
   }
-  const long long W = __shfl_sync(0xffffffffu, incl, 31);
-  const long long G = min(static_cast<long long>(p.walkers), W);   // every run has a chunk
+  const int W = __shfl_sync(0xffffffffu, incl, 31);
+  const int G = min(p.walkers, W);             // every run has a chunk
   Walk4 x{};
   if (w >= G) return x;
-  const long long x0 = w * W / G;
-  const long long at0 = incl - sum;
-  const bool mine = x0 >= at0 && x0 < incl;
+  const int x0 = part_of(w, W, G);
+  int at = incl - sum;
+  const bool mine = x0 >= at && x0 < incl;
   int b = 0, u = 0, t = 0;
   if (mine) {
-    long long at = at0;
     for (int i = b0; i < b1; ++i) {
-      const int T = Seen4(p, i).chunks;
-      const long long here = static_cast<long long>(T) * p.n_kv;
-      if (x0 < at + here) {
+      const int T = Seen4(p, i).chunks, here = T * p.n_kv;
+      if (x0 - at < here) {
         b = i;
-        u = static_cast<int>((x0 - at) / T);
-        t = static_cast<int>((x0 - at) % T);
+        u = static_cast<int>(static_cast<uint32_t>(x0 - at) / static_cast<uint32_t>(T));
+        t = x0 - at - u * T;
         break;
       }
       at += here;
@@ -193,23 +222,40 @@ __device__ __forceinline__ Walk4 walk_start(const Params4& p, int w) {
   x.b = __shfl_sync(0xffffffffu, b, src);
   x.u = __shfl_sync(0xffffffffu, u, src);
   x.t = __shfl_sync(0xffffffffu, t, src);
-  x.left = static_cast<int>((w + 1) * W / G - x0);
+  x.left = part_of(w + 1, W, G) - x0;
   x.enter(p);
   return x;
 }
 
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
-                                          uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
-      : "memory");
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// All but the last `kAfter` groups of this thread's copies have landed.
+template <int kAfter>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kAfter) : "memory");
 }
 
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   uint4 v;
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ int4 lds_desc(uint32_t addr) {
+  int4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
 }
 
@@ -229,17 +275,22 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   return r;
 }
 
-// Codes n and n + 4 of a word (or the n-th of its two halves) as bf16 16 + code.
+// Codes n and n + 4 of a word (or the n-th of its two halves) as bf16 16 + code: one
+// shift and one logic instruction, which takes the 16s from a register (`sixteens`,
+// from the parameters: a constant that the compiler knows becomes a second
+// instruction with another immediate, 64 more of 400 a chunk).
 template <int n>
-__device__ __forceinline__ uint32_t codes16(uint32_t w) {
+__device__ __forceinline__ uint32_t codes16(uint32_t w, uint32_t sixteens) {
   const uint32_t at = n == 0 ? w << 3 : w >> (4 * n - 3);
-  return (at & 0x00780078u) | 0x41804180u;
+  uint32_t r;
+  asm("lop3.b32 %0, %1, 0x00780078, %2, 0xEA;" : "=r"(r) : "r"(at), "r"(sixteens));   // (at & m) | 16s
+  return r;
 }
 // The same less 16: the codes themselves, exactly.
 template <int n>
-__device__ __forceinline__ uint32_t codes0(uint32_t w) {
+__device__ __forceinline__ uint32_t codes0(uint32_t w, uint32_t sixteens) {
   uint32_t r;
-  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(codes16<n>(w)), "r"(0x41804180u));
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(codes16<n>(w, sixteens)), "r"(sixteens));
   return r;
 }
 
@@ -294,67 +345,199 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1)
 decode4_split_kernel(const Params4 p) {
   constexpr int kWarps = kWarpsOf<NT>;
   extern __shared__ __align__(128) uint8_t dyn_smem[];
-  __shared__ __align__(8) uint64_t full[kWarps][kStages];
+  __shared__ __align__(16) int4 note[kWarps][kNotes];
   __shared__ int head_of[kWarps];             // head that the warp ended in, -1: had no run
-  __shared__ float2 ml_of[kWarps][8 * NT];
+  __shared__ float m_of[kWarps][8 * NT], l_of[kWarps][8 * NT];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r = lane >> 2, t = lane & 3;
   const int cta = static_cast<int>(blockIdx.x), w = cta * kWarps + warp;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (lane < kStages) mbar_init(smem_addr(&full[warp][lane]), 1);
-  fence_mbar_init();
-  __syncwarp();
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
   const uint32_t ring = smem_addr(dyn_smem) + warp * kWarpBytes;
-  Walk4 cur = walk_start(p, w);
   Sender ahead;
-  ahead.w = cur;
-  ahead.rows = 0;
-  uint32_t sent = 0, taken = 0;               // steps under way or done, and done
+  ahead.begin(walk_start(p, w));
+  int slot_in = 0;                            // ring slot of the next copies
   auto send = [&]() {                         // the next step's rows of K and V
-    if (!ahead.more(p)) return;
-    if (lane == 0) {
-      const int slot = sent % kStages;
-      const uint32_t bar = smem_addr(&full[warp][slot]);
-      const uint32_t dst = ring + slot * 2 * kStepBytes;
-      const int n = min(ahead.rows, kStep) * kRow4Bytes;
-      mbar_arrive_expect_tx(bar, 2 * n);
-      bulk_load(dst, p.k4 + ahead.at, n, bar);
-      bulk_load(dst + kStepBytes, p.v4 + ahead.at, n, bar);
+    if (ahead.rows <= 0 && ahead.w.left > 0) {
+      const int4 n = ahead.next(p);
+      if (lane == 0) note[warp][(ahead.parts - 1) % kNotes] = n;
     }
-    ++sent;
-    ahead.rows -= kStep;
-    ahead.at += kStepBytes;
+    if (ahead.rows > 0) {
+      const uint32_t dst = ring + slot_in * 2 * kStepBytes + 16 * lane;
+      const uint8_t *k = p.k4 + ahead.at + 16 * lane, *v = p.v4 + ahead.at + 16 * lane;
+      const int left = min(ahead.rows, kStep) * kRow4Bytes - 16 * lane;   // bytes from the lane's on
+#pragma unroll
+      for (int i = 0; i < kStepBytes / 512; ++i)
+        if (i * 512 < left) {
+          copy16(dst + i * 512, k + i * 512);
+          copy16(dst + kStepBytes + i * 512, v + i * 512);
+        }
+      ahead.rows -= kStep;
+      ahead.at += kStepBytes;
+    }
+    copies_commit();
+    slot_in = slot_in + 1 == kStages ? 0 : slot_in + 1;
   };
-  for (int i = 0; i < kStages; ++i) send();
 
   // position of row i of a chunk's products (i < 8; the others are 8 further on): rows
   // 2 a and 2 a + 1 are positions a and a + 4, so that eight lanes' 16-byte loads of a
   // chunk's 80-byte rows, of K (two rows) and of V (four), fall into different banks
   const int kpos = (r >> 1) + 4 * (r & 1);
   const uint32_t half = (r & 1) ? 0x7632u : 0x5410u;
+  const uint32_t sixteens = p.sixteens;
   Acc<NT> acc;
   uint32_t qf[NT][4][4];                      // Q as the products' second operand
-  float qs[NT][4][2], qb[NT][4][2];           // sums of a head's channels of a group; -16 of them
-  bool ok = true;
-  int hd = -1, t0 = 0, t_end = 0, T = 0;      // the segment: head, chunks [t0, t_end) of T
+  uint32_t qo[NT][3];                         // (-16 sum q, sum q) of group t, three bf16 parts
+  int hd = -1, where = 0;                     // the segment: head, kHeadStart and kHeadEnd
 
-  while (ok && cur.left > 0) {
-    hd = cur.b * p.n_kv + cur.u;
-    t0 = cur.t;
-    T = cur.chunks;
-    t_end = min(t0 + cur.left, T);
-    acc.clear();
+  // One step's products; kFull: all of its rows count.
+  auto step = [&](auto full_step, int slot, int valid) {
+    constexpr bool kFull = decltype(full_step)::value;
+    const uint32_t sk = ring + slot * 2 * kStepBytes, sv = sk + kStepBytes;
+    const uint32_t row0 = kpos * kRow4Bytes, row1 = row0 + 8 * kRow4Bytes;
+
+    // S^T: rows r and r + 8 of each chunk, heads 2 t and 2 t + 1 of each tile
+    float s[2][NT][4];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int h = 8 * n + r;
+    for (int c = 0; c < 2; ++c) {
+      const uint32_t at = sk + c * kChunk * kRow4Bytes;
+      const uint4 k0 = lds128(at + row0 + 16 * t), k1 = lds128(at + row1 + 16 * t);
+      const uint4 p0 = lds128(at + row0 + kRow4Codes), p1 = lds128(at + row1 + kRow4Codes);
+      const uint32_t c0[4] = {k0.x, k0.y, k0.z, k0.w}, c1[4] = {k1.x, k1.y, k1.z, k1.w};
+      const uint32_t m0[4] = {p0.x, p0.y, p0.z, p0.w}, m1[4] = {p1.x, p1.y, p1.z, p1.w};
+      const uint32_t w0 = lds32(at + row0 + kRow4Codes + 4 * t);
+      const uint32_t w1 = lds32(at + row1 + kRow4Codes + 4 * t);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        float d[4];
+        mma16816(d, w0, w1, w0, w1, qo[n][0], qo[n][1], 0.0f, 0.0f, 0.0f, 0.0f);
+        mma16816(s[c][n], w0, w1, 0u, 0u, qo[n][2], 0u, d[0], d[1], d[2], d[3]);
+      }
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (h < p.g)
-          v = *reinterpret_cast<const uint4*>(
-              p.q + (static_cast<int64_t>(hd) * p.g + h) * kRow4Dim + 32 * g + 8 * t);
+        const uint32_t a00 = codes16<0>(c0[g], sixteens), a01 = codes16<0>(c1[g], sixteens);
+        const uint32_t a02 = codes16<1>(c0[g], sixteens), a03 = codes16<1>(c1[g], sixteens);
+        const uint32_t a10 = codes16<2>(c0[g], sixteens), a11 = codes16<2>(c1[g], sixteens);
+        const uint32_t a12 = codes16<3>(c0[g], sixteens), a13 = codes16<3>(c1[g], sixteens);
+        const float s0 = row4_scale(m0[g]), s1 = row4_scale(m1[g]);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          float d[4], f[4];
+          mma16816(d, a00, a01, a02, a03, qf[n][g][0], qf[n][g][1], 0.0f, 0.0f, 0.0f, 0.0f);
+          mma16816(f, a10, a11, a12, a13, qf[n][g][2], qf[n][g][3], d[0], d[1], d[2], d[3]);
+          s[c][n][0] = fmaf(s0, f[0], s[c][n][0]);
+          s[c][n][1] = fmaf(s0, f[1], s[c][n][1]);
+          s[c][n][2] = fmaf(s1, f[2], s[c][n][2]);
+          s[c][n][3] = fmaf(s1, f[3], s[c][n][3]);
+        }
+      }
+    }
+    bool need = false;
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          s[c][n][e] = kFull || c * kChunk + kpos + 4 * (e & 2) < valid ? s[c][n][e] * p.c
+                                                                        : -INFINITY;
+          need |= s[c][n][e] > acc.m[n][e & 1] + kRescale;
+        }
+    if (__any_sync(0xffffffffu, need)) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float top = fmaxf(fmaxf(s[0][n][e], s[0][n][2 + e]), fmaxf(s[1][n][e], s[1][n][2 + e]));
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1)
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+          const float m = fmaxf(acc.m[n][e], top);
+          const float alpha = ex2_approx(acc.m[n][e] - m);
+          acc.m[n][e] = m;
+          acc.l[n][e] *= alpha;
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            acc.lows[n][g][e] *= alpha;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              acc.o[n][g][j][e] *= alpha;
+              acc.o[n][g][j][2 + e] *= alpha;
+            }
+          }
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          s[c][n][e] = ex2_approx(s[c][n][e] - acc.m[n][e & 1]);
+          acc.l[n][e & 1] += s[c][n][e];
+        }
+
+    // O^T: P times the scale of its position's group, turned, against V's codes
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const uint32_t at = sv + c * kChunk * kRow4Bytes;
+      const uint4 p0 = lds128(at + row0 + kRow4Codes), p1 = lds128(at + row1 + kRow4Codes);
+      // (rows that do not count may hold anything)
+      const uint32_t keep0 = kFull || c * kChunk + kpos < valid ? ~0u : 0u;
+      const uint32_t keep1 = kFull || c * kChunk + kpos + 8 < valid ? ~0u : 0u;
+      const uint32_t m0[4] = {p0.x & keep0, p0.y & keep0, p0.z & keep0, p0.w & keep0};
+      const uint32_t m1[4] = {p1.x & keep1, p1.y & keep1, p1.z & keep1, p1.w & keep1};
+      // rows 2 t, 2 t + 1 (positions t, t + 4) and 8 further on; codes of block r / 2
+      const uint32_t base = at + t * kRow4Bytes + 16 * (r >> 1);
+      const uint4 va = lds128(base), vb = lds128(base + 4 * kRow4Bytes);
+      const uint4 vc = lds128(base + 8 * kRow4Bytes), vd = lds128(base + 12 * kRow4Bytes);
+      const uint32_t ca[4] = {va.x, va.y, va.z, va.w}, cb[4] = {vb.x, vb.y, vb.z, vb.w};
+      const uint32_t cc[4] = {vc.x, vc.y, vc.z, vc.w}, cd[4] = {vd.x, vd.y, vd.z, vd.w};
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const uint32_t ab = __byte_perm(ca[g], cb[g], half), gh = __byte_perm(cc[g], cd[g], half);
+        const uint32_t a0 = codes0<0>(ab, sixteens), a1 = codes0<1>(ab, sixteens), a2 = codes0<0>(gh, sixteens),
+                       a3 = codes0<1>(gh, sixteens);
+        const uint32_t b0 = codes0<2>(ab, sixteens), b1 = codes0<3>(ab, sixteens), b2 = codes0<2>(gh, sixteens),
+                       b3 = codes0<3>(gh, sixteens);
+        const float s0 = row4_scale(m0[g]), s1 = row4_scale(m1[g]);
+        const float l0 = row4_low(m0[g]), l1 = row4_low(m1[g]);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const float* x = s[c][n];
+          const uint32_t x0 = transpose8x8(pack_bf16x2(x[0] * s0, x[1] * s0));
+          const uint32_t x1 = transpose8x8(pack_bf16x2(x[2] * s1, x[3] * s1));
+          acc.lows[n][g][0] = fmaf(x[0], l0, fmaf(x[2], l1, acc.lows[n][g][0]));
+          acc.lows[n][g][1] = fmaf(x[1], l0, fmaf(x[3], l1, acc.lows[n][g][1]));
+          float(&d0)[4] = acc.o[n][g][0];
+          float(&d1)[4] = acc.o[n][g][1];
+          mma16816(d0, a0, a1, a2, a3, x0, x1, d0[0], d0[1], d0[2], d0[3]);
+          mma16816(d1, b0, b1, b2, b3, x0, x1, d1[0], d1[1], d1[2], d1[3]);
+        }
+      }
+    }
+  };
+  // Q of a head: on its way, and as operands.
+  uint4 raw[NT][4];
+  auto fetch_q = [&](int head) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        raw[n][g] = make_uint4(0u, 0u, 0u, 0u);
+        if (8 * n + r < p.g)
+          raw[n][g] = *reinterpret_cast<const uint4*>(
+              p.q + (static_cast<int64_t>(head) * p.g + 8 * n + r) * kRow4Dim + 32 * g + 8 * t);
+      }
+  };
+  auto turn_q = [&]() {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      float own = 0.0f;                       // the sum of group t
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const uint4 v = raw[n][g];
         // channels e and e + 4 of the lane's eight, as the codes come
         qf[n][g][0] = __byte_perm(v.x, v.z, 0x5410);
         qf[n][g][1] = __byte_perm(v.x, v.z, 0x7632);
@@ -367,201 +550,95 @@ decode4_split_kernel(const Params4 p) {
           sum += __uint_as_float(u[e] << 16) + __uint_as_float(u[e] & 0xFFFF0000u);
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        qs[n][g][0] = __shfl_sync(0xffffffffu, sum, 8 * t);
-        qs[n][g][1] = __shfl_sync(0xffffffffu, sum, 8 * t + 4);
-        qb[n][g][0] = -16.0f * qs[n][g][0];
-        qb[n][g][1] = -16.0f * qs[n][g][1];
+        if (g == t) own = sum;
+      }
+      float rest[2] = {-16.0f * own, own};
+#pragma unroll
+      for (int k = 0; k < 3; ++k) {
+        qo[n][k] = pack_bf16x2(rest[0], rest[1]);
+        rest[0] -= __uint_as_float(qo[n][k] << 16);
+        rest[1] -= __uint_as_float(qo[n][k] & 0xFFFF0000u);
       }
     }
+  };
 
-    // One step's products; kFull: all of its rows count.
-    auto step = [&](auto full_step, int slot, int valid) {
-      constexpr bool kFull = decltype(full_step)::value;
-      const uint32_t sk = ring + slot * 2 * kStepBytes, sv = sk + kStepBytes;
-      const uint32_t row0 = kpos * kRow4Bytes, row1 = row0 + 8 * kRow4Bytes;
-
-      // S^T: rows r and r + 8 of each chunk, heads 2 t and 2 t + 1 of each tile
-      float s[2][NT][4];
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const uint32_t at = sk + c * kChunk * kRow4Bytes;
-        const uint4 k0 = lds128(at + row0 + 16 * t), k1 = lds128(at + row1 + 16 * t);
-        const uint4 p0 = lds128(at + row0 + kRow4Codes), p1 = lds128(at + row1 + kRow4Codes);
-        const uint32_t c0[4] = {k0.x, k0.y, k0.z, k0.w}, c1[4] = {k1.x, k1.y, k1.z, k1.w};
-        const uint32_t m0[4] = {p0.x, p0.y, p0.z, p0.w}, m1[4] = {p1.x, p1.y, p1.z, p1.w};
-#pragma unroll
-        for (int n = 0; n < NT; ++n) s[c][n][0] = s[c][n][1] = s[c][n][2] = s[c][n][3] = 0.0f;
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const uint32_t a00 = codes16<0>(c0[g]), a01 = codes16<0>(c1[g]);
-          const uint32_t a02 = codes16<1>(c0[g]), a03 = codes16<1>(c1[g]);
-          const uint32_t a10 = codes16<2>(c0[g]), a11 = codes16<2>(c1[g]);
-          const uint32_t a12 = codes16<3>(c0[g]), a13 = codes16<3>(c1[g]);
-          const float s0 = row4_scale(m0[g]), s1 = row4_scale(m1[g]);
-          const float l0 = row4_low(m0[g]), l1 = row4_low(m1[g]);
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            // (from -16 sum q: the products are with 16 + code)
-            float d[4];
-            mma16816(d, a00, a01, a02, a03, qf[n][g][0], qf[n][g][1], qb[n][g][0], qb[n][g][1],
-                     qb[n][g][0], qb[n][g][1]);
-            mma16816(d, a10, a11, a12, a13, qf[n][g][2], qf[n][g][3], d[0], d[1], d[2], d[3]);
-            s[c][n][0] = fmaf(s0, d[0], fmaf(l0, qs[n][g][0], s[c][n][0]));
-            s[c][n][1] = fmaf(s0, d[1], fmaf(l0, qs[n][g][1], s[c][n][1]));
-            s[c][n][2] = fmaf(s1, d[2], fmaf(l1, qs[n][g][0], s[c][n][2]));
-            s[c][n][3] = fmaf(s1, d[3], fmaf(l1, qs[n][g][1], s[c][n][3]));
-          }
-        }
-      }
-      bool need = false;
-#pragma unroll
-      for (int c = 0; c < 2; ++c)
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            s[c][n][e] = kFull || c * kChunk + kpos + 4 * (e & 2) < valid ? s[c][n][e] * p.c
-                                                                          : -INFINITY;
-            need |= s[c][n][e] > acc.m[n][e & 1] + kRescale;
-          }
-      if (__any_sync(0xffffffffu, need)) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float top = fmaxf(fmaxf(s[0][n][e], s[0][n][2 + e]), fmaxf(s[1][n][e], s[1][n][2 + e]));
-#pragma unroll
-            for (int off = 4; off < 32; off <<= 1)
-              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-            const float m = fmaxf(acc.m[n][e], top);
-            const float alpha = ex2_approx(acc.m[n][e] - m);
-            acc.m[n][e] = m;
-            acc.l[n][e] *= alpha;
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-              acc.lows[n][g][e] *= alpha;
-#pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                acc.o[n][g][j][e] *= alpha;
-                acc.o[n][g][j][2 + e] *= alpha;
-              }
-            }
-          }
-      }
-#pragma unroll
-      for (int c = 0; c < 2; ++c)
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            s[c][n][e] = ex2_approx(s[c][n][e] - acc.m[n][e & 1]);
-            acc.l[n][e & 1] += s[c][n][e];
-          }
-
-      // O^T: P times the scale of its position's group, turned, against V's codes
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const uint32_t at = sv + c * kChunk * kRow4Bytes;
-        const uint4 p0 = lds128(at + row0 + kRow4Codes), p1 = lds128(at + row1 + kRow4Codes);
-        // (rows that do not count may hold anything)
-        const uint32_t keep0 = kFull || c * kChunk + kpos < valid ? ~0u : 0u;
-        const uint32_t keep1 = kFull || c * kChunk + kpos + 8 < valid ? ~0u : 0u;
-        const uint32_t m0[4] = {p0.x & keep0, p0.y & keep0, p0.z & keep0, p0.w & keep0};
-        const uint32_t m1[4] = {p1.x & keep1, p1.y & keep1, p1.z & keep1, p1.w & keep1};
-        // rows 2 t, 2 t + 1 (positions t, t + 4) and 8 further on; codes of block r / 2
-        const uint32_t base = at + t * kRow4Bytes + 16 * (r >> 1);
-        const uint4 va = lds128(base), vb = lds128(base + 4 * kRow4Bytes);
-        const uint4 vc = lds128(base + 8 * kRow4Bytes), vd = lds128(base + 12 * kRow4Bytes);
-        const uint32_t ca[4] = {va.x, va.y, va.z, va.w}, cb[4] = {vb.x, vb.y, vb.z, vb.w};
-        const uint32_t cc[4] = {vc.x, vc.y, vc.z, vc.w}, cd[4] = {vd.x, vd.y, vd.z, vd.w};
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const uint32_t ab = __byte_perm(ca[g], cb[g], half), gh = __byte_perm(cc[g], cd[g], half);
-          const uint32_t a0 = codes0<0>(ab), a1 = codes0<1>(ab), a2 = codes0<0>(gh),
-                         a3 = codes0<1>(gh);
-          const uint32_t b0 = codes0<2>(ab), b1 = codes0<3>(ab), b2 = codes0<2>(gh),
-                         b3 = codes0<3>(gh);
-          const float s0 = row4_scale(m0[g]), s1 = row4_scale(m1[g]);
-          const float l0 = row4_low(m0[g]), l1 = row4_low(m1[g]);
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            const float* x = s[c][n];
-            const uint32_t x0 = transpose8x8(pack_bf16x2(x[0] * s0, x[1] * s0));
-            const uint32_t x1 = transpose8x8(pack_bf16x2(x[2] * s1, x[3] * s1));
-            acc.lows[n][g][0] = fmaf(x[0], l0, fmaf(x[2], l1, acc.lows[n][g][0]));
-            acc.lows[n][g][1] = fmaf(x[1], l0, fmaf(x[3], l1, acc.lows[n][g][1]));
-            float(&d0)[4] = acc.o[n][g][0];
-            float(&d1)[4] = acc.o[n][g][1];
-            mma16816(d0, a0, a1, a2, a3, x0, x1, d0[0], d0[1], d0[2], d0[3]);
-            mma16816(d1, b0, b1, b2, b3, x0, x1, d1[0], d1[1], d1[2], d1[3]);
-          }
-        }
-      }
-    };
-    while (ok && cur.left > 0 && cur.b * p.n_kv + cur.u == hd) {
-      const Part4 part(cur);
-      for (int rows = part.rows; rows > 0; rows -= kStep) {
-        const int slot = taken % kStages;
-        const uint32_t bar = smem_addr(&full[warp][slot]), parity = (taken / kStages) & 1;
-        bool there = mbar_try_wait(bar, parity);
-        if (!there) {
-          const uint64_t since = clock64_now();
-          while (!(there = mbar_try_wait(bar, parity)))
-            if (static_cast<long long>(clock64_now() - since) > kSpinLimit) break;
-        }
-        if (!__all_sync(0xffffffffu, there)) {
-          if (lane == 0) atomicOr(p.status, kStatusTimeout);
-          ok = false;
-          break;
-        }
-        if (rows >= kStep) step(std::true_type{}, slot, kStep);
-        else step(std::false_type{}, slot, rows);
-        ++taken;
-        __syncwarp();
-        send();
-      }
-      cur.move(p, part.units);
+  // Copies go out first, but for the first head's Q: behind them it would wait for all
+  // that the other warps ask for as well.
+  bool going = ahead.w.left > 0;
+  if (going) fetch_q(ahead.w.b * p.n_kv + ahead.w.u);
+  for (int i = 0; i < kStages; ++i) send();
+  __syncwarp();
+  int slot = 0;
+  for (uint32_t part = 0; going; ++part) {
+    const int4 now = lds_desc(smem_addr(&note[warp][part % kNotes]));
+    if (now.z & kFirst) {
+      hd = now.y;
+      where = 0;
+      acc.clear();
+      if (part > 0) fetch_q(hd);
+      turn_q();
     }
-    if (!ok || cur.left == 0) break;
+    where |= now.z;
+    for (int rows = now.x; rows > 0; rows -= kStep) {
+      copies_wait<kStages - 1>();
+      __syncwarp();
+      if (rows >= kStep) step(std::true_type{}, slot, kStep);
+      else step(std::false_type{}, slot, rows);
+      __syncwarp();
+      send();
+      slot = slot + 1 == kStages ? 0 : slot + 1;
+    }
+    going = !(now.z & kRunEnd);
+    if (!(now.z & kLast) || !going) continue;
 
     // the head goes on in no other warp's run but earlier ones: its end goes out as it is
     acc.finish();
     if (lane == 0) {
-      if (t0 == 0) p.ends[2 * hd] = cta;
+      if (where & kHeadStart) p.ends[2 * hd] = cta;
       p.ends[2 * hd + 1] = cta;
     }
-    const int64_t slot = 2 * (static_cast<int64_t>(hd) + cta) + 1;
+    const int64_t place = 2 * (static_cast<int64_t>(hd) + cta) + 1;
     // without a run of this CTA before it, the run's place stays empty
-    const bool alone = t0 == 0 || warp == 0;
+    const bool alone = (where & kHeadStart) || warp == 0;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int h = 8 * n + 2 * t + e;
         if (h >= p.g) continue;
-        float* out = p.part_o + (slot * p.g + h) * kRow4Dim + 4 * r;
+        float* out = p.part_o + (place * p.g + h) * kRow4Dim + 4 * r;
 #pragma unroll
         for (int g = 0; g < 4; ++g)
           *reinterpret_cast<float4*>(out + 32 * g) = acc.channels(n, g, e);
         if (r == 0) {
-          p.part_ml[slot * p.g + h] = make_float2(acc.m[n][e], acc.l[n][e]);
-          if (alone) p.part_ml[(slot - 1) * p.g + h] = make_float2(kNoMax, 0.0f);
+          p.part_ml[place * p.g + h] = make_float2(acc.m[n][e], acc.l[n][e]);
+          if (alone) p.part_ml[(place - 1) * p.g + h] = make_float2(kNoMax, 0.0f);
         }
       }
   }
 
-  // Every copy this warp started has landed before the CTA can end.
-  for (uint32_t c = taken; c < sent; ++c) {
-    const uint32_t bar = smem_addr(&full[warp][c % kStages]);
-    const uint64_t since = clock64_now();
-    while (!mbar_try_wait(bar, (c / kStages) & 1))
-      if (static_cast<long long>(clock64_now() - since) > kSpinLimit) break;
-  }
-  __syncwarp();
-
-  // The warps that ended in one head are neighbours: their results meet in shared memory.
+  // The warps that ended in one head are neighbours: their results meet in shared memory,
+  // first the maxima and then, brought to the largest, sums and outputs.
   if (hd >= 0) {
     acc.finish();
+    if (r == 0) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        m_of[warp][8 * n + 2 * t] = acc.m[n][0];
+        m_of[warp][8 * n + 2 * t + 1] = acc.m[n][1];
+      }
+    }
+    if (lane == 0) {
+      if (where & kHeadStart) p.ends[2 * hd] = cta;
+      if (where & kHeadEnd) p.ends[2 * hd + 1] = cta;
+    }
+  }
+  if (lane == 0) head_of[warp] = hd;
+  __syncthreads();
+  int first = warp, last = warp + 1;
+  while (first > 0 && head_of[first - 1] == hd) --first;
+  while (last < kWarps && head_of[last] == hd) ++last;
+  if (hd >= 0) {
     float* own = reinterpret_cast<float*>(dyn_smem + warp * kWarpBytes);
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -569,47 +646,47 @@ decode4_split_kernel(const Params4 p) {
       for (int e = 0; e < 2; ++e) {
         const int h = 8 * n + 2 * t + e;
         if (h >= p.g) continue;
+        float m = kNoMax;
+        for (int i = first; i < last; ++i) m = fmaxf(m, m_of[i][h]);
+        const float f = ex2_approx(acc.m[n][e] - m);
 #pragma unroll
-        for (int g = 0; g < 4; ++g)
-          *reinterpret_cast<float4*>(own + h * kRow4Dim + 32 * g + 4 * r) = acc.channels(n, g, e);
-        if (r == 0) ml_of[warp][h] = make_float2(acc.m[n][e], acc.l[n][e]);
+        for (int g = 0; g < 4; ++g) {
+          const float4 v = acc.channels(n, g, e);
+          *reinterpret_cast<float4*>(own + h * kRow4Dim + 32 * g + 4 * r) =
+              make_float4(f * v.x, f * v.y, f * v.z, f * v.w);
+        }
+        if (r == 0) l_of[warp][h] = f * acc.l[n][e];
       }
-    if (lane == 0) {
-      if (t0 == 0) p.ends[2 * hd] = cta;
-      if (t_end == T) p.ends[2 * hd + 1] = cta;
-    }
   }
-  if (lane == 0) head_of[warp] = hd;
   __syncthreads();
   if (hd < 0) return;
-  int first = warp, last = warp + 1;
-  while (first > 0 && head_of[first - 1] == hd) --first;
-  while (last < kWarps && head_of[last] == hd) ++last;
-  const int64_t slot = 2 * (static_cast<int64_t>(hd) + cta);
+  const int64_t place = 2 * (static_cast<int64_t>(hd) + cta);
   // the head's end is in this CTA, in the next warp's first segment, or not here
-  const bool tail = last < kWarps && head_of[last] >= 0 && t_end < T;
+  const bool tail = last < kWarps && head_of[last] >= 0 && !(where & kHeadEnd);
   for (int item = (warp - first) * 32 + lane; item < p.g * 32; item += (last - first) * 32) {
     const int h = item >> 5, quad = item & 31;
-    float m = kNoMax;
-    for (int i = first; i < last; ++i) m = fmaxf(m, ml_of[i][h].x);
     float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    float l = 0.0f;
+#pragma unroll 4
     for (int i = first; i < last; ++i) {
-      const float2 ml = ml_of[i][h];
-      const float f = ex2_approx(ml.x - m);
       const float4 v =
           *reinterpret_cast<const float4*>(dyn_smem + i * kWarpBytes + (h * kRow4Dim + 4 * quad) * 4);
-      sum.x = fmaf(f, v.x, sum.x);
-      sum.y = fmaf(f, v.y, sum.y);
-      sum.z = fmaf(f, v.z, sum.z);
-      sum.w = fmaf(f, v.w, sum.w);
-      l = fmaf(f, ml.y, l);
+      sum.x += v.x;
+      sum.y += v.y;
+      sum.z += v.z;
+      sum.w += v.w;
     }
-    *reinterpret_cast<float4*>(p.part_o + (slot * p.g + h) * kRow4Dim + 4 * quad) = sum;
-    if (quad == 0) p.part_ml[slot * p.g + h] = make_float2(m, l);
+    *reinterpret_cast<float4*>(p.part_o + (place * p.g + h) * kRow4Dim + 4 * quad) = sum;
+    if (quad == 0) {
+      float m = kNoMax, l = 0.0f;
+      for (int i = first; i < last; ++i) {
+        m = fmaxf(m, m_of[i][h]);
+        l += l_of[i][h];
+      }
+      p.part_ml[place * p.g + h] = make_float2(m, l);
+    }
   }
   if (warp == last - 1 && !tail && lane < p.g)
-    p.part_ml[(slot + 1) * p.g + lane] = make_float2(kNoMax, 0.0f);
+    p.part_ml[(place + 1) * p.g + lane] = make_float2(kNoMax, 0.0f);
 }
 
 // O = sum_s 2^(m_s - m) O_s / sum_s 2^(m_s - m) l_s over a row's places (two per
@@ -753,7 +830,7 @@ bool sizes_ok(int64_t B, int64_t C, int32_t n_q, int32_t n_kv, int32_t d_h, int6
 bool supported(int64_t B, int64_t C, int32_t n_q, int32_t n_kv, int32_t d_h) {
   return d_h == kRow4Dim && n_q / n_kv <= kMaxG && C <= (int64_t{1} << 30) &&
          B <= (int64_t{1} << 24) && B * n_kv <= (int64_t{1} << 24) &&
-         B * n_kv * (C / kChunk + 1) <= (int64_t{1} << 40);
+         B * n_kv * (C / kChunk + 2) < (int64_t{1} << 31);
 }
 
 // Grid and workspace: two places for each head and each CTA that may stand in it.
@@ -818,7 +895,6 @@ attn_status_t attn_decode4_fwd(const void* q, const void* k4, const void* v4, co
   p.part_o = reinterpret_cast<float*>(ws);
   p.part_ml = reinterpret_cast<float2*>(ws + s.ml_at);
   p.ends = reinterpret_cast<int*>(ws + s.ends_at);
-  p.status = status;
   p.B = static_cast<int>(B);
   p.C = static_cast<int>(C);
   p.n_q = n_q;
@@ -829,6 +905,7 @@ attn_status_t attn_decode4_fwd(const void* q, const void* k4, const void* v4, co
   const bool two = p.g > 8;
   p.walkers = static_cast<int>(s.ctas) * (two ? kWarpsOf<2> : kWarpsOf<1>);
   p.c = scale * 1.4426950408889634f;
+  p.sixteens = 0x41804180u;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
