@@ -53,7 +53,9 @@
 // lens[b] positions and the first S) the ragged step's tiles are those of the
 // visible positions only: the sinks' from position 0 on, then the window's from its
 // own first position on (a TMA box may start at any row), so a window of W costs
-// ceil(W / 128) tiles wherever it lies. Hidden positions that share a tile with
+// ceil(W / 128) tiles wherever it lies. A few sinks come through maps with boxes of as
+// few rows (64 steps with 4 sinks read 255 MB, 284 with whole boxes: 47 and 51 us). Hidden
+// positions that share a tile with
 // visible ones are masked and zeroed like those past a length.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -359,6 +361,16 @@ struct RaggedWalk {
   }
 };
 
+// kWindow: K and V in boxes of `rows` rows (a multiple of 8) for the sinks, where they are
+// fewer than a tile.
+template <bool kWindow>
+struct SinkMaps {};
+template <>
+struct SinkMaps<true> {
+  CUtensorMap k, v;
+  int rows;
+};
+
 template <bool kRagged, bool kWindow>
 struct WalkOf {
   using type = SegmentWalk;
@@ -375,7 +387,8 @@ template <int GP, bool kRagged, bool kWeights, bool kWindow = false>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_decode_split_kernel(const __grid_constant__ CUtensorMap tmQ,
                          const __grid_constant__ CUtensorMap tmK,
-                         const __grid_constant__ CUtensorMap tmV, const DecodeParams p) {
+                         const __grid_constant__ CUtensorMap tmV, const DecodeParams p,
+                         const __grid_constant__ SinkMaps<kWindow> sinks) {
   extern __shared__ uint8_t dyn_smem[];
   __shared__ DecodeCtl ctl;
   // smem: kRing K/V tiles | Q[kQBufs] (16 heads x 128, two 2 KiB chunks) | P[2]
@@ -467,6 +480,18 @@ attn_decode_split_kernel(const __grid_constant__ CUtensorMap tmQ,
               break;
             }
             const uint32_t bar = smem_addr(&ctl.full[slot]);
+            if constexpr (kWindow) {
+              // (rows of the slot past the box keep what they held: they do not count, and
+              // are masked and zeroed as such)
+              if (sg.t0 + t < sg.na && sinks.rows < kKeys) {
+                mbar_arrive_expect_tx(bar, 2 * 128 * sinks.rows);
+                for (int ch = 0; ch < 2; ++ch)
+                  tma_load_4d(sRing + slot * kTileBytes + ch * kChunkBytes,
+                              kind ? &sinks.v : &sinks.k, bar, ch * 64, kvh, 0, b);
+                ++it;
+                continue;
+              }
+            }
             mbar_arrive_expect_tx(bar, kTileBytes);
             for (int ch = 0; ch < 2; ++ch)
               tma_load_4d(sRing + slot * kTileBytes + ch * kChunkBytes, kind ? &tmV : &tmK, bar,
@@ -1011,15 +1036,16 @@ bool set_smem() {
 // The split kernel for groups of g query heads.
 template <bool kRagged, bool kWeights, bool kWindow = false>
 cudaError_t launch_split(const cudaLaunchConfig_t& cfg, const CUtensorMap& mq,
-                         const CUtensorMap& mk, const CUtensorMap& mv, const DecodeParams& p) {
+                         const CUtensorMap& mk, const CUtensorMap& mv, const DecodeParams& p,
+                         const SinkMaps<kWindow>& sinks = {}) {
   if (p.g <= 4)
     return cudaLaunchKernelEx(&cfg, attn_decode_split_kernel<4, kRagged, kWeights, kWindow>, mq,
-                              mk, mv, p);
+                              mk, mv, p, sinks);
   if (p.g <= 8)
     return cudaLaunchKernelEx(&cfg, attn_decode_split_kernel<8, kRagged, kWeights, kWindow>, mq,
-                              mk, mv, p);
+                              mk, mv, p, sinks);
   return cudaLaunchKernelEx(&cfg, attn_decode_split_kernel<16, kRagged, kWeights, kWindow>, mq, mk,
-                            mv, p);
+                            mv, p, sinks);
 }
 
 attn_status_t decode_device_ready(cudaStream_t stream, int** status) {
@@ -1053,12 +1079,13 @@ attn_status_t decode_device_ready(cudaStream_t stream, int** status) {
 
 // K or V [B, Lk, H, 128] bf16 as (D, H, L, B): 64 x 1 x 128 x 1 boxes,
 // 128-byte swizzle (the tensor cores' operand layout).
-bool encode_kv(CUtensorMap* map, const void* ptr, int H, int64_t Lk, int64_t B) {
+bool encode_kv(CUtensorMap* map, const void* ptr, int H, int64_t Lk, int64_t B,
+               int rows = kKeys) {
   const cuuint64_t dims[4] = {kDim, static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(Lk),
                               static_cast<cuuint64_t>(B)};
   const cuuint64_t strides[3] = {kDim * 2, static_cast<cuuint64_t>(H) * kDim * 2,
                                  static_cast<cuuint64_t>(Lk) * H * kDim * 2};
-  const cuuint32_t box[4] = {64, 1, kKeys, 1};
+  const cuuint32_t box[4] = {64, 1, static_cast<cuuint32_t>(rows), 1};
   const cuuint32_t estride[4] = {1, 1, 1, 1};
   return g_decode_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims,
                          strides, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -1171,7 +1198,12 @@ attn_status_t launch_ragged_split(const void* q, const void* k, const void* v, c
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = window > 0 ? launch_split<true, false, true>(cfg, mq, mk, mv, p)
+  SinkMaps<true> sm;
+  sm.rows = p.sinks < kKeys ? (p.sinks + 7) / 8 * 8 : kKeys;
+  if (window > 0 && p.sinks > 0 && sm.rows < kKeys &&
+      (!encode_kv(&sm.k, k, n_kv, C, B, sm.rows) || !encode_kv(&sm.v, v, n_kv, C, B, sm.rows)))
+    return ATTN_ERR_CUDA;
+  const cudaError_t e = window > 0 ? launch_split<true, false, true>(cfg, mq, mk, mv, p, sm)
                         : weighted ? launch_split<true, true>(cfg, mq, mk, mv, p)
                                    : launch_split<true, false>(cfg, mq, mk, mv, p);
   *out = p;

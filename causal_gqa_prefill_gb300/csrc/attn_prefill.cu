@@ -110,6 +110,15 @@ struct Tile {
   static_assert(kRowBytes % 128 == 0, "rows must fill whole 128-byte swizzle chunks");
 };
 
+// Division by a fixed number of values below 2^31: q = (umulhi(m, x) + x) >> s.
+struct FastDiv {
+  uint32_t m, s;
+  __device__ int of(int x) const {
+    const uint32_t u = static_cast<uint32_t>(x);
+    return static_cast<int>((__umulhi(m, u) + u) >> s);
+  }
+};
+
 struct Params {
   uint16_t* o;          // bf16 [B, L, n_q, D]
   float* lse;           // fp32 [B, n_q, L]
@@ -122,6 +131,7 @@ struct Params {
   int scale_pos;        // 1 when c > 0
   int window, sinks;    // kWin instances: W and S, both at most Lk
   int first;            // kWin instances: position where the window's tensor maps begin
+  FastDiv by_groups, by_n_kv, by_g;   // kWin instances: divisions of decode_unit
   float c;              // scale * log2(e) (times the Q and K descale factors for fp8)
   float o_scale;        // multiplies O / l in the epilogue (the V descale for fp8, else 1)
   int groups;           // B * n_kv
@@ -220,22 +230,31 @@ __device__ __forceinline__ int list_tile(const Unit& x, int j) {
 template <bool kWin>
 __device__ __forceinline__ Unit decode_unit(int u, const Params& p) {
   Unit x;
-  const int per_batch = p.batch * p.pairs;
-  const int bi = u / per_batch;
-  const int v = u - bi * per_batch;
-  const int g0 = bi * p.batch;
-  const int nb = min(p.batch, p.groups - g0);
-  const int pair = v / nb;
-  const int grp = g0 + (v - pair * nb);
-  x.b = grp / p.n_kv;
+  int pair, grp;
+  if (kWin) {
+    // one batch, and no division: every role decodes each unit between two units' work
+    pair = p.by_groups.of(u);
+    grp = u - pair * p.groups;
+    x.b = p.by_n_kv.of(grp);
+  } else {
+    const int per_batch = p.batch * p.pairs;
+    const int bi = u / per_batch;
+    const int v = u - bi * per_batch;
+    const int g0 = bi * p.batch;
+    const int nb = min(p.batch, p.groups - g0);
+    pair = v / nb;
+    grp = g0 + (v - pair * nb);
+    x.b = grp / p.n_kv;
+  }
   x.kvh = grp - x.b * p.n_kv;
   const int total = p.g * p.Tq;
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
     const int k = 2 * pair + (1 - s);
     if (k < total) {
-      const int i = p.Tq - 1 - k / p.g;
-      x.head[s] = x.kvh * p.g + (k % p.g);
+      const int kt = kWin ? p.by_g.of(k) : k / p.g;
+      const int i = p.Tq - 1 - kt;
+      x.head[s] = x.kvh * p.g + (kWin ? k - kt * p.g : k % p.g);
       x.qtile[s] = i;
       // Causal: key tiles up to the one holding the tile's last query position.
       const int last_row = min(i * kBM + kBM - 1, p.Lq - 1);
@@ -597,6 +616,11 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
+// A word whose lowest n bits are set (none for n <= 0, all from 32 on).
+__device__ __forceinline__ uint32_t below(int n) {
+  return n >= 32 ? ~0u : (1u << max(n, 0)) - 1u;
+}
+
 // Row maximum of 128 scores with three-input max instructions.
 __device__ __forceinline__ float row_max128(const float* v) {
   float m[8];
@@ -675,27 +699,20 @@ __device__ void softmax_role(int slot, Ctl& ctl, const Params& p, uint32_t tmem,
       if (kWin) {
         // A sinks' tile holds the keys below min(S, low); a window's tile the keys
         // from `low` on, of which a row sees those up to its position and either
-        // within W of it or below S. In-tile indices:
+        // within W of it or below S. As bits of the tile's keys, 32 at a time.
         const int key0 = list_tile<true>(x, j) * kBN;
-        if (j < x.na) {
-          const int keep = min(p.sinks, x.low) - 1 - key0;
-          if (keep < kBN - 1) {
+        const bool sink = j < x.na;
+        const int end = sink ? min(p.sinks, x.low) - key0 : qrow0 + r - key0 + 1;   // past the last
+        if (sink ? end < kBN : (key0 + kBN - 1 > qrow0 || key0 <= qrow0 + kBM - 1 - p.window)) {
+          const int begin = sink ? 0 : end - p.window;             // the window's first
+          const int sink0 = x.low - key0, sink1 = sink ? 0 : p.sinks - key0;
 #pragma unroll
-            for (int i = 0; i < 128; ++i)
-              if (i > keep) s[i] = -INFINITY;
-          }
-        } else if (key0 + kBN - 1 > qrow0 || key0 <= qrow0 + kBM - 1 - p.window) {
-          const int keep = qrow0 + r - key0;
-          const int out = keep - p.window;                    // up to here out of the window
-          const int sink0 = x.low - key0, sink1 = p.sinks - key0;
-          if (sink1 > max(sink0, 0)) {
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t seen = below(end - 32 * c) & (~below(begin - 32 * c) |
+                                                        (below(sink1 - 32 * c) & ~below(sink0 - 32 * c)));
 #pragma unroll
-            for (int i = 0; i < 128; ++i)
-              if (i > keep || (i <= out && (i < sink0 || i >= sink1))) s[i] = -INFINITY;
-          } else {
-#pragma unroll
-            for (int i = 0; i < 128; ++i)
-              if (i > keep || i <= out) s[i] = -INFINITY;
+            for (int i = 0; i < 32; ++i)
+              if (!((seen >> i) & 1u)) s[32 * c + i] = -INFINITY;
           }
         }
       } else {
@@ -1048,6 +1065,13 @@ bool encode_bhld(CUtensorMap* map, const void* ptr, int D, int H, int64_t L, int
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+FastDiv fast_div(int64_t n) {
+  FastDiv d{0, 0};
+  while ((int64_t{1} << d.s) < n) ++d.s;
+  d.m = static_cast<uint32_t>((((uint64_t{1} << d.s) - static_cast<uint64_t>(n)) << 32) / n + 1);
+  return d;
+}
+
 // Sizes -> work units; returns false when they exceed 32-bit tile indexing.
 bool count_units(int64_t B, int64_t Lq, int64_t Lk, int32_t n_q, int32_t n_kv, int* Tq_out,
                  int* units_out) {
@@ -1158,6 +1182,9 @@ attn_status_t launch_forward(const void* q, const void* k, const void* v, void* 
   p.window = static_cast<int>(window);
   p.sinks = static_cast<int>(sinks);
   p.first = static_cast<int>(first);
+  p.by_groups = fast_div(B * n_kv);
+  p.by_n_kv = fast_div(n_kv);
+  p.by_g = fast_div(n_q / n_kv);
   p.groups = static_cast<int>(B * n_kv);
   p.units = units;
   p.pairs = units / p.groups;
