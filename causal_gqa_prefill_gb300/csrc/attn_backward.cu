@@ -23,7 +23,8 @@
 //           tile i) units longest first in snake order: S = Q K^T (Q_i in
 //           TMEM) and dP = dO V^T (dO_i in shared memory), dS in its own TMEM
 //           columns, dQ += dS K over the key tiles it sees; the next unit's
-//           K/V tiles stream in while the current unit drains.
+//           K/V tiles, Q_i and dO_i come in, and its first scores run, while the
+//           current unit's last dQ product is done and stored.
 // Both tile kernels step over whole 128-column score tiles (128 queries of a
 // query tile in dkdv, 128 keys of a key tile in dq), so every product is
 // N = 128 (or D) wide, and order their products so that the tensor cores run
@@ -34,7 +35,8 @@
 // reach it and a query tile only the sinks' and its window's key tiles. Key tiles
 // that hold a sink are seen by every later row; they come first, each cut into
 // `pieces` CTAs of equal runs of (head, query tile) steps, which write fp32 parts
-// that a join kernel adds in order (no atomics).
+// that a join kernel adds in order (no atomics). So are, where a call has few key
+// tiles, the others (key_split).
 //
 // Each kernel has a TMA producer warp, an MMA warp (warp-wide loop, one elected
 // issuing lane) and kComputeWGs compute warpgroups that split the 128 columns
@@ -92,8 +94,18 @@ struct BwdParams {
   // kWin instances
   int window, sinks;        // W and S, both at most L
   int heavy, pieces;        // key tiles that hold a sink, and CTAs per such tile
-  float* parts;             // fp32 [groups * heavy][pieces][dV, dK][128][D] (pieces > 1)
+  int others;               // CTAs per other key tile
+  // where a tile has more than one CTA: fp32 [dV, dK][128][D] of each, [groups][heavy]
+  // [pieces] and, behind them, [groups][T - heavy][others]
+  float* parts;
 };
+
+// Number of the first part of key tile j of group grp.
+__device__ __forceinline__ size_t first_part(const BwdParams& p, int groups, size_t grp, int j) {
+  const size_t first = p.pieces > 1 ? static_cast<size_t>(groups) * p.heavy * p.pieces : 0;
+  return j < p.heavy ? (grp * p.heavy + j) * p.pieces
+                     : first + (grp * (p.T - p.heavy) + j - p.heavy) * p.others;
+}
 
 // The key tiles that query tile i sees, in order: tiles [0, na), which hold sinks
 // before its window, then tiles lo .. i.
@@ -117,7 +129,7 @@ __device__ __forceinline__ int seen_tile(const SeenTiles& x, int t) {
 // One CTA's work in the dK/dV kernel: steps first .. first + n - 1 of the
 // (head, query tile) pairs of key tile j, `per_head` query tiles from i0 on each.
 struct KeyWork {
-  int j, grp, i0, per_head, first, n, piece;
+  int j, grp, i0, per_head, first, n, piece, pieces, groups;
 };
 template <bool kWin>
 __device__ __forceinline__ KeyWork key_work(const BwdParams& p) {
@@ -131,15 +143,20 @@ __device__ __forceinline__ KeyWork key_work(const BwdParams& p) {
     w.first = 0;
     w.n = p.g * w.per_head;
     w.piece = 0;
+    w.pieces = 1;
+    w.groups = groups;
     return w;
   }
-  const int rows = p.heavy * p.pieces + p.T - p.heavy;
-  const int groups = static_cast<int>(gridDim.x) / rows;
-  const int slot = blockIdx.x / groups;
-  w.grp = blockIdx.x - slot * groups;
+  const int rows = p.heavy * p.pieces + (p.T - p.heavy) * p.others;
+  w.groups = static_cast<int>(gridDim.x) / rows;
+  int slot = blockIdx.x / w.groups;
+  w.grp = blockIdx.x - slot * w.groups;
   const bool heavy = slot < p.heavy * p.pieces;
-  w.j = heavy ? slot / p.pieces : slot - p.heavy * p.pieces + p.heavy;
-  w.piece = heavy ? slot - w.j * p.pieces : 0;
+  if (!heavy) slot -= p.heavy * p.pieces;
+  w.pieces = heavy ? p.pieces : p.others;
+  w.j = slot / w.pieces;
+  w.piece = slot - w.j * w.pieces;
+  if (!heavy) w.j += p.heavy;
   w.i0 = w.j;
   // the last row that sees the tile's last key
   const int last = heavy ? p.T - 1
@@ -147,9 +164,8 @@ __device__ __forceinline__ KeyWork key_work(const BwdParams& p) {
                                (static_cast<long long>(w.j) * kT + kT - 1 + p.window - 1) / kT));
   w.per_head = last - w.i0 + 1;
   const long long total = static_cast<long long>(p.g) * w.per_head;
-  w.first = heavy ? static_cast<int>(total * w.piece / p.pieces) : 0;
-  w.n = (heavy ? static_cast<int>(total * (w.piece + 1) / p.pieces) : static_cast<int>(total)) -
-        w.first;
+  w.first = static_cast<int>(total * w.piece / w.pieces);
+  w.n = static_cast<int>(total * (w.piece + 1) / w.pieces) - w.first;
   return w;
 }
 
@@ -163,6 +179,7 @@ struct Sync {
   uint64_t s_full[2], p_full[2];    // scores ready (commit) / P or dS ready (compute threads)
   uint64_t dp_full, ds_full;        // dP (dP^T) ready (commit) / dS (dS^T) ready (compute threads)
   uint64_t dp_free, dq_done;        // dQ: dP read out (compute threads) / dQ += dS K done (commit)
+  uint64_t do_free;                 // dQ: the unit's last product with dO done (commit)
   uint64_t done, drain;
   uint32_t tmem_base;
   int abort;
@@ -306,6 +323,7 @@ __device__ __forceinline__ void setup(Sync& sy) {
     mbar_init(smem_addr(&sy.ds_full), kComputeThreads);
     mbar_init(smem_addr(&sy.dp_free), kComputeThreads);
     mbar_init(smem_addr(&sy.dq_done), 1);
+    mbar_init(smem_addr(&sy.do_free), 1);
     mbar_init(smem_addr(&sy.done), 1);
     mbar_init(smem_addr(&sy.drain), 1);
     sy.abort = 0;
@@ -433,14 +451,14 @@ __device__ __forceinline__ void p_from_s(uint32_t taddr, uint64_t c2, uint64_t n
 
 // ------------------------------------------------------------------ rowdot
 
-// Half a warp per padded row (b, h, t), t < Lp: 16 lanes x 8 dimensions, with
-// 16-byte loads; a warp takes four rows at a time so that its loads of all
-// four are in flight together, and walks the rows grid-stride (at most eight
-// blocks per SM: a long-lived grid instead of thousands of short blocks).
-// Rows past L get -inf and 0 without touching O or dO. The dK/dV kernel is
-// launched as this grid's programmatic dependent and waits for it before it
-// reads the statistics.
-constexpr int kRowdotRowsPerWarp = 4;
+// Half a warp per row: 16 lanes x D / 16 dimensions. A block takes kRowdotT positions of
+// up to kRowdotH neighbouring heads, so that it reads O and dO in their own order,
+// four rows (eight loads) under way per half-warp, and writes whole pieces of the
+// [b, h, t] statistics out of shared memory. (One row (b, h, t) after another, with
+// three divisions each, took 41 us where 134 MB take 20.) Positions past L get -inf
+// and 0 without touching O or dO. The dK/dV kernel is launched as this grid's
+// programmatic dependent and waits for it before it reads the statistics.
+constexpr int kRowdotT = 32, kRowdotH = 8;
 __device__ __forceinline__ float dot2_bf16(uint32_t a, uint32_t d, float acc) {
   acc = fmaf(__uint_as_float(a << 16), __uint_as_float(d << 16), acc);
   return fmaf(__uint_as_float(a & 0xFFFF0000u), __uint_as_float(d & 0xFFFF0000u), acc);
@@ -460,29 +478,30 @@ __device__ __forceinline__ float dot8_bf16(uint4 a, uint4 d) {
 // Lanes of a half-warp hold D / 16 dimensions each (8 for D = 128: one
 // 16-byte load; 4 for D = 64: the first half of it).
 template <int D>
-__global__ void rowdot_kernel(const uint16_t* o, const uint16_t* dout, const float* lse,
-                              float* nlse2, float* nrowdot, int B, int L, int n_q, int Lp) {
+__global__ void __launch_bounds__(256)
+rowdot_kernel(const uint16_t* o, const uint16_t* dout, const float* lse, float* nlse2,
+              float* nrowdot, int L, int n_q, int Lp) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int64_t total = static_cast<int64_t>(B) * n_q * Lp;
-  const int64_t warps = (total + kRowdotRowsPerWarp - 1) / kRowdotRowsPerWarp;
-  const int64_t wstride = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
-  const int half = (threadIdx.x >> 4) & 1, l16 = threadIdx.x & 15;
-  for (int64_t warp_id = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
-       warp_id < warps; warp_id += wstride) {
-  uint4 a[kRowdotRowsPerWarp / 2], d[kRowdotRowsPerWarp / 2];
-  bool live[kRowdotRowsPerWarp / 2];
+  __shared__ float dots[kRowdotH][kRowdotT + 1];
+  constexpr int kAhead = 4, kHalves = 16;               // half-warps of a block
+  const int t_blocks = Lp / kRowdotT, h_blocks = (n_q + kRowdotH - 1) / kRowdotH;
+  const int rest = blockIdx.x / t_blocks;
+  const int t0 = (blockIdx.x - rest * t_blocks) * kRowdotT, h0 = rest % h_blocks * kRowdotH;
+  const int heads = min(kRowdotH, n_q - h0);
+  const size_t b = rest / h_blocks;
+  // row of the block's [position][head] order -> position
+  auto position = [&](int row) { return heads == kRowdotH ? row / kRowdotH : row / heads; };
+  const int half = threadIdx.x >> 4, l16 = threadIdx.x & 15;
+  const int rows = heads * min(kRowdotT, L - t0);       // (may be none: then below zero)
+  for (int r0 = half; r0 < heads * kRowdotT; r0 += kAhead * kHalves) {
+    uint4 a[kAhead], d[kAhead];
 #pragma unroll
-  for (int k = 0; k < kRowdotRowsPerWarp / 2; ++k) {
-    const int64_t row = warp_id * kRowdotRowsPerWarp + 2 * k + half;
-    live[k] = false;
-    a[k] = d[k] = make_uint4(0u, 0u, 0u, 0u);
-    if (row < total) {
-      const int t = static_cast<int>(row % Lp);
-      const int64_t bh = row / Lp;
-      if (t < L) {
-        const int h = static_cast<int>(bh % n_q);
-        const int b = static_cast<int>(bh / n_q);
-        const size_t off = ((static_cast<size_t>(b) * L + t) * n_q + h) * D + (D / 16) * l16;
+    for (int k = 0; k < kAhead; ++k) {
+      const int row = r0 + k * kHalves;                 // position major
+      const int t = position(row), h = row - t * heads;
+      a[k] = d[k] = make_uint4(0u, 0u, 0u, 0u);
+      if (row < rows) {
+        const size_t off = ((b * L + t0 + t) * n_q + h0 + h) * D + (D / 16) * l16;
         if (D == 128) {
           a[k] = *reinterpret_cast<const uint4*>(o + off);
           d[k] = *reinterpret_cast<const uint4*>(dout + off);
@@ -492,24 +511,27 @@ __global__ void rowdot_kernel(const uint16_t* o, const uint16_t* dout, const flo
           a[k] = make_uint4(a2.x, a2.y, 0u, 0u);
           d[k] = make_uint4(d2.x, d2.y, 0u, 0u);
         }
-        live[k] = true;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int row = r0 + k * kHalves;
+      float dd = (D == 128) ? dot8_bf16(a[k], d[k])
+                            : dot2_bf16(a[k].y, d[k].y, dot2_bf16(a[k].x, d[k].x, 0.0f));
+#pragma unroll
+      for (int off = 8; off > 0; off >>= 1) dd += __shfl_xor_sync(0xffffffffu, dd, off);
+      if (l16 == 0 && row < heads * kRowdotT) {
+        const int t = position(row);
+        dots[row - t * heads][t] = row < rows ? dd : 0.0f;
       }
     }
   }
-#pragma unroll
-  for (int k = 0; k < kRowdotRowsPerWarp / 2; ++k) {
-    float dd = 0.0f;
-    if (live[k]) dd = (D == 128) ? dot8_bf16(a[k], d[k])
-                                 : dot2_bf16(a[k].y, d[k].y, dot2_bf16(a[k].x, d[k].x, 0.0f));
-#pragma unroll
-    for (int off = 8; off > 0; off >>= 1) dd += __shfl_xor_sync(0xffffffffu, dd, off);
-    const int64_t row = warp_id * kRowdotRowsPerWarp + 2 * k + half;
-    if (l16 == 0 && row < total) {
-      const int t = static_cast<int>(row % Lp);
-      nrowdot[row] = -dd;
-      nlse2[row] = (t < L) ? -lse[(row / Lp) * L + t] * kLog2e : -INFINITY;
-    }
-  }
+  __syncthreads();
+  const int h = threadIdx.x / kRowdotT, t = threadIdx.x % kRowdotT;
+  if (h < heads) {
+    const size_t head = b * n_q + h0 + h;
+    nrowdot[head * Lp + t0 + t] = -dots[h][t];
+    nlse2[head * Lp + t0 + t] = t0 + t < L ? -lse[head * L + t0 + t] * kLog2e : -INFINITY;
   }
 }
 
@@ -713,9 +735,9 @@ dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
 #pragma unroll 1
       for (int q = cw * kPer; q < (cw + 1) * kPer; ++q) {
         const int col = (q % kHalfOut) * 32;
-        if (kWin && j < p.heavy && p.pieces > 1) {
+        if (kWin && work.pieces > 1) {
           // (rows past L are zeros: their keys are, and no row sees them)
-          const size_t part = (static_cast<size_t>(grp) * p.heavy + j) * p.pieces + work.piece;
+          const size_t part = first_part(p, work.groups, grp, j) + work.piece;
           float* dst = p.parts + ((2 * part + (q < kHalfOut ? 0 : 1)) * kT + r) * D + col;
           store_chunk_f32(lane_base + (q < kHalfOut ? cDV : cDK) + col, dst, 1.0f);
           continue;
@@ -728,11 +750,12 @@ dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
   teardown(sy, p, false);
 }
 
-// The parts of the key tiles that hold a sink, added in order of the pieces:
-// a thread per four columns of one row of dV or dK.
+// The parts of key tiles that several CTAs took, added in order of the pieces: a thread
+// per four columns of one row of dV or dK. Tiles j0 .. j0 + tiles - 1 of each group,
+// `pieces` each.
 template <int D>
 __global__ void __launch_bounds__(256)
-join_kernel(const BwdParams p, long long items) {
+join_kernel(const BwdParams p, int groups, int j0, int tiles, int pieces, long long items) {
   // (the grid before this one ends only once dK/dV has)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -744,14 +767,14 @@ join_kernel(const BwdParams p, long long items) {
   const long long rest = item / (kQuads * kT);         // (tile, dV or dK)
   const int which = static_cast<int>(rest & 1);
   const long long tile = rest >> 1;
-  const int j = static_cast<int>(tile % p.heavy);
-  const long long grp = tile / p.heavy;
+  const int j = j0 + static_cast<int>(tile % tiles);
+  const long long grp = tile / tiles;
   const int row = j * kT + r;
   if (row >= p.L) return;
-  const float* src = p.parts + ((2 * tile * p.pieces + which) * kT + r) * D + col;
+  const float* src = p.parts + ((2 * first_part(p, groups, grp, j) + which) * kT + r) * D + col;
   float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
-  for (int k = 0; k < p.pieces; ++k) {
+  for (int k = 0; k < pieces; ++k) {
     const float4 v = *reinterpret_cast<const float4*>(src + static_cast<size_t>(k) * 2 * kT * D);
     sum.x += v.x;
     sum.y += v.y;
@@ -830,21 +853,10 @@ dq_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
         if (u >= units) continue;
         const DqUnit x = dq_unit<kWin>(u, p);
         const int kvh = x.h / p.g;
-        // The first ring's worth of this unit's K/V tiles goes out while the
-        // previous unit still runs; dO_i's buffer is free only once every
-        // product of the previous unit is done.
-        const int pre = x.n < kStages ? x.n : kStages;
+        // The unit's first K/V tile, then dO_i, whose buffer is free once the last product
+        // with the dO of the unit before is done (its dQ products may still run), then
+        // the other tiles.
         for (int t = 0; t < x.n; ++t, ++it) {
-          if (t == pre) {
-            if (uc > 0 && !wait_bounded(smem_addr(&sy.done), (uc - 1) & 1, sy, p)) {
-              ok = false;
-              break;
-            }
-            mbar_arrive_expect_tx(fb, kTileBytes);
-            for (int c = 0; c < D / 64; ++c)
-              tma_load_4d(sdO + c * kT * 128, &tmdO, fb, c * 64, x.h, x.i * kT, x.b);
-            ++uc;
-          }
           const int st = it % kStages, use = it / kStages;
           if (use > 0 && !wait_bounded(smem_addr(&sy.empty[st]), (use - 1) & 1, sy, p)) {
             ok = false;
@@ -857,14 +869,17 @@ dq_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
             tma_load_4d(dst + c * kT * 128, &tmK, bar, c * 64, kvh, key0, x.b);
             tma_load_4d(dst + kTileBytes + c * kT * 128, &tmV, bar, c * 64, kvh, key0, x.b);
           }
-        }
-        if (ok && pre == x.n) {
-          // every tile fitted in the ring ahead of dO
-          if (uc > 0 && !wait_bounded(smem_addr(&sy.done), (uc - 1) & 1, sy, p)) break;
-          mbar_arrive_expect_tx(fb, kTileBytes);
-          for (int c = 0; c < D / 64; ++c)
-            tma_load_4d(sdO + c * kT * 128, &tmdO, fb, c * 64, x.h, x.i * kT, x.b);
-          ++uc;
+          if (t == 0) {
+            if (uc > 0 && !wait_bounded(smem_addr(&sy.do_free), (uc - 1) & 1, sy, p)) {
+              ok = false;
+              ++it;
+              break;
+            }
+            mbar_arrive_expect_tx(fb, kTileBytes);
+            for (int c = 0; c < D / 64; ++c)
+              tma_load_4d(sdO + c * kT * 128, &tmdO, fb, c * 64, x.h, x.i * kT, x.b);
+            ++uc;
+          }
         }
       }
       if (uc > 0) wait_drain(fb, (uc - 1) & 1);
@@ -896,6 +911,7 @@ dq_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
       if (leader) mma_commit(smem_addr(&sy.s_full[0]));
       mma_scores_full_ss<D>(leader, tmem + cP, sdO, stage_of(0) + kTileBytes);  // dP = dO V^T
       if (leader) mma_commit(smem_addr(&sy.dp_full));
+      if (leader && n == 1) mma_commit(smem_addr(&sy.do_free));
       for (int t = 0; t < n; ++t) {
         const bool more = t + 1 < n;
         // S(t) read out: the next tile's scores may overwrite it
@@ -910,6 +926,7 @@ dq_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
         if (more) {
           mma_scores_full_ss<D>(leader, tmem + cP, sdO, stage_of(t + 1) + kTileBytes);
           if (leader) mma_commit(smem_addr(&sy.dp_full));
+          if (leader && t + 2 == n) mma_commit(smem_addr(&sy.do_free));
         }
         if (!wait_all(sy.ds_full, gt + t)) { ok = false; break; }
         mma_accum_dq<D>(leader, tmem + cDQ, tmem + cDS, stage_of(t), t > 0);      // dQ += dS K
@@ -932,23 +949,41 @@ dq_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
     const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint64_t c2 = f32x2_pack(p.c, p.c);
     const int k0 = cw * kColsQ;                        // first key column (in the tile)
-    int gt = 0, uc = 0;
+    int gt = 0, uc = 0, rr = 0;
     bool ok = true;
-    for (int rr = 0; rr * G < units && ok; ++rr) {
-      const int u = dq_snake(rr);
-      if (u >= units) continue;
-      const DqUnit x = dq_unit<kWin>(u, p);
-      const int i = x.i, n = x.n;
-      const int row = i * kT + r;
+    // the CTA's next unit, if there is one
+    auto next_unit = [&](DqUnit& x) {
+      for (; rr * G < units; ++rr) {
+        const int u = dq_snake(rr);
+        if (u < units) {
+          ++rr;
+          x = dq_unit<kWin>(u, p);
+          return true;
+        }
+      }
+      return false;
+    };
+    // Q_i becomes the A operand of S in TMEM (64 channels per warpgroup); the last scores
+    // with the Q there have been read by the time this is called
+    float nl = 0.0f, nd = 0.0f;
+    auto bring_q = [&](const DqUnit& x) {
+      const int row = x.i * kT + r;
       const size_t qoff = ((static_cast<size_t>(x.b) * p.L + row) * p.n_q + x.h) * D;
-      // Q_i becomes the A operand of S in TMEM (first warpgroup); the previous
-      // unit's products are all done (its epilogue waited for them)
-      if (cw == 0) row_to_tmem<D>(lane_base + cQ, q_rows + qoff, row < p.L);
+      if (64 * cw < D) row_to_tmem<64>(lane_base + cQ + 32 * cw, q_rows + qoff + 64 * cw, row < p.L);
+      const size_t srow = (static_cast<size_t>(x.b) * p.n_q + x.h) * (p.T * kT) + row;
+      nl = p.nlse2[srow];
+      nd = p.nrowdot[srow];
       tmem_wait_st();
       tc_fence_before_sync();
       mbar_arrive(smem_addr(&sy.a_ready));
-      const size_t srow = (static_cast<size_t>(x.b) * p.n_q + x.h) * (p.T * kT) + row;
-      const float nl = p.nlse2[srow], nd = p.nrowdot[srow];
+    };
+    DqUnit x, y;
+    bool more = next_unit(x);
+    if (more) bring_q(x);
+    while (more) {
+      const int i = x.i, n = x.n;
+      const int row = i * kT + r;
+      const size_t qoff = ((static_cast<size_t>(x.b) * p.L + row) * p.n_q + x.h) * D;
       const uint64_t nl2 = f32x2_pack(nl, nl), nd2 = f32x2_pack(nd, nd);
       for (int t = 0; t < n; ++t) {
         // phase 1: P from S, kept in registers
@@ -1007,7 +1042,12 @@ dq_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
         tc_fence_before_sync();
         mbar_arrive(smem_addr(&sy.ds_full));
       }
-      if (!ok || !__all_sync(0xffffffffu, wait_bounded(smem_addr(&sy.done), uc & 1, sy, p))) break;
+      if (!ok) break;
+      // the next unit's Q goes in while this one's last product runs, so that its first
+      // scores do while this one's dQ is stored
+      more = next_unit(y);
+      if (more) bring_q(y);
+      if (!__all_sync(0xffffffffu, wait_bounded(smem_addr(&sy.done), uc & 1, sy, p))) break;
       tc_fence_after_sync();
       constexpr int kPer = (D / 32) / kComputeWGs;    // chunks of 32 dQ columns per warpgroup
 #pragma unroll 1
@@ -1015,6 +1055,7 @@ dq_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
         store_chunk(lane_base + cDQ + 32 * q, p.dq + qoff + 32 * q, p.scale, row < p.L);
       gt += n;
       ++uc;
+      x = y;
     }
   }
   teardown(sy, p, false);
@@ -1123,7 +1164,9 @@ cudaError_t launch_dq(unsigned grid, cudaStream_t stream, const CUtensorMap& mk,
 // The join is dQ's programmatic dependent: it waits until that grid, and with it
 // dK/dV, has ended.
 template <int D>
-cudaError_t launch_join(cudaStream_t stream, const BwdParams& p, long long items) {
+cudaError_t launch_join(cudaStream_t stream, const BwdParams& p, int groups, int j0, int tiles,
+                        int pieces) {
+  const long long items = static_cast<long long>(groups) * tiles * 2 * kT * (D / 4);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>((items + 255) / 256));
   cfg.blockDim = dim3(256);
@@ -1133,7 +1176,7 @@ cudaError_t launch_join(cudaStream_t stream, const BwdParams& p, long long items
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_kernel<D>, p, items);
+  return cudaLaunchKernelEx(&cfg, join_kernel<D>, p, groups, j0, tiles, pieces, items);
 }
 
 bool encode_tile_map(CUtensorMap* map, const void* ptr, int D, int H, int64_t L, int64_t B) {
@@ -1162,33 +1205,49 @@ int64_t row_bytes(int64_t B, int64_t L, int32_t n_q) {
   return 2 * B * n_q * ((L + kT - 1) / kT) * kT * 4;
 }
 
-// How the key tiles that hold a sink are cut. Such a tile meets every later query
+// Into how many CTAs key tiles are cut. Those that hold a sink meet every later query
 // tile, up to T * g steps where the others take about W / 128 * g: left whole, the
 // few of them would run on long after the rest. A piece is at least as long as
 // another tile's CTA, and all pieces together are about two per SM, which also
-// bounds the parts' memory (128 KiB each at d_h = 128). A rule on the shape alone,
-// not on the device, so that the workspace's size is.
-struct SinkSplit {
-  int64_t heavy, pieces, bytes;
+// bounds the parts' memory (128 KiB each at d_h = 128). The other tiles are cut where
+// that fills SMs that would be idle: a CTA costs about nine steps beside its own, so of
+// 1, 2, 3 ... pieces the number with the shortest rounds is taken (1000 rows of 8
+// heads on 2 behind 256: 16 CTAs of 12 steps 22 us, 64 of 3 and the join 14). A
+// rule on the shape alone, not on the device, so that the workspace's size is.
+struct KeySplit {
+  int64_t heavy, pieces, others, bytes;
 };
-SinkSplit sink_split(int64_t B, int64_t L, int32_t n_q, int32_t n_kv, int32_t d_h, int64_t window,
-                     int64_t sinks) {
-  const int64_t T = (L + kT - 1) / kT, g = n_q / n_kv;
+KeySplit key_split(int64_t B, int64_t L, int32_t n_q, int32_t n_kv, int32_t d_h, int64_t window,
+                   int64_t sinks) {
+  constexpr int64_t kSms = 152, kCtaSteps = 9, kJoinSteps = 4;
+  const int64_t T = (L + kT - 1) / kT, g = n_q / n_kv, groups = B * n_kv;
   window = window < L ? window : L;
   sinks = sinks < L ? sinks : L;
-  SinkSplit s;
-  s.heavy = window < L ? (sinks + kT - 1) / kT : 0;
-  s.pieces = 1;
-  s.bytes = 0;
-  if (s.heavy == 0) return s;
-  const int64_t others = g * ((window + kT - 2) / kT + 1);
-  const int64_t most = g * T / (others > 8 ? others : 8);
-  const int64_t fill = 2 * 152 / (B * n_kv * s.heavy);
-  s.pieces = most < fill ? most : fill;
-  const int64_t least = g * (T - s.heavy + 1);          // steps of the shortest such tile
-  if (s.pieces > least) s.pieces = least;
-  if (s.pieces < 1) s.pieces = 1;
-  if (s.pieces > 1) s.bytes = B * n_kv * s.heavy * s.pieces * 2 * kT * d_h * 4;
+  KeySplit s{window < L ? (sinks + kT - 1) / kT : 0, 1, 1, 0};
+  const int64_t reach = (window + kT - 2) / kT + 1, steps = g * (reach < T ? reach : T);
+  if (s.heavy > 0) {
+    const int64_t most = g * T / (steps > 8 ? steps : 8);
+    const int64_t fill = 2 * kSms / (groups * s.heavy);
+    s.pieces = most < fill ? most : fill;
+    const int64_t least = g * (T - s.heavy + 1);          // steps of the shortest such tile
+    if (s.pieces > least) s.pieces = least;
+    if (s.pieces < 1) s.pieces = 1;
+  }
+  const int64_t ctas = groups * (T - s.heavy);
+  if (ctas > 0 && ctas < kSms && window < L) {
+    int64_t best = 0;
+    for (int64_t n = 1; n <= g && n * ctas <= 2 * kSms; ++n) {   // (a tile has g steps at least)
+      const int64_t rounds = (n * ctas + kSms - 1) / kSms;
+      const int64_t cost = rounds * ((steps + n - 1) / n + kCtaSteps) + (n > 1 ? kJoinSteps : 0);
+      if (n == 1 || cost < best) {
+        best = cost;
+        s.others = n;
+      }
+    }
+  }
+  const int64_t parts = (s.pieces > 1 ? groups * s.heavy * s.pieces : 0) +
+                        (s.others > 1 ? ctas * s.others : 0);
+  s.bytes = parts * 2 * kT * d_h * 4;
   return s;
 }
 
@@ -1198,16 +1257,19 @@ attn_status_t launch_all(cudaStream_t stream, unsigned row_blocks, unsigned kv_c
                          const float* lse, const uint16_t* q, float* nlse2, float* nrowdot, int B,
                          const CUtensorMap& mq, const CUtensorMap& mdo, const CUtensorMap& mk,
                          const CUtensorMap& mv, const BwdParams& p) {
-  rowdot_kernel<D><<<row_blocks, 256, 0, stream>>>(o, dout, lse, nlse2, nrowdot, B, p.L, p.n_q,
+  rowdot_kernel<D><<<row_blocks, 256, 0, stream>>>(o, dout, lse, nlse2, nrowdot, p.L, p.n_q,
                                                    p.T * kT);
   if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
   if (launch_dkdv<D, kWin>(kv_ctas, stream, mq, mdo, mk, mv, p) != cudaSuccess)
     return ATTN_ERR_CUDA;
   if (launch_dq<D, kWin>(dq_grid, stream, mk, mv, mdo, q, p) != cudaSuccess) return ATTN_ERR_CUDA;
-  if (kWin && p.pieces > 1) {
-    const long long items = static_cast<long long>(B) * p.n_kv * p.heavy * 2 * kT * (D / 4);
-    if (launch_join<D>(stream, p, items) != cudaSuccess) return ATTN_ERR_CUDA;
-  }
+  const int groups = B * p.n_kv;
+  if (kWin && p.pieces > 1 &&
+      launch_join<D>(stream, p, groups, 0, p.heavy, p.pieces) != cudaSuccess)
+    return ATTN_ERR_CUDA;
+  if (kWin && p.others > 1 &&
+      launch_join<D>(stream, p, groups, p.heavy, p.T - p.heavy, p.others) != cudaSuccess)
+    return ATTN_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
@@ -1232,7 +1294,8 @@ attn_status_t backward(const void* q, const void* k, const void* v, const void* 
   const int64_t T = (L + kT - 1) / kT;
   if (!sizes_fit(B, L, n_q, n_kv)) return ATTN_ERR_UNSUPPORTED;
   const bool win = window > 0;
-  const SinkSplit split = win ? sink_split(B, L, n_q, n_kv, d_h, window, sinks) : SinkSplit{0, 1, 0};
+  const KeySplit split =
+      win ? key_split(B, L, n_q, n_kv, d_h, window, sinks) : KeySplit{0, 1, 1, 0};
   if (workspace_bytes < row_bytes(B, L, n_q) + split.bytes) return ATTN_ERR_INVALID_ARG;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
   int* status = nullptr;
@@ -1265,21 +1328,20 @@ attn_status_t backward(const void* q, const void* k, const void* v, const void* 
   p.sinks = static_cast<int>(sinks < L ? sinks : L);
   p.heavy = static_cast<int>(split.heavy);
   p.pieces = static_cast<int>(split.pieces);
+  p.others = static_cast<int>(split.others);
   p.parts = nrowdot + B * n_q * T * kT;
 
-  const int64_t rows = B * n_q * T * kT;
-  constexpr int kRowdotRowsPerBlock = 8 * kRowdotRowsPerWarp;   // 256 threads
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
     sms = 1;
-  const int64_t need_blocks = (rows + kRowdotRowsPerBlock - 1) / kRowdotRowsPerBlock;
-  const unsigned row_blocks = static_cast<unsigned>(need_blocks < 8 * sms ? need_blocks : 8 * sms);
+  const unsigned row_blocks =
+      static_cast<unsigned>(B * ((n_q + kRowdotH - 1) / kRowdotH) * (T * kT / kRowdotT));
   const uint16_t* oh = static_cast<const uint16_t*>(o);
   const uint16_t* qh = static_cast<const uint16_t*>(q);
   const uint16_t* doh = static_cast<const uint16_t*>(dout);
   const unsigned kv_ctas =
-      static_cast<unsigned>(B * n_kv * (T - split.heavy + split.heavy * split.pieces));
+      static_cast<unsigned>(B * n_kv * ((T - split.heavy) * split.others + split.heavy * split.pieces));
   const unsigned dq_grid = static_cast<unsigned>(B * n_q * T < sms ? B * n_q * T : sms);
   const int batch = static_cast<int>(B);
   if (d_h == 128)
@@ -1317,7 +1379,7 @@ int64_t attn_prefill_window_bwd_workspace_bytes(int64_t B, int64_t L, int32_t n_
   if (B < 1 || L < 1 || n_q < 1 || n_kv < 1 || n_q % n_kv != 0 || (d_h != 64 && d_h != 128) ||
       window < 1 || sinks < 0 || !sizes_fit(B, L, n_q, n_kv))
     return -1;
-  return row_bytes(B, L, n_q) + sink_split(B, L, n_q, n_kv, d_h, window, sinks).bytes;
+  return row_bytes(B, L, n_q) + key_split(B, L, n_q, n_kv, d_h, window, sinks).bytes;
 }
 
 attn_status_t attn_prefill_window_bwd(const void* q, const void* k, const void* v, const void* o,
