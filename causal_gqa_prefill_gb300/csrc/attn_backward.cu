@@ -458,7 +458,7 @@ __device__ __forceinline__ void p_from_s(uint32_t taddr, uint64_t c2, uint64_t n
 // three divisions each, took 41 us where 134 MB take 20.) Positions past L get -inf
 // and 0 without touching O or dO. The dK/dV kernel is launched as this grid's
 // programmatic dependent and waits for it before it reads the statistics.
-constexpr int kRowdotT = 32, kRowdotH = 8;
+constexpr int kRowdotT = 8, kRowdotH = 8;
 __device__ __forceinline__ float dot2_bf16(uint32_t a, uint32_t d, float acc) {
   acc = fmaf(__uint_as_float(a << 16), __uint_as_float(d << 16), acc);
   return fmaf(__uint_as_float(a & 0xFFFF0000u), __uint_as_float(d & 0xFFFF0000u), acc);
