@@ -380,6 +380,11 @@ __device__ __forceinline__ void store_chunk_f32(uint32_t taddr, float* dst, floa
                         __uint_as_float(v[4 * q + 2]) * mul, __uint_as_float(v[4 * q + 3]) * mul);
 }
 
+// A word whose lowest n bits are set (none for n <= 0, all from 32 on).
+__device__ __forceinline__ uint32_t low_bits(int n) {
+  return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u;
+}
+
 // dK/dV phase 1 for one warpgroup: P^T = 2^(c S^T + nl) for its kColsQ query
 // columns of this thread's key row (S^T read from TMEM at `taddr`, the row
 // statistics nl from shared memory), kept in `pr` and written back as bf16
@@ -394,6 +399,10 @@ __device__ __forceinline__ void pt_from_st(uint32_t taddr, const float4* nl4, ui
     uint32_t sv[32];
     tmem_ld32(taddr + 32 * cc, sv);
     tmem_wait_ld(sv);
+    // (behind a window the seen queries as bits, which cost a select each; compared with
+    // both ends one by one the 8192-token layer's kernel took 245 us where it takes 240)
+    uint32_t seen = 0;
+    if (kWin) seen = low_bits(q_to_end + 1 - 32 * cc) & ~low_bits(-q_minus_r - 32 * cc);
     uint32_t pk[16];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -407,8 +416,8 @@ __device__ __forceinline__ void pt_from_st(uint32_t taddr, const float4* nl4, ui
         f32x2_unpack(x, x0, x1);
         float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
         if (kMask) {
-          if (q_minus_r + 32 * cc + jj < 0 || (kWin && 32 * cc + jj > q_to_end)) p0 = 0.0f;
-          if (q_minus_r + 32 * cc + jj + 1 < 0 || (kWin && 32 * cc + jj + 1 > q_to_end)) p1 = 0.0f;
+          if (kWin ? !(seen >> jj & 1u) : q_minus_r + 32 * cc + jj < 0) p0 = 0.0f;
+          if (kWin ? !(seen >> (jj + 1) & 1u) : q_minus_r + 32 * cc + jj + 1 < 0) p1 = 0.0f;
         }
         pr[32 * cc + jj] = p0;
         pr[32 * cc + jj + 1] = p1;
@@ -431,6 +440,11 @@ __device__ __forceinline__ void p_from_s(uint32_t taddr, uint64_t c2, uint64_t n
     uint32_t sv[32];
     tmem_ld32(taddr + 32 * c, sv);
     tmem_wait_ld(sv);
+    uint32_t seen = 0;
+    if (kWin) {
+      const int at = k0 + 32 * c;
+      seen = low_bits(keep + 1 - at) & (~low_bits(out + 1 - at) | low_bits(sink - at));
+    }
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
       const uint64_t x = ffma2(
@@ -440,8 +454,8 @@ __device__ __forceinline__ void p_from_s(uint32_t taddr, uint64_t c2, uint64_t n
       float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
       if (kMask) {
         const int at = k0 + 32 * c + 2 * e;
-        if (at > keep || (kWin && at <= out && at >= sink)) p0 = 0.0f;
-        if (at + 1 > keep || (kWin && at + 1 <= out && at + 1 >= sink)) p1 = 0.0f;
+        if (kWin ? !(seen >> (2 * e) & 1u) : at > keep) p0 = 0.0f;
+        if (kWin ? !(seen >> (2 * e + 1) & 1u) : at + 1 > keep) p1 = 0.0f;
       }
       pr[32 * c + 2 * e] = p0;
       pr[32 * c + 2 * e + 1] = p1;
@@ -455,7 +469,8 @@ __device__ __forceinline__ void p_from_s(uint32_t taddr, uint64_t c2, uint64_t n
 // up to kRowdotH neighbouring heads, so that it reads O and dO in their own order,
 // four rows (eight loads) under way per half-warp, and writes whole pieces of the
 // [b, h, t] statistics out of shared memory. (One row (b, h, t) after another, with
-// three divisions each, took 41 us where 134 MB take 20.) Positions past L get -inf
+// three divisions each, took 41 us for 134 MB, this 25; 32 positions a block took 8 us
+// for 1000 rows of 8 heads, this 5.) Positions past L get -inf
 // and 0 without touching O or dO. The dK/dV kernel is launched as this grid's
 // programmatic dependent and waits for it before it reads the statistics.
 constexpr int kRowdotT = 8, kRowdotH = 8;
@@ -1212,7 +1227,7 @@ int64_t row_bytes(int64_t B, int64_t L, int32_t n_q) {
 // bounds the parts' memory (128 KiB each at d_h = 128). The other tiles are cut where
 // that fills SMs that would be idle: a CTA costs about nine steps beside its own, so of
 // 1, 2, 3 ... pieces the number with the shortest rounds is taken (1000 rows of 8
-// heads on 2 behind 256: 16 CTAs of 12 steps 22 us, 64 of 3 and the join 14). A
+// heads on 2 behind 256: 16 CTAs of 12 steps 22 us, 64 of 3 and the join 15). A
 // rule on the shape alone, not on the device, so that the workspace's size is.
 struct KeySplit {
   int64_t heavy, pieces, others, bytes;
