@@ -170,12 +170,14 @@ __device__ __forceinline__ KeyWork key_work(const BwdParams& p) {
 }
 
 constexpr int kStages = 3;               // dQ: ring of streamed K/V tiles
-constexpr int kStagesKV = 2;             // dK/dV: ring of streamed Q/dO tiles (V_j is resident)
+constexpr int kStagesQ = 3, kStagesDO = 2;   // dK/dV: rings of streamed Q and dO tiles (K_j, V_j stay)
 
 struct Sync {
   uint64_t a_ready;                 // the CTA's fixed A operands are in TMEM
   uint64_t fixed_full;              // dK/dV: V_j has landed in shared memory
-  uint64_t full[kStages], empty[kStages];
+  uint64_t full[kStages], empty[kStages];  // dQ: K/V tiles; dK/dV: Q tiles
+  uint64_t do_full[kStagesDO], do_empty[kStagesDO];   // dK/dV: dO tiles
+  uint64_t row_full[2];             // dK/dV: row statistics of a step
   uint64_t s_full[2], p_full[2];    // scores ready (commit) / P or dS ready (compute threads)
   uint64_t dp_full, ds_full;        // dP (dP^T) ready (commit) / dS (dS^T) ready (compute threads)
   uint64_t dp_free, dq_done;        // dQ: dP read out (compute threads) / dQ += dS K done (commit)
@@ -315,6 +317,11 @@ __device__ __forceinline__ void setup(Sync& sy) {
       mbar_init(smem_addr(&sy.full[s]), 1);
       mbar_init(smem_addr(&sy.empty[s]), 1);
     }
+    for (int s = 0; s < kStagesDO; ++s) {
+      mbar_init(smem_addr(&sy.do_full[s]), 1);
+      mbar_init(smem_addr(&sy.do_empty[s]), 1);
+    }
+    for (int s = 0; s < 2; ++s) mbar_init(smem_addr(&sy.row_full[s]), 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(smem_addr(&sy.s_full[s]), 1);
       mbar_init(smem_addr(&sy.p_full[s]), kComputeThreads);
@@ -555,11 +562,21 @@ rowdot_kernel(const uint16_t* o, const uint16_t* dout, const float* lse, float* 
 // Producer side shared by both tile kernels: drains the ring so that no copy is
 // still in flight when the CTA exits; `issued` tiles were put in flight.
 template <int S>
-__device__ __forceinline__ void drain_ring(Sync& sy, int issued) {
+__device__ __forceinline__ void drain_ring(uint64_t* full, int issued) {
   for (int s = 0; s < S && s < issued; ++s) {
     const int last = s + ((issued - 1 - s) / S) * S;
-    wait_drain(smem_addr(&sy.full[s]), (last / S) & 1);
+    wait_drain(smem_addr(&full[s]), (last / S) & 1);
   }
+}
+
+// The kernel's dynamic shared memory: its tiles, statistics and barriers, and what may be
+// lost to alignment as far as an SM's 227 KiB go.
+template <int D>
+__host__ __device__ constexpr int dkdv_smem() {
+  constexpr int need = (2 + kStagesQ + kStagesDO) * tile_bytes<D>() + 2 * 1024 + sizeof(Sync);
+  constexpr int most = 227 * 1024;
+  static_assert(need <= most, "dK/dV's tiles do not fit");
+  return need + 1024 < most ? need + 1024 : most;
 }
 
 template <int D, bool kWin>
@@ -568,12 +585,17 @@ dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
             const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
             const BwdParams p) {
   extern __shared__ uint8_t dyn_smem[];
-  __shared__ Sync sy;
-  // smem: K_j | V_j | kStagesKV x [Q_i | dO_i | -LSE*log2 e [128] | -D [128]]
+  // smem: K_j | V_j | kStagesQ x Q_i | kStagesDO x dO_i | 2 x [-LSE*log2 e [128] | -D [128]] | Sync
   constexpr int kTileBytes = tile_bytes<D>();
   const uint32_t base = (smem_addr(dyn_smem) + 1023u) & ~1023u;
-  const uint32_t sK = base, sV = base + kTileBytes, sRing = base + 2 * kTileBytes;
-  constexpr uint32_t kStage = 2 * kTileBytes + 1024;
+  const uint32_t sK = base, sV = base + kTileBytes, sQ0 = base + 2 * kTileBytes;
+  const uint32_t sDO0 = sQ0 + kStagesQ * kTileBytes, sRow0 = sDO0 + kStagesDO * kTileBytes;
+  Sync& sy = *reinterpret_cast<Sync*>(dyn_smem + (sRow0 + 2 * 1024 - smem_addr(dyn_smem)));
+  if (sRow0 + 2 * 1024 + sizeof(Sync) > smem_addr(dyn_smem) + dkdv_smem<D>()) {
+    // (at d_h = 128 all of an SM's memory, which holds if it begins on a 1 KiB boundary)
+    if (threadIdx.x == 0) atomicOr(p.status, 1);
+    return;
+  }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const KeyWork work = key_work<kWin>(p);
   const int j = work.j, grp = work.grp;                // key tile, (sequence, K/V head)
@@ -603,64 +625,84 @@ dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
         tma_load_4d(sK + c * kT * 128, &tmK, fb, c * 64, kvh, j * kT, b);
         tma_load_4d(sV + c * kT * 128, &tmV, fb, c * 64, kvh, j * kT, b);
       }
-      int t = 0;
-      for (; t < nsteps; ++t) {
-        const int st = t % kStagesKV, use = t / kStagesKV;
-        if (use > 0 && !wait_bounded(smem_addr(&sy.empty[st]), (use - 1) & 1, sy, p)) break;
+      // Rings of their own for Q, dO and the row statistics: S^T needs Q first and dK
+      // last, dO is free once dV has it. (8192 tokens, 32 heads on 8, window 1024 and 4
+      // sinks: one ring of two stages for all of it 240 us, with the tensor cores
+      // waiting 340 of a step's 2600 cycles for Q; two stages of each 226; this 220.)
+      int nq = 0, ndo = 0, nrow = 0;                     // copies in flight so far
+      for (int t = 0; t < nsteps; ++t) {
         const int h = kvh * p.g + (work.first + t) / work.per_head;
         const int i = i0 + (work.first + t) % work.per_head;
-        const uint32_t dst = sRing + st * kStage, bar = smem_addr(&sy.full[st]);
-        mbar_arrive_expect_tx(bar, 2 * kTileBytes + 1024);
-        for (int c = 0; c < D / 64; ++c) {
-          tma_load_4d(dst + c * kT * 128, &tmQ, bar, c * 64, h, i * kT, b);
-          tma_load_4d(dst + kTileBytes + c * kT * 128, &tmdO, bar, c * 64, h, i * kT, b);
-        }
+        const int sq = t % kStagesQ, sd = t % kStagesDO;
+        if (t >= kStagesQ &&
+            !wait_bounded(smem_addr(&sy.empty[sq]), (t / kStagesQ - 1) & 1, sy, p))
+          break;
+        const uint32_t qbar = smem_addr(&sy.full[sq]);
+        mbar_arrive_expect_tx(qbar, kTileBytes);
+        for (int c = 0; c < D / 64; ++c)
+          tma_load_4d(sQ0 + sq * kTileBytes + c * kT * 128, &tmQ, qbar, c * 64, h, i * kT, b);
+        ++nq;
+        if (t >= kStagesDO &&
+            !wait_bounded(smem_addr(&sy.do_empty[sd]), (t / kStagesDO - 1) & 1, sy, p))
+          break;
+        const uint32_t dbar = smem_addr(&sy.do_full[sd]);
+        mbar_arrive_expect_tx(dbar, kTileBytes);
+        for (int c = 0; c < D / 64; ++c)
+          tma_load_4d(sDO0 + sd * kTileBytes + c * kT * 128, &tmdO, dbar, c * 64, h, i * kT, b);
+        ++ndo;
+        // the statistics of step t - 2 have been read once its dK product was issued
+        if (t >= 2 && !wait_bounded(smem_addr(&sy.empty[(t - 2) % kStagesQ]),
+                                    ((t - 2) / kStagesQ) & 1, sy, p))
+          break;
+        const uint32_t rbar = smem_addr(&sy.row_full[t & 1]), row = sRow0 + (t & 1) * 1024;
         const size_t row0 = (static_cast<size_t>(b) * p.n_q + h) * (p.T * kT) + i * kT;
-        bulk_load(dst + 2 * kTileBytes, p.nlse2 + row0, 512, bar);
-        bulk_load(dst + 2 * kTileBytes + 512, p.nrowdot + row0, 512, bar);
+        mbar_arrive_expect_tx(rbar, 1024);
+        bulk_load(row, p.nlse2 + row0, 512, rbar);
+        bulk_load(row + 512, p.nrowdot + row0, 512, rbar);
+        ++nrow;
       }
       wait_drain(fb, 0);
-      drain_ring<kStagesKV>(sy, t);
+      drain_ring<kStagesQ>(sy.full, nq);
+      drain_ring<kStagesDO>(sy.do_full, ndo);
+      drain_ring<2>(sy.row_full, nrow);
     }
   } else if (warp == kMmaWarp) {
     const bool leader = elect_one();
     bool ok = __all_sync(0xffffffffu, wait_bounded(smem_addr(&sy.fixed_full), 0, sy, p));
     tc_fence_after_sync();
-    auto stage_of = [&](int t) { return sRing + (t % kStagesKV) * kStage; };
-    auto wait_stage = [&](int t) -> bool {
-      if (!__all_sync(0xffffffffu, wait_bounded(smem_addr(&sy.full[t % kStagesKV]),
-                                                (t / kStagesKV) & 1, sy, p)))
-        return false;
+    auto q_of = [&](int t) { return sQ0 + (t % kStagesQ) * kTileBytes; };
+    auto do_of = [&](int t) { return sDO0 + (t % kStagesDO) * kTileBytes; };
+    auto wait_all = [&](uint64_t& bar, int use) -> bool {
+      if (!__all_sync(0xffffffffu, wait_bounded(smem_addr(&bar), use & 1, sy, p))) return false;
       tc_fence_after_sync();
       return true;
     };
-    auto wait_all = [&](uint64_t& bar, int t) -> bool {
-      if (!__all_sync(0xffffffffu, wait_bounded(smem_addr(&bar), t & 1, sy, p))) return false;
-      tc_fence_after_sync();
-      return true;
-    };
-    if (ok && (ok = wait_stage(0))) {
-      mma_scores_full_ss<D>(leader, tmem + cS, sK, stage_of(0));                  // S^T  = K Q^T
+    auto wait_q = [&](int t) { return wait_all(sy.full[t % kStagesQ], t / kStagesQ); };
+    auto wait_do = [&](int t) { return wait_all(sy.do_full[t % kStagesDO], t / kStagesDO); };
+    if (ok && (ok = wait_q(0))) {
+      mma_scores_full_ss<D>(leader, tmem + cS, sK, q_of(0));                      // S^T  = K Q^T
       if (leader) mma_commit(smem_addr(&sy.s_full[0]));
-      mma_scores_full_ss<D>(leader, tmem + cP, sV, stage_of(0) + kTileBytes);     // dP^T = V dO^T
+      if ((ok = wait_do(0)))
+        mma_scores_full_ss<D>(leader, tmem + cP, sV, do_of(0));                   // dP^T = V dO^T
       if (leader) mma_commit(smem_addr(&sy.dp_full));
     }
     for (int t = 0; t < nsteps && ok; ++t) {
-      const uint32_t sQ = stage_of(t), sdO = sQ + kTileBytes;
       const bool more = t + 1 < nsteps;
+      if (more && !wait_q(t + 1)) break;
       if (!wait_all(sy.p_full[0], t)) break;
-      mma_accum_full<D>(leader, tmem + cDV, tmem + cS, sdO, t > 0);              // dV += P^T dO
+      mma_accum_full<D>(leader, tmem + cDV, tmem + cS, do_of(t), t > 0);         // dV += P^T dO
+      if (leader) mma_commit(smem_addr(&sy.do_empty[t % kStagesDO]));
       // S^T(t+1) overwrites P^T(t), which the dV product issued above reads first
       if (more) {
-        if (!wait_stage(t + 1)) break;
-        mma_scores_full_ss<D>(leader, tmem + cS, sK, stage_of(t + 1));
+        mma_scores_full_ss<D>(leader, tmem + cS, sK, q_of(t + 1));
         if (leader) mma_commit(smem_addr(&sy.s_full[0]));
+        if (!wait_do(t + 1)) break;
       }
       if (!wait_all(sy.ds_full, t)) break;
-      mma_accum_full<D>(leader, tmem + cDK, tmem + cP, sQ, t > 0);               // dK += dS^T Q
-      if (leader) mma_commit(smem_addr(&sy.empty[t % kStagesKV]));
+      mma_accum_full<D>(leader, tmem + cDK, tmem + cP, q_of(t), t > 0);          // dK += dS^T Q
+      if (leader) mma_commit(smem_addr(&sy.empty[t % kStagesQ]));
       if (more) {
-        mma_scores_full_ss<D>(leader, tmem + cP, sV, stage_of(t + 1) + kTileBytes);
+        mma_scores_full_ss<D>(leader, tmem + cP, sV, do_of(t + 1));
         if (leader) mma_commit(smem_addr(&sy.dp_full));
       }
     }
@@ -679,18 +721,17 @@ dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
     const int q0 = cw * kColsQ;                        // first query column (in the tile)
     bool ok = true;
     for (int t = 0; t < nsteps; ++t) {
-      const int st = t % kStagesKV;
       const int i = i0 + (work.first + t) % work.per_head;
       if (!__all_sync(0xffffffffu, wait_bounded(smem_addr(&sy.s_full[0]), t & 1, sy, p)) ||
-          // the staged row statistics arrived with the stage's copies
+          // the row statistics
           !__all_sync(0xffffffffu,
-                      wait_bounded(smem_addr(&sy.full[st]), (t / kStagesKV) & 1, sy, p))) {
+                      wait_bounded(smem_addr(&sy.row_full[t & 1]), (t >> 1) & 1, sy, p))) {
         ok = false;
         break;
       }
       tc_fence_after_sync();
       const float4* nl4 = reinterpret_cast<const float4*>(
-          dyn_smem + (sRing + st * kStage + 2 * kTileBytes - smem_addr(dyn_smem))) + q0 / 4;
+          dyn_smem + (sRow0 + (t & 1) * 1024 - smem_addr(dyn_smem))) + q0 / 4;
       const float4* nd4 = nl4 + 32;
       const bool diag = p.causal && i == j;           // query c < key r is masked
       // phase 1: P^T from S^T, kept in registers for phase 2, and written (bf16)
@@ -898,7 +939,7 @@ dq_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
         }
       }
       if (uc > 0) wait_drain(fb, (uc - 1) & 1);
-      drain_ring<kStages>(sy, it);
+      drain_ring<kStages>(sy.full, it);
     }
   } else if (warp == kMmaWarp) {
     const bool leader = elect_one();
@@ -1091,8 +1132,6 @@ constexpr int kMaxDevices = 64;
 std::mutex g_bwd_mutex;
 bool g_bwd_ready[kMaxDevices];
 EncodeTiledFn g_bwd_encode = nullptr;
-template <int D>
-constexpr int dkdv_smem() { return 2 * tile_bytes<D>() + kStagesKV * (2 * tile_bytes<D>() + 1024) + 1024; }
 template <int D>
 constexpr int dq_smem() { return tile_bytes<D>() + kStages * (2 * tile_bytes<D>()) + 1024; }
 
