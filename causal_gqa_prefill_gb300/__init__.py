@@ -1,4 +1,5 @@
-"""GB300-native causal GQA prefill attention (forward, decode and backward).
+"""GB300-native causal GQA prefill attention: forward, decode and backward, whole or
+behind a sliding window with sinks, cache operators, and caches held in 4 bits.
 
 The computation runs in a hand-written sm_103a CUDA library
 (``lib/libattn_prefill.so``, C ABI in ``include/attn_prefill.h``); this

@@ -4,7 +4,9 @@
 //
 // over each group of 32 channels of a row and head. Inputs are bf16, so lo is
 // one of them and exact. Both kernels move bytes (256 of bf16 and 80 of codes per
-// row), but packing's arithmetic costs as much as they do unless it is kept short:
+// row), but packing's arithmetic costs as much as they do unless it is kept short
+// (32768 rows of 8 heads, 134 MB and 42 MB: packing 34 us, issue slots 71 % full;
+// unpacking 27.5 us, 5 TB/s read while written; 20.6 at the copy rate):
 // eight lanes take a row, half a group each (with four a lane the group's extremes
 // and scale are worked out twice as often: 49 us where this takes less than half),
 // extremes on packed pairs, quotients by a reciprocal and one correction, rounding
@@ -231,7 +233,7 @@ unpack4_kernel(const Cache4Params p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Rows rows(p, nullptr);
   // a lane takes block l of eight channels and block l + 8, so that a warp's stores cover
-  // whole 128-byte pieces (neighbouring blocks a lane: 37 us where this takes 30)
+  // whole 128-byte pieces (neighbouring blocks a lane: 37 us where this takes 27.5)
   uint16_t* __restrict__ x = (blockIdx.y ? p.x[1] : p.x[0]) + rows.x + 8 * rows.l;
   const uint8_t* __restrict__ cache = blockIdx.y ? p.cache[1] : p.cache[0];
   const int g = rows.l >> 2, t = rows.l & 3;

@@ -11,8 +11,8 @@
 //     are contiguous) through a ring of kStages steps and works alone: it waits for
 //     nothing but its own copies until the end. They are 16-byte asynchronous copies,
 //     ten a lane and step, and not bulk ones: those cost a warp of this size some
-//     sixty instructions a step in moves to uniform registers and barriers (419 a
-//     chunk in all, where it is now 350);
+//     sixty instructions a step in moves to uniform registers and barriers, of
+//     344 a 16-position chunk with these;
 //   * S^T = K Q^T with m16n8k16 products, 16 positions x 8 heads. A code is put
 //     into the upper mantissa bits of a bf16 16 (bits 3..6: 16 + code, exact),
 //     one shift and one logic instruction for two codes; a group's scale is
@@ -31,6 +31,12 @@
 // runs, one per warp. At the end the warps of a CTA that stand in the same head
 // merge their results in shared memory, and a combine kernel merges what the
 // CTAs left. Lengths are read on the device.
+//
+// Measured: 16 sequences of 1024 to 8192 positions, 32 heads on 8, 31.5 us (95 MB of
+// rows: 14 us at the copy rate); one of 131072, 36 heads on 6, 35.6 us (126 MB: 19 us).
+// Longer lists cost 20.1 us more per 126 MB, 94 % of the copy rate; some 13 us are there
+// whatever the length: finding the runs, the first step's copies, the merge and the
+// combine.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -278,7 +284,7 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
 // Codes n and n + 4 of a word (or the n-th of its two halves) as bf16 16 + code: one
 // shift and one logic instruction, which takes the 16s from a register (`sixteens`,
 // from the parameters: a constant that the compiler knows becomes a second
-// instruction with another immediate, 64 more of 400 a chunk).
+// instruction with another immediate, 54 more a chunk).
 template <int n>
 __device__ __forceinline__ uint32_t codes16(uint32_t w, uint32_t sixteens) {
   const uint32_t at = n == 0 ? w << 3 : w >> (4 * n - 3);

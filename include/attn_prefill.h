@@ -37,7 +37,8 @@
  *     |O - O_exact| <= 2^-8 ((1 + 2^-6) A + |O_exact|)
  * where the 2^-6 covers the fp32 parts. (Measured on normal inputs, ||error|| is
  * 2.0e-3 to 2.4e-3 of ||O||; 1.7e-3 is O's own rounding.) This holds for the
- * forward, decode, ragged decode and decode behind a shared prefix; with e4m3
+ * forward, decode, ragged decode, decode behind a shared prefix and the windowed
+ * forward and decode (decode over 4-bit caches: below); with e4m3
  * inputs the weights are rounded to e4m3 (2^-4).
  *
  * Ownership: the caller allocates and owns q, k, v, o, lse and the stream.
@@ -50,10 +51,11 @@
  * once the stream has reached that point. q, k, v are not modified. Results
  * are deterministic: the same inputs give bit-identical o and lse.
  *
- * CUDA graphs: the first call of each family (forward, decode, backward) on a
- * device does a one-time set-up and must not be made while a stream capture
- * is under way; made there, it returns ATTN_ERR_UNSUPPORTED and sets up
- * nothing. After it, every compute entry point can be captured with the
+ * CUDA graphs: the first call of each family (forward, decode and backward, each
+ * with its windowed form; key weights; shared prefix; eviction; the rows of 4-bit
+ * caches; decode over them) on a device does a one-time set-up and must not be
+ * made while a stream capture is under way; made there, it returns
+ * ATTN_ERR_UNSUPPORTED and sets up nothing. After it, every compute entry point can be captured with the
  * stream it is given (attn_decode_fwd as two kernel nodes joined by a
  * programmatic dependency); replaying the graph recomputes from whatever the
  * captured input buffers hold then. attn_device_check synchronizes and cannot
