@@ -20,9 +20,11 @@
 //     own, in which a position's words of (scale, lo) are the operand as they are:
 //       s = sum_g scale_g (sum (16 + code) q) + (scale_g, lo_g) . (-16 sum q, sum q)
 //     (the sums of q in three bf16 parts), so no value of K is rounded;
-//   * O^T += V^T P^T likewise, 16 channels x 8 heads, with codes (the 16 taken off
-//     again, exactly) and scale_g P (rounded to bf16); sum_j P_j lo_gj is kept in
-//     fp32 beside it. P^T is turned by movmatrix; the two rows that a lane's operand
+//   * O^T += V^T P^T likewise, 16 channels x 8 heads, with codes less 7.5 (exact) and
+//     scale_g P (rounded to bf16); sum_j P_j (lo_gj + 7.5 scale_gj) is kept in fp32
+//     beside it. (With codes of 0 .. 15 the roundings of scale_g P all count with one
+//     sign, and O, a mean of values around 0 over a long cache, was 0.005 of itself
+//     off where it is now 0.002.) P^T is turned by movmatrix; the two rows that a lane's operand
 //     pairs up are brought together by one byte permutation per four codes.
 // (mma.sync and not tcgen05: those operands come from shared memory or tensor
 // memory, and writing the bf16 values there would cost more than the product.)
@@ -292,21 +294,22 @@ __device__ __forceinline__ uint32_t codes16(uint32_t w, uint32_t sixteens) {
   asm("lop3.b32 %0, %1, 0x00780078, %2, 0xEA;" : "=r"(r) : "r"(at), "r"(sixteens));   // (at & m) | 16s
   return r;
 }
-// The same less 16: the codes themselves, exactly.
+// The codes less 7.5, exactly: the same less 23.5.
 template <int n>
-__device__ __forceinline__ uint32_t codes0(uint32_t w, uint32_t sixteens) {
+__device__ __forceinline__ uint32_t codes_mid(uint32_t w, uint32_t sixteens) {
   uint32_t r;
-  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(codes16<n>(w, sixteens)), "r"(sixteens));
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(codes16<n>(w, sixteens)), "r"(0x41BC41BCu));
   return r;
 }
 
 // What a warp holds of one head: lane (r = lane / 4, t = lane % 4) has, for heads
 // 8 n + 2 t and + 1, channels 32 g + 4 r + 2 j (o[.][0..1]) and + 1 (o[.][2..3]),
-// its own share of sum_j P_j lo_gj and of the row sum, and the running maximum.
+// its own share of sum_j P_j (lo_gj + 7.5 scale_gj) and of the row sum, and the running
+// maximum.
 template <int NT>
 struct Acc {
   float o[NT][4][2][4];
-  float lows[NT][4][2];
+  float mids[NT][4][2];
   float m[NT][2], l[NT][2];
   __device__ void clear() {
 #pragma unroll
@@ -317,7 +320,7 @@ struct Acc {
         for (int j = 0; j < 2; ++j)
 #pragma unroll
           for (int e = 0; e < 4; ++e) o[n][g][j][e] = 0.0f;
-        lows[n][g][0] = lows[n][g][1] = 0.0f;
+        mids[n][g][0] = mids[n][g][1] = 0.0f;
       }
       m[n][0] = m[n][1] = kNoMax;
       l[n][0] = l[n][1] = 0.0f;
@@ -334,15 +337,15 @@ struct Acc {
           l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], off);
 #pragma unroll
           for (int g = 0; g < 4; ++g)
-            lows[n][g][e] += __shfl_xor_sync(0xffffffffu, lows[n][g][e], off);
+            mids[n][g][e] += __shfl_xor_sync(0xffffffffu, mids[n][g][e], off);
         }
       }
   }
   // Channels 32 g + 4 r .. + 3 of head 8 n + 2 t + e.
   __device__ float4 channels(int n, int g, int e) const {
-    const float low = lows[n][g][e];
-    return make_float4(o[n][g][0][e] + low, o[n][g][0][2 + e] + low, o[n][g][1][e] + low,
-                       o[n][g][1][2 + e] + low);
+    const float mid = mids[n][g][e];
+    return make_float4(o[n][g][0][e] + mid, o[n][g][0][2 + e] + mid, o[n][g][1][e] + mid,
+                       o[n][g][1][2 + e] + mid);
   }
 };
 
@@ -465,7 +468,7 @@ decode4_split_kernel(const Params4 p) {
           acc.l[n][e] *= alpha;
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
-            acc.lows[n][g][e] *= alpha;
+            acc.mids[n][g][e] *= alpha;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               acc.o[n][g][j][e] *= alpha;
@@ -503,19 +506,19 @@ decode4_split_kernel(const Params4 p) {
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         const uint32_t ab = __byte_perm(ca[g], cb[g], half), gh = __byte_perm(cc[g], cd[g], half);
-        const uint32_t a0 = codes0<0>(ab, sixteens), a1 = codes0<1>(ab, sixteens), a2 = codes0<0>(gh, sixteens),
-                       a3 = codes0<1>(gh, sixteens);
-        const uint32_t b0 = codes0<2>(ab, sixteens), b1 = codes0<3>(ab, sixteens), b2 = codes0<2>(gh, sixteens),
-                       b3 = codes0<3>(gh, sixteens);
+        const uint32_t a0 = codes_mid<0>(ab, sixteens), a1 = codes_mid<1>(ab, sixteens);
+        const uint32_t a2 = codes_mid<0>(gh, sixteens), a3 = codes_mid<1>(gh, sixteens);
+        const uint32_t b0 = codes_mid<2>(ab, sixteens), b1 = codes_mid<3>(ab, sixteens);
+        const uint32_t b2 = codes_mid<2>(gh, sixteens), b3 = codes_mid<3>(gh, sixteens);
         const float s0 = row4_scale(m0[g]), s1 = row4_scale(m1[g]);
-        const float l0 = row4_low(m0[g]), l1 = row4_low(m1[g]);
+        const float l0 = fmaf(7.5f, s0, row4_low(m0[g])), l1 = fmaf(7.5f, s1, row4_low(m1[g]));
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           const float* x = s[c][n];
           const uint32_t x0 = transpose8x8(pack_bf16x2(x[0] * s0, x[1] * s0));
           const uint32_t x1 = transpose8x8(pack_bf16x2(x[2] * s1, x[3] * s1));
-          acc.lows[n][g][0] = fmaf(x[0], l0, fmaf(x[2], l1, acc.lows[n][g][0]));
-          acc.lows[n][g][1] = fmaf(x[1], l0, fmaf(x[3], l1, acc.lows[n][g][1]));
+          acc.mids[n][g][0] = fmaf(x[0], l0, fmaf(x[2], l1, acc.mids[n][g][0]));
+          acc.mids[n][g][1] = fmaf(x[1], l0, fmaf(x[3], l1, acc.mids[n][g][1]));
           float(&d0)[4] = acc.o[n][g][0];
           float(&d1)[4] = acc.o[n][g][1];
           mma16816(d0, a0, a1, a2, a3, x0, x1, d0[0], d0[1], d0[2], d0[3]);

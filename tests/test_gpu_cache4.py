@@ -4,10 +4,10 @@ against the fp64 reference on the values that the codes stand for.
 Tolerance of decode. A score is an fp32 sum over groups of scale_g sum (16 + code) q
 and (lo_g - 16 scale_g) sum q: with every magnitude added up, S_abs = scale sum_g
 sum|q| (47 scale_g + |lo_g|), some six roundings of 2^-23 make E = 2^-20 S_abs. LSE
-is off by E + 2^-20 + 2^-22 |LSE|. O: bf16 (p scale_g) times the codes is off by
-2^-8 A, A = sum p (V - lo); the fp32 parts (scores, exponentials, sum p lo) by
-(2 E + 2^-20) (sum p (|lo| + |V|) + |O|); 2^-6 A 2^-8 covers both on A; O rounds
-once: 2^-8 |O|.
+is off by E + 2^-20 + 2^-22 |LSE|. O: bf16 (p scale_g) times the codes less 7.5 is
+off by 2^-8 A, A = sum p |V - mid|, mid = lo + 7.5 scale; the fp32 parts (scores,
+exponentials, sum p mid) by (2 E + 2^-20) (sum p (|lo| + |V|) + |O|), where
+|mid| <= |V| + |V - mid|; 2^-6 A 2^-8 covers both on A; O rounds once: 2^-8 |O|.
 """
 
 import numpy as np
@@ -183,7 +183,10 @@ def check_step(q, k4, v4, lens, o, lse, window, sinks, scale=None, what=""):
             E = 2.0 ** -20 * abs(scale) * (np.abs(Q) @ (47 * step + np.abs(klo)).T).max(1)
             off = np.abs(lse[b, u * g:u * g + g, 0] - ref_lse)
             assert (off <= E + 2.0 ** -20 + 2.0 ** -22 * np.abs(ref_lse)).all(), (what, off.max())
-            bound = 2.0 ** -8 * ((1 + 2.0 ** -6) * (p @ (V - vlo)) + np.abs(ref)) + (
+            scales = cache4.bf16_value(v4[b, u, at].cpu().numpy()[:, 64:].reshape(-1, 4, 4)[..., :2]
+                                       .copy().view(np.uint16)[..., 0].astype(np.uint32))
+            mid = vlo + 7.5 * np.repeat(scales, 32, axis=1)
+            bound = 2.0 ** -8 * ((1 + 2.0 ** -6) * (p @ np.abs(V - mid)) + np.abs(ref)) + (
                 2 * E[:, None] + 2.0 ** -20) * (p @ (np.abs(vlo) + np.abs(V)) + np.abs(ref))
             err = np.abs(o[b, 0, u * g:u * g + g] - ref)
             assert (err <= bound).all(), (what, (err - bound).max())
@@ -260,6 +263,29 @@ def test_decode_other_scales(scale):
     q, k4, v4, lens = make_step(2, 500, 8, 2, [500, 123], None, 0, seed=9)
     o, lse = attn_decode4(q, k4, v4, lens, scale=scale)
     check_step(q, k4, v4, [500, 123], o, lse, None, 0, scale=scale)
+
+
+def test_decode_of_long_caches_is_as_exact_as_its_roundings():
+    """Over long caches of values around 0, O is small beside them, and what the weights'
+    roundings do must shrink with it: two roundings of up to half a bf16 step, 2^-8 /
+    sqrt(3) in the mean at most, one on O and one on values less mid, which are no
+    larger than V but for a tenth: sqrt(2 / 3) 1.1 2^-8 of O."""
+    B, C, n_q, n_kv = 2, 6000, 8, 2
+    lens = [6000, 3500]
+    k, v = rows(B, C, n_kv, 30), rows(B, C, n_kv, 31)
+    k4, v4 = (torch.zeros(B, n_kv, C, 80, dtype=torch.uint8, device="cuda") for _ in range(2))
+    attn_pack4(k, v, k4, v4)
+    q = W.make_inputs(W.custom(B, 1, n_q, n_kv, 128, Lk=4), "cuda", seed=32)[0]
+    o = to_np(attn_decode4(q, k4, v4, i32(*lens))[0])
+    err = size = 0.0
+    for b in range(B):
+        for h in range(n_q):
+            K, V = (cache4.unpack(c[b, h // 4, :lens[b]].cpu().numpy())[0] for c in (k4, v4))
+            s = K @ to_np(q)[b, 0, h] * 128 ** -0.5
+            p = np.exp(s - s.max())
+            ref = p @ V / p.sum()
+            err, size = err + ((o[b, 0, h] - ref) ** 2).sum(), size + (ref ** 2).sum()
+    assert (err / size) ** 0.5 <= (2 / 3) ** 0.5 * 1.1 * 2.0 ** -8
 
 
 def test_decode_what_is_not_a_number_stays_in_its_head():
