@@ -12,7 +12,7 @@
 //     nothing but its own copies until the end. They are 16-byte asynchronous copies,
 //     ten a lane and step, and not bulk ones: those cost a warp of this size some
 //     sixty instructions a step in moves to uniform registers and barriers, of
-//     344 a 16-position chunk with these;
+//     some 350 a 16-position chunk with these;
 //   * S^T = K Q^T with m16n8k16 products, 16 positions x 8 heads. A code is put
 //     into the upper mantissa bits of a bf16 16 (bits 3..6: 16 + code, exact),
 //     one shift and one logic instruction for two codes; a group's scale is
@@ -20,12 +20,18 @@
 //     own, in which a position's words of (scale, lo) are the operand as they are:
 //       s = sum_g scale_g (sum (16 + code) q) + (scale_g, lo_g) . (-16 sum q, sum q)
 //     (the sums of q in three bf16 parts), so no value of K is rounded;
-//   * O^T += V^T P^T likewise, 16 channels x 8 heads, with codes less 7.5 (exact) and
-//     scale_g P (rounded to bf16); sum_j P_j (lo_gj + 7.5 scale_gj) is kept in fp32
-//     beside it. (With codes of 0 .. 15 the roundings of scale_g P all count with one
-//     sign, and O, a mean of values around 0 over a long cache, was 0.005 of itself
-//     off where it is now 0.002.) P^T is turned by movmatrix; the two rows that a lane's operand
-//     pairs up are brought together by one byte permutation per four codes.
+//   * O^T += V^T P^T likewise, 16 channels x 8 heads: with a position's and group's
+//     center c, the code next to a value of 0, V = (lo + scale c) + scale (code - c),
+//     the codes less c (exact) against scale_g P (rounded to bf16), and
+//     sum_j P_j (lo_gj + scale_gj c_gj) in fp32 beside it. So a rounding counts as
+//     much as one of P counts for V itself. (With c = 0 it counts for V - lo, up to 15
+//     steps of one sign: over 131072 positions, a channel of each group six times the
+//     others, O was 0.0056 of itself off, with c = 7.5 0.0037, now 0.0021, of which O's
+//     own rounding is 0.0016.) Each lane works the centers of one position out, while
+//     the scores' products run, and leaves them in shared memory (36.5 us where those
+//     positions took 35.5 without; P^T in two bf16 parts, 0.0016, 40.3). P^T is
+//     turned by movmatrix; the two rows that a lane's operand pairs up are brought
+//     together by one byte permutation per four codes.
 // (mma.sync and not tcgen05: those operands come from shared memory or tensor
 // memory, and writing the bf16 values there would cost more than the product.)
 //
@@ -34,9 +40,9 @@
 // merge their results in shared memory, and a combine kernel merges what the
 // CTAs left. Lengths are read on the device.
 //
-// Measured: 16 sequences of 1024 to 8192 positions, 32 heads on 8, 31.5 us (95 MB of
-// rows: 14 us at the copy rate); one of 131072, 36 heads on 6, 35.6 us (126 MB: 19 us).
-// Longer lists cost 20.1 us more per 126 MB, 94 % of the copy rate; some 13 us are there
+// Measured: 16 sequences of 1024 to 8192 positions, 32 heads on 8, 32 us (95 MB of
+// rows: 14 us at the copy rate); one of 131072, 36 heads on 6, 36.5 us (126 MB: 19 us).
+// Longer lists cost 22 us more per 126 MB, 87 % of the copy rate; some 13 us are there
 // whatever the length: finding the runs, the first step's copies, the merge and the
 // combine.
 #include <cuda_runtime.h>
@@ -62,7 +68,12 @@ constexpr int kChunk = 16;                         // positions per product, uni
 constexpr int kStep = 2 * kChunk;                  // positions per step of a warp
 constexpr int kStepBytes = kStep * kRow4Bytes;     // of K, and of V
 constexpr int kStages = 2;                           // steps under way per warp
-constexpr int kWarpBytes = kStages * 2 * kStepBytes;
+constexpr int kRingBytes = kStages * 2 * kStepBytes;
+// Behind its ring a warp keeps, of a step's V, mid = lo + scale c [position][group] in
+// fp32, and bf16 16 + c of positions t + 8 h and t + 8 h + 4 of its chunks, [h][t][group]
+// [which of the two].
+constexpr int kMidBytes = kStep * kRow4Groups * 4;
+constexpr int kWarpBytes = kRingBytes + kMidBytes + kStep * kRow4Groups * 2;
 constexpr int kCtas = 152;                         // one per SM
 constexpr int kMaxG = 16;
 constexpr float kRescale = 8.0f;                   // lazy running maximum (log2 units)
@@ -294,17 +305,17 @@ __device__ __forceinline__ uint32_t codes16(uint32_t w, uint32_t sixteens) {
   asm("lop3.b32 %0, %1, 0x00780078, %2, 0xEA;" : "=r"(r) : "r"(at), "r"(sixteens));   // (at & m) | 16s
   return r;
 }
-// The codes less 7.5, exactly: the same less 23.5.
+// The codes less their centers, exactly: `center` is bf16 16 + c of each.
 template <int n>
-__device__ __forceinline__ uint32_t codes_mid(uint32_t w, uint32_t sixteens) {
+__device__ __forceinline__ uint32_t codes_less(uint32_t w, uint32_t sixteens, uint32_t center) {
   uint32_t r;
-  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(codes16<n>(w, sixteens)), "r"(0x41BC41BCu));
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(codes16<n>(w, sixteens)), "r"(center));
   return r;
 }
 
 // What a warp holds of one head: lane (r = lane / 4, t = lane % 4) has, for heads
 // 8 n + 2 t and + 1, channels 32 g + 4 r + 2 j (o[.][0..1]) and + 1 (o[.][2..3]),
-// its own share of sum_j P_j (lo_gj + 7.5 scale_gj) and of the row sum, and the running
+// its own share of sum_j P_j (lo_gj + scale_gj c_gj) and of the row sum, and the running
 // maximum.
 template <int NT>
 struct Acc {
@@ -395,6 +406,9 @@ decode4_split_kernel(const Params4 p) {
   const int kpos = (r >> 1) + 4 * (r & 1);
   const uint32_t half = (r & 1) ? 0x7632u : 0x5410u;
   const uint32_t sixteens = p.sixteens;
+  const uint32_t mid_out = ring + kRingBytes + 16 * lane, mid_in = ring + kRingBytes + 16 * kpos;
+  const uint32_t center_in = ring + kRingBytes + kMidBytes + 16 * t;
+  const uint32_t center_out = center_in + 64 * (lane >> 3) + 2 * (r & 1);
   Acc<NT> acc;
   uint32_t qf[NT][4][4];                      // Q as the products' second operand
   uint32_t qo[NT][3];                         // (-16 sum q, sum q) of group t, three bf16 parts
@@ -442,6 +456,29 @@ decode4_split_kernel(const Params4 p) {
         }
       }
     }
+    // the centers of V's position `lane`
+    {
+      const uint4 pv = lds128(sv + lane * kRow4Bytes + kRow4Codes);
+      const uint32_t words[4] = {pv.x, pv.y, pv.z, pv.w};
+      float mid[4];
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const float scale = row4_scale(words[g]), lo = row4_low(words[g]);
+        float inv;                            // (near enough: any whole c will do)
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(scale));
+        // 2^23 + c, c = -lo / scale rounded and kept in 0 .. 15 (0 where that is not a number)
+        const float at = fmaf(__saturatef(lo * (-1.0f / 15.0f) * inv), 15.0f, 8388608.0f);
+        mid[g] = kFull || lane < valid ? fmaf(scale, at - 8388608.0f, lo) : 0.0f;
+        // bf16 16 + c is 0x4180 + 8 c
+        asm volatile("st.shared.b16 [%0], %1;" ::"r"(center_out + 4 * g),
+                     "h"(static_cast<uint16_t>(__float_as_uint(at) * 8u + 0x4180u))
+                     : "memory");
+      }
+      asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(mid_out), "f"(mid[0]), "f"(mid[1]),
+                   "f"(mid[2]), "f"(mid[3])
+                   : "memory");
+    }
+
     bool need = false;
 #pragma unroll
     for (int c = 0; c < 2; ++c)
@@ -488,6 +525,7 @@ decode4_split_kernel(const Params4 p) {
         }
 
     // O^T: P times the scale of its position's group, turned, against V's codes
+    __syncwarp();
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       const uint32_t at = sv + c * kChunk * kRow4Bytes;
@@ -501,17 +539,21 @@ decode4_split_kernel(const Params4 p) {
       const uint32_t base = at + t * kRow4Bytes + 16 * (r >> 1);
       const uint4 va = lds128(base), vb = lds128(base + 4 * kRow4Bytes);
       const uint4 vc = lds128(base + 8 * kRow4Bytes), vd = lds128(base + 12 * kRow4Bytes);
+      const uint4 l0 = lds128(mid_in + c * kChunk * 16), l1 = lds128(mid_in + (c * kChunk + 8) * 16);
+      const uint32_t mid0[4] = {l0.x, l0.y, l0.z, l0.w}, mid1[4] = {l1.x, l1.y, l1.z, l1.w};
+      const uint4 cl = lds128(center_in + 128 * c), ch = lds128(center_in + 128 * c + 64);
+      const uint32_t cen0[4] = {cl.x, cl.y, cl.z, cl.w}, cen1[4] = {ch.x, ch.y, ch.z, ch.w};
       const uint32_t ca[4] = {va.x, va.y, va.z, va.w}, cb[4] = {vb.x, vb.y, vb.z, vb.w};
       const uint32_t cc[4] = {vc.x, vc.y, vc.z, vc.w}, cd[4] = {vd.x, vd.y, vd.z, vd.w};
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         const uint32_t ab = __byte_perm(ca[g], cb[g], half), gh = __byte_perm(cc[g], cd[g], half);
-        const uint32_t a0 = codes_mid<0>(ab, sixteens), a1 = codes_mid<1>(ab, sixteens);
-        const uint32_t a2 = codes_mid<0>(gh, sixteens), a3 = codes_mid<1>(gh, sixteens);
-        const uint32_t b0 = codes_mid<2>(ab, sixteens), b1 = codes_mid<3>(ab, sixteens);
-        const uint32_t b2 = codes_mid<2>(gh, sixteens), b3 = codes_mid<3>(gh, sixteens);
+        const uint32_t a0 = codes_less<0>(ab, sixteens, cen0[g]), a1 = codes_less<1>(ab, sixteens, cen0[g]);
+        const uint32_t a2 = codes_less<0>(gh, sixteens, cen1[g]), a3 = codes_less<1>(gh, sixteens, cen1[g]);
+        const uint32_t b0 = codes_less<2>(ab, sixteens, cen0[g]), b1 = codes_less<3>(ab, sixteens, cen0[g]);
+        const uint32_t b2 = codes_less<2>(gh, sixteens, cen1[g]), b3 = codes_less<3>(gh, sixteens, cen1[g]);
         const float s0 = row4_scale(m0[g]), s1 = row4_scale(m1[g]);
-        const float l0 = fmaf(7.5f, s0, row4_low(m0[g])), l1 = fmaf(7.5f, s1, row4_low(m1[g]));
+        const float l0 = __uint_as_float(mid0[g]), l1 = __uint_as_float(mid1[g]);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           const float* x = s[c][n];

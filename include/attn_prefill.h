@@ -371,10 +371,10 @@ attn_status_t attn_cache_unpack4(const void* k4, const void* v4, void* k, void* 
  *   window   0: the whole of lens[b] (sinks must be 0); else window and sinks of
  *            attn_decode_window_fwd
  *   Rounding: the values of K and V are not rounded; scores, statistics, LSE and
- *   sum_j p_j mid_j, mid = lo + 7.5 scale, are fp32; a softmax weight times the
- *   scale of a group of V is rounded to bf16 (the matrix instructions' operand),
- *   and O once, so with A = sum_j p_j |V_j - mid_j| and the scores off by at most
- *   E in fp32
+ *   sum_j p_j mid_j are fp32, mid being that of a group's 16 values which is next
+ *   to 0; a softmax weight times the scale of a group of V is rounded to bf16 (the
+ *   matrix instructions' operand), and O once, so with A = sum_j p_j |V_j - mid_j|
+ *   and the scores off by at most E in fp32
  *       |O - O_exact| <= 2^-8 ((1 + 2^-6) A + |O_exact|)
  *                        + (2 E + 2^-20) (sum_j p_j (|lo_j| + |V_j|) + |O_exact|)
  *   Everything else as attn_decode_ragged_fwd. Two kernels, programmatic

@@ -4,10 +4,12 @@ against the fp64 reference on the values that the codes stand for.
 Tolerance of decode. A score is an fp32 sum over groups of scale_g sum (16 + code) q
 and (lo_g - 16 scale_g) sum q: with every magnitude added up, S_abs = scale sum_g
 sum|q| (47 scale_g + |lo_g|), some six roundings of 2^-23 make E = 2^-20 S_abs. LSE
-is off by E + 2^-20 + 2^-22 |LSE|. O: bf16 (p scale_g) times the codes less 7.5 is
-off by 2^-8 A, A = sum p |V - mid|, mid = lo + 7.5 scale; the fp32 parts (scores,
-exponentials, sum p mid) by (2 E + 2^-20) (sum p (|lo| + |V|) + |O|), where
-|mid| <= |V| + |V - mid|; 2^-6 A 2^-8 covers both on A; O rounds once: 2^-8 |O|.
+is off by E + 2^-20 + 2^-22 |LSE|. O: bf16 (p scale_g) times the codes less c is off
+by 2^-8 A, A = sum p |V - mid|, mid = lo + scale c, c the nearest of 0 .. 15 to
+-lo / scale (to within 15 2^-22, three fp32 roundings: where two are that near, either,
+a scale further off); the fp32 parts (scores, exponentials, sum p mid) by (2 E + 2^-20)
+(sum p (|lo| + |V|) + |O|), where |mid| <= |V| + |V - mid|; 2^-6 A 2^-8 covers both on
+A; O rounds once: 2^-8 |O|.
 """
 
 import numpy as np
@@ -185,8 +187,13 @@ def check_step(q, k4, v4, lens, o, lse, window, sinks, scale=None, what=""):
             assert (off <= E + 2.0 ** -20 + 2.0 ** -22 * np.abs(ref_lse)).all(), (what, off.max())
             scales = cache4.bf16_value(v4[b, u, at].cpu().numpy()[:, 64:].reshape(-1, 4, 4)[..., :2]
                                        .copy().view(np.uint16)[..., 0].astype(np.uint32))
-            mid = vlo + 7.5 * np.repeat(scales, 32, axis=1)
-            bound = 2.0 ** -8 * ((1 + 2.0 ** -6) * (p @ np.abs(V - mid)) + np.abs(ref)) + (
+            scales = np.repeat(scales, 32, axis=1)
+            with np.errstate(divide="ignore", invalid="ignore"):
+                code = np.where(scales > 0, -vlo / scales, 0.0)
+            near = np.abs(code - np.floor(code) - 0.5) < 2.0 ** -16
+            mid = vlo + scales * np.clip(np.rint(code), 0, 15)
+            A = p @ (np.abs(V - mid) + near * scales)
+            bound = 2.0 ** -8 * ((1 + 2.0 ** -6) * A + np.abs(ref)) + (
                 2 * E[:, None] + 2.0 ** -20) * (p @ (np.abs(vlo) + np.abs(V)) + np.abs(ref))
             err = np.abs(o[b, 0, u * g:u * g + g] - ref)
             assert (err <= bound).all(), (what, (err - bound).max())
@@ -265,14 +272,16 @@ def test_decode_other_scales(scale):
     check_step(q, k4, v4, [500, 123], o, lse, None, 0, scale=scale)
 
 
-def test_decode_of_long_caches_is_as_exact_as_its_roundings():
+@pytest.mark.parametrize("kind", ["normal", "outliers"])
+def test_decode_of_long_caches_is_as_exact_as_its_roundings(kind):
     """Over long caches of values around 0, O is small beside them, and what the weights'
     roundings do must shrink with it: two roundings of up to half a bf16 step, 2^-8 /
-    sqrt(3) in the mean at most, one on O and one on values less mid, which are no
-    larger than V but for a tenth: sqrt(2 / 3) 1.1 2^-8 of O."""
+    sqrt(3) in the mean at most, one on O and one on V less the code's value next to 0,
+    which in the mean square is larger than V by what half a step is at most, a tenth
+    for groups of normal values and less for outliers: sqrt(2 / 3) 1.1 2^-8 of O."""
     B, C, n_q, n_kv = 2, 6000, 8, 2
     lens = [6000, 3500]
-    k, v = rows(B, C, n_kv, 30), rows(B, C, n_kv, 31)
+    k, v = rows(B, C, n_kv, 30), rows(B, C, n_kv, 31, kind)
     k4, v4 = (torch.zeros(B, n_kv, C, 80, dtype=torch.uint8, device="cuda") for _ in range(2))
     attn_pack4(k, v, k4, v4)
     q = W.make_inputs(W.custom(B, 1, n_q, n_kv, 128, Lk=4), "cuda", seed=32)[0]
