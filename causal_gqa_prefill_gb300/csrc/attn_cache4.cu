@@ -5,12 +5,12 @@
 // over each group of 32 channels of a row and head. Inputs are bf16, so lo is
 // one of them and exact. Both kernels move bytes (256 of bf16 and 80 of codes per
 // row), but packing's arithmetic costs as much as they do unless it is kept short
-// (32768 rows of 8 heads, 134 MB and 42 MB: packing 34 us, issue slots 71 % full;
+// (32768 rows of 8 heads, 134 MB and 42 MB: packing 31 us, issue slots 70 % full;
 // unpacking 27.5 us, 5 TB/s read while written; 20.6 at the copy rate):
 // eight lanes take a row, half a group each (with four a lane the group's extremes
 // and scale are worked out twice as often: 49 us where this takes less than half),
-// extremes on packed pairs, quotients by a reciprocal and one correction, rounding
-// and joining of the codes in fp32's and integer multiply-adds.
+// extremes on packed pairs, quotients by a reciprocal and one correction, two at once,
+// rounding and joining of the codes in fp32's and integer multiply-adds.
 //
 // The code is the nearest integer to the exact quotient, ties to even, and the
 // scale the exact quotient rounded to fp32 and then to bf16. While |x| and |lo| are
@@ -36,7 +36,7 @@ namespace {
 
 using namespace gb300;
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;                       // (64: 38 us of packing, 256: 32, 512: 36)
 constexpr int kLanes = 8;                           // lanes per row, 16 channels each
 constexpr int kRowsAtOnce = kThreads / kLanes;
 constexpr int kAhead = 2;                           // rows under way per thread
@@ -81,6 +81,17 @@ __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
+}
+// The smaller magnitude (its sign means nothing).
+__device__ __forceinline__ uint32_t min_abs2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("min.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
 }
 __device__ __forceinline__ float low_half(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float high_half(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
@@ -140,7 +151,7 @@ struct Rows {
   }
 };
 
-__global__ void __launch_bounds__(kThreads, 4)
+__global__ void __launch_bounds__(kThreads, 9)
 pack4_kernel(const Cache4Params p) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -166,12 +177,12 @@ pack4_kernel(const Cache4Params p) {
   for (int a = 0; a < kAhead; ++a) {
     if (!__any_sync(0xffffffffu, rows.at[a].cache >= 0)) continue;
     auto value = [&](int e) { return e & 1 ? high_half(u[a][e >> 1]) : low_half(u[a][e >> 1]); };
-    uint32_t lo2 = u[a][0], hi2 = u[a][0], near2 = u[a][0] & 0x7FFF7FFFu;
+    uint32_t lo2 = u[a][0], hi2 = u[a][0], near2 = u[a][0];
 #pragma unroll
     for (int e = 1; e < 8; ++e) {
       lo2 = min2(lo2, u[a][e]);
       hi2 = max2(hi2, u[a][e]);
-      near2 = min2(near2, u[a][e] & 0x7FFF7FFFu);
+      near2 = min_abs2(near2, u[a][e]);
     }
     lo2 = min2(lo2, __shfl_xor_sync(0xffffffffu, lo2, 1));
     hi2 = max2(hi2, __shfl_xor_sync(0xffffffffu, hi2, 1));
@@ -185,7 +196,8 @@ pack4_kernel(const Cache4Params p) {
     if (finite && s > 0.0f) {
       float inv;                            // (within a unit; the correction takes care of it)
       asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
-      const float smallest = fminf(fminf(low_half(near2), high_half(near2)), fabsf(lo));
+      const float smallest =
+          fminf(fminf(fabsf(low_half(near2)), fabsf(high_half(near2))), fabsf(lo));
       if (s < 0x1p-100f || s > 0x1p100f) {
 #pragma unroll 1
         for (int e = 0; e < 16; ++e) {
@@ -195,10 +207,13 @@ pack4_kernel(const Cache4Params p) {
         }
       } else {
         float c[16];                        // 1.5 * 2^23 + code
+        // (two at once)
+        const uint64_t lo_2 = f32x2_pack(-lo, -lo), inv_2 = f32x2_pack(inv, inv);
+        const uint64_t s_2 = f32x2_pack(-s, -s), one_2 = f32x2_pack(12582912.0f, 12582912.0f);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float d = value(e) - lo, q = d * inv;
-          c[e] = fmaf(fmaf(-s, q, d), inv, q) + 12582912.0f;
+        for (int e = 0; e < 16; e += 2) {
+          const uint64_t d = fadd2(f32x2_pack(value(e), value(e + 1)), lo_2), q = fmul2(d, inv_2);
+          f32x2_unpack(fadd2(ffma2(ffma2(s_2, q, d), inv_2, q), one_2), c[e], c[e + 1]);
         }
         if (smallest < 0x1p-11f * s) {
 #pragma unroll
