@@ -477,15 +477,18 @@ __device__ __forceinline__ void p_from_s(uint32_t taddr, uint64_t c2, uint64_t n
 
 // ------------------------------------------------------------------ rowdot
 
-// Half a warp per row: 16 lanes x D / 16 dimensions. A block takes kRowdotT positions of
-// up to kRowdotH neighbouring heads, so that it reads O and dO in their own order,
-// four rows (eight loads) under way per half-warp, and writes whole pieces of the
-// [b, h, t] statistics out of shared memory. (One row (b, h, t) after another, with
-// three divisions each, took 41 us for 134 MB, this 25; 32 positions a block took 8 us
-// for 1000 rows of 8 heads, this 5.) Positions past L get -inf
-// and 0 without touching O or dO. The dK/dV kernel is launched as this grid's
-// programmatic dependent and waits for it before it reads the statistics.
-constexpr int kRowdotT = 8, kRowdotH = 8;
+// Half a warp per row: 16 lanes x D / 16 dimensions. A block takes up to kRowdotH
+// neighbouring heads of 8 << more positions, 64 rows or nearly, so that it reads O and dO
+// in their own order, four rows (eight loads) under way per half-warp, and writes whole
+// pieces of the [b, h, t] statistics out of shared memory. (One row (b, h, t) after
+// another, with three divisions each, took 41 us for 134 MB, this 25; 32 positions of
+// 8 heads a block took 8 us for 1000 rows of 8 heads, 8 take 5; 8 positions of a single
+// head took 14 us for 32768 rows, 64 take 8.) Positions past L get -inf and 0 without
+// touching O or dO. The dK/dV kernel is launched as this grid's programmatic dependent
+// and waits for it before it reads the statistics.
+constexpr int kRowdotH = 8;
+// Doublings of a block's 8 positions: as many as keep its rows at 64.
+int row_doublings(int64_t n_q) { return n_q >= 5 ? 0 : n_q >= 3 ? 1 : n_q == 2 ? 2 : 3; }
 __device__ __forceinline__ float dot2_bf16(uint32_t a, uint32_t d, float acc) {
   acc = fmaf(__uint_as_float(a << 16), __uint_as_float(d << 16), acc);
   return fmaf(__uint_as_float(a & 0xFFFF0000u), __uint_as_float(d & 0xFFFF0000u), acc);
@@ -504,23 +507,24 @@ __device__ __forceinline__ float dot8_bf16(uint4 a, uint4 d) {
 
 // Lanes of a half-warp hold D / 16 dimensions each (8 for D = 128: one
 // 16-byte load; 4 for D = 64: the first half of it).
-template <int D>
+template <int D, int more>
 __global__ void __launch_bounds__(256)
 rowdot_kernel(const uint16_t* o, const uint16_t* dout, const float* lse, float* nlse2,
               float* nrowdot, int L, int n_q, int Lp) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  __shared__ float dots[kRowdotH][kRowdotT + 1];
+  constexpr int positions = 8 << more;
+  __shared__ float dots[72];                            // [head][position], one more to a head
   constexpr int kAhead = 4, kHalves = 16;               // half-warps of a block
-  const int t_blocks = Lp / kRowdotT, h_blocks = (n_q + kRowdotH - 1) / kRowdotH;
+  const int t_blocks = Lp / positions, h_blocks = (n_q + kRowdotH - 1) / kRowdotH;
   const int rest = blockIdx.x / t_blocks;
-  const int t0 = (blockIdx.x - rest * t_blocks) * kRowdotT, h0 = rest % h_blocks * kRowdotH;
+  const int t0 = (blockIdx.x - rest * t_blocks) * positions, h0 = rest % h_blocks * kRowdotH;
   const int heads = min(kRowdotH, n_q - h0);
   const size_t b = rest / h_blocks;
   // row of the block's [position][head] order -> position
   auto position = [&](int row) { return heads == kRowdotH ? row / kRowdotH : row / heads; };
   const int half = threadIdx.x >> 4, l16 = threadIdx.x & 15;
-  const int rows = heads * min(kRowdotT, L - t0);       // (may be none: then below zero)
-  for (int r0 = half; r0 < heads * kRowdotT; r0 += kAhead * kHalves) {
+  const int rows = heads * min(positions, L - t0);       // (may be none: then below zero)
+  for (int r0 = half; r0 < heads * positions; r0 += kAhead * kHalves) {
     uint4 a[kAhead], d[kAhead];
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
@@ -547,17 +551,17 @@ rowdot_kernel(const uint16_t* o, const uint16_t* dout, const float* lse, float* 
                             : dot2_bf16(a[k].y, d[k].y, dot2_bf16(a[k].x, d[k].x, 0.0f));
 #pragma unroll
       for (int off = 8; off > 0; off >>= 1) dd += __shfl_xor_sync(0xffffffffu, dd, off);
-      if (l16 == 0 && row < heads * kRowdotT) {
+      if (l16 == 0 && row < heads * positions) {
         const int t = position(row);
-        dots[row - t * heads][t] = row < rows ? dd : 0.0f;
+        dots[(row - t * heads) * (positions + 1) + t] = row < rows ? dd : 0.0f;
       }
     }
   }
   __syncthreads();
-  const int h = threadIdx.x / kRowdotT, t = threadIdx.x % kRowdotT;
+  const int h = threadIdx.x >> (3 + more), t = threadIdx.x & (positions - 1);
   if (h < heads) {
     const size_t head = b * n_q + h0 + h;
-    nrowdot[head * Lp + t0 + t] = -dots[h][t];
+    nrowdot[head * Lp + t0 + t] = -dots[h * (positions + 1) + t];
     nlse2[head * Lp + t0 + t] = t0 + t < L ? -lse[head * L + t0 + t] * kLog2e : -INFINITY;
   }
 }
@@ -1252,11 +1256,16 @@ bool encode_tile_map(CUtensorMap* map, const void* ptr, int D, int H, int64_t L,
                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// 32-bit tile indexing, and the row kernel's grid (128 rows x B*n_q*T / 32)
+int64_t row_blocks_of(int64_t B, int64_t T, int64_t n_q) {
+  return B * ((n_q + kRowdotH - 1) / kRowdotH) * ((T * kT / 8) >> row_doublings(n_q));
+}
+
+// 32-bit tile indexing, and the row kernel's grid
 bool sizes_fit(int64_t B, int64_t L, int32_t n_q, int32_t n_kv) {
   const int64_t T = (L + kT - 1) / kT;
   return L <= (int64_t{1} << 30) && B <= INT32_MAX && B * n_q <= INT32_MAX &&
-         B * n_kv * T <= INT32_MAX && B * n_q * T <= INT32_MAX / 4;
+         B * n_kv * T <= INT32_MAX && B * n_q * T <= INT32_MAX / 4 &&
+         row_blocks_of(B, T, n_q) <= INT32_MAX;
 }
 
 // Row statistics of a call, in bytes: two fp32 per query row, rows padded to tiles.
@@ -1316,8 +1325,10 @@ attn_status_t launch_all(cudaStream_t stream, unsigned row_blocks, unsigned kv_c
                          const float* lse, const uint16_t* q, float* nlse2, float* nrowdot, int B,
                          const CUtensorMap& mq, const CUtensorMap& mdo, const CUtensorMap& mk,
                          const CUtensorMap& mv, const BwdParams& p) {
-  rowdot_kernel<D><<<row_blocks, 256, 0, stream>>>(o, dout, lse, nlse2, nrowdot, p.L, p.n_q,
-                                                   p.T * kT);
+  constexpr decltype(&rowdot_kernel<D, 0>) kRows[4] = {rowdot_kernel<D, 0>, rowdot_kernel<D, 1>,
+                                                       rowdot_kernel<D, 2>, rowdot_kernel<D, 3>};
+  kRows[row_doublings(p.n_q)]<<<row_blocks, 256, 0, stream>>>(o, dout, lse, nlse2, nrowdot, p.L,
+                                                              p.n_q, p.T * kT);
   if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
   if (launch_dkdv<D, kWin>(kv_ctas, stream, mq, mdo, mk, mv, p) != cudaSuccess)
     return ATTN_ERR_CUDA;
@@ -1394,8 +1405,7 @@ attn_status_t backward(const void* q, const void* k, const void* v, const void* 
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
     sms = 1;
-  const unsigned row_blocks =
-      static_cast<unsigned>(B * ((n_q + kRowdotH - 1) / kRowdotH) * (T * kT / kRowdotT));
+  const unsigned row_blocks = static_cast<unsigned>(row_blocks_of(B, T, n_q));
   const uint16_t* oh = static_cast<const uint16_t*>(o);
   const uint16_t* qh = static_cast<const uint16_t*>(q);
   const uint16_t* doh = static_cast<const uint16_t*>(dout);
