@@ -58,6 +58,7 @@
 #include <cstdint>
 #include <cstring>
 #include <mutex>
+#include <type_traits>
 
 #include "attn_prefill.h"
 #include "sm103_ptx.cuh"
@@ -132,9 +133,6 @@ struct Params {
   int Tq, Tk;           // 128-row query tiles and 128-key tiles
   int causal;
   int scale_pos;        // 1 when c > 0
-  int window, sinks;    // kWin instances: W and S, both at most Lk
-  int first;            // kWin instances: position where the window's tensor maps begin
-  FastDiv by_groups, by_n_kv, by_g;   // kWin instances: divisions of decode_unit
   float c;              // scale * log2(e) (times the Q and K descale factors for fp8)
   float o_scale;        // multiplies O / l in the epilogue (the V descale for fp8, else 1)
   int groups;           // B * n_kv
@@ -143,6 +141,15 @@ struct Params {
   int batch;            // groups per batch (see decode_unit)
   long long spin_limit;
 };
+// A type of its own, so that what the plain instances are given (and so their code, to
+// the last register) does not depend on it.
+struct WindowParams : Params {
+  int window, sinks;    // W and S, both at most Lk
+  int first;            // position where the window's tensor maps begin
+  FastDiv by_groups, by_n_kv, by_g;   // divisions of decode_unit
+};
+template <bool kWin>
+using ParamsOf = std::conditional_t<kWin, WindowParams, Params>;
 
 #ifdef ATTN_DEBUG
 // Debug build: how many phases each barrier's producer has started (TMA loads
@@ -231,10 +238,10 @@ __device__ __forceinline__ int list_tile(const Unit& x, int j) {
 // and paired neighbour by neighbour: slot 1 holds the longer (or equal) tile,
 // slot 0 the next one, and their key-tile counts differ by at most one.
 template <bool kWin>
-__device__ __forceinline__ Unit decode_unit(int u, const Params& p) {
+__device__ __forceinline__ Unit decode_unit(int u, const ParamsOf<kWin>& p) {
   Unit x;
   int pair, grp;
-  if (kWin) {
+  if constexpr (kWin) {
     // one batch, and no division: every role decodes each unit between two units' work
     pair = p.by_groups.of(u);
     grp = u - pair * p.groups;
@@ -255,7 +262,9 @@ __device__ __forceinline__ Unit decode_unit(int u, const Params& p) {
   for (int s = 0; s < 2; ++s) {
     const int k = 2 * pair + (1 - s);
     if (k < total) {
-      const int kt = kWin ? p.by_g.of(k) : k / p.g;
+      int kt;
+      if constexpr (kWin) kt = p.by_g.of(k);
+      else kt = k / p.g;
       const int i = p.Tq - 1 - kt;
       x.head[s] = x.kvh * p.g + (kWin ? k - kt * p.g : k % p.g);
       x.qtile[s] = i;
@@ -268,7 +277,7 @@ __device__ __forceinline__ Unit decode_unit(int u, const Params& p) {
       x.n[s] = 0;
     }
   }
-  if (kWin) {
+  if constexpr (kWin) {
     // (slot 0 holds the earlier of two different query tiles: the list begins
     // where its window does, and slot 1 may find one whole tile masked)
     const int q0 = p.offset + (x.n[0] > 0 ? x.qtile[0] : x.qtile[1]) * kBM;
@@ -347,7 +356,7 @@ __global__ void __launch_bounds__(64, 1) wait_selftest_kernel(const Params p) {
 template <int D, bool F8, bool kWin>
 __device__ void load_role(const CUtensorMap* tmQ, const CUtensorMap* tmK,
                           const CUtensorMap* tmV, const CUtensorMap* tmKs,
-                          const CUtensorMap* tmVs, Ctl& ctl, const Params& p,
+                          const CUtensorMap* tmVs, Ctl& ctl, const ParamsOf<kWin>& p,
                           uint32_t sQ0, uint32_t sQ1, uint32_t sKV, uint32_t smem_end) {
   using TL = Tile<D, F8>;
   // Run by lane 0 alone: a whole warp polling the ring barriers would cost
@@ -397,7 +406,8 @@ __device__ void load_role(const CUtensorMap* tmQ, const CUtensorMap* tmK,
       // (kWin: the sinks' maps begin at position 0; the window's begin at p.first, before
       // which a tile that starts there reads zeros)
       const bool sink = kWin && j < x.na;
-      const int key0 = list_tile<kWin>(x, j) * kBN - (kWin && !sink ? p.first : 0);
+      int key0 = list_tile<kWin>(x, j) * kBN;
+      if constexpr (kWin) key0 -= sink ? 0 : p.first;
 #pragma unroll
       for (int kind = 0; kind < 2; ++kind) {
         const CUtensorMap* tm = kind ? (sink ? tmVs : tmV) : (sink ? tmKs : tmK);
@@ -476,7 +486,7 @@ __device__ __forceinline__ void issue_pv(bool leader, uint32_t d_tmem, uint32_t 
 }
 
 template <int D, bool F8, bool kWin>
-__device__ void mma_role(Ctl& ctl, const Params& p, uint32_t tmem, uint32_t sQ0, uint32_t sQ1,
+__device__ void mma_role(Ctl& ctl, const ParamsOf<kWin>& p, uint32_t tmem, uint32_t sQ0, uint32_t sQ1,
                          uint32_t sKV, uint32_t smem_end) {
   using TL = Tile<D, F8>;
   // The whole warp runs this loop (so its control flow and descriptor math
@@ -637,7 +647,7 @@ __device__ __forceinline__ float row_max128(const float* v) {
 }
 
 template <int D, bool F8, bool kPos, bool kWin>
-__device__ void softmax_role(int slot, Ctl& ctl, const Params& p, uint32_t tmem,
+__device__ void softmax_role(int slot, Ctl& ctl, const ParamsOf<kWin>& p, uint32_t tmem,
                              uint32_t o_stage) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r = (warp & 3) * 32 + lane;                         // tile row = TMEM lane
@@ -699,7 +709,7 @@ __device__ void softmax_role(int slot, Ctl& ctl, const Params& p, uint32_t tmem,
       // Keys after in-tile index `keep` are masked: past the row's absolute
       // position (causal; the diagonal tile, or the last two tiles when the
       // chunk offset is not a multiple of the tile), or past the last key.
-      if (kWin) {
+      if constexpr (kWin) {
         // A sinks' tile holds the keys below min(S, low); a window's tile the keys
         // from `low` on, of which a row sees those up to its position and either
         // within W of it or below S. As bits of the tile's keys, 32 at a time.
@@ -863,7 +873,8 @@ __device__ void softmax_role(int slot, Ctl& ctl, const Params& p, uint32_t tmem,
 template <int D, bool F8, bool kPos, bool kWin>
 __device__ __forceinline__ void forward_body(const CUtensorMap& tmQ, const CUtensorMap& tmK,
                                              const CUtensorMap& tmV, const CUtensorMap& tmKs,
-                                             const CUtensorMap& tmVs, const Params& p) {
+                                             const CUtensorMap& tmVs,
+                                             const ParamsOf<kWin>& p) {
   using TL = Tile<D, F8>;
   extern __shared__ uint8_t dyn_smem[];
   __shared__ Ctl ctl;
@@ -945,7 +956,7 @@ attn_prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
                            const __grid_constant__ CUtensorMap tmK,
                            const __grid_constant__ CUtensorMap tmV,
                            const __grid_constant__ CUtensorMap tmKs,
-                           const __grid_constant__ CUtensorMap tmVs, const Params p) {
+                           const __grid_constant__ CUtensorMap tmVs, const WindowParams p) {
   forward_body<D, F8, kPos, true>(tmQ, tmK, tmV, tmKs, tmVs, p);
 }
 
@@ -1130,7 +1141,7 @@ void launch_instance(int grid, cudaStream_t stream, const CUtensorMap& mq, const
 template <bool kPos>
 void launch_window(int grid, cudaStream_t stream, const CUtensorMap& mq, const CUtensorMap& mk,
                    const CUtensorMap& mv, const CUtensorMap& mks, const CUtensorMap& mvs,
-                   const Params& p, int d_h) {
+                   const WindowParams& p, int d_h) {
   if (d_h == 128)
     attn_prefill_window_kernel<128, false, kPos>
         <<<grid, kThreads, Tile<128, false>::kSmemBytes, stream>>>(mq, mk, mv, mks, mvs, p);
@@ -1166,7 +1177,7 @@ attn_status_t launch_forward(const void* q, const void* k, const void* v, void* 
                      !encode_bhld(&mvs, v, d_h, n_kv, Lk, B, f8, 0, sinks)))
     return ATTN_ERR_CUDA;
 
-  Params p;
+  WindowParams p;        // (the plain instances take its first part)
   p.o = static_cast<uint16_t*>(o);
   p.lse = lse;
   p.status = status;
