@@ -625,6 +625,11 @@ dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
   // is a whole 128-query tile, so every product has N = 128 (or D): the
   // tensor cores get 64-cycle MMAs, which one issuing thread keeps up with.
   constexpr uint32_t cS = 0, cP = 128, cDV = 256, cDK = 256 + D;
+  // Whether dO is waited for by itself: at d_h = 64 the products are so short that the
+  // MMA warp's wait costs more than S^T gains by not waiting for dO (32768 tokens of one
+  // head 483 us for the whole gradient, 465 with Q and dO on one barrier; at 128 dK/dV
+  // behind a window of 4096 490 and 502).
+  constexpr bool kApart = D == 128;
 
   if (warp == kLoadWarp) {
     if (lane == 0) {
@@ -646,19 +651,24 @@ dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
         if (t >= kStagesQ &&
             !wait_bounded(smem_addr(&sy.empty[sq]), (t / kStagesQ - 1) & 1, sy, p))
           break;
+        auto do_free = [&]() {
+          return t < kStagesDO ||
+                 wait_bounded(smem_addr(&sy.do_empty[sd]), (t / kStagesDO - 1) & 1, sy, p);
+        };
+        if (!kApart && !do_free()) break;
         const uint32_t qbar = smem_addr(&sy.full[sq]);
-        mbar_arrive_expect_tx(qbar, kTileBytes);
+        mbar_arrive_expect_tx(qbar, (kApart ? 1 : 2) * kTileBytes);
         for (int c = 0; c < D / 64; ++c)
           tma_load_4d(sQ0 + sq * kTileBytes + c * kT * 128, &tmQ, qbar, c * 64, h, i * kT, b);
         ++nq;
-        if (t >= kStagesDO &&
-            !wait_bounded(smem_addr(&sy.do_empty[sd]), (t / kStagesDO - 1) & 1, sy, p))
-          break;
-        const uint32_t dbar = smem_addr(&sy.do_full[sd]);
-        mbar_arrive_expect_tx(dbar, kTileBytes);
+        if (kApart && !do_free()) break;
+        const uint32_t dbar = kApart ? smem_addr(&sy.do_full[sd]) : qbar;
+        if (kApart) {
+          mbar_arrive_expect_tx(dbar, kTileBytes);
+          ++ndo;
+        }
         for (int c = 0; c < D / 64; ++c)
           tma_load_4d(sDO0 + sd * kTileBytes + c * kT * 128, &tmdO, dbar, c * 64, h, i * kT, b);
-        ++ndo;
         // the statistics of step t - 2 have been read once its dK product was issued
         if (t >= 2 && !wait_bounded(smem_addr(&sy.empty[(t - 2) % kStagesQ]),
                                     ((t - 2) / kStagesQ) & 1, sy, p))
@@ -687,11 +697,14 @@ dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
       return true;
     };
     auto wait_q = [&](int t) { return wait_all(sy.full[t % kStagesQ], t / kStagesQ); };
-    auto wait_do = [&](int t) { return wait_all(sy.do_full[t % kStagesDO], t / kStagesDO); };
+    auto wait_do = [&](int t) {
+      return !kApart || wait_all(sy.do_full[t % kStagesDO], t / kStagesDO);
+    };
     if (ok && (ok = wait_q(0))) {
       mma_scores_full_ss<D>(leader, tmem + cS, sK, q_of(0));                      // S^T  = K Q^T
       if (leader) mma_commit(smem_addr(&sy.s_full[0]));
-      if ((ok = wait_do(0)))
+      ok = wait_do(0);
+      if (ok)
         mma_scores_full_ss<D>(leader, tmem + cP, sV, do_of(0));                   // dP^T = V dO^T
       if (leader) mma_commit(smem_addr(&sy.dp_full));
     }
