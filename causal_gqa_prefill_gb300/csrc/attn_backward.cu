@@ -96,6 +96,13 @@ struct BwdParams {
   uint16_t* dv;
   int* status;
   int q_units;              // dQ work units: B * n_q * T query tiles
+  // Rows that see one key: the first `one_key_rows` (0, 1 or all L). Their weight is 1
+  // whatever the score, so dS is 0; what rounding leaves of dP - D (the tensor cores' sum
+  // less the row kernel's, 1e-6 of |dO| |V|) would be all that their dQ is. So is it of
+  // dK where all rows are such: dk_scale, what dK is multiplied by, is then 0. (Both keep
+  // what is not a number.)
+  int one_key_rows;
+  float dk_scale;           // else scale
   // kWin instances
   int window, sinks;        // W and S, both at most L
   int heavy, pieces;        // key tiles that hold a sink, and CTAs per such tile
@@ -821,7 +828,7 @@ dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
           continue;
         }
         if (q < kHalfOut) store_chunk(lane_base + cDV + col, p.dv + koff + col, 1.0f, valid);
-        else store_chunk(lane_base + cDK + col, p.dk + koff + col, p.scale, valid);
+        else store_chunk(lane_base + cDK + col, p.dk + koff + col, p.dk_scale, valid);
       }
     }
   }
@@ -859,7 +866,7 @@ join_kernel(const BwdParams p, int groups, int j0, int tiles, int pieces, long l
     sum.z += v.z;
     sum.w += v.w;
   }
-  const float mul = which ? p.scale : 1.0f;
+  const float mul = which ? p.dk_scale : 1.0f;
   const long long b = grp / p.n_kv, kvh = grp % p.n_kv;
   uint16_t* out = (which ? p.dk : p.dv) + ((b * p.L + row) * p.n_kv + kvh) * D + col;
   *reinterpret_cast<uint2*>(out) =
@@ -1050,6 +1057,8 @@ dq_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUten
       if (64 * cw < D) row_to_tmem<64>(lane_base + cQ + 32 * cw, q_rows + qoff + 64 * cw, row < p.L);
       const size_t srow = (static_cast<size_t>(x.b) * p.n_q + x.h) * (p.T * kT) + row;
       nl = p.nlse2[srow];
+      // a row that sees one key: P, which is for dS alone here, is 0
+      if (row < p.one_key_rows) nl -= INFINITY;
       nd = p.nrowdot[srow];
       tmem_wait_st();
       tc_fence_before_sync();
@@ -1407,6 +1416,9 @@ attn_status_t backward(const void* q, const void* k, const void* v, const void* 
   p.dv = static_cast<uint16_t*>(dv);
   p.status = status;
   p.q_units = static_cast<int>(B * n_q * T);
+  const bool all_one = L == 1 || (win && window == 1 && sinks == 0);
+  p.one_key_rows = all_one ? p.L : causal ? 1 : 0;
+  p.dk_scale = all_one ? 0.0f : scale;
   p.window = static_cast<int>(window < L ? window : L);
   p.sinks = static_cast<int>(sinks < L ? sinks : L);
   p.heavy = static_cast<int>(split.heavy);

@@ -438,6 +438,9 @@ attn_status_t attn_cache_evict(const void* k, const void* v, const float* weight
  * where the sums for dK and dV run over every query head of the K/V head's
  * group. No atomics: results are deterministic.
  *
+ * A row that sees one key (position 0 with causal = 1, or L = 1) has the weight 1 and
+ * dS = 0 exactly: its dq is 0, and with L = 1 so is dk.
+ *
  *   q, k, v, o, lse   the forward's inputs and outputs (layouts above)
  *   dout              bf16 [B, L, n_q, d_h], 16-byte aligned
  *   dq                bf16 [B, L, n_q, d_h]   written
@@ -467,7 +470,8 @@ attn_status_t attn_prefill_bwd(const void* q, const void* k, const void* v, cons
 
 /*
  * Backward of attn_prefill_window_fwd with Lq = Lk = L: attn_prefill_bwd with the
- * sums over J(i) of that call. Key tiles that hold sinks, which every later row
+ * sums over J(i) of that call (behind a window of 1 without sinks every row sees one
+ * key: dq = dk = 0). Key tiles that hold sinks, which every later row
  * sees, are cut into parts that a fourth kernel adds, in a fixed order: results
  * are deterministic. Its workspace depends on window and sinks too; window >= 1
  * and sinks >= 0 (ATTN_ERR_INVALID_ARG otherwise). Everything else as
