@@ -146,9 +146,12 @@ attn_status_t attn_prefill_fwd_chunk(const void* q, const void* k, const void* v
  *            nothing
  *   sinks    >= 0 (ATTN_ERR_INVALID_ARG otherwise); 0: a plain window
  *   Positions of k and v that no row of the call sees (of a chunk: those from
- *   `sinks` up to Lk - Lq - window) may hold anything, NaN included. A position
- *   that some rows see must be finite for the results of the other rows in its
- *   256 neighbours to be. Everything else as attn_prefill_fwd_chunk.
+ *   `sinks` up to Lk - Lq - window) may hold anything, NaN included. A row multiplies
+ *   whole tiles of V, by 0 where it does not see them, so what is not finite in V at a
+ *   position j that some rows see may reach every row from position j - 254 to
+ *   j + window + 381 (the last that sees j is at j + window - 1; of a sink, every row
+ *   from j - 254 on); in K it reaches only the rows that see j. Everything else as
+ *   attn_prefill_fwd_chunk.
  */
 attn_status_t attn_prefill_window_fwd(const void* q, const void* k, const void* v,
                                       void* o, float* lse, int64_t B, int64_t Lq, int64_t Lk,
@@ -441,6 +444,10 @@ attn_status_t attn_cache_evict(const void* k, const void* v, const float* weight
  *
  * where the sums for dK and dV run over every query head of the K/V head's
  * group. No atomics: results are deterministic.
+ *
+ * Whole tiles of 128 rows by 128 keys are multiplied: what is not finite in q, k, v, o
+ * or dout may also reach the gradients of rows and keys of its tiles that it is masked
+ * from.
  *
  * A row that sees one key (position 0 with causal = 1, or L = 1) has the weight 1 and
  * dS = 0 exactly: its dq is 0, and with L = 1 so is dk.
