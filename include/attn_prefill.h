@@ -282,8 +282,10 @@ attn_status_t attn_decode_ragged_fwd(const void* q, const void* k, const void* v
  *     j < lens[b]  with  j >= lens[b] - window  or  j < sinks
  *
  *   window >= 1, sinks >= 0 (ATTN_ERR_INVALID_ARG otherwise). Only the visible
- *   positions are read; the others of k and v may hold anything (NaN included).
- *   Everything else as attn_decode_ragged_fwd without weights.
+ *   positions count; rows of the cache that come along in a copy (up to 127 behind
+ *   lens[b], and those that fill the sinks up to a multiple of 8, or of 128 where they
+ *   are more than 120) are dropped, and those and all others of k and v may hold
+ *   anything (NaN included). Everything else as attn_decode_ragged_fwd without weights.
  */
 int64_t attn_decode_window_workspace_bytes(int64_t B, int64_t C, int32_t n_q, int32_t n_kv,
                                            int32_t d_h, int64_t window,
