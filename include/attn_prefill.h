@@ -484,9 +484,11 @@ attn_status_t attn_prefill_bwd(const void* q, const void* k, const void* v, cons
 /*
  * Backward of attn_prefill_window_fwd with Lq = Lk = L: attn_prefill_bwd with the
  * sums over J(i) of that call (behind a window of 1 without sinks every row sees one
- * key: dq = dk = 0). Key tiles that hold sinks, which every later row
- * sees, are cut into parts that a fourth kernel adds, in a fixed order: results
- * are deterministic. Its workspace depends on window and sinks too; window >= 1
+ * key: dq = dk = 0). Key tiles that hold sinks, which every later row sees, are cut
+ * into parts; so are, behind a window shorter than L, all other key tiles where a call
+ * has fewer of them than the GPU has SMs and that shortens it. One further kernel for
+ * each of the two adds the parts in a fixed order (three to five kernels in all):
+ * results are deterministic. Its workspace depends on window and sinks too; window >= 1
  * and sinks >= 0 (ATTN_ERR_INVALID_ARG otherwise). Everything else as
  * attn_prefill_bwd.
  */
