@@ -371,15 +371,21 @@ __device__ __forceinline__ void teardown(Sync& sy, const BwdParams& p, bool lead
   }
 }
 
+// What is added to a product with `mul`: nothing (x + -0 is x), but products with 0 all
+// become +0.
+__device__ __forceinline__ float plus_zero(float mul) { return mul == 0.0f ? 0.0f : -0.0f; }
+
 // 32 bf16 outputs of this thread's row from 32 fp32 TMEM columns, times `mul`.
 __device__ __forceinline__ void store_chunk(uint32_t taddr, uint16_t* dst, float mul, bool valid) {
   uint32_t v[32];
   tmem_ld32(taddr, v);
   tmem_wait_ld(v);
+  const float zero = plus_zero(mul);
   uint32_t w[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i)
-    w[i] = pack_bf16x2(__uint_as_float(v[2 * i]) * mul, __uint_as_float(v[2 * i + 1]) * mul);
+    w[i] = pack_bf16x2(fmaf(__uint_as_float(v[2 * i]), mul, zero),
+                       fmaf(__uint_as_float(v[2 * i + 1]), mul, zero));
   if (valid) {
     uint4* d4 = reinterpret_cast<uint4*>(dst);
 #pragma unroll
@@ -866,11 +872,12 @@ join_kernel(const BwdParams p, int groups, int j0, int tiles, int pieces, long l
     sum.z += v.z;
     sum.w += v.w;
   }
-  const float mul = which ? p.dk_scale : 1.0f;
+  const float mul = which ? p.dk_scale : 1.0f, zero = plus_zero(mul);
   const long long b = grp / p.n_kv, kvh = grp % p.n_kv;
   uint16_t* out = (which ? p.dk : p.dv) + ((b * p.L + row) * p.n_kv + kvh) * D + col;
   *reinterpret_cast<uint2*>(out) =
-      make_uint2(pack_bf16x2(sum.x * mul, sum.y * mul), pack_bf16x2(sum.z * mul, sum.w * mul));
+      make_uint2(pack_bf16x2(fmaf(sum.x, mul, zero), fmaf(sum.y, mul, zero)),
+                 pack_bf16x2(fmaf(sum.z, mul, zero), fmaf(sum.w, mul, zero)));
 }
 
 // ------------------------------------------------------------------------ dQ

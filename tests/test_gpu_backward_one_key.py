@@ -2,7 +2,7 @@
 so dS = P (dP - D) is 0 and with it what the row gives to dQ and dK, exactly.
 
 A row sees one key at position 0 of a causal call, everywhere behind a window of 1
-without sinks, and in a call over one position. Zeros are compared as they are. dV is
+without sinks, and in a call over one position. Zeros are compared bit by bit (no -0). dV is
 the sum of the group's dO in fp32 and rounds to bf16 once: |dV - ref| <= 2^-8 |ref| +
 g 2^-23 sum |dO| (the weight is 1 to within 2^-20 and 1 in bf16). The other rows, keys
 and gradients: oracle.window.backward's sums and half a bf16 step of the result, as for
@@ -50,7 +50,7 @@ def gradients(B, L, n_q, n_kv, d, window=None, sinks=0, causal=True, seed=0, spo
 
 def check_only_dv(grads, do, n_kv):
     dq, dk, dv = grads
-    assert not dq.any() and not dk.any()
+    assert not dq.view(torch.int16).any() and not dk.view(torch.int16).any()
     B, L, n_q, d = do.shape
     do = to_np(do).reshape(B, L, n_kv, n_q // n_kv, d)
     ref, size = do.sum(3), np.abs(do).sum(3)
