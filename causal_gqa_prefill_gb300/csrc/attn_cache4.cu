@@ -4,11 +4,11 @@
 //
 // over each group of 32 channels of a row and head. Inputs are bf16, so lo is
 // one of them and exact. Both kernels move bytes (256 of bf16 and 80 of codes per
-// row), but packing's arithmetic costs as much as they do unless it is kept short
-// (32768 rows of 8 heads, 134 MB and 42 MB: packing 31 us, issue slots 70 % full;
-// unpacking 27.5 us, 5 TB/s read while written; 20.6 at the copy rate):
-// eight lanes take a row, half a group each (with four a lane the group's extremes
-// and scale are worked out twice as often: 49 us where this takes less than half),
+// row), but packing's arithmetic costs more than they do (18432 positions of 8 heads,
+// K and V, 99 MB in and out: 29 us where the copy rate would take 15, 31.6 alone and
+// cold, issue slots 71 % full; 32768 of them, 176 MB: 42 for 26.5; unpacking those 29,
+// 27.3 alone and cold, 97 % of the copy rate). What keeps it at that: eight lanes take a
+// row, half a group each, so that two of them work out a group's scale and not more,
 // extremes on packed pairs, quotients by a reciprocal and one correction, two at once,
 // rounding and joining of the codes in fp32's and integer multiply-adds.
 //

@@ -41,7 +41,9 @@
 // CTAs left. Lengths are read on the device.
 //
 // Measured: 16 sequences of 1024 to 8192 positions, 32 heads on 8, 32 us (95 MB of
-// rows: 14 us at the copy rate); one of 131072, 36 heads on 6, 36.5 us (126 MB: 19 us).
+// rows: 14 us at the copy rate); one of 131072, 36 heads on 6, 36.5 us (126 MB: 19 us);
+// 64 sequences behind a window of 1024 with 4 sinks, 32 heads on 8, 31.6 us (79 MB: 12;
+// 128 heads on 8: 50).
 // Longer lists cost 22 us more per 126 MB, 87 % of the copy rate; some 13 us are there
 // whatever the length: finding the runs, the first step's copies, the merge and the
 // combine.
@@ -81,8 +83,11 @@ constexpr float kRescale = 8.0f;                   // lazy running maximum (log2
 // so that nothing has to be told apart from a maximum of -inf.
 constexpr float kNoMax = -3.4028234663852886e38f;
 
-// NT: the group's query heads in tiles of 8. 12 warps fit the registers with one
-// tile, 8 with two.
+// NT: the group's query heads in tiles of 8: one where they fit, as 12 warps of it have
+// the registers, and 8 with two, whose second tile does the work of 8 heads for as few as
+// there are. (16 sequences of up to 8192 positions: 8 heads a group 32.6 us in one tile,
+// 42.3 in two; 9, 12 and 16 heads 43, 44 and 45. One of 131072: 36.6 and 48.4; 12 and 16
+// heads 50. With two the compiler spills: 32 bytes a thread stored, 16 loaded.)
 template <int NT>
 constexpr int kWarpsOf = NT == 1 ? 12 : 8;
 template <int NT>
