@@ -40,10 +40,10 @@
 // tiles, the others (key_split). Measured: 8192 tokens, 32 heads on 8, W = 1024 and
 // S = 4: rowdot 25, dkdv 220, dq 178, the join 6 us (323 GFLOP of five products: 171 at
 // the burst rate; seven are run, as S and dP are rebuilt twice). A dkdv step takes
-// about 2300 cycles where its four products are 2048 of the tensor pipe (at its own
-// rate; 2600 at what a library product reaches under the power cap), and a CTA 14000
-// beside its steps. A tile of dq takes 2200 for 1536, its exponentials' chain: 133 us
-// for the 19040 tiles, and the other 45 are the borders of 13.5 units an SM.
+// about 2300 cycles where its four products are 2048 of the tensor pipe at its own rate
+// (2600 at the burst rate), and a CTA 14000 beside its steps. A tile of dq takes 2200 for
+// 1536, its exponentials' chain: 133 us for the 19040 tiles; the other 45 are the borders
+// of 13.5 units an SM.
 //
 // Each kernel has a TMA producer warp, an MMA warp (warp-wide loop, one elected
 // issuing lane) and kComputeWGs compute warpgroups that split the 128 columns
