@@ -383,8 +383,8 @@ attn_status_t attn_cache_unpack4(const void* k4, const void* v4, void* k, void* 
  *       |O - O_exact| <= 2^-8 ((1 + 2^-6) A + |O_exact|)
  *                        + (2 E + (1 + n) 2^-20) (sum_j p_j (|lo_j| + |V_j|) + |O_exact|)
  *   where n counts the fp32 additions in a row: the chunks of 16 visible positions of
- *   the head that one warp adds, at most ceil(chunks of all sequences and K/V heads /
- *   1824) (1216 where n_q / n_kv > 8), and then the warps that the head is spread over.
+ *   the head that one warp adds, at most 1 + ceil(chunks of all sequences and K/V heads
+ *   / 1824) (1216 where n_q / n_kv > 8), and then the warps that the head is spread over.
  *   LSE is off by E + (2 + n) 2^-21 + 2^-22 |LSE|.
  *   Everything else as attn_decode_ragged_fwd. Two kernels, programmatic
  *   dependents; no atomics: results are deterministic.
